@@ -104,16 +104,22 @@ def load() -> ctypes.CDLL:
                                        ctypes.c_float, vp, i32, vp, ctypes.c_size_t,
                                        ctypes.POINTER(DecodeOpts), vp, vp]
             lib.gqa_decode.restype = ctypes.c_int
+            lib.gqa_decode_sinks.argtypes = [*lib.gqa_decode.argtypes[:-2], i32, vp, vp]
+            lib.gqa_decode_sinks.restype = ctypes.c_int
             lib.gqa_decode_noalloc.argtypes = [ctypes.POINTER(KVCacheDesc), vp, i32, i32, vp, i32,
                                                vp, i32, ctypes.c_float, vp, i32,
                                                ctypes.POINTER(DecodeOpts), vp, vp]
             lib.gqa_decode_noalloc.restype = ctypes.c_int
+            lib.gqa_decode_noalloc_sinks.argtypes = [*lib.gqa_decode_noalloc.argtypes[:-2], i32, vp, vp]
+            lib.gqa_decode_noalloc_sinks.restype = ctypes.c_int
             lib.gqa_kv_append_varlen.argtypes = [ctypes.POINTER(KVCacheDesc), vp, vp, i32, vp, i32, vp,
                                                  i32, vp, i32, vp, vp]
             lib.gqa_kv_append_varlen.restype = ctypes.c_int
             lib.gqa_prefill.argtypes = [ctypes.POINTER(KVCacheDesc), vp, i32, i32, vp, i32, vp, i32, vp,
                                         i32, ctypes.c_float, i32, vp, i32, i32, vp, vp]
             lib.gqa_prefill.restype = ctypes.c_int
+            lib.gqa_prefill_sinks.argtypes = [*lib.gqa_prefill.argtypes[:12], i32, *lib.gqa_prefill.argtypes[12:]]
+            lib.gqa_prefill_sinks.restype = ctypes.c_int
             _lib = lib
     return _lib
 
@@ -327,12 +333,13 @@ def gqa_decode(cache: PagedKVCache, q: torch.Tensor, block_tables: torch.Tensor,
                out_dtype: torch.dtype = torch.float32, workspace: Optional[torch.Tensor] = None,
                kernel: int = KERNEL_AUTO, max_warps: int = 0, min_blocks_per_warp: int = 0,
                events: Optional[tuple] = None, err: Optional[torch.Tensor] = None,
-               stream=None, window: int = 0, row_layout: int = 0) -> torch.Tensor:
+               stream=None, window: int = 0, row_layout: int = 0, sinks: int = 0) -> torch.Tensor:
     """out[b,h] = softmax(scale * q[b,h] . K_g^T) V_g over context_lens[b] cached tokens.
 
     q is [B, H, d] (one new token per sequence) or [B, T, H, d] (T new tokens,
     causal among themselves); ``window`` > 0 keeps each query's last ``window``
-    positions. ``out`` has q's shape."""
+    positions, and with ``sinks`` > 0 the sequence's first ``sinks`` as well
+    (without a window, ``sinks`` changes nothing). ``out`` has q's shape."""
     T = 1 if q.dim() == 3 else int(q.shape[1])
     B, H, d = q.shape[0], q.shape[-2], q.shape[-1]
     qp, tp, lp = _dev(q, "q"), _dev(block_tables, "block_tables", True), _dev(context_lens, "context_lens", True)
@@ -352,10 +359,10 @@ def gqa_decode(cache: PagedKVCache, q: torch.Tensor, block_tables: torch.Tensor,
         opts.event_main_begin = events[0].cuda_event
         opts.event_main_end = events[1].cuda_event
     desc = cache.desc()
-    st = load().gqa_decode(ctypes.byref(desc), qp, DTYPE_CODE[q.dtype], H, tp,
-                           int(block_tables.shape[1]), lp, B, float(scale),
-                           op, DTYPE_CODE[out.dtype], wp, workspace.numel() * workspace.element_size(),
-                           ctypes.byref(opts), ep, _stream_ptr(stream))
+    st = load().gqa_decode_sinks(ctypes.byref(desc), qp, DTYPE_CODE[q.dtype], H, tp,
+                                 int(block_tables.shape[1]), lp, B, float(scale),
+                                 op, DTYPE_CODE[out.dtype], wp, workspace.numel() * workspace.element_size(),
+                                 ctypes.byref(opts), int(sinks), ep, _stream_ptr(stream))
     _check(st, "gqa_decode")
     return out
 
@@ -364,7 +371,7 @@ def gqa_decode_noalloc(cache: PagedKVCache, q: torch.Tensor, block_tables: torch
                        context_lens: torch.Tensor, scale: float, out: Optional[torch.Tensor] = None,
                        out_dtype: torch.dtype = torch.float32, kernel: int = KERNEL_AUTO,
                        err: Optional[torch.Tensor] = None, stream=None,
-                       window: int = 0) -> torch.Tensor:
+                       window: int = 0, sinks: int = 0) -> torch.Tensor:
     """gqa_decode with the library's built-in scratch instead of a workspace.
 
     For callers that may not allocate device memory; the output tensor is still
@@ -383,11 +390,11 @@ def gqa_decode_noalloc(cache: PagedKVCache, q: torch.Tensor, block_tables: torch
     op = _dev(out, "out")
     opts = DecodeOpts(T, window, kernel, 0, 0, 0, None, None)
     desc = cache.desc()
-    st = load().gqa_decode_noalloc(ctypes.byref(desc), qp, DTYPE_CODE[q.dtype], H,
-                                   tp, int(block_tables.shape[1]),
-                                   lp, B, float(scale), op,
-                                   DTYPE_CODE[out.dtype], ctypes.byref(opts), ep,
-                                   _stream_ptr(stream))
+    st = load().gqa_decode_noalloc_sinks(ctypes.byref(desc), qp, DTYPE_CODE[q.dtype], H,
+                                         tp, int(block_tables.shape[1]),
+                                         lp, B, float(scale), op,
+                                         DTYPE_CODE[out.dtype], ctypes.byref(opts), int(sinks), ep,
+                                         _stream_ptr(stream))
     _check(st, "gqa_decode_noalloc")
     return out
 
@@ -421,9 +428,10 @@ def gqa_prefill(cache: PagedKVCache, q: torch.Tensor, q_start: torch.Tensor, max
                 block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float,
                 out: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.float32,
                 window: int = 0, err: Optional[torch.Tensor] = None, stream=None,
-                kernel: int = 0) -> torch.Tensor:
+                kernel: int = 0, sinks: int = 0) -> torch.Tensor:
     """Causal attention of each sequence's new tokens (rows q_start[b] .. of q
-    [total, H, d]) over its paged cache, new tokens included. kernel: 0 auto,
+    [total, H, d]) over its paged cache, new tokens included; ``window`` and
+    ``sinks`` as in ``gqa_decode``. kernel: 0 auto,
     1 tcgen05 one-tile (32-token chunks), 2 warp-level mma.sync, 3 tcgen05
     two-tile (64-token chunks, head_dim 128), 4 tcgen05 one-tile with 64-token
     chunks and two CTAs per SM (head_dim 128)."""
@@ -443,10 +451,11 @@ def gqa_prefill(cache: PagedKVCache, q: torch.Tensor, q_start: torch.Tensor, max
         out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
     op = _dev(out, "out")
     desc = cache.desc()
-    st = load().gqa_prefill(ctypes.byref(desc), args[0], DTYPE_CODE[q.dtype], int(q.shape[1]),
-                            args[1], int(max_new_tokens), args[2],
-                            int(block_tables.shape[1]), args[3], B, float(scale), int(window),
-                            op, DTYPE_CODE[out.dtype], int(kernel), args[4], _stream_ptr(stream))
+    st = load().gqa_prefill_sinks(ctypes.byref(desc), args[0], DTYPE_CODE[q.dtype], int(q.shape[1]),
+                                  args[1], int(max_new_tokens), args[2],
+                                  int(block_tables.shape[1]), args[3], B, float(scale), int(window),
+                                  int(sinks), op, DTYPE_CODE[out.dtype], int(kernel), args[4],
+                                  _stream_ptr(stream))
     _check(st, "gqa_prefill")
     return out
 

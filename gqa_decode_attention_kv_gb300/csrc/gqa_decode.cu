@@ -9,7 +9,7 @@ namespace gqa {
 namespace dec {
 
 bool pick_plain(int dtype, int kind, int d, int nw, Variant& v) {
-    return pick_variant<false>(dtype, kind, d, nw, v);
+    return pick_variant<false, false>(dtype, kind, d, nw, v);
 }
 
 }  // namespace dec
@@ -155,8 +155,11 @@ int launch_decode(const DecodeLaunch& L, int num_sms) {
     if (kind == 0) kind = (c.dtype == GQA_DTYPE_F32 || (dtype_coded(c.dtype) && D != 128)) ? kKernelFma : kKernelMma;
     Variant v{};
     const bool general = T > 1 || L.window > 0;
+    const bool sinks = L.window > 0 && L.sinks > 0;
     auto pick = [&](int warps) {
-        return general ? pick_general(c.dtype, kind, D, warps, v) : pick_plain(c.dtype, kind, D, warps, v);
+        return sinks     ? pick_sinks(c.dtype, kind, D, warps, v)
+               : general ? pick_general(c.dtype, kind, D, warps, v)
+                         : pick_plain(c.dtype, kind, D, warps, v);
     };
     // More than 8 rows: by default the CTA's warps share each tile (measured
     // faster than 8-row unit streams at 16, 32 and 64 rows: the per-block
@@ -203,7 +206,14 @@ int launch_decode(const DecodeLaunch& L, int num_sms) {
     }
 
     const int smem = v.smem(L.batch);
-    const int workers = workers_of(v, L.batch, num_sms);
+    int workers = workers_of(v, L.batch, num_sms);
+    if (sinks) {
+        // the workspace is sized from the other flavours' workers alone, so that
+        // its size does not depend on the options
+        Variant g{};
+        if (pick_general(c.dtype, kind, D, nrg > 1 || GT <= kHeadsPerWarp ? 1 : warps_for_rows(GT), g))
+            workers = std::min(workers, workers_of(g, L.batch, num_sms));
+    }
     if (workers < 1) return GQA_ERR_UNSUPPORTED;
     int grid = workers / v.workers_per_cta;
     cudaError_t e;
@@ -241,6 +251,7 @@ int launch_decode(const DecodeLaunch& L, int num_sms) {
     a.NRG = nrg;
     a.RS = RS;
     a.window = L.window;
+    a.sinks = sinks ? (int)std::min<long long>(L.sinks, (long long)L.max_blocks * kBlock) : 0;
     a.max_blocks = L.max_blocks;
     a.out_dtype = L.out_dtype;
     a.q_dtype = L.q_dtype;

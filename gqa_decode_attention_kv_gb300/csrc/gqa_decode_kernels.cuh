@@ -1,8 +1,9 @@
 // gqa_decode_kernels.cuh -- the split-KV decode kernel and the combine kernel
 // as templates, with the host-side variant table. Included by gqa_decode.cu
-// (the one-token, full-attention flavour and the combine kernels) and by
+// (the one-token, full-attention flavour and the combine kernels), by
 // gqa_decode_general.cu (the flavour for several queries per sequence or a
-// sliding window), so the two sets of instantiations compile in parallel.
+// sliding window) and by gqa_decode_sinks.cu (a sliding window with sink
+// tokens), so the three sets of instantiations compile in parallel.
 //
 // Split-KV grouped-query decode attention over a paged cache.
 //
@@ -12,7 +13,10 @@
 // With T new tokens per sequence (speculative verification / chunked prefill,
 // "LLM 推理性能优化实战" sections 14.2 and 11.7) query i of sequence b sits at
 // position L_b - T + i and attends positions up to its own; with a sliding
-// window W (section 6.4.1) only the last W of those. Every (sequence, kv-head)
+// window W (section 6.4.1) only the last W of those, and with S sink tokens the
+// first S as well. The blocks that hold sinks come before the window's blocks
+// in the unit order, so the blocks between the two are never read and sinks cost
+// ceil(S / 16) blocks per (sequence, kv-head) pair. Every (sequence, kv-head)
 // pair then serves G*T query rows (row = i*G + head-in-group), all reading the
 // same K/V tiles: T widens the MMA N dimension exactly like a larger group.
 //
@@ -72,6 +76,7 @@ struct DecodeArgs {
     int T;               // new tokens (queries) per sequence
     int GT;              // query rows per (sequence, kv-head) pair: G * T
     int window;          // sliding window in tokens; 0 = full attention
+    int sinks;           // sink flavour: first tokens that stay visible
     // Unit space: Kv = K * NRG heads per sequence. NRG > 1 splits a pair's GT
     // rows into groups of 8 ("virtual kv-heads" gv = g * NRG + group), each an
     // independent unit stream that re-reads the pair's tiles (from L2, since
@@ -143,11 +148,14 @@ constexpr int kHeadsPerWarp = 8;   // query heads one warp serves (the MMA N dim
 // cycles a block, which a row warp would add to the group's pace while the
 // others waited (measured; with eight row warps the ninth caps registers at 168
 // and still wins).
-template <int kKind, typename T, int D, int kHeadWarps = 1, bool kGeneral = false>
+template <int kKind, typename T, int D, int kHeadWarps = 1, bool kGeneral = false, bool kSinkTokens = false>
 struct Cfg {
     // kGen: T > 1 queries per sequence or a sliding window (per-row ranges);
     // false compiles the one-token, full-attention step with no range logic.
+    // kSinks (only with kGen): the window keeps the first a.sinks tokens visible.
     static constexpr bool kGen = kGeneral;
+    static constexpr bool kSinks = kSinkTokens;
+    static_assert(kGen || !kSinks, "sinks come with a window");
     static constexpr bool kI8 = std::is_same<T, int8_t>::value;
     static constexpr bool kFp8 = std::is_same<T, __nv_fp8_e4m3>::value;
     static constexpr bool kKc = std::is_same<T, int4kc>::value;   // K scales per channel
@@ -236,6 +244,24 @@ __device__ __forceinline__ int first_block(const DecodeArgs& a, int L) {
     return attend_lo<kGen>(a, L) / kBlock;
 }
 
+// Blocks of a length-L sequence that only its sinks make visible: those before
+// the window's first block, counted from 0.
+template <bool kSinks>
+__device__ __forceinline__ int sink_blocks(const DecodeArgs& a, int L) {
+    if constexpr (!kSinks) return 0;
+    else return min((a.sinks + kBlock - 1) / kBlock, first_block<true>(a, L));
+}
+// Logical block of attended block j (0, 1, ...): the sinks' blocks, then the window's.
+template <bool kGen, bool kSinks>
+__device__ __forceinline__ int logical_block(const DecodeArgs& a, int L, int j) {
+    const int fb = first_block<kGen>(a, L);
+    if constexpr (!kSinks) return fb + j;
+    else {
+        const int ns = sink_blocks<true>(a, L);
+        return j < ns ? j : fb - ns + j;
+    }
+}
+
 // Row rr (0 .. GT-1) of pair (b, g) -> its row of q and out ([B, T, H, d]).
 template <bool kGen>
 __device__ __forceinline__ long long q_row(const DecodeArgs& a, int b, int g, int rr) {
@@ -258,7 +284,7 @@ __device__ __forceinline__ void row_range(const DecodeArgs& a, int L, int rr, in
 
 // Validated lengths into lens_s and the prefix pref[0..B] (pref[0] = 0) of the
 // blocks each sequence's query rows attend.
-template <bool kGen>
+template <bool kGen, bool kSinks>
 __device__ void block_prefix(const DecodeArgs& a, int* lens_s, int* pref, int* tmp) {
     const int tid = threadIdx.x, nthr = blockDim.x, lane = tid & 31, wid = tid >> 5;
     const int nw = nthr >> 5;
@@ -275,7 +301,7 @@ __device__ void block_prefix(const DecodeArgs& a, int* lens_s, int* pref, int* t
             }
             lens_s[i] = L;
         }
-        int x = (L + kBlock - 1) / kBlock - first_block<kGen>(a, L);
+        int x = (L + kBlock - 1) / kBlock - first_block<kGen>(a, L) + sink_blocks<kSinks>(a, L);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(kFull, x, o);
@@ -600,17 +626,21 @@ __device__ __forceinline__ void mma_load(MmaFrags<C, D>& f, uint32_t stage, int 
 }
 
 // Which tokens of a block the two query rows of a lane (2c, 2c+1) attend:
-// lo <= token < hi, block-relative. `partial` is false when every row of the
-// pair attends the whole block (the masks are then skipped, and the block lies
-// wholly inside the sequence).
+// lo <= token < hi, block-relative, and with sinks also the tokens below
+// min(sink, hi). `partial` is false when every row of the pair attends the whole
+// block (the masks are then skipped, and the block lies wholly inside the
+// sequence).
 struct BlockMask {
     bool partial;
     int lo0, hi0, lo1, hi1;
+    int sink;                     // sink flavour: block-relative end of the sinks
+    uint32_t seen;                // sink flavour: bit t set if some row of the pair attends token t
 };
 
 // One 16-token block on the tensor cores, from gathered operands. nvalid
 // counts the block's tokens inside the sequence; slots past it hold arbitrary
-// bits and are zeroed or masked.
+// bits and are zeroed or masked (the sink flavour does so for every token that no
+// row attends, since a page may keep tokens that left the window).
 template <class C, int D>
 __device__ __forceinline__ void mma_compute(MmaState<C, D>& st, MmaFrags<C, D>& f, int nvalid,
                                             const BlockMask& bm, int r, int c, float scale_log2) {
@@ -710,12 +740,13 @@ __device__ __forceinline__ void mma_compute(MmaState<C, D>& st, MmaFrags<C, D>& 
         if (r >= nvalid) { s0 = -INFINITY; s1 = -INFINITY; vr_s = 0.f; }
         if (r + 8 >= nvalid) { s2 = -INFINITY; s3 = -INFINITY; vr8_s = 0.f; }
     } else if (bm.partial) {
-        if (r >= nvalid) vr_s = 0.f;
-        if (r + 8 >= nvalid) vr8_s = 0.f;
-        if (r < bm.lo0 || r >= bm.hi0) s0 = -INFINITY;
-        if (r < bm.lo1 || r >= bm.hi1) s1 = -INFINITY;
-        if (r + 8 < bm.lo0 || r + 8 >= bm.hi0) s2 = -INFINITY;
-        if (r + 8 < bm.lo1 || r + 8 >= bm.hi1) s3 = -INFINITY;
+        if (C::kSinks ? !((bm.seen >> r) & 1u) : r >= nvalid) vr_s = 0.f;
+        if (C::kSinks ? !((bm.seen >> (r + 8)) & 1u) : r + 8 >= nvalid) vr8_s = 0.f;
+        const bool sink = C::kSinks && r < bm.sink, sink8 = C::kSinks && r + 8 < bm.sink;
+        if ((r < bm.lo0 && !sink) || r >= bm.hi0) s0 = -INFINITY;
+        if ((r < bm.lo1 && !sink) || r >= bm.hi1) s1 = -INFINITY;
+        if ((r + 8 < bm.lo0 && !sink8) || r + 8 >= bm.hi0) s2 = -INFINITY;
+        if ((r + 8 < bm.lo1 && !sink8) || r + 8 >= bm.hi1) s3 = -INFINITY;
     }
 
     // ---- online softmax (per head, over the 16 tokens of this block)
@@ -764,10 +795,11 @@ __device__ __forceinline__ void mma_compute(MmaState<C, D>& st, MmaFrags<C, D>& 
 
     // ---- O^T[dim][head] += V^T . P^T (high part, then low part)
     if constexpr (!C::kCoded) {
-        if (nvalid < kBlock) {
+        if (C::kSinks ? bm.partial : nvalid < kBlock) {
             // zero V of tokens past the end: the slots hold arbitrary (even NaN) bits
-            const uint32_t m01 = (2 * c < nvalid ? 0x0000ffffu : 0u) | (2 * c + 1 < nvalid ? 0xffff0000u : 0u);
-            const uint32_t m89 = (2 * c + 8 < nvalid ? 0x0000ffffu : 0u) | (2 * c + 9 < nvalid ? 0xffff0000u : 0u);
+            auto live = [&](int t) { return C::kSinks ? ((bm.seen >> t) & 1u) != 0u : t < nvalid; };
+            const uint32_t m01 = (live(2 * c) ? 0x0000ffffu : 0u) | (live(2 * c + 1) ? 0xffff0000u : 0u);
+            const uint32_t m89 = (live(2 * c + 8) ? 0x0000ffffu : 0u) | (live(2 * c + 9) ? 0xffff0000u : 0u);
 #pragma unroll
             for (int j = 0; j < C::kMt; ++j) {
                 f.v[j][0] &= m01; f.v[j][1] &= m01; f.v[j][2] &= m89; f.v[j][3] &= m89;
@@ -781,11 +813,11 @@ __device__ __forceinline__ void mma_compute(MmaState<C, D>& st, MmaFrags<C, D>& 
     } else {
         // f.v[i][w] holds dims 16r + 4w .. +3 (one byte each) of token i in
         // {2c, 2c+1, 2c+8, 2c+9}. Tokens past the end hold arbitrary codes.
-        if (nvalid < kBlock) {
+        if (C::kSinks ? bm.partial : nvalid < kBlock) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int tok = 2 * c + (i & 1) + 8 * (i >> 1);
-                if (tok >= nvalid) f.v[i][0] = f.v[i][1] = f.v[i][2] = f.v[i][3] = 0u;
+                if (C::kSinks ? !((bm.seen >> tok) & 1u) : tok >= nvalid) f.v[i][0] = f.v[i][1] = f.v[i][2] = f.v[i][3] = 0u;
             }
         }
         if constexpr (C::kFp8) {
@@ -964,7 +996,7 @@ __device__ __forceinline__ void fma_block(const DecodeArgs& a, FmaState<C, D>& s
                 if (partial) {                   // row outside its attended range?
                     int lo, hi;
                     row_range(a, len, hbase + h, lo, hi);
-                    if (bpos + t < lo || bpos + t >= hi) continue;
+                    if ((bpos + t < lo && !(C::kSinks && bpos + t < a.sinks)) || bpos + t >= hi) continue;
                 }
             }
             float dot = 0.f;
@@ -1036,12 +1068,12 @@ __device__ __forceinline__ Partition make_partition(const DecodeArgs& a, int U) 
     return pt;
 }
 
-template <int kKind, typename T, int D, int kHeadWarps, bool kGen>
-__global__ void __launch_bounds__(Cfg<kKind, T, D, kHeadWarps, kGen>::kWarps * 32,
-                                  Cfg<kKind, T, D, kHeadWarps, kGen>::kMinCtas)
+template <int kKind, typename T, int D, int kHeadWarps, bool kGen, bool kSinks>
+__global__ void __launch_bounds__(Cfg<kKind, T, D, kHeadWarps, kGen, kSinks>::kWarps * 32,
+                                  Cfg<kKind, T, D, kHeadWarps, kGen, kSinks>::kMinCtas)
 split_kv_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                 const DecodeArgs a) {
-    using C = Cfg<kKind, T, D, kHeadWarps, kGen>;
+    using C = Cfg<kKind, T, D, kHeadWarps, kGen, kSinks>;
     using S = Smem<C>;
     constexpr bool kShared = kHeadWarps > 1;     // one ring, one worker per CTA
     extern __shared__ uint8_t smem_raw[];
@@ -1058,7 +1090,7 @@ split_kv_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
     }
     launch_dependents();                       // the combine kernel may take its place now
     grid_dependency_wait();                    // inputs may come from the previous kernel
-    block_prefix<kGen>(a, lens_s, pref, tmp);
+    block_prefix<kGen, kSinks>(a, lens_s, pref, tmp);
     const Partition pt = make_partition(a, a.Kv * pref[a.B]);
     if (blockIdx.x == 0) {
         for (int i = threadIdx.x; i <= a.B; i += blockDim.x) a.ws_pref[i] = pref[i];
@@ -1132,7 +1164,7 @@ split_kv_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
         if (u < pt.U) {
             int b, g, j;
             locate(u, pref, a.B, a.Kv, b, g, j);
-            const int ph = a.block_tables[(long long)b * a.max_blocks + first_block<C::kGen>(a, lens_s[b]) + j];
+            const int ph = a.block_tables[(long long)b * a.max_blocks + logical_block<kGen, kSinks>(a, lens_s[b], j)];
             if (ph < 0 || ph >= a.num_blocks) flag_error(a.err, GQA_DEVERR_BLOCK_INDEX);
             else win_phys = ph;
             win_g = g / a.NRG;                 // the real kv-head
@@ -1292,7 +1324,7 @@ split_kv_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
     int nb_b = 0, nb_g = 0, next_u = -1;
     // Blocks cj in [cjf_lo, cjf_lo + cjf_n) of the current pair are attended
     // whole by every row (all rows attend positions [max(0, L - W), L - T + 1));
-    // the others need masks.
+    // the others need masks, the sinks' blocks among them.
     int cjf_lo = 0, cjf_n = 0;
     auto pair_ranges = [&]() {
         if constexpr (!C::kGen) return;
@@ -1302,6 +1334,7 @@ split_kv_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
         cjf_lo = (max(0, flo - c0) + kBlock - 1) / kBlock;
         const int cjf_hi = fhi - c0 >= kBlock ? (fhi - c0 - kBlock) / kBlock : -1;
         cjf_n = max(0, cjf_hi - cjf_lo + 1);
+        if constexpr (C::kSinks) cjf_lo += sink_blocks<true>(a, clen);
     };
 
     for (int k = 0;; ++k) {
@@ -1349,7 +1382,7 @@ split_kv_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
             bpos = 0;
             nvalid = kBlock;
             if (partial) {
-                bpos = (first_block<C::kGen>(a, clen) + cj) * kBlock;
+                bpos = logical_block<kGen, kSinks>(a, clen, cj) * kBlock;
                 nvalid = min((int)kBlock, clen - bpos);
             }
         }
@@ -1362,7 +1395,14 @@ split_kv_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
                 bail(k + 1);
                 return;
             }
-            BlockMask bm{partial, 0, 0, 0, 0};
+            BlockMask bm{partial, 0, 0, 0, 0, 0, 0};
+            if (C::kSinks && partial) {
+                bm.sink = a.sinks - bpos;
+                // tokens from the first query's window start on, and the sinks
+                const uint32_t below = bm.sink >= kBlock ? 0xffffu : bm.sink > 0 ? (1u << bm.sink) - 1u : 0u;
+                const int lo = min(max(attend_lo<C::kGen>(a, clen) - bpos, 0), (int)kBlock);
+                bm.seen = ((0xffffu << lo) | below) & ((1u << nvalid) - 1u);
+            }
             if (C::kGen && partial) {
                 row_range(a, clen, hbase + 2 * c, bm.lo0, bm.hi0);
                 row_range(a, clen, hbase + 2 * c + 1, bm.lo1, bm.hi1);
@@ -1560,22 +1600,22 @@ struct Variant {
     int (*smem)(int);
 };
 
-template <int kKind, typename T, int D, int NW, bool kGen>
+template <int kKind, typename T, int D, int NW, bool kGen, bool kSinks>
 Variant make_variant() {
-    using C = Cfg<kKind, T, D, NW, kGen>;
-    return Variant{reinterpret_cast<const void*>(&split_kv_kernel<kKind, T, D, NW, kGen>), C::kTailChunks, C::kWarps,
+    using C = Cfg<kKind, T, D, NW, kGen, kSinks>;
+    return Variant{reinterpret_cast<const void*>(&split_kv_kernel<kKind, T, D, NW, kGen, kSinks>), C::kTailChunks, C::kWarps,
                    NW == 1 ? C::kWarps : 1, C::kBoxInner, C::kSwizzleBytes, &Smem<C>::bytes};
 }
 
-template <int kKind, typename T, int D, bool kGen>
+template <int kKind, typename T, int D, bool kGen, bool kSinks>
 Variant pick_width(int nw) {
-    if (nw == 1) return make_variant<kKind, T, D, 1, kGen>();
-    if (nw == 2) return make_variant<kKind, T, D, 2, kGen>();
-    if (nw == 4) return make_variant<kKind, T, D, 4, kGen>();
-    return make_variant<kKind, T, D, 8, kGen>();
+    if (nw == 1) return make_variant<kKind, T, D, 1, kGen, kSinks>();
+    if (nw == 2) return make_variant<kKind, T, D, 2, kGen, kSinks>();
+    if (nw == 4) return make_variant<kKind, T, D, 4, kGen, kSinks>();
+    return make_variant<kKind, T, D, 8, kGen, kSinks>();
 }
 
-template <typename T, int D, bool kGen>
+template <typename T, int D, bool kGen, bool kSinks>
 bool pick_kind(int kind, int nw, Variant& v) {
     if (kind == kKernelMma) {
         if constexpr (std::is_same<T, float>::value ||
@@ -1583,47 +1623,49 @@ bool pick_kind(int kind, int nw, Variant& v) {
                         std::is_same<T, int4x2>::value || std::is_same<T, int4kc>::value) && D != 128)) {
             return false;
         } else {
-            v = pick_width<kKernelMma, T, D, kGen>(nw);
+            v = pick_width<kKernelMma, T, D, kGen, kSinks>(nw);
             return true;
         }
     }
     if constexpr (std::is_same<T, float>::value) {
-        v = pick_width<kKernelFma, T, D, kGen>(nw);
+        v = pick_width<kKernelFma, T, D, kGen, kSinks>(nw);
         return true;
     } else {
         // the CUDA-core kernel serves fp32 caches, and <= 8-head groups of the others
         if (nw > 1) return false;
-        v = make_variant<kKernelFma, T, D, 1, kGen>();
+        v = make_variant<kKernelFma, T, D, 1, kGen, kSinks>();
         return true;
     }
 }
 
-template <typename T, bool kGen>
+template <typename T, bool kGen, bool kSinks>
 bool pick_dim(int kind, int d, int nw, Variant& v) {
-    if (d == 64) return pick_kind<T, 64, kGen>(kind, nw, v);
-    if (d == 128) return pick_kind<T, 128, kGen>(kind, nw, v);
+    if (d == 64) return pick_kind<T, 64, kGen, kSinks>(kind, nw, v);
+    if (d == 128) return pick_kind<T, 128, kGen, kSinks>(kind, nw, v);
     return false;
 }
 
 // The split-KV kernel for a cache dtype, kernel kind, head_dim and warps per
-// pair, in its plain (one token, full attention) or general flavour.
-template <bool kGen>
+// pair, in its plain (one token, full attention), general or sink flavour.
+template <bool kGen, bool kSinks>
 bool pick_variant(int dtype, int kind, int d, int nw, Variant& v) {
     switch (dtype) {
-        case GQA_DTYPE_F32: return pick_dim<float, kGen>(kind, d, nw, v);
-        case GQA_DTYPE_F16: return pick_dim<__half, kGen>(kind, d, nw, v);
-        case GQA_DTYPE_BF16: return pick_dim<__nv_bfloat16, kGen>(kind, d, nw, v);
-        case GQA_DTYPE_I8: return pick_dim<int8_t, kGen>(kind, d, nw, v);
-        case GQA_DTYPE_FP8_E4M3: return pick_dim<__nv_fp8_e4m3, kGen>(kind, d, nw, v);
-        case GQA_DTYPE_I4: return pick_dim<int4x2, kGen>(kind, d, nw, v);
-        case GQA_DTYPE_I4_KC: return pick_dim<int4kc, kGen>(kind, d, nw, v);
+        case GQA_DTYPE_F32: return pick_dim<float, kGen, kSinks>(kind, d, nw, v);
+        case GQA_DTYPE_F16: return pick_dim<__half, kGen, kSinks>(kind, d, nw, v);
+        case GQA_DTYPE_BF16: return pick_dim<__nv_bfloat16, kGen, kSinks>(kind, d, nw, v);
+        case GQA_DTYPE_I8: return pick_dim<int8_t, kGen, kSinks>(kind, d, nw, v);
+        case GQA_DTYPE_FP8_E4M3: return pick_dim<__nv_fp8_e4m3, kGen, kSinks>(kind, d, nw, v);
+        case GQA_DTYPE_I4: return pick_dim<int4x2, kGen, kSinks>(kind, d, nw, v);
+        case GQA_DTYPE_I4_KC: return pick_dim<int4kc, kGen, kSinks>(kind, d, nw, v);
         default: return false;
     }
 }
 
-// Defined in gqa_decode.cu (plain) and gqa_decode_general.cu (general).
+// Defined in gqa_decode.cu (plain), gqa_decode_general.cu (general) and
+// gqa_decode_sinks.cu (a window with sink tokens).
 bool pick_plain(int dtype, int kind, int d, int nw, Variant& v);
 bool pick_general(int dtype, int kind, int d, int nw, Variant& v);
+bool pick_sinks(int dtype, int kind, int d, int nw, Variant& v);
 
 }  // namespace dec
 }  // namespace gqa

@@ -60,6 +60,7 @@ struct PrefillLaunch {
     int batch;
     float scale;
     int window;
+    int sinks;                  // first tokens that stay visible beside the window
     void* out;
     int out_dtype;
     int kernel;                 // GQA_PREFILL_* (0 = tcgen05)
@@ -86,6 +87,7 @@ struct DecodeLaunch {
     size_t workspace_bytes;
     int tokens_per_seq;         // T >= 1 queries per sequence (q, out: [B, T, H, d])
     int window;                 // sliding window in tokens, 0 = full attention
+    int sinks;                  // first tokens that stay visible beside the window
     int kernel;                 // KernelKind
     int max_warps;              // 0 = fill the GPU
     int min_blocks_per_warp;

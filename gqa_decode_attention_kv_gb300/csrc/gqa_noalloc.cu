@@ -29,6 +29,20 @@ void* scratch_on_current_device() {
 
 }  // namespace
 
+extern "C" GQA_API int gqa_decode_noalloc_sinks(const gqa_kv_cache_t* cache, const void* q,
+                                                int32_t q_dtype, int32_t num_heads,
+                                                const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                                const int32_t* context_lens, int32_t batch, float scale,
+                                                void* out, int32_t out_dtype,
+                                                const gqa_decode_opts_t* opts, int32_t sink_tokens,
+                                                int32_t* err_flag, void* stream) {
+    void* scratch = scratch_on_current_device();
+    if (scratch == nullptr) return GQA_ERR_CUDA;
+    return gqa_decode_sinks(cache, q, q_dtype, num_heads, block_tables, max_blocks_per_seq, context_lens,
+                            batch, scale, out, out_dtype, scratch, GQA_NOALLOC_SCRATCH_BYTES, opts,
+                            sink_tokens, err_flag, stream);
+}
+
 extern "C" GQA_API int gqa_decode_noalloc(const gqa_kv_cache_t* cache, const void* q,
                                           int32_t q_dtype, int32_t num_heads,
                                           const int32_t* block_tables, int32_t max_blocks_per_seq,

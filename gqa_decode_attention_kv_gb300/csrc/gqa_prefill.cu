@@ -17,6 +17,13 @@
 // in a ring of stages shared by the CTA's warps (full/empty mbarriers), one
 // thread issuing. Tiles run heaviest first (the last query tiles of a
 // sequence attend the most blocks).
+//
+// With a sliding window, sink tokens (the first S of the sequence) may stay
+// visible: kSinks instantiations of every kernel walk the blocks that hold the
+// sinks and then, without a gap, the blocks from the tile's window start on
+// (BlockWalk below), so a chunk can hold blocks of both and the ones between are
+// never read. Sinks cost ceil(S / 16) blocks a tile; the other instantiations
+// are the same code as before them.
 #include <algorithm>
 #include <cstring>
 #include <type_traits>
@@ -55,11 +62,36 @@ struct PrefillArgs {
     int32_t* err;
     long long num_blocks;
     int B, H, K, G, max_blocks, out_dtype, tiles_per_seq, max_new, window;
+    int sinks;                  // kSinks: first tokens that stay visible
     int map_perm[3];
     int page_perm[2];           // tcgen05 kernel, d = 128: dims 3, 4 of the V page map
     int out_tma;                // 64-token tcgen05 forms: the output map is valid (fp32 out, G | 32 or 32 | G)
     float scale_log2;
 };
+
+// The blocks a query tile attends, in walking order: with kSinks the blocks
+// 0 .. ns-1 that only the sinks make visible (none from jb_lo on), then jb_lo ..
+// jb_hi-1.
+template <bool kSinks>
+struct BlockWalk {
+    int jb_lo, jb_hi, ns;
+    __device__ __forceinline__ int count() const { return jb_hi - jb_lo + ns; }
+    __device__ __forceinline__ int block(int v) const {    // v-th block -> logical block
+        if constexpr (!kSinks) return jb_lo + v;
+        else return v < ns ? v : jb_lo + (v - ns);
+    }
+};
+template <bool kSinks>
+__device__ __forceinline__ int sink_blocks(const PrefillArgs& a, int jb_lo) {
+    if constexpr (!kSinks) return 0;
+    else return min((a.sinks + kBlock - 1) / kBlock, jb_lo);
+}
+// Whether a row that attends [lo, hi) and the sinks does not attend position pos.
+template <bool kSinks>
+__device__ __forceinline__ bool hidden(const PrefillArgs& a, int pos, int lo, int hi) {
+    if constexpr (!kSinks) return pos < lo || pos >= hi;
+    else return (pos < lo && pos >= a.sinks) || pos >= hi;
+}
 
 template <typename T, int D>
 struct PfCfg {
@@ -103,7 +135,7 @@ __device__ __forceinline__ void store4(void* out, int dt, long long idx, float4 
     }
 }
 
-template <typename T, int D>
+template <typename T, int D, bool kSinks>
 __global__ void __launch_bounds__(kPfWarps * 32)
 prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                const PrefillArgs a) {
@@ -147,7 +179,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     const int att_lo = a.window > 0 ? max(0, base_pos + tok_lo - a.window + 1) : 0;
     const int jb_lo = att_lo / kBlock;
     const int jb_hi = (base_pos + tok_hi + kBlock) / kBlock;
-    const int nblk = jb_hi - jb_lo;
+    const BlockWalk<kSinks> walk{jb_lo, jb_hi, sink_blocks<kSinks>(a, jb_lo)};
+    const int nblk = walk.count();
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kPfStages; ++s) {
@@ -193,22 +226,20 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     for (int i = 0; i < C::kNd; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
 
-    // ---- producer (warp 0): lane l holds the table entry of block win_base + l
+    // ---- producer (warp 0): lane l holds the table entry of walk step win_base + l
     const uint64_t pol = l2_policy_evict_last();   // every query tile of the sequence re-reads these
     int win_base = -(1 << 30), win_phys = -1;
     auto issue = [&](int it) {                 // warp 0 only (warp-uniform)
-        const int j = jb_lo + it;
-        if (j - win_base >= 32 || j < win_base) {
-            win_base = j;
-            const int jj = j + lane;
+        if (it - win_base >= 32 || it < win_base) {
+            win_base = it;
             win_phys = -1;
-            if (jj < jb_hi) {
-                const int ph = a.block_tables[(long long)b * a.max_blocks + jj];
+            if (it + lane < nblk) {
+                const int ph = a.block_tables[(long long)b * a.max_blocks + walk.block(it + lane)];
                 if (ph < 0 || ph >= a.num_blocks) flag_error(a.err, GQA_DEVERR_BLOCK_INDEX);
                 else win_phys = ph;
             }
         }
-        const int ph = __shfl_sync(kFull, win_phys, j - win_base);
+        const int ph = __shfl_sync(kFull, win_phys, it - win_base);
         if (lane == 0) {
             const int s = it % kPfStages;
             const uint32_t bar = full0 + 8 * s;
@@ -248,8 +279,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     mbar_wait(full0 + 8 * (q % kPfStages), (uint32_t)(q / kPfStages) & 1u, kWaitLimitNs / 4);
             return;
         }
-        const int j = jb_lo + it;
-        const int bpos = j * kBlock;
+        const int bpos = walk.block(it) * kBlock;
         if (!skip_s[s]) {
             const uint32_t sk = ring + s * C::kStage, sv = sk + C::kTile;
             // ---- S = Q K^T for tokens 0-7 (sa) and 8-15 (sb)
@@ -273,7 +303,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     const int tp = bpos + 2 * c + (e & 1) + 8 * ((e >> 1) & 1);
                     const bool row1 = e >= 4;
                     const int lo = row1 ? lo1 : lo0, hi = row1 ? hi1 : hi0;
-                    if (tp < lo || tp >= hi) s_[e] = -INFINITY;
+                    if (hidden<kSinks>(a, tp, lo, hi)) s_[e] = -INFINITY;
                 }
             }
             // ---- online softmax per row (rows r: e 0..3, r+8: e 4..7)
@@ -310,9 +340,11 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 pl[q] = pack2<kB>(x - f.x, y - f.y);
             }
             // ---- O += P V; tokens past the sequence hold arbitrary bits: zero them
-            const bool tail = bpos + kBlock > L;
-            const uint32_t m01 = (bpos + 2 * c < L ? 0x0000ffffu : 0u) | (bpos + 2 * c + 1 < L ? 0xffff0000u : 0u);
-            const uint32_t m89 = (bpos + 2 * c + 8 < L ? 0x0000ffffu : 0u) | (bpos + 2 * c + 9 < L ? 0xffff0000u : 0u);
+            // (with sinks also those that no row of the tile attends)
+            const bool tail = bpos + kBlock > L || (kSinks && bpos < att_lo);
+            auto live = [&](int t) { return !hidden<kSinks>(a, bpos + t, kSinks ? att_lo : 0, L); };
+            const uint32_t m01 = (live(2 * c) ? 0x0000ffffu : 0u) | (live(2 * c + 1) ? 0xffff0000u : 0u);
+            const uint32_t m89 = (live(2 * c + 8) ? 0x0000ffffu : 0u) | (live(2 * c + 9) ? 0xffff0000u : 0u);
 #pragma unroll
             for (int pp = 0; pp < C::kNd / 2; ++pp) {
                 uint32_t vb[4];
@@ -430,7 +462,7 @@ __device__ __forceinline__ void tc_mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, 
         : "memory");
 }
 
-template <typename T, int D>
+template <typename T, int D, bool kSinks>
 __global__ void __launch_bounds__(kTcThreads, 2)
 prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                   const PrefillArgs a) {
@@ -485,7 +517,9 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     const int att_lo = a.window > 0 ? max(0, base_pos + tok_lo - a.window + 1) : 0;
     const int jb_lo = att_lo / kBlock;
     const int jb_hi = (base_pos + tok_hi + kBlock) / kBlock;
-    const int nchunks = (jb_hi - jb_lo + kTcBlocks - 1) / kTcBlocks;
+    const BlockWalk<kSinks> walk{jb_lo, jb_hi, sink_blocks<kSinks>(a, jb_lo)};
+    const int nblk = walk.count();
+    const int nchunks = (nblk + kTcBlocks - 1) / kTcBlocks;
 
     // ---- this thread's row (softmax warps) and the positions it attends, [lo, hi)
     const int rr = row0 + (softmax ? tid : 0);
@@ -545,19 +579,18 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             int ph[kTcBlocks];
 #pragma unroll
             for (int q = 0; q < kTcBlocks; ++q) {
-                const int j = jb_lo + kTcBlocks * c + q;
-                if (j - win_base >= 32 || j < win_base) {
-                    win_base = j;
-                    const int jj = j + lane;
+                const int v = kTcBlocks * c + q;
+                if (v - win_base >= 32 || v < win_base) {
+                    win_base = v;
                     win_phys = -1;
-                    if (jj < jb_hi) {
-                        const int p = a.block_tables[(long long)b * a.max_blocks + jj];
+                    if (v + lane < nblk) {
+                        const int p = a.block_tables[(long long)b * a.max_blocks + walk.block(v + lane)];
                         if (p < 0 || p >= a.num_blocks) flag_error(a.err, GQA_DEVERR_BLOCK_INDEX);
                         else win_phys = p;
                     }
                 }
-                ph[q] = __shfl_sync(kFull, win_phys, j - win_base);
-                if (j >= jb_hi) ph[q] = -1;
+                ph[q] = __shfl_sync(kFull, win_phys, v - win_base);
+                if (v >= nblk) ph[q] = -1;
             }
             const uint32_t bar = is_k ? bar_k(c) : bar_v(c);
             if (lane == 0) {
@@ -695,7 +728,13 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             ok = ok && __all_sync(kFull, mbar_wait(bar_m(c), par8(c)));
             if (!ok) break;
             tc_fence_after();
-            const int cpos = (jb_lo + kTcBlocks * c) * kBlock;
+            // position of the chunk's first token were its blocks all past the sinks'
+            const int cpos = (jb_lo + kTcBlocks * c - walk.ns) * kBlock;
+            const bool mixed = kSinks && kTcBlocks * c < walk.ns;    // blocks of the sinks in it
+            auto pos_of = [&](int t) {                               // position of the chunk's token t
+                if constexpr (!kSinks) return cpos + t;
+                else return walk.block(kTcBlocks * c + t / kBlock) * kBlock + t % kBlock;
+            };
             const uint32_t bm = cmask[c & (kTcMasks - 1)];
             const uint32_t t_buf = t_lane + (uint32_t)(c & 1) * kColBuf;
             float sv[kTcChunk];
@@ -709,12 +748,11 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 #pragma unroll
                     for (int j = 0; j < 16; ++j) sv[16 * u + j] = __uint_as_float(r[u][j]) * a.scale_log2;
             }
-            const bool whole = bm == (1u << kTcBlocks) - 1u && cpos >= lo && cpos + kTcChunk <= hi;
+            const bool whole = bm == (1u << kTcBlocks) - 1u && !mixed && cpos >= lo && cpos + kTcChunk <= hi;
             if (!whole) {
 #pragma unroll
                 for (int j = 0; j < kTcChunk; ++j) {
-                    const int pos = cpos + j;
-                    if (!((bm >> (j / kBlock)) & 1u) || pos < lo || pos >= hi) sv[j] = -INFINITY;
+                    if (!((bm >> (j / kBlock)) & 1u) || hidden<kSinks>(a, pos_of(j), lo, hi)) sv[j] = -INFINITY;
                 }
             }
             float mx4[4] = {sv[0], sv[1], sv[2], sv[3]};      // short chains
@@ -764,13 +802,14 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             }
             tmem_wait_st();
             l += (ps4[0] + ps4[1]) + (ps4[2] + ps4[3]);
-            // V rows of tokens outside the sequence or of missing blocks hold arbitrary bits
-            if (bm != (1u << kTcBlocks) - 1u || cpos + kTcChunk > L) {
+            // V rows of tokens outside the sequence or of missing blocks hold arbitrary
+            // bits (with sinks, so may those that no row of the tile attends)
+            if (bm != (1u << kTcBlocks) - 1u || pos_of(kTcChunk - 1) >= L || (kSinks && (mixed || cpos < att_lo))) {
                 ok = __all_sync(kFull, mbar_wait(bar_v(c), par4(c)));
                 const uint32_t vb = sV + (c & 3) * C::kVc;
                 for (int i = tid; i < kTcChunk * C::kHalves * 8; i += kTcRows) {
                     const int t = i / (C::kHalves * 8), h = (i / 8) % C::kHalves, ck = i % 8;
-                    if (((bm >> (t / kBlock)) & 1u) && cpos + t < L) continue;
+                    if (((bm >> (t / kBlock)) & 1u) && !hidden<kSinks>(a, pos_of(t), kSinks ? att_lo : 0, L)) continue;
                     sts128(vb + (t / kBlock) * C::kVb + h * (kBlock * 128) + (t % kBlock) * 128 + ck * 16,
                            make_uint4(0u, 0u, 0u, 0u));
                 }
@@ -926,7 +965,7 @@ struct W2Cfg {
     static_assert(kSmem * kCtasPerSm <= 227 * 1024, "CTAs per SM fit the shared memory");
 };
 
-template <typename T, int kTiles>
+template <typename T, int kTiles, bool kSinks>
 __global__ void __launch_bounds__(W2Cfg<kTiles>::kThreads, W2Cfg<kTiles>::kCtasPerSm)
 prefill_tc2_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                    const __grid_constant__ CUtensorMap omap, const PrefillArgs a) {
@@ -978,7 +1017,8 @@ prefill_tc2_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     // to right when r is even, right to left when odd) so each CTA's total stays
     // close to the others'.
     struct Item {
-        int g, b, q0, n, L, rows, row0, base_pos, jb_lo, jb_hi, nchunks;
+        int g, b, q0, n, L, rows, row0, base_pos, att_lo, nblk, nchunks;
+        BlockWalk<kSinks> walk;
     };
     const int tps = a.tiles_per_seq, n_groups = a.K * a.B;
     const int n_items = tps * n_groups;
@@ -1003,10 +1043,12 @@ prefill_tc2_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         if (it.row0 >= it.rows) return false;
         it.base_pos = it.L - it.n;
         const int tok_lo = it.row0 / a.G, tok_hi = min(it.rows - 1, it.row0 + C::kRows - 1) / a.G;
-        const int att_lo = a.window > 0 ? max(0, it.base_pos + tok_lo - a.window + 1) : 0;
-        it.jb_lo = att_lo / kBlock;
-        it.jb_hi = (it.base_pos + tok_hi + kBlock) / kBlock;
-        it.nchunks = (it.jb_hi - it.jb_lo + kW2Blocks - 1) / kW2Blocks;
+        it.att_lo = a.window > 0 ? max(0, it.base_pos + tok_lo - a.window + 1) : 0;
+        it.walk.jb_lo = it.att_lo / kBlock;
+        it.walk.jb_hi = (it.base_pos + tok_hi + kBlock) / kBlock;
+        it.walk.ns = sink_blocks<kSinks>(a, it.walk.jb_lo);
+        it.nblk = it.walk.count();
+        it.nchunks = (it.nblk + kW2Blocks - 1) / kW2Blocks;
         return true;
     };
     auto next_item = [&](int& r, Item& it) -> bool {  // the next valid item from round r on
@@ -1069,19 +1111,18 @@ prefill_tc2_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 int ph[kW2Blocks];
 #pragma unroll
                 for (int q = 0; q < kW2Blocks; ++q) {
-                    const int jb = it.jb_lo + kW2Blocks * c + q;
-                    if (jb - win_base >= 32 || jb < win_base) {
-                        win_base = jb;
-                        const int jj = jb + lane;
+                    const int v = kW2Blocks * c + q;
+                    if (v - win_base >= 32 || v < win_base) {
+                        win_base = v;
                         win_phys = -1;
-                        if (jj < it.jb_hi) {
-                            const int p = a.block_tables[(long long)it.b * a.max_blocks + jj];
+                        if (v + lane < it.nblk) {
+                            const int p = a.block_tables[(long long)it.b * a.max_blocks + it.walk.block(v + lane)];
                             if (p < 0 || p >= a.num_blocks) flag_error(a.err, GQA_DEVERR_BLOCK_INDEX);
                             else win_phys = p;
                         }
                     }
-                    ph[q] = __shfl_sync(kFull, win_phys, jb - win_base);
-                    if (jb >= it.jb_hi) ph[q] = -1;
+                    ph[q] = __shfl_sync(kFull, win_phys, v - win_base);
+                    if (v >= it.nblk) ph[q] = -1;
                 }
                 const uint32_t bar = k_warp ? bar_k(G) : bar_v(G);
                 if (lane == 0) {
@@ -1264,7 +1305,13 @@ prefill_tc2_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 ok = ok && __all_sync(kFull, mbar_wait(bar_m(G), par8(G)));
                 if (!ok) break;
                 tc_fence_after();
-                const int cpos = (it.jb_lo + kW2Blocks * c) * kBlock;
+                // position of the chunk's first token were its blocks all past the sinks'
+                const int cpos = (it.walk.jb_lo + kW2Blocks * c - it.walk.ns) * kBlock;
+                const bool mixed = kSinks && kW2Blocks * c < it.walk.ns;   // blocks of the sinks in it
+                auto pos_of = [&](int t) {                                 // position of the chunk's token t
+                    if constexpr (!kSinks) return cpos + t;
+                    else return it.walk.block(kW2Blocks * c + t / kBlock) * kBlock + t % kBlock;
+                };
                 const uint32_t bm = cmask[G & 7];
                 const uint32_t t_buf = t_lane + kW2Chunk * (G & 1);
                 float sv[kW2Chunk];
@@ -1286,12 +1333,11 @@ prefill_tc2_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 // the item's last S_t is in registers, and with it every S_t of the
                 // item is done: Q_t's buffer is free for the next item's rows
                 if (c == it.nchunks - 1 && have_nx) load_q(nx);
-                const bool whole = bm == (1u << kW2Blocks) - 1u && cpos >= lo && cpos + kW2Chunk <= hi;
+                const bool whole = bm == (1u << kW2Blocks) - 1u && !mixed && cpos >= lo && cpos + kW2Chunk <= hi;
                 if (!whole) {
 #pragma unroll
                     for (int q = 0; q < kW2Chunk; ++q) {
-                        const int pos = cpos + q;
-                        if (!((bm >> (q / kBlock)) & 1u) || pos < lo || pos >= hi) sv[q] = -INFINITY;
+                        if (!((bm >> (q / kBlock)) & 1u) || hidden<kSinks>(a, pos_of(q), lo, hi)) sv[q] = -INFINITY;
                     }
                 }
                 float mx4[4];                                     // four short chains of 3-input maxima
@@ -1356,13 +1402,15 @@ prefill_tc2_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 }
                 // V rows of tokens outside the sequence or of missing blocks hold
                 // arbitrary bits: each tile zeroes them before its P(G) is ready (its
-                // MMA warp issues P_t(G).V(G) only then); both tiles write the same zeros
-                if (bm != (1u << kW2Blocks) - 1u || cpos + kW2Chunk > it.L) {
+                // MMA warp issues P_t(G).V(G) only then); both tiles write the same zeros.
+                // With sinks, so may those of tokens that no row of the item attends.
+                if (bm != (1u << kW2Blocks) - 1u || pos_of(kW2Chunk - 1) >= it.L ||
+                    (kSinks && (mixed || cpos < it.att_lo))) {
                     ok = __all_sync(kFull, mbar_wait(bar_v(G), par_st(G)));
                     const uint32_t vb = sV + stage(G) * C::kVc;
                     for (int i = tid & (kTcRows - 1); i < kW2Chunk * 2 * 8; i += kTcRows) {
                         const int tk2 = i / 16, h = (i / 8) % 2, ck = i % 8;
-                        if (((bm >> (tk2 / kBlock)) & 1u) && cpos + tk2 < it.L) continue;
+                        if (((bm >> (tk2 / kBlock)) & 1u) && !hidden<kSinks>(a, pos_of(tk2), kSinks ? it.att_lo : 0, it.L)) continue;
                         sts128(vb + (tk2 / kBlock) * C::kVb + h * (kBlock * 128) + (tk2 % kBlock) * 128 + ck * 16,
                                make_uint4(0u, 0u, 0u, 0u));
                     }
@@ -1463,18 +1511,21 @@ prefill_tc2_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
 }
 
 template <typename T, int kTiles>
-const void* prefill_tc2_fn() {
-    return reinterpret_cast<const void*>(&prefill_tc2_kernel<T, kTiles>);
+const void* prefill_tc2_fn(bool sinks) {
+    return sinks ? reinterpret_cast<const void*>(&prefill_tc2_kernel<T, kTiles, true>)
+                 : reinterpret_cast<const void*>(&prefill_tc2_kernel<T, kTiles, false>);
 }
 
 template <typename T, int D>
-const void* prefill_tc_fn() {
-    return reinterpret_cast<const void*>(&prefill_tc_kernel<T, D>);
+const void* prefill_tc_fn(bool sinks) {
+    return sinks ? reinterpret_cast<const void*>(&prefill_tc_kernel<T, D, true>)
+                 : reinterpret_cast<const void*>(&prefill_tc_kernel<T, D, false>);
 }
 
 template <typename T, int D>
-const void* prefill_fn() {
-    return reinterpret_cast<const void*>(&prefill_kernel<T, D>);
+const void* prefill_fn(bool sinks) {
+    return sinks ? reinterpret_cast<const void*>(&prefill_kernel<T, D, true>)
+                 : reinterpret_cast<const void*>(&prefill_kernel<T, D, false>);
 }
 
 }  // namespace
@@ -1486,6 +1537,7 @@ int launch_prefill(const PrefillLaunch& L) {
     const gqa_kv_cache_t& c = *L.cache;
     const int D = c.head_dim, K = c.num_kv_heads, G = L.num_heads / K;
     const bool tc = L.kernel != GQA_PREFILL_MMA_SYNC;
+    const bool sinks = L.window > 0 && L.sinks > 0;
     // the 64-token-chunk tcgen05 forms serve head_dim 128: two query tiles per
     // CTA (one CTA per SM) or one (two CTAs per SM)
     const bool wide2 = tc && D == 128 && (L.kernel == GQA_PREFILL_AUTO || L.kernel == GQA_PREFILL_TCGEN05_WIDE);
@@ -1497,23 +1549,23 @@ int launch_prefill(const PrefillLaunch& L) {
     if (wide) {
         if (c.dtype != GQA_DTYPE_BF16 && c.dtype != GQA_DTYPE_F16) return GQA_ERR_UNSUPPORTED;
         const bool bf = c.dtype == GQA_DTYPE_BF16;
-        fn = wide2 ? (bf ? prefill_tc2_fn<__nv_bfloat16, 2>() : prefill_tc2_fn<__half, 2>())
-                   : (bf ? prefill_tc2_fn<__nv_bfloat16, 1>() : prefill_tc2_fn<__half, 1>());
+        fn = wide2 ? (bf ? prefill_tc2_fn<__nv_bfloat16, 2>(sinks) : prefill_tc2_fn<__half, 2>(sinks))
+                   : (bf ? prefill_tc2_fn<__nv_bfloat16, 1>(sinks) : prefill_tc2_fn<__half, 1>(sinks));
         smem = wide2 ? W2Cfg<2>::kSmem : W2Cfg<1>::kSmem;
     } else if (c.dtype == GQA_DTYPE_BF16) {
         if (tc) {
-            fn = D == 64 ? prefill_tc_fn<__nv_bfloat16, 64>() : prefill_tc_fn<__nv_bfloat16, 128>();
+            fn = D == 64 ? prefill_tc_fn<__nv_bfloat16, 64>(sinks) : prefill_tc_fn<__nv_bfloat16, 128>(sinks);
             smem = D == 64 ? TcCfg<__nv_bfloat16, 64>::kSmem : TcCfg<__nv_bfloat16, 128>::kSmem;
         } else {
-            fn = D == 64 ? prefill_fn<__nv_bfloat16, 64>() : prefill_fn<__nv_bfloat16, 128>();
+            fn = D == 64 ? prefill_fn<__nv_bfloat16, 64>(sinks) : prefill_fn<__nv_bfloat16, 128>(sinks);
             smem = D == 64 ? PfCfg<__nv_bfloat16, 64>::kSmem : PfCfg<__nv_bfloat16, 128>::kSmem;
         }
     } else if (c.dtype == GQA_DTYPE_F16) {
         if (tc) {
-            fn = D == 64 ? prefill_tc_fn<__half, 64>() : prefill_tc_fn<__half, 128>();
+            fn = D == 64 ? prefill_tc_fn<__half, 64>(sinks) : prefill_tc_fn<__half, 128>(sinks);
             smem = D == 64 ? TcCfg<__half, 64>::kSmem : TcCfg<__half, 128>::kSmem;
         } else {
-            fn = D == 64 ? prefill_fn<__half, 64>() : prefill_fn<__half, 128>();
+            fn = D == 64 ? prefill_fn<__half, 64>(sinks) : prefill_fn<__half, 128>(sinks);
             smem = D == 64 ? PfCfg<__half, 64>::kSmem : PfCfg<__half, 128>::kSmem;
         }
     } else {
@@ -1546,6 +1598,7 @@ int launch_prefill(const PrefillLaunch& L) {
     a.max_new = L.max_new_tokens;
     a.tiles_per_seq = (int)(((long long)L.max_new_tokens * G + rows_per_cta - 1) / rows_per_cta);
     a.window = L.window;
+    a.sinks = sinks ? (int)std::min<long long>(L.sinks, (long long)L.max_blocks * kBlock) : 0;
     a.map_perm[0] = perm[0];
     a.map_perm[1] = perm[1];
     a.map_perm[2] = perm[2];

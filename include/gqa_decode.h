@@ -272,6 +272,21 @@ GQA_API int gqa_prefill(const gqa_kv_cache_t *cache, const void *q, int32_t q_dt
                 void *stream);
 
 /*
+ * gqa_prefill with sink tokens: with sliding_window W > 0 and sink_tokens S > 0 a
+ * query at position p attends every position t <= p with t > p - W or t < S, so
+ * the first S tokens of a sequence stay visible however far its window has moved.
+ * Blocks that lie wholly behind the sinks and before every query's window are
+ * never read (their table entries may hold anything). S = 0, or W = 0 (full
+ * attention), is gqa_prefill. sink_tokens < 0 is GQA_ERR_INVALID; an S beyond the
+ * context makes every position up to p visible.
+ */
+GQA_API int gqa_prefill_sinks(const gqa_kv_cache_t *cache, const void *q, int32_t q_dtype, int32_t num_heads,
+                const int32_t *q_start, int32_t max_new_tokens, const int32_t *block_tables,
+                int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t batch, float scale,
+                int32_t sliding_window, int32_t sink_tokens, void *out, int32_t out_dtype, int32_t kernel,
+                int32_t *err_flag, void *stream);
+
+/*
  * Bytes of device workspace gqa_decode needs for this shape (tokens_per_seq as
  * in gqa_decode_opts_t, 0 meaning 1) on `device` (-1 = the current device).
  * Returns 0 on bad arguments. The bound covers every kernel choice, window and
@@ -324,6 +339,22 @@ GQA_API int gqa_decode(const gqa_kv_cache_t *cache, const void *q, int32_t q_dty
                const gqa_decode_opts_t *opts, int32_t *err_flag, void *stream);
 
 /*
+ * gqa_decode with sink tokens: with W = opts->sliding_window > 0 and sink_tokens
+ * S > 0 a query at position p attends every position t <= p with t > p - W or
+ * t < S. Blocks wholly behind the sinks and before every query's window are never
+ * read, so a caller may recycle them (gqa_kv_pages_trim releases exactly those no
+ * later query sees). S = 0, or W = 0 (full attention), is gqa_decode; sink_tokens
+ * < 0 is GQA_ERR_INVALID. Everything else (T new tokens, cache dtypes, limits,
+ * workspace size) is as for gqa_decode. The sinks keep the positions they were
+ * written with: nothing is rotated again.
+ */
+GQA_API int gqa_decode_sinks(const gqa_kv_cache_t *cache, const void *q, int32_t q_dtype,
+               int32_t num_heads, const int32_t *block_tables, int32_t max_blocks_per_seq,
+               const int32_t *context_lens, int32_t batch, float scale, void *out,
+               int32_t out_dtype, void *workspace, size_t workspace_bytes,
+               const gqa_decode_opts_t *opts, int32_t sink_tokens, int32_t *err_flag, void *stream);
+
+/*
  * gqa_decode without a caller-supplied workspace. The pages have no
  * counterpart for this call; it exists for callers that cannot allocate device
  * memory: a plugin running inside a host engine whose device allocator it does
@@ -355,6 +386,14 @@ GQA_API int gqa_decode_noalloc(const gqa_kv_cache_t *cache, const void *q, int32
                                int32_t max_blocks_per_seq, const int32_t *context_lens,
                                int32_t batch, float scale, void *out, int32_t out_dtype,
                                const gqa_decode_opts_t *opts, int32_t *err_flag, void *stream);
+
+/* gqa_decode_noalloc with sink tokens (see gqa_decode_sinks); same scratch, same rules. */
+GQA_API int gqa_decode_noalloc_sinks(const gqa_kv_cache_t *cache, const void *q, int32_t q_dtype,
+                               int32_t num_heads, const int32_t *block_tables,
+                               int32_t max_blocks_per_seq, const int32_t *context_lens,
+                               int32_t batch, float scale, void *out, int32_t out_dtype,
+                               const gqa_decode_opts_t *opts, int32_t sink_tokens, int32_t *err_flag,
+                               void *stream);
 
 #ifdef __cplusplus
 }
