@@ -14,6 +14,9 @@ would repeat the module name):
                               (one or T causal new tokens per sequence, optional
                               sliding window)
 * ``kv_append_varlen``     -- the same for a different number of new tokens per sequence
+* ``rope_table``           -- (cos, sin) of every position and pair, for the two calls below
+* ``qk_norm_rope``         -- per-head norm of queries and keys and their rotation, one pass
+* ``qk_norm_rope_append``  -- the same with K and V written into the paged cache
 * ``gqa_prefill``          -- causal attention of prompts (any length) over the paged cache
 * ``decode_workspace_size``-- workspace bytes ``gqa_decode`` needs
 * ``kv_pool_elements``     -- elements a pool of ``num_blocks`` blocks holds (K and V)
@@ -70,6 +73,13 @@ class DecodeOpts(ctypes.Structure):
                 ("event_main_begin", ctypes.c_void_p), ("event_main_end", ctypes.c_void_p)]
 
 
+class NormRopeDesc(ctypes.Structure):
+    """Mirror of gqa_norm_rope_t."""
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("rope", ctypes.c_void_p),
+                ("weight_dtype", ctypes.c_int32), ("eps", ctypes.c_float), ("rope_rows", ctypes.c_int32),
+                ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 _lib = None
 _lock = threading.Lock()
 
@@ -120,6 +130,15 @@ def load() -> ctypes.CDLL:
             lib.gqa_prefill.restype = ctypes.c_int
             lib.gqa_prefill_sinks.argtypes = [*lib.gqa_prefill.argtypes[:12], i32, *lib.gqa_prefill.argtypes[12:]]
             lib.gqa_prefill_sinks.restype = ctypes.c_int
+            lib.gqa_rope_table.argtypes = [vp, i32, i32, ctypes.c_double, vp]
+            lib.gqa_rope_table.restype = ctypes.c_int
+            lib.gqa_qk_norm_rope.argtypes = [ctypes.POINTER(NormRopeDesc), vp, i64, vp, i32, vp, i64, vp, i32, i32,
+                                             i32, i64, vp, vp, vp]
+            lib.gqa_qk_norm_rope.restype = ctypes.c_int
+            lib.gqa_qk_norm_rope_append.argtypes = [ctypes.POINTER(KVCacheDesc), ctypes.POINTER(NormRopeDesc), vp, i64,
+                                                    vp, i32, vp, i64, vp, i64, i32, i64, vp, i32, vp, i32, vp, vp, i32,
+                                                    vp, vp]
+            lib.gqa_qk_norm_rope_append.restype = ctypes.c_int
             _lib = lib
     return _lib
 
@@ -422,6 +441,180 @@ def kv_append_varlen(cache: PagedKVCache, k_new: torch.Tensor, v_new: torch.Tens
                                      args[3], int(block_tables.shape[1]), args[4],
                                      int(positions.shape[0]), args[5], _stream_ptr(stream))
     _check(st, "gqa_kv_append_varlen")
+
+
+def rope_table(positions: int, rotary_dim: int, base: float = 10000.0, device="cuda", stream=None) -> torch.Tensor:
+    """fp32 [positions, rotary_dim/2, 2]: cos and sin of p * base^(-2i/rotary_dim),
+    the angles in fp64. Made once and kept; for another rule of angles pass a
+    table of your own to the calls below."""
+    if positions < 0 or rotary_dim <= 0 or rotary_dim % 2:
+        raise ValueError(f"no table of {positions} positions and rotary_dim {rotary_dim}")
+    s = stream if stream is not None else torch.cuda.current_stream(torch.device(device))
+    with torch.cuda.stream(s):
+        table = torch.empty((positions, rotary_dim // 2, 2), dtype=torch.float32, device=device)
+        _check(load().gqa_rope_table(table.data_ptr(), int(positions), int(rotary_dim), float(base), s.cuda_stream),
+               "gqa_rope_table")
+    return table
+
+
+def _token_rows(t: torch.Tensor, name: str, like: torch.Tensor, heads: Optional[int] = None):
+    """(pointer, elements between tokens) of rows [..., heads, d] whose heads are
+    contiguous and whose tokens are evenly spaced (a view into a fused projection)."""
+    if t.dim() not in (3, 4) or tuple(t.shape[:-2]) != tuple(like.shape[:-2]) or t.shape[-1] != like.shape[-1]:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, which does not go with q's {tuple(like.shape)}")
+    if heads is not None and t.shape[-2] != heads:
+        raise ValueError(f"{name} has {t.shape[-2]} heads, not {heads}")
+    if t.dtype not in (torch.float32, torch.float16, torch.bfloat16) or t.dtype != like.dtype:
+        raise ValueError(f"{name} must have q's dtype, one of float32, float16, bfloat16, not {t.dtype}")
+    H, d = int(t.shape[-2]), int(t.shape[-1])
+    st = t.stride()
+    if t.numel() and (st[-1] != 1 or (H > 1 and st[-2] != d)):
+        raise ValueError(f"{name}'s heads must be contiguous, not strided by {st}")
+    if t.dim() == 4 and t.shape[0] > 1 and t.shape[1] > 1 and st[0] != t.shape[1] * st[1]:
+        raise ValueError(f"{name}'s tokens must be evenly spaced, not strided by {st}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    tokens = 1
+    for n in t.shape[:-2]:
+        tokens *= int(n)
+    if tokens <= 1:
+        stride = H * d
+    else:
+        stride = st[-3] if t.shape[-3] > 1 else st[0]
+    if tokens and stride < H * d:
+        raise ValueError(f"{name}'s tokens overlap (strides {st})")
+    return t.data_ptr(), int(stride)
+
+
+def _norm_rope_desc(q, rope, q_weight, k_weight, eps, interleaved) -> NormRopeDesc:
+    d = int(q.shape[-1])
+    desc = NormRopeDesc(None, None, None, 0, float(eps), 0, 0, int(bool(interleaved)), 0)
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is None:
+            continue
+        if tuple(w.shape) != (d,):
+            raise ValueError(f"{name} must be [{d}], not {tuple(w.shape)}")
+        if w.dtype not in (torch.float32, torch.float16, torch.bfloat16):
+            raise ValueError(f"{name} has unsupported dtype {w.dtype}")
+        setattr(desc, name, _dev(w, name))
+        desc.weight_dtype = DTYPE_CODE[w.dtype]
+    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
+        raise ValueError("q_weight and k_weight must have one dtype")
+    if rope is not None:
+        if rope.dim() != 3 or rope.shape[2] != 2 or rope.dtype != torch.float32:
+            raise ValueError(f"rope must be float32 [positions, rotary_dim/2, 2], not {rope.dtype} {tuple(rope.shape)}")
+        desc.rope, desc.rope_rows, desc.rotary_dim = _dev(rope, "rope"), int(rope.shape[0]), 2 * int(rope.shape[1])
+    return desc
+
+
+def _same_or_apart(out: torch.Tensor, src: torch.Tensor, name: str):
+    """out may be src itself (dense) or memory that src does not touch."""
+    if out.untyped_storage().data_ptr() != src.untyped_storage().data_ptr() or not out.numel():
+        return
+    if out.data_ptr() == src.data_ptr() and src.is_contiguous():
+        return
+    end = lambda t: t.data_ptr() + (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * t.element_size()  # noqa: E731
+    if out.data_ptr() < end(src) and src.data_ptr() < end(out):
+        raise ValueError(f"{name} overlaps its input without being it")
+
+
+def _q_out(q: torch.Tensor, q_out: Optional[torch.Tensor], name: str) -> torch.Tensor:
+    if q_out is None:
+        return torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if tuple(q_out.shape) != tuple(q.shape) or q_out.dtype != q.dtype:
+        raise ValueError(f"{name} must have the input's shape and dtype, not {tuple(q_out.shape)} {q_out.dtype}")
+    _dev(q_out, name)
+    _same_or_apart(q_out, q, name)
+    return q_out
+
+
+def _on_one_device(**tensors):
+    """Every array on the current CUDA device."""
+    cur = torch.device("cuda", torch.cuda.current_device()) if torch.cuda.is_available() else None
+    for name, t in tensors.items():
+        if t is not None and cur is not None and t.device != cur:
+            raise ValueError(f"{name} is on {t.device}, the current device is {cur}")
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: Optional[torch.Tensor] = None,
+                 rope: Optional[torch.Tensor] = None, q_weight: Optional[torch.Tensor] = None,
+                 k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, interleaved: bool = False,
+                 q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                 err: Optional[torch.Tensor] = None, stream=None):
+    """Norm of every head of q [..., H, d] and k [..., K, d] (x / sqrt(mean(x^2) + eps)
+    * weight; no weight, no norm), then the rotation by each token's position.
+
+    ``rope`` is a table as ``rope_table`` makes it, ``positions`` int32 with one
+    entry per token. q and k may be views into one fused projection; the dense
+    results (q_out, k_out) may be q and k themselves where those are dense."""
+    qp, qs = _token_rows(q, "q", q)
+    kp, ks = _token_rows(k, "k", q)
+    desc = _norm_rope_desc(q, rope, q_weight, k_weight, eps, interleaved)
+    tokens = q.numel() // max(1, int(q.shape[-2]) * int(q.shape[-1]))
+    pp = _dev(positions, "positions", True, rope is None)
+    if positions is not None and positions.numel() != tokens:
+        raise ValueError(f"positions must have {tokens} entries, not {positions.numel()}")
+    ep = _dev(err, "err", True, True)
+    _on_one_device(q=q, k=k, positions=positions, rope=rope, q_weight=q_weight, k_weight=k_weight, q_out=q_out,
+                   k_out=k_out, err=err)
+    q_out, k_out = _q_out(q, q_out, "q_out"), _q_out(k, k_out, "k_out")
+    st = load().gqa_qk_norm_rope(ctypes.byref(desc), qp, qs, q_out.data_ptr(), int(q.shape[-2]), kp, ks,
+                                 k_out.data_ptr(), int(k.shape[-2]), int(q.shape[-1]), DTYPE_CODE[q.dtype], tokens, pp,
+                                 ep, _stream_ptr(stream))
+    _check(st, "gqa_qk_norm_rope")
+    return q_out, k_out
+
+
+def qk_norm_rope_append(cache: PagedKVCache, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                        block_tables: torch.Tensor, positions: torch.Tensor, rope: Optional[torch.Tensor] = None,
+                        q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+                        eps: float = 1e-6, interleaved: bool = False, token_start: Optional[torch.Tensor] = None,
+                        max_new_tokens: Optional[int] = None, rope_positions: Optional[torch.Tensor] = None,
+                        q_out: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None,
+                        stream=None) -> torch.Tensor:
+    """``qk_norm_rope`` with the append in the same pass: returns q_out, and K and V
+    are in the cache. Tokens as in ``kv_append`` (q [B, H, d] or [B, T, H, d], new
+    tokens at positions[b], ...) or, with ``token_start`` [B+1] and
+    ``max_new_tokens``, as in ``kv_append_varlen`` (q [total, H, d]). A token is
+    turned by its position in the cache, or by ``rope_positions`` [tokens].
+    A KIVI-style cache takes ``qk_norm_rope`` and ``kv_append`` instead."""
+    _check_query(cache, q, (3,) if token_start is not None else (3, 4))
+    qp, qs = _token_rows(q, "q", q)
+    kp, ks = _token_rows(k, "k", q, cache.num_kv_heads)
+    vp, vs = _token_rows(v, "v", q, cache.num_kv_heads)
+    desc = _norm_rope_desc(q, rope, q_weight, k_weight, eps, interleaved)
+    tp, pp = _dev(block_tables, "block_tables", True), _dev(positions, "positions", True)
+    sp, rp = _dev(token_start, "token_start", True, True), _dev(rope_positions, "rope_positions", True, True)
+    ep = _dev(err, "err", True, True)
+    B = int(positions.shape[0]) if positions.dim() == 1 else -1
+    tokens = int(q.shape[0]) * (int(q.shape[1]) if q.dim() == 4 else 1)
+    if token_start is not None:
+        if B < 0 or token_start.dim() != 1 or token_start.numel() != B + 1:
+            raise ValueError("token_start must be [B + 1] and positions [B]")
+        if max_new_tokens is None:
+            raise ValueError("max_new_tokens is required with token_start")
+        T = int(max_new_tokens)
+    else:
+        T = 1 if q.dim() == 3 else int(q.shape[1])
+        if B != int(q.shape[0]):
+            raise ValueError(f"positions must be [B] with B = q.shape[0] = {int(q.shape[0])}")
+        if max_new_tokens is not None and int(max_new_tokens) != T:
+            raise ValueError(f"q holds {T} tokens per sequence, max_new_tokens is {max_new_tokens}")
+    _check_table_and_lens(block_tables, positions, B, "positions", B)
+    if rope_positions is not None and rope_positions.numel() != tokens:
+        raise ValueError(f"rope_positions must have {tokens} entries, not {rope_positions.numel()}")
+    _on_cache_device(cache, q=q, k=k, v=v, block_tables=block_tables, positions=positions, rope=rope,
+                     q_weight=q_weight, k_weight=k_weight, token_start=token_start, rope_positions=rope_positions,
+                     q_out=q_out, err=err)
+    q_out = _q_out(q, q_out, "q_out")
+    if tokens == 0 or T == 0:
+        return q_out
+    cdesc = cache.desc()
+    st = load().gqa_qk_norm_rope_append(ctypes.byref(cdesc), ctypes.byref(desc), qp, qs, q_out.data_ptr(),
+                                        int(q.shape[-2]), kp, ks, vp, vs, DTYPE_CODE[q.dtype], tokens, sp, T, tp,
+                                        int(block_tables.shape[1]), pp, rp, B, ep, _stream_ptr(stream))
+    _check(st, "gqa_qk_norm_rope_append")
+    return q_out
 
 
 def gqa_prefill(cache: PagedKVCache, q: torch.Tensor, q_start: torch.Tensor, max_new_tokens: int,

@@ -78,6 +78,32 @@ int check_residual(const gqa_kv_cache_t* c, int batch) {
     return GQA_OK;
 }
 
+bool plain_dtype(int dt) { return dt == GQA_DTYPE_F32 || dt == GQA_DTYPE_F16 || dt == GQA_DTYPE_BF16; }
+
+// The description of a norm and rotation, for rows of head_dim elements of dtype.
+int check_norm_rope(const gqa_norm_rope_t* r, int head_dim, int dtype) {
+    if (!r) return GQA_ERR_INVALID;
+    if (!plain_dtype(dtype)) return GQA_ERR_UNSUPPORTED;
+    if (r->q_weight || r->k_weight) {
+        if (!plain_dtype(r->weight_dtype)) return GQA_ERR_UNSUPPORTED;
+        if (!aligned16(r->q_weight) || !aligned16(r->k_weight)) return GQA_ERR_INVALID;
+        if (!(r->eps >= 0.f) || !std::isfinite(r->eps)) return GQA_ERR_INVALID;
+    }
+    if (r->interleaved != 0 && r->interleaved != 1) return GQA_ERR_INVALID;
+    if (r->rope) {
+        if (!aligned16(r->rope) || r->rope_rows <= 0) return GQA_ERR_INVALID;
+        if (r->rotary_dim <= 0 || r->rotary_dim > head_dim) return GQA_ERR_INVALID;
+        if (r->rotary_dim % 16) return GQA_ERR_UNSUPPORTED;
+    }
+    return GQA_OK;
+}
+
+// Rows of `heads` heads a token, tokens `stride` elements apart.
+int check_rows(const void* p, int64_t stride, int heads, int head_dim, int dtype, int64_t tokens) {
+    if (stride < (int64_t)heads * head_dim || (stride * dtype_bits(dtype)) % 128) return GQA_ERR_INVALID;
+    return tokens == 0 || (p && aligned16(p)) ? GQA_OK : GQA_ERR_INVALID;
+}
+
 // Tensor maps already encoded, keyed by everything an encoding reads (the
 // base address, the cache's shape, strides and element type, the box and the
 // swizzle): a serving loop calls with the same cache every step, and encoding
@@ -322,6 +348,95 @@ int gqa_kv_append_varlen(const gqa_kv_cache_t* cache, const void* k_new, const v
                                            max_blocks_per_seq, positions, batch, max_new_tokens,
                                            token_start, err_flag, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
+}
+
+int gqa_rope_table(float* table, int32_t positions, int32_t rotary_dim, double base, void* stream) {
+    if (positions < 0 || rotary_dim <= 0 || rotary_dim % 2 || !(base > 0.0) || !std::isfinite(base)) return GQA_ERR_INVALID;
+    if ((long long)positions * (rotary_dim / 2) > 256LL * 0x7fffffffLL) return GQA_ERR_UNSUPPORTED;
+    if (positions == 0) return GQA_OK;
+    if (!table || !aligned16(table)) return GQA_ERR_INVALID;
+    const cudaError_t e =
+        launch_rope_table(table, positions, rotary_dim, std::log(base), static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
+}
+
+int gqa_qk_norm_rope(const gqa_norm_rope_t* desc, const void* q, int64_t q_stride, void* q_out, int32_t num_heads,
+                     const void* k, int64_t k_stride, void* k_out, int32_t num_kv_heads, int32_t head_dim,
+                     int32_t dtype, int64_t tokens, const int32_t* positions, int32_t* err_flag, void* stream) {
+    if (head_dim != 64 && head_dim != 128) return GQA_ERR_UNSUPPORTED;
+    int st = check_norm_rope(desc, head_dim, dtype);
+    if (st != GQA_OK) return st;
+    if (num_heads <= 0 || num_kv_heads <= 0 || tokens < 0) return GQA_ERR_INVALID;
+    if ((st = check_rows(q, q_stride, num_heads, head_dim, dtype, tokens)) != GQA_OK) return st;
+    if ((st = check_rows(k, k_stride, num_kv_heads, head_dim, dtype, tokens)) != GQA_OK) return st;
+    if (tokens == 0) return GQA_OK;
+    if (!q_out || !k_out || !aligned16(q_out) || !aligned16(k_out)) return GQA_ERR_INVALID;
+    if (desc->rope && !positions) return GQA_ERR_INVALID;
+    NormRopeLaunch L = {};
+    L.desc = desc;
+    L.q = q;
+    L.k = k;
+    L.q_stride = q_stride;
+    L.k_stride = k_stride;
+    L.num_heads = num_heads;
+    L.num_kv_heads = num_kv_heads;
+    L.head_dim = head_dim;
+    L.dtype = dtype;
+    L.tokens = tokens;
+    L.rope_positions = positions;
+    L.q_out = q_out;
+    L.k_out = k_out;
+    L.err = err_flag;
+    L.stream = static_cast<cudaStream_t>(stream);
+    return launch_norm_rope(L) == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
+}
+
+int gqa_qk_norm_rope_append(const gqa_kv_cache_t* cache, const gqa_norm_rope_t* desc, const void* q, int64_t q_stride,
+                            void* q_out, int32_t num_heads, const void* k, int64_t k_stride, const void* v,
+                            int64_t v_stride, int32_t dtype, int64_t tokens, const int32_t* token_start,
+                            int32_t max_new_tokens, const int32_t* block_tables, int32_t max_blocks_per_seq,
+                            const int32_t* positions, const int32_t* rope_positions, int32_t batch, int32_t* err_flag,
+                            void* stream) {
+    int st = check_cache(cache);
+    if (st != GQA_OK) return st;
+    if (cache->dtype == GQA_DTYPE_I4_KC) return GQA_ERR_UNSUPPORTED;
+    if ((st = check_norm_rope(desc, cache->head_dim, dtype)) != GQA_OK) return st;
+    if (!dtype_coded(cache->dtype) && dtype != cache->dtype) return GQA_ERR_UNSUPPORTED;
+    if (num_heads <= 0 || tokens < 0 || batch < 0 || max_new_tokens < 0 || max_blocks_per_seq <= 0)
+        return GQA_ERR_INVALID;
+    if ((long long)max_blocks_per_seq * GQA_BLOCK_SIZE > 0x7fffffffLL) return GQA_ERR_INVALID;
+    const int T = std::max(1, (int)max_new_tokens);
+    if (!token_start && tokens != (long long)batch * T) return GQA_ERR_INVALID;
+    if ((st = check_rows(q, q_stride, num_heads, cache->head_dim, dtype, tokens)) != GQA_OK) return st;
+    if ((st = check_rows(k, k_stride, cache->num_kv_heads, cache->head_dim, dtype, tokens)) != GQA_OK) return st;
+    if ((st = check_rows(v, v_stride, cache->num_kv_heads, cache->head_dim, dtype, tokens)) != GQA_OK) return st;
+    if (tokens == 0 || batch == 0) return GQA_OK;
+    if (!q_out || !aligned16(q_out) || !block_tables || !positions) return GQA_ERR_INVALID;
+    NormRopeLaunch L = {};
+    L.desc = desc;
+    L.q = q;
+    L.k = k;
+    L.v = v;
+    L.q_stride = q_stride;
+    L.k_stride = k_stride;
+    L.v_stride = v_stride;
+    L.num_heads = num_heads;
+    L.num_kv_heads = cache->num_kv_heads;
+    L.head_dim = cache->head_dim;
+    L.dtype = dtype;
+    L.tokens = tokens;
+    L.rope_positions = rope_positions;
+    L.q_out = q_out;
+    L.cache = cache;
+    L.token_start = token_start;
+    L.tokens_per_seq = token_start ? max_new_tokens : T;
+    L.block_tables = block_tables;
+    L.max_blocks = max_blocks_per_seq;
+    L.positions = positions;
+    L.batch = batch;
+    L.err = err_flag;
+    L.stream = static_cast<cudaStream_t>(stream);
+    return launch_norm_rope(L) == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
 }
 
 int gqa_prefill(const gqa_kv_cache_t* cache, const void* q, int32_t q_dtype, int32_t num_heads,

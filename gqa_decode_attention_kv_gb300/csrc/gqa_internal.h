@@ -48,6 +48,29 @@ cudaError_t launch_kv_append(const gqa_kv_cache_t& c, const void* k_new, const v
                              const int32_t* positions, int batch, int tokens_per_seq,
                              const int32_t* token_start, int32_t* err, cudaStream_t stream);
 
+struct NormRopeLaunch {
+    const gqa_norm_rope_t* desc;
+    const void *q, *k, *v;
+    long long q_stride, k_stride, v_stride;   // elements between tokens
+    int num_heads, num_kv_heads, head_dim, dtype;
+    long long tokens;
+    const int32_t* rope_positions;            // [tokens]; NULL: the cache position
+    void* q_out;
+    void* k_out;                              // without a cache
+    const gqa_kv_cache_t* cache;              // NULL: K goes to k_out
+    const int32_t* token_start;
+    int tokens_per_seq;                       // T, or the bound with token_start
+    const int32_t* block_tables;
+    int max_blocks;
+    const int32_t* positions;
+    int batch;
+    int32_t* err;
+    cudaStream_t stream;
+};
+
+cudaError_t launch_norm_rope(const NormRopeLaunch& L);
+cudaError_t launch_rope_table(float* table, int positions, int rotary_dim, double log_base, cudaStream_t stream);
+
 struct PrefillLaunch {
     const gqa_kv_cache_t* cache;
     const void* q;

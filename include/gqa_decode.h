@@ -231,6 +231,77 @@ GQA_API int gqa_kv_append_varlen(const gqa_kv_cache_t *cache, const void *k_new,
                   const int32_t *positions, int32_t batch, int32_t *err_flag, void *stream);
 
 /*
+ * Norm and rotation of query and key heads. A head row x of d elements becomes
+ *   y = x / sqrt(mean(x^2) + eps) * weight          (a NULL weight skips the norm)
+ * and the pairs of its first rotary_dim elements turn by the angle of the token's
+ * position, (a, b) -> (a cos - b sin, b cos + a sin): pairs (i, i + rotary_dim/2),
+ * or (2i, 2i + 1) with interleaved = 1. cos and sin of position p and pair i are
+ * rope[p][i][0] and [1] (gqa_rope_table makes such a table; a caller with another
+ * rule for its angles passes its own). NULL rope: no rotation. All of it is fp32,
+ * rounded once where it is stored.
+ */
+typedef struct {
+    const void  *q_weight;    /* device [head_dim] of weight_dtype, or NULL */
+    const void  *k_weight;    /* device [head_dim] of weight_dtype, or NULL */
+    const float *rope;        /* device fp32 [rope_rows, rotary_dim/2, 2], or NULL */
+    int32_t weight_dtype;     /* F32, F16 or BF16 */
+    float   eps;              /* >= 0 */
+    int32_t rope_rows;        /* positions the table holds */
+    int32_t rotary_dim;       /* a multiple of 16, at most head_dim */
+    int32_t interleaved;      /* 0 or 1 */
+    int32_t reserved;         /* zero */
+} gqa_norm_rope_t;
+
+/*
+ * The rotation table of the usual angles: table[p][i] = (cos, sin) of
+ * p * base^(-2i / rotary_dim), p < positions, i < rotary_dim/2, computed in fp64 and
+ * rounded to fp32. base > 0, rotary_dim > 0 even; table 16-byte aligned.
+ */
+GQA_API int gqa_rope_table(float *table, int32_t positions, int32_t rotary_dim, double base, void *stream);
+
+/*
+ * Norm and rotation of q and k rows without a cache: q_out and k_out, dense
+ * [tokens, heads, head_dim] of `dtype` (F32, F16 or BF16, that of q and k).
+ *  q, k       device; heads of a token contiguous, tokens q_stride / k_stride
+ *             elements apart (so both may lie inside one fused projection), 16-byte
+ *             aligned, strides a multiple of 16 bytes. q_out == q (k_out == k) is
+ *             allowed where the stride is dense; any other overlap is not.
+ *  positions  device int32 [tokens], table rows (may be NULL without rope). A
+ *             position outside [0, rope_rows) leaves the token's rows unwritten and
+ *             flags GQA_DEVERR_POSITION.
+ */
+GQA_API int gqa_qk_norm_rope(const gqa_norm_rope_t *desc, const void *q, int64_t q_stride, void *q_out,
+                  int32_t num_heads, const void *k, int64_t k_stride, void *k_out, int32_t num_kv_heads,
+                  int32_t head_dim, int32_t dtype, int64_t tokens, const int32_t *positions, int32_t *err_flag,
+                  void *stream);
+
+/*
+ * The same with the paged append in the pass: q_out as above, K normed, turned and
+ * written to its cache slot, V written next to it, as gqa_kv_append (token_start
+ * NULL: `tokens` = batch * max_new_tokens rows, max_new_tokens per sequence, 0
+ * meaning 1) or gqa_kv_append_varlen (token_start: [batch + 1] row offsets). K is
+ * rounded, or quantised, straight from fp32: a coded cache skips the rounding to
+ * `dtype` that a separate append would read. V gets the separate append's bits.
+ *  dtype      of q, k and v: the cache's for F32, F16 and BF16 caches, any of the
+ *             three for I8, FP8_E4M3 and I4. An I4_KC cache is GQA_ERR_UNSUPPORTED
+ *             (its append re-quantises whole blocks): gqa_qk_norm_rope, then
+ *             gqa_kv_append.
+ *  rope_positions  device int32 [tokens], table row of every token; NULL: its
+ *             position in the cache.
+ *  A token whose table row is out of range is skipped (GQA_DEVERR_POSITION), a
+ *  token whose cache position or block is out of range keeps its q_out row but
+ *  writes no K and V (GQA_DEVERR_POSITION / _BLOCK_INDEX), a sequence with more than
+ *  max_new_tokens rows is skipped (GQA_DEVERR_POSITION), rows of no sequence are not
+ *  touched.
+ */
+GQA_API int gqa_qk_norm_rope_append(const gqa_kv_cache_t *cache, const gqa_norm_rope_t *desc, const void *q,
+                  int64_t q_stride, void *q_out, int32_t num_heads, const void *k, int64_t k_stride,
+                  const void *v, int64_t v_stride, int32_t dtype, int64_t tokens, const int32_t *token_start,
+                  int32_t max_new_tokens, const int32_t *block_tables, int32_t max_blocks_per_seq,
+                  const int32_t *positions, const int32_t *rope_positions, int32_t batch, int32_t *err_flag,
+                  void *stream);
+
+/*
  * Paged prefill attention: the n_b = q_start[b+1] - q_start[b] new tokens of
  * sequence b, at positions context_lens[b] - n_b .. context_lens[b] - 1, each
  * attend causally to the sequence's cache (their own K/V already appended, e.g.
