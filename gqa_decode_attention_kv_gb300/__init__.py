@@ -17,6 +17,9 @@ would repeat the module name):
 * ``rope_table``           -- (cos, sin) of every position and pair, for the two calls below
 * ``qk_norm_rope``         -- per-head norm of queries and keys and their rotation, one pass
 * ``qk_norm_rope_append``  -- the same with K and V written into the paged cache
+* ``kv_pages_reserve``, ``kv_pages_fork``, ``kv_pages_free``, ``kv_pages_trim``,
+  ``kv_pages_compact``     -- the pages of a pool: counts and block tables kept in step on the device
+* ``kv_copy_pages``        -- the page copies a fork or compaction asks for, in every layer's cache
 * ``gqa_prefill``          -- causal attention of prompts (any length) over the paged cache
 * ``decode_workspace_size``-- workspace bytes ``gqa_decode`` needs
 * ``kv_pool_elements``     -- elements a pool of ``num_blocks`` blocks holds (K and V)
@@ -41,6 +44,9 @@ GQA_DEVERR_BLOCK_INDEX = 1
 GQA_DEVERR_CONTEXT_LEN = 2
 GQA_DEVERR_POSITION = 4
 GQA_DEVERR_TIMEOUT = 8
+GQA_DEVERR_ROW = 16
+GQA_DEVERR_NO_PAGES = 32
+GQA_DEVERR_REF_COUNT = 64
 
 KERNEL_AUTO, KERNEL_MMA, KERNEL_FMA = 0, 1, 2
 GQA_DTYPE_I4 = 5
@@ -130,6 +136,18 @@ def load() -> ctypes.CDLL:
             lib.gqa_prefill.restype = ctypes.c_int
             lib.gqa_prefill_sinks.argtypes = [*lib.gqa_prefill.argtypes[:12], i32, *lib.gqa_prefill.argtypes[12:]]
             lib.gqa_prefill_sinks.restype = ctypes.c_int
+            lib.gqa_kv_pages_workspace_size.argtypes = [i64, i32]
+            lib.gqa_kv_pages_workspace_size.restype = ctypes.c_size_t
+            lib.gqa_kv_pages_reserve.argtypes = [vp, i64, vp, i32, vp, vp, i32, i32, vp, ctypes.c_size_t, vp, vp]
+            lib.gqa_kv_pages_fork.argtypes = [vp, i64, vp, i32, i32, vp, vp, vp, i32, vp, vp, vp, vp, ctypes.c_size_t,
+                                              vp, vp]
+            lib.gqa_kv_pages_free.argtypes = [vp, i64, vp, i32, i32, vp, vp, i32, vp, vp]
+            lib.gqa_kv_pages_trim.argtypes = [vp, i64, vp, i32, vp, i32, i32, i32, vp, vp]
+            lib.gqa_kv_pages_compact.argtypes = [vp, i64, vp, i32, i32, vp, i32, vp, vp, ctypes.c_size_t, vp, vp]
+            lib.gqa_kv_copy_pages.argtypes = [ctypes.POINTER(KVCacheDesc), i32, vp, vp, i32, vp, i32, vp, vp]
+            for f in (lib.gqa_kv_pages_reserve, lib.gqa_kv_pages_fork, lib.gqa_kv_pages_free, lib.gqa_kv_pages_trim,
+                      lib.gqa_kv_pages_compact, lib.gqa_kv_copy_pages):
+                f.restype = ctypes.c_int
             lib.gqa_rope_table.argtypes = [vp, i32, i32, ctypes.c_double, vp]
             lib.gqa_rope_table.restype = ctypes.c_int
             lib.gqa_qk_norm_rope.argtypes = [ctypes.POINTER(NormRopeDesc), vp, i64, vp, i32, vp, i64, vp, i32, i32,
@@ -615,6 +633,205 @@ def qk_norm_rope_append(cache: PagedKVCache, q: torch.Tensor, k: torch.Tensor, v
                                         int(block_tables.shape[1]), pp, rp, B, ep, _stream_ptr(stream))
     _check(st, "gqa_qk_norm_rope_append")
     return q_out
+
+
+@dataclasses.dataclass
+class PageCopies:
+    """What a fork or a compaction moves: ``pairs`` int32 [capacity, 2] (from, to),
+    ``count`` int32 (copies; for a compaction also the live pages), and for a fork
+    ``rows`` int32 [n, 2], the table rows of every fork that was done."""
+    pairs: torch.Tensor
+    count: torch.Tensor
+    rows: Optional[torch.Tensor] = None
+
+
+_pages_ws_cache: dict = {}
+
+
+def _pages_workspace(num_blocks: int, rows: int, device: torch.device, workspace, stream) -> torch.Tensor:
+    """The caller's workspace, or a cached one per (device, stream)."""
+    if workspace is not None:
+        _dev(workspace, "workspace")
+        return workspace
+    need = int(load().gqa_kv_pages_workspace_size(num_blocks, rows))
+    if need == 0:
+        raise ValueError(f"no workspace size for {num_blocks} pages and {rows} rows")
+    s = stream if stream is not None else torch.cuda.current_stream(device)
+    key = (device.index, s.cuda_stream)
+    buf = _pages_ws_cache.get(key)
+    if buf is None or buf.numel() < need:
+        with torch.cuda.stream(s):
+            buf = torch.empty(need, dtype=torch.uint8, device=device)
+        _pages_ws_cache[key] = buf
+    return buf
+
+
+def _check_pool(ref_counts: torch.Tensor, block_tables: torch.Tensor, lens: Optional[torch.Tensor], **more):
+    """The pool's arrays: shapes, types, and one device, which must be the current one."""
+    _dev(ref_counts, "ref_counts", True)
+    _dev(block_tables, "block_tables", True)
+    if ref_counts.dim() != 1 or block_tables.dim() != 2:
+        raise ValueError(f"ref_counts must be [num_blocks] and block_tables [rows, max_blocks], not "
+                         f"{tuple(ref_counts.shape)} and {tuple(block_tables.shape)}")
+    if lens is not None:
+        _dev(lens, "context_lens", True)
+        if lens.dim() != 1 or lens.shape[0] != block_tables.shape[0]:
+            raise ValueError(f"context_lens must be [{int(block_tables.shape[0])}], not {tuple(lens.shape)}")
+    dev = ref_counts.device
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"the pool is on {dev} but the current device is cuda:{torch.cuda.current_device()}")
+    for name, t in (("block_tables", block_tables), ("context_lens", lens), *more.items()):
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, the pool on {dev}")
+
+
+def _row_list(rows: torch.Tensor, name: str) -> int:
+    p = _dev(rows, name, True)
+    if rows.dim() != 1:
+        raise ValueError(f"{name} must be 1-D, not {tuple(rows.shape)}")
+    return p
+
+
+def kv_pages_reserve(ref_counts: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor, new_tokens,
+                     err: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                     stream=None) -> None:
+    """Pages for the next ``new_tokens`` (a number, or int32 [rows]) of every sequence:
+    the table entries they need that are still empty get the lowest free pages.
+    Entries that hold one keep it. Lengths stay as they are."""
+    many = isinstance(new_tokens, torch.Tensor)
+    np_ = _dev(new_tokens, "new_tokens", True) if many else None
+    ep = _dev(err, "err", True, True)
+    _check_pool(ref_counts, block_tables, context_lens, new_tokens=new_tokens if many else None, err=err,
+                workspace=workspace)
+    B = int(block_tables.shape[0])
+    if many and tuple(new_tokens.shape) != (B,):
+        raise ValueError(f"new_tokens must be a number or [{B}], not {tuple(new_tokens.shape)}")
+    nb = int(ref_counts.shape[0])
+    ws = _pages_workspace(nb, B, ref_counts.device, workspace, stream)
+    st = load().gqa_kv_pages_reserve(ref_counts.data_ptr(), nb, block_tables.data_ptr(), int(block_tables.shape[1]),
+                                     context_lens.data_ptr(), np_, 0 if many else int(new_tokens), B, ws.data_ptr(),
+                                     ws.numel() * ws.element_size(), ep, _stream_ptr(stream))
+    _check(st, "gqa_kv_pages_reserve")
+
+
+def kv_pages_fork(ref_counts: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
+                  src_rows: torch.Tensor, dst_rows: torch.Tensor, copies: Optional[PageCopies] = None,
+                  err: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                  stream=None) -> PageCopies:
+    """Sequences ``dst_rows[i]`` (empty rows) continue ``src_rows[i]``: full pages are
+    shared, an unfinished last page gets a fresh one, to be filled by
+    ``kv_copy_pages`` with the list returned, in every layer's cache, before the
+    sequences are read or written."""
+    sp, dp = _row_list(src_rows, "src_rows"), _row_list(dst_rows, "dst_rows")
+    if src_rows.shape != dst_rows.shape:
+        raise ValueError(f"src_rows and dst_rows differ in length: {tuple(src_rows.shape)}, {tuple(dst_rows.shape)}")
+    n = int(src_rows.shape[0])
+    ep = _dev(err, "err", True, True)
+    _check_pool(ref_counts, block_tables, context_lens, src_rows=src_rows, dst_rows=dst_rows, err=err,
+                workspace=workspace)
+    if copies is None:
+        buf = torch.empty((2 * n + 1, 2), dtype=torch.int32, device=ref_counts.device)
+        copies = PageCopies(buf[:n], buf[2 * n, :1], buf[n:2 * n])
+    elif copies.rows is None or copies.pairs.shape[0] < n or copies.rows.shape[0] != n:
+        raise ValueError(f"copies must have room for {n} pairs and exactly {n} rows")
+    else:
+        _check_copies(copies, ref_counts.device)
+    nb = int(ref_counts.shape[0])
+    ws = _pages_workspace(nb, n, ref_counts.device, workspace, stream)
+    st = load().gqa_kv_pages_fork(ref_counts.data_ptr(), nb, block_tables.data_ptr(), int(block_tables.shape[0]),
+                                  int(block_tables.shape[1]), context_lens.data_ptr(), sp, dp, n,
+                                  copies.pairs.data_ptr(), copies.count.data_ptr(), copies.rows.data_ptr(),
+                                  ws.data_ptr(), ws.numel() * ws.element_size(), ep, _stream_ptr(stream))
+    _check(st, "gqa_kv_pages_fork")
+    return copies
+
+
+def _check_copies(copies: PageCopies, device):
+    for name, t in (("pairs", copies.pairs), ("count", copies.count), ("rows", copies.rows)):
+        if t is None and name == "rows":
+            continue
+        _dev(t, f"copies.{name}", True)
+        if t.device != device:
+            raise ValueError(f"copies.{name} is on {t.device}, not {device}")
+        if name != "count" and (t.dim() != 2 or t.shape[1] != 2):
+            raise ValueError(f"copies.{name} must be [n, 2], not {tuple(t.shape)}")
+    if copies.count.numel() < 1:
+        raise ValueError("copies.count is empty")
+
+
+def kv_pages_free(ref_counts: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
+                  rows: torch.Tensor, err: Optional[torch.Tensor] = None, stream=None) -> None:
+    """The sequences in ``rows`` ended: their pages' counts fall, their entries become
+    -1 and their lengths 0."""
+    rp = _row_list(rows, "rows")
+    ep = _dev(err, "err", True, True)
+    _check_pool(ref_counts, block_tables, context_lens, rows=rows, err=err)
+    st = load().gqa_kv_pages_free(ref_counts.data_ptr(), int(ref_counts.shape[0]), block_tables.data_ptr(),
+                                  int(block_tables.shape[0]), int(block_tables.shape[1]), context_lens.data_ptr(), rp,
+                                  int(rows.shape[0]), ep, _stream_ptr(stream))
+    _check(st, "gqa_kv_pages_free")
+
+
+def kv_pages_trim(ref_counts: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor, window: int,
+                  sinks: int = 0, err: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Releases the pages that no later token of ``gqa_decode`` or ``gqa_prefill`` with
+    this ``window`` and ``sinks`` sees; their entries become -1."""
+    ep = _dev(err, "err", True, True)
+    _check_pool(ref_counts, block_tables, context_lens, err=err)
+    st = load().gqa_kv_pages_trim(ref_counts.data_ptr(), int(ref_counts.shape[0]), block_tables.data_ptr(),
+                                  int(block_tables.shape[1]), context_lens.data_ptr(), int(block_tables.shape[0]),
+                                  int(window), int(sinks), ep, _stream_ptr(stream))
+    _check(st, "gqa_kv_pages_trim")
+
+
+def kv_pages_compact(ref_counts: torch.Tensor, block_tables: torch.Tensor, max_copies: Optional[int] = None,
+                     copies: Optional[PageCopies] = None, err: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None, stream=None) -> PageCopies:
+    """Moves the highest live pages into the lowest holes until the live pages are the
+    pool's first ones, ``max_copies`` of them at most (default: as many as it takes).
+    ``kv_copy_pages`` applies the list returned; its count[1] is the number of live
+    pages. ``block_tables`` must hold every entry that names a page of the pool."""
+    ep = _dev(err, "err", True, True)
+    _check_pool(ref_counts, block_tables, None, err=err, workspace=workspace)
+    nb = int(ref_counts.shape[0])
+    if copies is None:
+        n = nb // 2 if max_copies is None else int(max_copies)
+        if n < 0:
+            raise ValueError(f"max_copies must not be negative: {n}")
+        buf = torch.empty((n + 1, 2), dtype=torch.int32, device=ref_counts.device)
+        copies = PageCopies(buf[:n], buf[n])
+    else:
+        _check_copies(copies, ref_counts.device)
+        n = int(copies.pairs.shape[0]) if max_copies is None else int(max_copies)
+        if not 0 <= n <= copies.pairs.shape[0] or copies.count.numel() < 2:
+            raise ValueError(f"copies must have room for {n} pairs and two counts")
+    ws = _pages_workspace(nb, 0, ref_counts.device, workspace, stream)
+    st = load().gqa_kv_pages_compact(ref_counts.data_ptr(), nb, block_tables.data_ptr(), int(block_tables.shape[0]),
+                                     int(block_tables.shape[1]), copies.pairs.data_ptr(), n, copies.count.data_ptr(),
+                                     ws.data_ptr(), ws.numel() * ws.element_size(), ep, _stream_ptr(stream))
+    _check(st, "gqa_kv_pages_compact")
+    return copies
+
+
+def kv_copy_pages(caches, copies: PageCopies, err: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Copies the pages of ``copies`` (K, V and scales, and for a fork of KIVI-style
+    caches the residual rows) in ``caches``: one cache, or those of all layers, which
+    must be alike in shape, layout and type."""
+    caches = [caches] if isinstance(caches, PagedKVCache) else list(caches)
+    if not caches:
+        return
+    dev = caches[0].k.device
+    _on_cache_device(caches[0], err=err)
+    _check_copies(copies, dev)
+    for c in caches[1:]:
+        if c.k.device != dev:
+            raise ValueError(f"a cache is on {c.k.device}, the first on {dev}")
+    descs = (KVCacheDesc * len(caches))(*[c.desc() for c in caches])
+    st = load().gqa_kv_copy_pages(descs, len(caches), copies.pairs.data_ptr(), copies.count.data_ptr(),
+                                  int(copies.pairs.shape[0]), copies.rows.data_ptr() if copies.rows is not None else None,
+                                  int(copies.rows.shape[0]) if copies.rows is not None else 0,
+                                  _dev(err, "err", True, True), _stream_ptr(stream))
+    _check(st, "gqa_kv_copy_pages")
 
 
 def gqa_prefill(cache: PagedKVCache, q: torch.Tensor, q_start: torch.Tensor, max_new_tokens: int,

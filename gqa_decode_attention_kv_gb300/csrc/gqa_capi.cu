@@ -78,6 +78,21 @@ int check_residual(const gqa_kv_cache_t* c, int batch) {
     return GQA_OK;
 }
 
+// The page bookkeeping's pool and tables.
+constexpr int64_t kMaxPages = 0x7fffffffLL - 65536;   // indices of a scan's last round stay below 2^31
+constexpr int kMaxTableRows = 1 << 20;
+constexpr int kMaxForkRows = 8192;                    // rows whose claims fit shared memory
+int check_pool(const int32_t* refs, int64_t num_blocks, const int32_t* tables, int rows, int max_blocks) {
+    if (!refs || !aligned16(refs) || num_blocks <= 0 || rows < 0 || max_blocks <= 0) return GQA_ERR_INVALID;
+    if ((long long)max_blocks * GQA_BLOCK_SIZE > 0x7fffffffLL) return GQA_ERR_INVALID;
+    if (num_blocks > kMaxPages || rows > kMaxTableRows) return GQA_ERR_UNSUPPORTED;
+    return rows > 0 && !tables ? GQA_ERR_INVALID : GQA_OK;
+}
+int check_pages_ws(const void* ws, size_t bytes, int64_t num_blocks, int rows) {
+    if (!ws || bytes < gqa_kv_pages_workspace_size(num_blocks, rows)) return GQA_ERR_WORKSPACE;
+    return aligned16(ws) ? GQA_OK : GQA_ERR_INVALID;
+}
+
 bool plain_dtype(int dt) { return dt == GQA_DTYPE_F32 || dt == GQA_DTYPE_F16 || dt == GQA_DTYPE_BF16; }
 
 // The description of a norm and rotation, for rows of head_dim elements of dtype.
@@ -348,6 +363,168 @@ int gqa_kv_append_varlen(const gqa_kv_cache_t* cache, const void* k_new, const v
                                            max_blocks_per_seq, positions, batch, max_new_tokens,
                                            token_start, err_flag, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
+}
+
+size_t gqa_kv_pages_workspace_size(int64_t num_blocks, int32_t rows) {
+    if (num_blocks <= 0 || num_blocks > kMaxPages || rows < 0 || rows > kMaxTableRows) return 0;
+    return (size_t)(64 + pages_ws_rows(num_blocks, rows) + num_blocks) * sizeof(int32_t);
+}
+
+int gqa_kv_pages_reserve(int32_t* ref_counts, int64_t num_blocks, int32_t* block_tables, int32_t max_blocks_per_seq,
+                         const int32_t* context_lens, const int32_t* new_tokens, int32_t tokens_per_seq, int32_t batch,
+                         void* workspace, size_t workspace_bytes, int32_t* err_flag, void* stream) {
+    int st = check_pool(ref_counts, num_blocks, block_tables, batch, max_blocks_per_seq);
+    if (st != GQA_OK) return st;
+    if (!new_tokens && tokens_per_seq < 0) return GQA_ERR_INVALID;
+    if (batch == 0 || (!new_tokens && tokens_per_seq == 0)) return GQA_OK;
+    if (!context_lens) return GQA_ERR_INVALID;
+    if ((st = check_pages_ws(workspace, workspace_bytes, num_blocks, batch)) != GQA_OK) return st;
+    PagesLaunch L = {};
+    L.ref_counts = ref_counts;
+    L.num_blocks = num_blocks;
+    L.block_tables = block_tables;
+    L.table_rows = batch;
+    L.max_blocks = max_blocks_per_seq;
+    L.context_lens = const_cast<int32_t*>(context_lens);
+    L.n = batch;
+    L.new_tokens = new_tokens;
+    L.tokens = tokens_per_seq;
+    L.workspace = workspace;
+    L.err = err_flag;
+    L.stream = static_cast<cudaStream_t>(stream);
+    return launch_pages_reserve(L) == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
+}
+
+int gqa_kv_pages_fork(int32_t* ref_counts, int64_t num_blocks, int32_t* block_tables, int32_t table_rows,
+                      int32_t max_blocks_per_seq, int32_t* context_lens, const int32_t* src_rows,
+                      const int32_t* dst_rows, int32_t n, int32_t* pairs, int32_t* count, int32_t* row_pairs,
+                      void* workspace, size_t workspace_bytes, int32_t* err_flag, void* stream) {
+    int st = check_pool(ref_counts, num_blocks, block_tables, table_rows, max_blocks_per_seq);
+    if (st != GQA_OK) return st;
+    if (n < 0) return GQA_ERR_INVALID;
+    if (table_rows > kMaxForkRows || n > kMaxForkRows) return GQA_ERR_UNSUPPORTED;
+    if (!count) return GQA_ERR_INVALID;
+    if (n > 0 && (table_rows == 0 || !context_lens || !src_rows || !dst_rows || !pairs || !row_pairs))
+        return GQA_ERR_INVALID;
+    if ((st = check_pages_ws(workspace, workspace_bytes, num_blocks, n)) != GQA_OK) return st;
+    PagesLaunch L = {};
+    L.ref_counts = ref_counts;
+    L.num_blocks = num_blocks;
+    L.block_tables = block_tables;
+    L.table_rows = table_rows;
+    L.max_blocks = max_blocks_per_seq;
+    L.context_lens = context_lens;
+    L.n = n;
+    L.src_rows = src_rows;
+    L.dst_rows = dst_rows;
+    L.pairs = pairs;
+    L.count = count;
+    L.row_pairs = row_pairs;
+    L.max_copies = n;
+    L.workspace = workspace;
+    L.err = err_flag;
+    L.stream = static_cast<cudaStream_t>(stream);
+    return launch_pages_fork(L) == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
+}
+
+int gqa_kv_pages_free(int32_t* ref_counts, int64_t num_blocks, int32_t* block_tables, int32_t table_rows,
+                      int32_t max_blocks_per_seq, int32_t* context_lens, const int32_t* rows, int32_t n,
+                      int32_t* err_flag, void* stream) {
+    const int st = check_pool(ref_counts, num_blocks, block_tables, table_rows, max_blocks_per_seq);
+    if (st != GQA_OK) return st;
+    if (n < 0) return GQA_ERR_INVALID;
+    if (n == 0) return GQA_OK;
+    if (table_rows == 0 || !context_lens || !rows) return GQA_ERR_INVALID;
+    PagesLaunch L = {};
+    L.ref_counts = ref_counts;
+    L.num_blocks = num_blocks;
+    L.block_tables = block_tables;
+    L.table_rows = table_rows;
+    L.max_blocks = max_blocks_per_seq;
+    L.context_lens = context_lens;
+    L.n = n;
+    L.src_rows = rows;
+    L.err = err_flag;
+    L.stream = static_cast<cudaStream_t>(stream);
+    return launch_pages_free(L) == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
+}
+
+int gqa_kv_pages_trim(int32_t* ref_counts, int64_t num_blocks, int32_t* block_tables, int32_t max_blocks_per_seq,
+                      const int32_t* context_lens, int32_t batch, int32_t sliding_window, int32_t sink_tokens,
+                      int32_t* err_flag, void* stream) {
+    const int st = check_pool(ref_counts, num_blocks, block_tables, batch, max_blocks_per_seq);
+    if (st != GQA_OK) return st;
+    if (sliding_window < 1 || sink_tokens < 0) return GQA_ERR_INVALID;
+    if (batch == 0) return GQA_OK;
+    if (!context_lens) return GQA_ERR_INVALID;
+    PagesLaunch L = {};
+    L.ref_counts = ref_counts;
+    L.num_blocks = num_blocks;
+    L.block_tables = block_tables;
+    L.table_rows = batch;
+    L.max_blocks = max_blocks_per_seq;
+    L.context_lens = const_cast<int32_t*>(context_lens);
+    L.n = batch;
+    L.window = sliding_window;
+    L.sinks = sink_tokens;
+    L.err = err_flag;
+    L.stream = static_cast<cudaStream_t>(stream);
+    return launch_pages_trim(L) == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
+}
+
+int gqa_kv_pages_compact(int32_t* ref_counts, int64_t num_blocks, int32_t* block_tables, int32_t table_rows,
+                         int32_t max_blocks_per_seq, int32_t* pairs, int32_t max_copies, int32_t* count,
+                         void* workspace, size_t workspace_bytes, int32_t* err_flag, void* stream) {
+    int st = check_pool(ref_counts, num_blocks, block_tables, table_rows, max_blocks_per_seq);
+    if (st != GQA_OK) return st;
+    if (max_copies < 0 || !count || (max_copies > 0 && !pairs)) return GQA_ERR_INVALID;
+    if ((st = check_pages_ws(workspace, workspace_bytes, num_blocks, 0)) != GQA_OK) return st;
+    PagesLaunch L = {};
+    L.ref_counts = ref_counts;
+    L.num_blocks = num_blocks;
+    L.block_tables = block_tables;
+    L.table_rows = table_rows;
+    L.max_blocks = max_blocks_per_seq;
+    L.pairs = pairs;
+    L.count = count;
+    L.max_copies = max_copies;
+    L.workspace = workspace;
+    L.err = err_flag;
+    L.stream = static_cast<cudaStream_t>(stream);
+    return launch_pages_compact(L) == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
+}
+
+int gqa_kv_copy_pages(const gqa_kv_cache_t* caches, int32_t num_caches, const int32_t* pairs, const int32_t* count,
+                      int32_t max_copies, const int32_t* row_pairs, int32_t rows, int32_t* err_flag, void* stream) {
+    if (num_caches < 0 || max_copies < 0 || rows < 0) return GQA_ERR_INVALID;
+    if (num_caches == 0) return GQA_OK;
+    if (!caches) return GQA_ERR_INVALID;
+    const gqa_kv_cache_t& c0 = caches[0];
+    for (int i = 0; i < num_caches; ++i) {
+        const gqa_kv_cache_t& c = caches[i];
+        const int st = check_cache(&c);
+        if (st != GQA_OK) return st;
+        if (c.num_blocks != c0.num_blocks || c.num_kv_heads != c0.num_kv_heads || c.head_dim != c0.head_dim ||
+            c.dtype != c0.dtype || c.stride_block != c0.stride_block || c.stride_head != c0.stride_head ||
+            c.stride_token != c0.stride_token || c.residual_rows != c0.residual_rows)
+            return GQA_ERR_INVALID;
+        if (c.dtype == GQA_DTYPE_I4_KC && row_pairs && rows > 0 && (!c.k_residual || !aligned16(c.k_residual)))
+            return GQA_ERR_INVALID;
+    }
+    const bool with_rows = c0.dtype == GQA_DTYPE_I4_KC && row_pairs && rows > 0;
+    if (max_copies == 0 && !with_rows) return GQA_OK;
+    if (!count || (max_copies > 0 && !pairs)) return GQA_ERR_INVALID;
+    CopyPagesLaunch L = {};
+    L.caches = caches;
+    L.num_caches = num_caches;
+    L.pairs = pairs;
+    L.count = count;
+    L.max_copies = max_copies;
+    L.row_pairs = with_rows ? row_pairs : nullptr;
+    L.rows = with_rows ? rows : 0;
+    L.err = err_flag;
+    L.stream = static_cast<cudaStream_t>(stream);
+    return launch_copy_pages(L) == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
 }
 
 int gqa_rope_table(float* table, int32_t positions, int32_t rotary_dim, double base, void* stream) {

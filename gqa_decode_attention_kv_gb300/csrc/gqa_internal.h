@@ -71,6 +71,39 @@ struct NormRopeLaunch {
 cudaError_t launch_norm_rope(const NormRopeLaunch& L);
 cudaError_t launch_rope_table(float* table, int positions, int rotary_dim, double log_base, cudaStream_t stream);
 
+// The page bookkeeping: which fields a call reads is said at its entry point.
+struct PagesLaunch {
+    int32_t* ref_counts;
+    long long num_blocks;
+    int32_t* block_tables;
+    int table_rows, max_blocks;
+    int32_t* context_lens;
+    int n;                                    // rows of the call (reserve, trim: the table's first n)
+    const int32_t *src_rows, *dst_rows, *new_tokens;
+    int tokens, window, sinks;
+    int32_t *pairs, *count, *row_pairs;
+    int max_copies;
+    void* workspace;
+    int32_t* err;
+    cudaStream_t stream;
+};
+long long pages_ws_rows(long long num_blocks, int rows);
+cudaError_t launch_pages_reserve(const PagesLaunch& L);
+cudaError_t launch_pages_fork(const PagesLaunch& L);
+cudaError_t launch_pages_free(const PagesLaunch& L);
+cudaError_t launch_pages_trim(const PagesLaunch& L);
+cudaError_t launch_pages_compact(const PagesLaunch& L);
+
+struct CopyPagesLaunch {
+    const gqa_kv_cache_t* caches;             // one geometry
+    int num_caches;
+    const int32_t *pairs, *count, *row_pairs;
+    int max_copies, rows;
+    int32_t* err;
+    cudaStream_t stream;
+};
+cudaError_t launch_copy_pages(const CopyPagesLaunch& L);
+
 struct PrefillLaunch {
     const gqa_kv_cache_t* cache;
     const void* q;

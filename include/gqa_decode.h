@@ -69,6 +69,9 @@ typedef enum {
 #define GQA_DEVERR_CONTEXT_LEN 2   /* context length < 0 or > max_blocks_per_seq * 16 */
 #define GQA_DEVERR_POSITION    4   /* append position < 0 or >= max_blocks_per_seq * 16 */
 #define GQA_DEVERR_TIMEOUT     8   /* a bounded wait for an asynchronous copy expired */
+#define GQA_DEVERR_ROW        16   /* a row index outside the table, or a fork that may not be (see gqa_kv_pages_fork) */
+#define GQA_DEVERR_NO_PAGES   32   /* not enough free pages for a row */
+#define GQA_DEVERR_REF_COUNT  64   /* a released page that no entry held */
 
 #define GQA_BLOCK_SIZE 16
 
@@ -300,6 +303,108 @@ GQA_API int gqa_qk_norm_rope_append(const gqa_kv_cache_t *cache, const gqa_norm_
                   int32_t max_new_tokens, const int32_t *block_tables, int32_t max_blocks_per_seq,
                   const int32_t *positions, const int32_t *rope_positions, int32_t batch, int32_t *err_flag,
                   void *stream);
+
+/*
+ * Pages. A page is one physical block of every layer's cache; ref_counts[p] is the
+ * number of block-table entries that hold page p (0: free), an entry < 0 holds none.
+ * A pool starts as zero counts and tables of -1, and these calls keep both in step:
+ *   gqa_kv_pages_reserve  pages for the next tokens of every sequence
+ *   gqa_kv_pages_fork     a sequence continued by others that share its full pages
+ *   gqa_kv_pages_free     sequences that ended
+ *   gqa_kv_pages_trim     pages that left the sliding window
+ *   gqa_kv_pages_compact  the live pages moved to the front of the pool
+ * Choices go by index alone, so equal calls on equal states give equal tables. Fork and
+ * compact write a list of page copies that gqa_kv_copy_pages applies to the caches of
+ * all layers (they share the tables). All calls run on device data, without the host
+ * reading any of it, and may be captured; calls on one pool must not overlap.
+ *
+ *  ref_counts    device int32 [num_blocks], 16-byte aligned; num_blocks < 2^31.
+ *  block_tables  device int32 [table_rows, max_blocks_per_seq].
+ *  context_lens  device int32 [table_rows].
+ *  workspace     device, 16-byte aligned, gqa_kv_pages_workspace_size(num_blocks, rows)
+ *                bytes (rows: those of the call), clobbered.
+ */
+GQA_API size_t gqa_kv_pages_workspace_size(int64_t num_blocks, int32_t rows);
+
+/*
+ * Pages for the next tokens: for every row b < batch the empty entries of blocks
+ * ceil(L/16) .. ceil((L + n)/16) - 1 (L = context_lens[b]; n = new_tokens[b], or
+ * tokens_per_seq where new_tokens is NULL) get the lowest free pages, row by row and
+ * block by block. Entries that hold a page keep it, so a repeated call changes nothing.
+ * A row that the free pages do not cover whole gets none, and neither do the rows
+ * after it that need any (GQA_DEVERR_NO_PAGES); a row with L < 0, n < 0 or L + n beyond its table
+ * gets none (GQA_DEVERR_POSITION). batch <= table_rows; context_lens is not changed.
+ */
+GQA_API int gqa_kv_pages_reserve(int32_t *ref_counts, int64_t num_blocks, int32_t *block_tables,
+                  int32_t max_blocks_per_seq, const int32_t *context_lens, const int32_t *new_tokens,
+                  int32_t tokens_per_seq, int32_t batch, void *workspace, size_t workspace_bytes,
+                  int32_t *err_flag, void *stream);
+
+/*
+ * Forks: row dst_rows[i] becomes a copy of row src_rows[i], i < n. It shares the
+ * parent's full pages (their counts rise; empty entries stay empty); an unfinished
+ * last page (L % 16 != 0) is copied to a fresh one, so each sequence may append. One
+ * parent may have many children. Fork i is refused, and its row left alone, with
+ * GQA_DEVERR_ROW if a row index is outside the table, the destination is named by an
+ * earlier fork or is not empty (context_lens != 0; its entries must be empty too: free
+ * it first), or the parent is some fork's destination;
+ * GQA_DEVERR_NO_PAGES if no page is left for it; GQA_DEVERR_BLOCK_INDEX if the parent's
+ * last entry is no page; GQA_DEVERR_CONTEXT_LEN if the parent's length is out of range.
+ *  pairs      device int32 [n, 2]: (from, to) pages of the copies, count[0] of them.
+ *  row_pairs  device int32 [n, 2]: (src, dst) of every fork done, (-1, -1) else (for
+ *             the residual rows of a KIVI-style cache).
+ *  table_rows <= 8192.
+ */
+GQA_API int gqa_kv_pages_fork(int32_t *ref_counts, int64_t num_blocks, int32_t *block_tables, int32_t table_rows,
+                  int32_t max_blocks_per_seq, int32_t *context_lens, const int32_t *src_rows,
+                  const int32_t *dst_rows, int32_t n, int32_t *pairs, int32_t *count, int32_t *row_pairs,
+                  void *workspace, size_t workspace_bytes, int32_t *err_flag, void *stream);
+
+/*
+ * Sequences that ended: every entry of rows[i], i < n, is emptied and its page's count
+ * falls by one; context_lens of the row becomes 0. A row may be named twice. A page
+ * whose count was 0 stays at 0 (GQA_DEVERR_REF_COUNT); a row outside the table is
+ * skipped (GQA_DEVERR_ROW).
+ */
+GQA_API int gqa_kv_pages_free(int32_t *ref_counts, int64_t num_blocks, int32_t *block_tables, int32_t table_rows,
+                  int32_t max_blocks_per_seq, int32_t *context_lens, const int32_t *rows, int32_t n,
+                  int32_t *err_flag, void *stream);
+
+/*
+ * Pages that no later token sees under a sliding window W >= 1 with S sink tokens: in
+ * rows b < batch, blocks j with 16 j >= S and 16 (j + 1) <= context_lens[b] + 1 - W are
+ * released as by gqa_kv_pages_free. A row whose length is out of range is skipped
+ * (GQA_DEVERR_CONTEXT_LEN). (A caller that may take tokens back lowers context_lens
+ * first: a released page is gone.)
+ */
+GQA_API int gqa_kv_pages_trim(int32_t *ref_counts, int64_t num_blocks, int32_t *block_tables,
+                  int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t batch,
+                  int32_t sliding_window, int32_t sink_tokens, int32_t *err_flag, void *stream);
+
+/*
+ * Compaction: with N live pages, the i-th highest live page at or past index N moves to
+ * the i-th lowest hole below N, for i < max_copies (fewer than all leaves a pool that the
+ * next call goes on with). Counts and every entry of block_tables follow; table rows must
+ * cover all entries that hold pages of the pool.
+ *  pairs  device int32 [max_copies, 2]; count  device int32 [2]: copies, live pages N.
+ */
+GQA_API int gqa_kv_pages_compact(int32_t *ref_counts, int64_t num_blocks, int32_t *block_tables, int32_t table_rows,
+                  int32_t max_blocks_per_seq, int32_t *pairs, int32_t max_copies, int32_t *count,
+                  void *workspace, size_t workspace_bytes, int32_t *err_flag, void *stream);
+
+/*
+ * Page copies in the caches of all layers: for i < min(count[0], max_copies), K, V and
+ * scales of page pairs[i][0] to page pairs[i][1], bit for bit. A destination must be
+ * named once and be no source (the lists of fork and compact are so). A pair outside
+ * the pool is skipped (GQA_DEVERR_BLOCK_INDEX).
+ *  caches     num_caches descriptions of one geometry (all but their pointers equal).
+ *  row_pairs  NULL, or device int32 [rows, 2]: residual rows of a KIVI-style cache to
+ *             copy with a fork, negative ones skipped, ones past residual_rows too
+ *             (GQA_DEVERR_ROW). Ignored for other caches. Compaction moves none.
+ */
+GQA_API int gqa_kv_copy_pages(const gqa_kv_cache_t *caches, int32_t num_caches, const int32_t *pairs,
+                  const int32_t *count, int32_t max_copies, const int32_t *row_pairs, int32_t rows,
+                  int32_t *err_flag, void *stream);
 
 /*
  * Paged prefill attention: the n_b = q_start[b+1] - q_start[b] new tokens of
