@@ -10,8 +10,9 @@
 // every layer's cache by the list that the bookkeeping wrote.
 //
 // Bound: the bookkeeping by latency (kilobytes are read; one CTA finds the free pages,
-// 32 warps scanning 1024 counts each a round, and a second, wide launch writes the
-// tables), the copies by memory (every moved byte is read and written once).
+// 32 warps scanning 1024 counts each a round; it also writes the tables where they are
+// few entries, a second, wide launch where they are many), the copies by memory (every
+// moved byte is read and written once).
 #include <algorithm>
 #include <climits>
 
@@ -28,6 +29,9 @@ constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kChunk = 1024;                 // ref counts one warp scans at a time
 constexpr int kWideThreads = 256;
+// Table entries up to which the planning CTA writes them itself (four a thread): a
+// second launch costs 4-5 us of host time and ~2 us on the GPU.
+constexpr long long kFewEntries = 4 * kPlanThreads;
 
 struct PageArgs {
     int32_t* refs;
@@ -188,6 +192,8 @@ __device__ __forceinline__ bool reserve_range(const PageArgs& a, int b, int& lo,
     return true;
 }
 
+// kAll: the CTA also hands the pages out, a thread per row (host: few blocks a row).
+template <bool kAll>
 __global__ void __launch_bounds__(kPlanThreads) reserve_plan_kernel(const PageArgs a) {
     __shared__ int tmp[kPlanWarps + 1];
     grid_dependency_wait();
@@ -220,6 +226,25 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_plan_kernel(const PageAr
     if (threadIdx.x == 0) a.ws_rows[a.n] = carry;
     const int found = find_free(a, carry, a.ws_list, tmp);
     if (threadIdx.x == 0) a.ws_hdr[0] = found;
+    if constexpr (kAll) {
+        for (int b = threadIdx.x; b < a.n; b += kPlanThreads) {
+            int k = a.ws_rows[b], lo, hi;
+            const int end = b + 1 < a.n ? a.ws_rows[b + 1] : carry;
+            if (k == end) continue;
+            if (end > found) {                   // not enough pages for the whole row: none
+                flag_error(a.err, GQA_DEVERR_NO_PAGES);
+                continue;
+            }
+            if (!reserve_range(a, b, lo, hi)) continue;
+            int32_t* row = a.tables + (long long)b * a.max_blocks;
+            for (int j = lo; j < hi; ++j) {
+                if (row[j] >= 0) continue;
+                const int p = a.ws_list[k++];
+                row[j] = p;
+                a.refs[p] = 1;
+            }
+        }
+    }
 }
 
 __global__ void __launch_bounds__(kWideThreads) reserve_assign_kernel(const PageArgs a) {
@@ -256,6 +281,34 @@ __global__ void __launch_bounds__(kWideThreads) reserve_assign_kernel(const Page
 // ws_rows[i] of fork i: its rank among those that need a fresh page, or one of these.
 enum ForkKind : int { kForkSkip = -1, kForkWhole = -2 };
 
+// Table entries of the forks, from thread `at` on in steps of `step`.
+__device__ __forceinline__ void fork_entries(const PageArgs& a, long long at, long long step) {
+    const long long total = (long long)a.n * a.max_blocks;
+    for (long long x = at; x < total; x += step) {
+        const int i = (int)(x / a.max_blocks), j = (int)(x - (long long)i * a.max_blocks);
+        const int kind = a.ws_rows[i];
+        if (kind == kForkSkip) continue;
+        const int s = a.src[i], L = a.lens[s];
+        int p = -1;
+        if (j < blocks_of(L)) {
+            if (kind >= 0 && j == L / kBlock) {
+                p = a.ws_list[kind];         // its count was set with the plan
+            } else {
+                p = a.tables[(long long)s * a.max_blocks + j];
+                if (p >= a.num_blocks) {
+                    flag_error(a.err, GQA_DEVERR_BLOCK_INDEX);
+                    p = -1;
+                }
+                if (p >= 0) atomicAdd(a.refs + p, 1);
+                else p = -1;
+            }
+        }
+        a.tables[(long long)a.dst[i] * a.max_blocks + j] = p;
+    }
+}
+
+// kAll: the CTA writes the tables too (host: few entries).
+template <bool kAll>
 __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const PageArgs a) {
     extern __shared__ int claim[];           // [table_rows] the first fork that writes the row
     __shared__ int tmp[kPlanWarps + 1];
@@ -319,34 +372,16 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const PageArgs 
     // the children's lengths last: lens[s] of every fork has been read (no s is a d)
     for (int i = threadIdx.x; i < a.n; i += kPlanThreads)
         if (a.ws_rows[i] != kForkSkip) a.lens[a.dst[i]] = a.lens[a.src[i]];
+    if constexpr (kAll) {
+        __syncthreads();
+        fork_entries(a, threadIdx.x, kPlanThreads);
+    }
 }
 
 __global__ void __launch_bounds__(kWideThreads) fork_tables_kernel(const PageArgs a) {
     grid_dependency_wait();
     launch_dependents();
-    const long long total = (long long)a.n * a.max_blocks;
-    for (long long x = (long long)blockIdx.x * kWideThreads + threadIdx.x; x < total;
-         x += (long long)gridDim.x * kWideThreads) {
-        const int i = (int)(x / a.max_blocks), j = (int)(x - (long long)i * a.max_blocks);
-        const int kind = a.ws_rows[i];
-        if (kind == kForkSkip) continue;
-        const int s = a.src[i], L = a.lens[s];
-        int p = -1;
-        if (j < blocks_of(L)) {
-            if (kind >= 0 && j == L / kBlock) {
-                p = a.ws_list[kind];         // its count was set with the plan
-            } else {
-                p = a.tables[(long long)s * a.max_blocks + j];
-                if (p >= a.num_blocks) {
-                    flag_error(a.err, GQA_DEVERR_BLOCK_INDEX);
-                    p = -1;
-                }
-                if (p >= 0) atomicAdd(a.refs + p, 1);
-                else p = -1;
-            }
-        }
-        a.tables[(long long)a.dst[i] * a.max_blocks + j] = p;
-    }
+    fork_entries(a, (long long)blockIdx.x * kWideThreads + threadIdx.x, (long long)gridDim.x * kWideThreads);
 }
 
 // ------------------------------------------------------------------ free, trim
@@ -427,7 +462,32 @@ __device__ __forceinline__ void compact_header(const PageArgs& a, int live) {
     if (live >= a.num_blocks) a.ws_hdr[0] = 0;   // a full pool has no holes
 }
 
+// Counts of the moved pages and the table entries that name them, from thread `at` on.
+__device__ __forceinline__ void compact_apply(const PageArgs& a, int moves, int live, long long at, long long step) {
+    if (at == 0) a.count[0] = moves;
+    for (long long i = at; i < moves; i += step) {
+        const int s = a.pairs[2 * i], d = a.pairs[2 * i + 1];
+        a.refs[d] = a.refs[s];
+        a.refs[s] = 0;
+    }
+    const long long total = (long long)a.table_rows * a.max_blocks;
+    for (long long x = at; x < total; x += step) {
+        const int p = a.tables[x];
+        if (p < live) continue;
+        if (p >= a.num_blocks) {
+            flag_error(a.err, GQA_DEVERR_BLOCK_INDEX);
+            continue;
+        }
+        // the list holds a rank for every live page from `live` on; an entry whose
+        // page nobody holds finds an old word there, which names another page's pair
+        const int r = a.ws_list[p];
+        if (r >= 0 && r < moves && a.pairs[2 * r] == p) a.tables[x] = a.pairs[2 * r + 1];
+    }
+}
+
 // Pools of at most 32 chunks: one CTA, the counts held in registers between the scans.
+// kAll: it also applies the moves (host: few entries).
+template <bool kAll>
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const PageArgs a) {
     __shared__ int tmp[kPlanWarps + 1];
     grid_dependency_wait();
@@ -439,6 +499,10 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const PageAr
     const int before = __shfl_sync(kFull, block_scan(lane == 0 ? cnt : 0, tmp, live), 0);
     if (base < a.num_blocks) compact_chunk(a, held, base, before, live, lane);
     if (threadIdx.x == 0) compact_header(a, live);
+    if constexpr (kAll) {
+        __syncthreads();
+        compact_apply(a, a.ws_hdr[0], live, threadIdx.x, kPlanThreads);
+    }
 }
 
 // Larger pools: the live pages of every chunk, then the same with the chunks' sums
@@ -473,27 +537,8 @@ __global__ void __launch_bounds__(kWideThreads) compact_pairs_kernel(const PageA
 __global__ void __launch_bounds__(kWideThreads) compact_apply_kernel(const PageArgs a) {
     grid_dependency_wait();
     launch_dependents();
-    const int moves = a.ws_hdr[0], live = a.ws_hdr[1];
-    const long long at = (long long)blockIdx.x * kWideThreads + threadIdx.x, step = (long long)gridDim.x * kWideThreads;
-    if (at == 0) a.count[0] = moves;
-    for (long long i = at; i < moves; i += step) {
-        const int s = a.pairs[2 * i], d = a.pairs[2 * i + 1];
-        a.refs[d] = a.refs[s];
-        a.refs[s] = 0;
-    }
-    const long long total = (long long)a.table_rows * a.max_blocks;
-    for (long long x = at; x < total; x += step) {
-        const int p = a.tables[x];
-        if (p < live) continue;
-        if (p >= a.num_blocks) {
-            flag_error(a.err, GQA_DEVERR_BLOCK_INDEX);
-            continue;
-        }
-        // the list holds a rank for every live page from `live` on; an entry whose
-        // page nobody holds finds an old word there, which names another page's pair
-        const int r = a.ws_list[p];
-        if (r >= 0 && r < moves && a.pairs[2 * r] == p) a.tables[x] = a.pairs[2 * r + 1];
-    }
+    compact_apply(a, a.ws_hdr[0], a.ws_hdr[1], (long long)blockIdx.x * kWideThreads + threadIdx.x,
+                  (long long)gridDim.x * kWideThreads);
 }
 
 // ------------------------------------------------------------------ copies
@@ -639,7 +684,10 @@ long long pages_ws_rows(long long num_blocks, int rows) {
 
 cudaError_t launch_pages_reserve(const PagesLaunch& L) {
     const PageArgs a = page_args(L);
-    cudaError_t e = launch_pages(&reserve_plan_kernel, 1, kPlanThreads, 0, a, L.stream);
+    // a thread per row hands out up to five pages; longer rows get a warp each
+    if (a.new_tokens == nullptr && a.tokens <= 4 * kBlock)
+        return launch_pages(&reserve_plan_kernel<true>, 1, kPlanThreads, 0, a, L.stream);
+    cudaError_t e = launch_pages(&reserve_plan_kernel<false>, 1, kPlanThreads, 0, a, L.stream);
     if (e != cudaSuccess) return e;
     void* args[] = {const_cast<PageArgs*>(&a)};
     const unsigned grid = (unsigned)((a.n + kWideThreads / 32 - 1) / (kWideThreads / 32));   // a warp per row
@@ -648,7 +696,9 @@ cudaError_t launch_pages_reserve(const PagesLaunch& L) {
 
 cudaError_t launch_pages_fork(const PagesLaunch& L) {
     const PageArgs a = page_args(L);
-    cudaError_t e = launch_pages(&fork_plan_kernel, 1, kPlanThreads, a.table_rows * 4, a, L.stream);
+    if ((long long)a.n * a.max_blocks <= kFewEntries)
+        return launch_pages(&fork_plan_kernel<true>, 1, kPlanThreads, a.table_rows * 4, a, L.stream);
+    cudaError_t e = launch_pages(&fork_plan_kernel<false>, 1, kPlanThreads, a.table_rows * 4, a, L.stream);
     if (e != cudaSuccess) return e;
     return launch_pages(&fork_tables_kernel, (long long)a.n * a.max_blocks, kWideThreads, 0, a, L.stream);
 }
@@ -667,8 +717,10 @@ cudaError_t launch_pages_compact(const PagesLaunch& L) {
     PageArgs a = page_args(L);
     int chunks = (a.num_blocks + kChunk - 1) / kChunk;
     cudaError_t e;
+    const long long entries = std::max<long long>((long long)a.table_rows * a.max_blocks, a.max_copies);
     if (chunks <= kPlanWarps) {
-        e = launch_pages(&compact_plan_kernel, 1, kPlanThreads, 0, a, L.stream);
+        if (entries <= kFewEntries) return launch_pages(&compact_plan_kernel<true>, 1, kPlanThreads, 0, a, L.stream);
+        e = launch_pages(&compact_plan_kernel<false>, 1, kPlanThreads, 0, a, L.stream);
     } else {
         const unsigned grid = (unsigned)((chunks + kWideThreads / 32 - 1) / (kWideThreads / 32));
         void* args[] = {&a};
@@ -678,8 +730,7 @@ cudaError_t launch_pages_compact(const PagesLaunch& L) {
         e = launch_pdl(reinterpret_cast<const void*>(&compact_pairs_kernel), grid, kWideThreads, 0, L.stream, args2);
     }
     if (e != cudaSuccess) return e;
-    return launch_pages(&compact_apply_kernel, std::max<long long>((long long)a.table_rows * a.max_blocks, a.max_copies),
-                        kWideThreads, 0, a, L.stream);
+    return launch_pages(&compact_apply_kernel, entries, kWideThreads, 0, a, L.stream);
 }
 
 // Runs of a page of K or V: the head dimension, then the axes that lie right behind

@@ -23,7 +23,12 @@
 // sinks and then, without a gap, the blocks from the tile's window start on
 // (BlockWalk below), so a chunk can hold blocks of both and the ones between are
 // never read. Sinks cost ceil(S / 16) blocks a tile; the other instantiations
-// are the same code as before them.
+// are the same code as before them. What a chunk of both costs is its masks and
+// the zeroing of V rows that nobody sees, so in the tcgen05 forms a tile's chunks
+// end with its last block (missing blocks pad the first chunk, and the diagonal
+// stays in as few chunks as without sinks), a row's mask is built a block at a time
+// as bits, and the V copy warp zeroes its rows as they land instead of the softmax
+// warps (8 x 2048-token prompts, W = 1024, S = 4: PREFILL_FIGURES).
 #include <algorithm>
 #include <cstring>
 #include <type_traits>
@@ -86,6 +91,29 @@ __device__ __forceinline__ int sink_blocks(const PrefillArgs& a, int jb_lo) {
     if constexpr (!kSinks) return 0;
     else return min((a.sinks + kBlock - 1) / kBlock, jb_lo);
 }
+// Missing blocks before the walk, so that chunks of `per` blocks end with its end.
+template <bool kSinks>
+__device__ __forceinline__ int walk_pad(const BlockWalk<kSinks>& w, int per) {
+    if constexpr (!kSinks) return 0;
+    else return (per - w.count() % per) % per;
+}
+// Bit t: a row that attends [lo, hi) and the first `sinks` attends position base + t,
+// t < 16.
+__device__ __forceinline__ uint32_t seen_bits(int base, int lo, int hi, int sinks) {
+    auto below = [&](int x) { return (1u << min(max(x - base, 0), (int)kBlock)) - 1u; };   // positions < x
+    return (~below(lo) | below(sinks)) & below(hi) & 0xffffu;
+}
+// The same for the blocks of a chunk that begins at step v of the walk (steps below 0
+// and blocks outside `present` hold nothing).
+template <int kBlocks>
+__device__ __forceinline__ uint64_t seen_chunk(const BlockWalk<true>& w, int v, uint32_t present, int lo, int hi, int sinks) {
+    uint64_t m = 0;
+#pragma unroll
+    for (int q = 0; q < kBlocks; ++q)
+        if ((present >> q) & 1u) m |= (uint64_t)seen_bits(w.block(v + q) * kBlock, lo, hi, sinks) << (16 * q);
+    return m;
+}
+
 // Whether a row that attends [lo, hi) and the sinks does not attend position pos.
 template <bool kSinks>
 __device__ __forceinline__ bool hidden(const PrefillArgs& a, int pos, int lo, int hi) {
@@ -482,6 +510,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     const uint32_t bar_q = bar0 + 224;         // "Q is in tensor memory": one arrival per softmax warp
     const uint32_t tslot = bar0 + 232;
     volatile uint32_t* cmask = reinterpret_cast<volatile uint32_t*>(gb + C::kOffBar + 236);   // [8]
+    const uint32_t bar_z = bar0 + 272;         // kSinks: a V chunk that the copy warp zeroes rows of has landed
     auto bar_k = [&](int c) { return bar0 + 8 * (c & 3); };
     auto bar_v = [&](int c) { return bar0 + 32 + 8 * (c & 3); };
     auto bar_s = [&](int c) { return bar0 + 64 + 8 * (c & 3); };
@@ -518,8 +547,8 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     const int jb_lo = att_lo / kBlock;
     const int jb_hi = (base_pos + tok_hi + kBlock) / kBlock;
     const BlockWalk<kSinks> walk{jb_lo, jb_hi, sink_blocks<kSinks>(a, jb_lo)};
-    const int nblk = walk.count();
-    const int nchunks = (nblk + kTcBlocks - 1) / kTcBlocks;
+    const int nblk = walk.count(), pad = walk_pad(walk, kTcBlocks);
+    const int nchunks = (nblk + pad + kTcBlocks - 1) / kTcBlocks;
 
     // ---- this thread's row (softmax warps) and the positions it attends, [lo, hi)
     const int rr = row0 + (softmax ? tid : 0);
@@ -543,6 +572,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         for (int i = 0; i < kTcBufs; ++i) mbar_init(bar_p(i), 4);         // one arrival per softmax warp
         for (int i = 0; i < kTcMasks; ++i) mbar_init(bar_m(i), 1);
         mbar_init(bar_q, 4);
+        if (kSinks) mbar_init(bar_z, 1);
         fence_mbar_init();
     }
     if (warp == 0) tmem_alloc(tslot, kTmemCols);
@@ -575,15 +605,16 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         const uint64_t pol = l2_policy_evict_last();   // every query tile of the sequence re-reads them
         int win_base = -(1 << 30), win_phys = -1;
         int k_issued = 0, v_issued = 0;
+        uint32_t z_par = 0;
         auto issue_kv = [&](int c, bool is_k) {
             int ph[kTcBlocks];
 #pragma unroll
             for (int q = 0; q < kTcBlocks; ++q) {
-                const int v = kTcBlocks * c + q;
+                const int v = kTcBlocks * c + q - pad;
                 if (v - win_base >= 32 || v < win_base) {
                     win_base = v;
                     win_phys = -1;
-                    if (v + lane < nblk) {
+                    if (v + lane < nblk && (!kSinks || v + lane >= 0)) {
                         const int p = a.block_tables[(long long)b * a.max_blocks + walk.block(v + lane)];
                         if (p < 0 || p >= a.num_blocks) flag_error(a.err, GQA_DEVERR_BLOCK_INDEX);
                         else win_phys = p;
@@ -592,13 +623,20 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                 ph[q] = __shfl_sync(kFull, win_phys, v - win_base);
                 if (v >= nblk) ph[q] = -1;
             }
-            const uint32_t bar = is_k ? bar_k(c) : bar_v(c);
-            if (lane == 0) {
-                uint32_t mask = 0;
-                int nval = 0;
+            uint32_t bar = is_k ? bar_k(c) : bar_v(c);
+            uint32_t mask = 0;
+            int nval = 0;
 #pragma unroll
-                for (int q = 0; q < kTcBlocks; ++q)
-                    if (ph[q] >= 0) mask |= 1u << q, ++nval;
+            for (int q = 0; q < kTcBlocks; ++q)
+                if (ph[q] >= 0) mask |= 1u << q, ++nval;
+            // kSinks: rows of V that no row of the tile attends may hold anything; they
+            // are zeroed here once the chunk has landed, and only then is V(c) ready
+            uint32_t seen = 0xffffffffu;
+            if constexpr (kSinks) {
+                if (!is_k) seen = (uint32_t)seen_chunk<kTcBlocks>(walk, kTcBlocks * c - pad, mask, att_lo, L, a.sinks);
+                if (seen != 0xffffffffu) bar = bar_z;
+            }
+            if (lane == 0) {
                 if (is_k) {
                     cmask[c & (kTcMasks - 1)] = mask;
                     mbar_arrive(bar_m(c));     // publishes the mask (release)
@@ -634,6 +672,21 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                     const uint32_t dst = is_k ? base + h * (kTcChunk * 128) + q * (kBlock * 128)
                                               : base + q * C::kVb + h * (kBlock * 128);
                     tma_load_4d(dst, is_k ? &kmap : &vmap, h * 64, y, z, w, bar, pol);
+                }
+            }
+            if constexpr (kSinks) {
+                if (seen != 0xffffffffu) {
+                    ok = __all_sync(kFull, mbar_wait(bar_z, z_par));
+                    z_par ^= 1u;
+                    for (int i = lane; ok && i < kTcChunk * C::kHalves * 8; i += 32) {
+                        const int t = i / (C::kHalves * 8), h = (i / 8) % C::kHalves, ck = i % 8;
+                        if (!((seen >> t) & 1u))
+                            sts128(sV + (c & 3) * C::kVc + (t / kBlock) * C::kVb + h * (kBlock * 128) + (t % kBlock) * 128 + ck * 16,
+                                   make_uint4(0u, 0u, 0u, 0u));
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0 && ok) mbar_arrive(bar_v(c));
                 }
             }
             if (is_k) ++k_issued;
@@ -729,12 +782,8 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             if (!ok) break;
             tc_fence_after();
             // position of the chunk's first token were its blocks all past the sinks'
-            const int cpos = (jb_lo + kTcBlocks * c - walk.ns) * kBlock;
-            const bool mixed = kSinks && kTcBlocks * c < walk.ns;    // blocks of the sinks in it
-            auto pos_of = [&](int t) {                               // position of the chunk's token t
-                if constexpr (!kSinks) return cpos + t;
-                else return walk.block(kTcBlocks * c + t / kBlock) * kBlock + t % kBlock;
-            };
+            const int cpos = (jb_lo + kTcBlocks * c - pad - walk.ns) * kBlock;
+            const bool mixed = kSinks && kTcBlocks * c - pad < walk.ns;    // blocks of the sinks in it
             const uint32_t bm = cmask[c & (kTcMasks - 1)];
             const uint32_t t_buf = t_lane + (uint32_t)(c & 1) * kColBuf;
             float sv[kTcChunk];
@@ -750,9 +799,17 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             }
             const bool whole = bm == (1u << kTcBlocks) - 1u && !mixed && cpos >= lo && cpos + kTcChunk <= hi;
             if (!whole) {
+                if constexpr (kSinks) {
+                    const uint32_t seen = (uint32_t)seen_chunk<kTcBlocks>(walk, kTcBlocks * c - pad, bm, lo, hi, a.sinks);
 #pragma unroll
-                for (int j = 0; j < kTcChunk; ++j) {
-                    if (!((bm >> (j / kBlock)) & 1u) || hidden<kSinks>(a, pos_of(j), lo, hi)) sv[j] = -INFINITY;
+                    for (int j = 0; j < kTcChunk; ++j)
+                        if (!((seen >> j) & 1u)) sv[j] = -INFINITY;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < kTcChunk; ++j) {
+                        const int pos = cpos + j;
+                        if (!((bm >> (j / kBlock)) & 1u) || pos < lo || pos >= hi) sv[j] = -INFINITY;
+                    }
                 }
             }
             float mx4[4] = {sv[0], sv[1], sv[2], sv[3]};      // short chains
@@ -803,13 +860,13 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             tmem_wait_st();
             l += (ps4[0] + ps4[1]) + (ps4[2] + ps4[3]);
             // V rows of tokens outside the sequence or of missing blocks hold arbitrary
-            // bits (with sinks, so may those that no row of the tile attends)
-            if (bm != (1u << kTcBlocks) - 1u || pos_of(kTcChunk - 1) >= L || (kSinks && (mixed || cpos < att_lo))) {
+            // bits (with sinks the V copy warp has zeroed them)
+            if (!kSinks && (bm != (1u << kTcBlocks) - 1u || cpos + kTcChunk > L)) {
                 ok = __all_sync(kFull, mbar_wait(bar_v(c), par4(c)));
                 const uint32_t vb = sV + (c & 3) * C::kVc;
                 for (int i = tid; i < kTcChunk * C::kHalves * 8; i += kTcRows) {
                     const int t = i / (C::kHalves * 8), h = (i / 8) % C::kHalves, ck = i % 8;
-                    if (((bm >> (t / kBlock)) & 1u) && !hidden<kSinks>(a, pos_of(t), kSinks ? att_lo : 0, L)) continue;
+                    if (((bm >> (t / kBlock)) & 1u) && cpos + t < L) continue;
                     sts128(vb + (t / kBlock) * C::kVb + h * (kBlock * 128) + (t % kBlock) * 128 + ck * 16,
                            make_uint4(0u, 0u, 0u, 0u));
                 }
@@ -898,35 +955,7 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// Packed fp32 pairs (one 64-bit register pair): add, subtract and multiply
-// both halves in one instruction, each half rounded to nearest like the scalar
-// operation; and the three-input maximum. They halve the softmax's arithmetic
-// instruction count per score.
-__device__ __forceinline__ uint64_t f2_make(float x, float y) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-    return r;
-}
-__device__ __forceinline__ float2 f2_split(uint64_t v) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t f2_sub(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
+// The three-input maximum.
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -996,6 +1025,7 @@ prefill_tc2_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     auto bar_q = [&](int t) { return bar0 + 320 + 8 * t; };
     const uint32_t tslot = bar0 + 336;
     volatile uint32_t* cmask = reinterpret_cast<volatile uint32_t*>(gb + C::kOffBar + 344);   // [8]
+    const uint32_t bar_z = bar0 + 376;         // kSinks: a V chunk that the copy warp zeroes rows of has landed
     auto par4 = [](int c) { return (uint32_t)(c >> 2) & 1u; };
     auto par8 = [](int c) { return (uint32_t)(c >> 3) & 1u; };
 
@@ -1017,7 +1047,7 @@ prefill_tc2_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     // to right when r is even, right to left when odd) so each CTA's total stays
     // close to the others'.
     struct Item {
-        int g, b, q0, n, L, rows, row0, base_pos, att_lo, nblk, nchunks;
+        int g, b, q0, n, L, rows, row0, base_pos, att_lo, nblk, pad, nchunks;
         BlockWalk<kSinks> walk;
     };
     const int tps = a.tiles_per_seq, n_groups = a.K * a.B;
@@ -1048,7 +1078,8 @@ prefill_tc2_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         it.walk.jb_hi = (it.base_pos + tok_hi + kBlock) / kBlock;
         it.walk.ns = sink_blocks<kSinks>(a, it.walk.jb_lo);
         it.nblk = it.walk.count();
-        it.nchunks = (it.nblk + kW2Blocks - 1) / kW2Blocks;
+        it.pad = walk_pad(it.walk, kW2Blocks);
+        it.nchunks = (it.nblk + it.pad + kW2Blocks - 1) / kW2Blocks;
         return true;
     };
     auto next_item = [&](int& r, Item& it) -> bool {  // the next valid item from round r on
@@ -1077,6 +1108,7 @@ prefill_tc2_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             mbar_init(bar_q(t), 4);
         }
         for (int i = 0; i < 8; ++i) mbar_init(bar_m(i), 1);
+        if (kSinks) mbar_init(bar_z, 1);
         fence_mbar_init();
     }
     if (warp == 0) tmem_alloc(tslot, C::kTmemCols);
@@ -1094,6 +1126,7 @@ prefill_tc2_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         const bool k_warp = warp == C::kSoftWarps + kTiles;
         const uint64_t pol = l2_policy_evict_last();   // every query tile of the sequence re-reads them
         int issued = 0, gc = 0;
+        uint32_t z_par = 0;
         while (have && ok) {
             int win_base = -(1 << 30), win_phys = -1;
             for (int c = 0; c < it.nchunks && ok; ++c) {
@@ -1111,11 +1144,11 @@ prefill_tc2_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 int ph[kW2Blocks];
 #pragma unroll
                 for (int q = 0; q < kW2Blocks; ++q) {
-                    const int v = kW2Blocks * c + q;
+                    const int v = kW2Blocks * c + q - it.pad;
                     if (v - win_base >= 32 || v < win_base) {
                         win_base = v;
                         win_phys = -1;
-                        if (v + lane < it.nblk) {
+                        if (v + lane < it.nblk && (!kSinks || v + lane >= 0)) {
                             const int p = a.block_tables[(long long)it.b * a.max_blocks + it.walk.block(v + lane)];
                             if (p < 0 || p >= a.num_blocks) flag_error(a.err, GQA_DEVERR_BLOCK_INDEX);
                             else win_phys = p;
@@ -1124,13 +1157,21 @@ prefill_tc2_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                     ph[q] = __shfl_sync(kFull, win_phys, v - win_base);
                     if (v >= it.nblk) ph[q] = -1;
                 }
-                const uint32_t bar = k_warp ? bar_k(G) : bar_v(G);
-                if (lane == 0) {
-                    uint32_t mask = 0;
-                    int nval = 0;
+                uint32_t bar = k_warp ? bar_k(G) : bar_v(G);
+                uint32_t mask = 0;
+                int nval = 0;
 #pragma unroll
-                    for (int q = 0; q < kW2Blocks; ++q)
-                        if (ph[q] >= 0) mask |= 1u << q, ++nval;
+                for (int q = 0; q < kW2Blocks; ++q)
+                    if (ph[q] >= 0) mask |= 1u << q, ++nval;
+                // kSinks: rows of V that no row of the item attends may hold anything;
+                // they are zeroed here once the chunk has landed, and only then is V(G)
+                // ready
+                uint64_t seen = ~0ull;
+                if constexpr (kSinks) {
+                    if (!k_warp) seen = seen_chunk<kW2Blocks>(it.walk, kW2Blocks * c - it.pad, mask, it.att_lo, it.L, a.sinks);
+                    if (seen != ~0ull) bar = bar_z;
+                }
+                if (lane == 0) {
                     if (k_warp) {
                         cmask[G & 7] = mask;
                         mbar_arrive(bar_m(G));     // publishes the mask (release)
@@ -1164,6 +1205,21 @@ prefill_tc2_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                         const int y = coord(a.map_perm[0]), z = coord(a.map_perm[1]), w = coord(a.map_perm[2]);
                         tma_load_4d(sK + stage(G) * C::kKc + h * (kW2Chunk * 128) + q * (kBlock * 128), &kmap,
                                     h * 64, y, z, w, bar, pol);
+                    }
+                }
+                if constexpr (kSinks) {
+                    if (seen != ~0ull) {
+                        ok = __all_sync(kFull, mbar_wait(bar_z, z_par));
+                        z_par ^= 1u;
+                        for (int i = lane; ok && i < kW2Chunk * 16; i += 32) {
+                            const int t = i / 16, h = (i / 8) % 2, ck = i % 8;
+                            if (!((seen >> t) & 1u))
+                                sts128(sV + stage(G) * C::kVc + (t / kBlock) * C::kVb + h * (kBlock * 128) + (t % kBlock) * 128 + ck * 16,
+                                       make_uint4(0u, 0u, 0u, 0u));
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0 && ok) mbar_arrive(bar_v(G));
                     }
                 }
                 ++issued;
@@ -1306,12 +1362,8 @@ prefill_tc2_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 if (!ok) break;
                 tc_fence_after();
                 // position of the chunk's first token were its blocks all past the sinks'
-                const int cpos = (it.walk.jb_lo + kW2Blocks * c - it.walk.ns) * kBlock;
-                const bool mixed = kSinks && kW2Blocks * c < it.walk.ns;   // blocks of the sinks in it
-                auto pos_of = [&](int t) {                                 // position of the chunk's token t
-                    if constexpr (!kSinks) return cpos + t;
-                    else return it.walk.block(kW2Blocks * c + t / kBlock) * kBlock + t % kBlock;
-                };
+                const int cpos = (it.walk.jb_lo + kW2Blocks * c - it.pad - it.walk.ns) * kBlock;
+                const bool mixed = kSinks && kW2Blocks * c - it.pad < it.walk.ns;   // blocks of the sinks in it
                 const uint32_t bm = cmask[G & 7];
                 const uint32_t t_buf = t_lane + kW2Chunk * (G & 1);
                 float sv[kW2Chunk];
@@ -1335,9 +1387,18 @@ prefill_tc2_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 if (c == it.nchunks - 1 && have_nx) load_q(nx);
                 const bool whole = bm == (1u << kW2Blocks) - 1u && !mixed && cpos >= lo && cpos + kW2Chunk <= hi;
                 if (!whole) {
+                    if constexpr (kSinks) {
+                        const uint64_t seen = seen_chunk<kW2Blocks>(it.walk, kW2Blocks * c - it.pad, bm, lo, hi, a.sinks);
+                        const uint32_t s0 = (uint32_t)seen, s1 = (uint32_t)(seen >> 32);
 #pragma unroll
-                    for (int q = 0; q < kW2Chunk; ++q) {
-                        if (!((bm >> (q / kBlock)) & 1u) || hidden<kSinks>(a, pos_of(q), lo, hi)) sv[q] = -INFINITY;
+                        for (int q = 0; q < kW2Chunk; ++q)
+                            if (!(((q < 32 ? s0 : s1) >> (q % 32)) & 1u)) sv[q] = -INFINITY;
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < kW2Chunk; ++q) {
+                            const int pos = cpos + q;
+                            if (!((bm >> (q / kBlock)) & 1u) || pos < lo || pos >= hi) sv[q] = -INFINITY;
+                        }
                     }
                 }
                 float mx4[4];                                     // four short chains of 3-input maxima
@@ -1402,15 +1463,14 @@ prefill_tc2_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 }
                 // V rows of tokens outside the sequence or of missing blocks hold
                 // arbitrary bits: each tile zeroes them before its P(G) is ready (its
-                // MMA warp issues P_t(G).V(G) only then); both tiles write the same zeros.
-                // With sinks, so may those of tokens that no row of the item attends.
-                if (bm != (1u << kW2Blocks) - 1u || pos_of(kW2Chunk - 1) >= it.L ||
-                    (kSinks && (mixed || cpos < it.att_lo))) {
+                // MMA warp issues P_t(G).V(G) only then); both tiles write the same zeros
+                // (with sinks the V copy warp has)
+                if (!kSinks && (bm != (1u << kW2Blocks) - 1u || cpos + kW2Chunk > it.L)) {
                     ok = __all_sync(kFull, mbar_wait(bar_v(G), par_st(G)));
                     const uint32_t vb = sV + stage(G) * C::kVc;
                     for (int i = tid & (kTcRows - 1); i < kW2Chunk * 2 * 8; i += kTcRows) {
                         const int tk2 = i / 16, h = (i / 8) % 2, ck = i % 8;
-                        if (((bm >> (tk2 / kBlock)) & 1u) && !hidden<kSinks>(a, pos_of(tk2), kSinks ? it.att_lo : 0, it.L)) continue;
+                        if (((bm >> (tk2 / kBlock)) & 1u) && cpos + tk2 < it.L) continue;
                         sts128(vb + (tk2 / kBlock) * C::kVb + h * (kBlock * 128) + (tk2 % kBlock) * 128 + ck * 16,
                                make_uint4(0u, 0u, 0u, 0u));
                     }

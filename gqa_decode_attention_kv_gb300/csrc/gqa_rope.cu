@@ -20,8 +20,9 @@
 // of a token (kRopeSteps query steps, or kKvSteps steps of K and of V) for a run of
 // consecutive tokens, so the sequence is looked up once a run. The rows, the table
 // row and the page entry of the next tokens are in flight while one is worked on:
-// each lane copies what it will read itself into a ring of stages with cp.async,
-// which needs no registers for data in flight and no barrier.
+// each lane copies the row pieces that it will read itself into a ring of stages
+// with cp.async (the table row and the page entry once for the warp), which needs no
+// registers for data in flight and no barrier.
 #include <algorithm>
 #include <type_traits>
 
@@ -73,15 +74,21 @@ struct RopeArgs {
     int run;                                  // consecutive tokens a warp serves
 };
 
-// Stages of a warp's ring, and their layout: 16-byte slots of 32 lanes each (rows
-// of kMost steps, then the table row), then 4 bytes a lane for the page entry.
+// Stages of a warp's ring, and their layout: the rows of kMost steps in 16-byte
+// slots of 32 lanes, then the table row (64 bytes a lane of a row), then the page
+// entry. Two stages and at most 102 registers let five CTAs share an SM: the kernel
+// waits on its own instruction latencies more than on memory (measured on 16384
+// tokens of 32 + 8 heads, d = 128: KERNEL_FIGURES).
 template <typename T>
 struct RopeCfg {
     static constexpr int kPieces = sizeof(T) / 2;                 // 16-byte pieces per chunk
     static constexpr int kRowSlots = kMost * 2 * kPieces;
-    static constexpr int kStage = (kRowSlots + 4) * 512 + 128;
-    static constexpr int kStages = sizeof(T) == 4 ? 2 : 3;
-    static constexpr int kSmem = kRopeWarps * kStages * kStage;
+    static constexpr int kTable = kRowSlots * 512, kEntry = kTable + 512;
+    static constexpr int kStage = kEntry + 16;
+    static constexpr int kStages = 2;
+    static constexpr int kWeights = kRopeWarps * kStages * kStage;   // fp32, q then k
+    static constexpr int kSmem = kWeights + 2 * 128 * 4;
+    static constexpr int kCtas = sizeof(T) == 4 ? 3 : 5;
 };
 
 __device__ __forceinline__ void async16(uint32_t dst, const void* src) {
@@ -113,32 +120,37 @@ __device__ __forceinline__ void store8r(T* p, const Raw8<T>& r) {
 #pragma unroll
     for (int i = 0; i < (int)(sizeof(T) / 2); ++i) reinterpret_cast<uint4*>(p)[i] = r.w[i];
 }
+// Eight elements as four packed fp32 pairs.
 template <typename T>
-__device__ __forceinline__ void widen8(const Raw8<T>& r, float (&x)[8]) {
+__device__ __forceinline__ void widen8(const Raw8<T>& r, uint64_t (&x)[4]) {
+    const uint4 w = r.w[0];
     if constexpr (sizeof(T) == 4) {
-        const uint32_t u[8] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w, r.w[1].x, r.w[1].y, r.w[1].z, r.w[1].w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(u[i]);
+        const uint4 v = r.w[sizeof(T) / 2 - 1];
+        x[0] = f2_make(__uint_as_float(w.x), __uint_as_float(w.y));
+        x[1] = f2_make(__uint_as_float(w.z), __uint_as_float(w.w));
+        x[2] = f2_make(__uint_as_float(v.x), __uint_as_float(v.y));
+        x[3] = f2_make(__uint_as_float(v.z), __uint_as_float(v.w));
     } else {
         constexpr bool kB = std::is_same<T, __nv_bfloat16>::value;
-        const uint32_t u[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float2 f = unpack2<kB>(u[i]);
-            x[2 * i] = f.x;
-            x[2 * i + 1] = f.y;
+            x[i] = f2_make(f.x, f.y);
         }
     }
 }
 template <typename T>
-__device__ __forceinline__ Raw8<T> narrow8(const float (&x)[8]) {
+__device__ __forceinline__ Raw8<T> narrow8(const uint64_t (&x)[4]) {
     Raw8<T> r;
+    const float2 a = f2_split(x[0]), b = f2_split(x[1]), c = f2_split(x[2]), d = f2_split(x[3]);
     if constexpr (sizeof(T) == 4) {
-        r.w[0] = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
-        r.w[1] = make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7]));
+        r.w[0] = make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
+        r.w[sizeof(T) / 2 - 1] =
+            make_uint4(__float_as_uint(c.x), __float_as_uint(c.y), __float_as_uint(d.x), __float_as_uint(d.y));
     } else {
         constexpr bool kB = std::is_same<T, __nv_bfloat16>::value;
-        r.w[0] = make_uint4(pack2<kB>(x[0], x[1]), pack2<kB>(x[2], x[3]), pack2<kB>(x[4], x[5]), pack2<kB>(x[6], x[7]));
+        r.w[0] = make_uint4(pack2<kB>(a.x, a.y), pack2<kB>(b.x, b.y), pack2<kB>(c.x, c.y), pack2<kB>(d.x, d.y));
     }
     return r;
 }
@@ -171,77 +183,156 @@ __device__ __forceinline__ bool sequence_of(const RopeArgs& a, long long tok, in
     return i < cnt;
 }
 
-// The norm of a row held by kLanes lanes, x <- x / sqrt(mean(x^2) + eps) * w, to
-// about half a step of fp32: the squares are summed pairwise, the inverse root
-// carries a low part (one Newton step's correction) and the products their exact
-// remainders (as in rotate). A code next to a border, or a scale next to one of
-// fp16, then falls where the exact value puts it far more often than with plain fp32
-// products, at a few more instructions an element in a kernel that waits for memory.
-template <int kLanes, int D>
-__device__ __forceinline__ void norm_row(float (&x0)[8], float (&x1)[8], const float (&w0)[8], const float (&w1)[8],
-                                         float eps) {
-    float sq[8];
+// The norm of a row held by kLanes lanes, x <- x / sqrt(mean(x^2) + eps) * w, two
+// elements an instruction. kExact carries what fp32 products round away (the inverse
+// root's low part by one Newton step, the products' remainders), to about half a step
+// of fp32: for rows that stay fp32 or are quantised next, where a code next to a
+// border, or a scale next to one of fp16, then falls where the exact value puts it.
+// Rows rounded to 16 bits do not need it, and the kernel is bound by issue as much as
+// by memory (carried everywhere it took 16384 tokens from 72 to 95 us).
+template <bool kExact, int kLanes, int D>
+__device__ __forceinline__ void norm_row(uint64_t (&x0)[4], uint64_t (&x1)[4], uint32_t wa, uint32_t wb, float eps) {
+    uint64_t sq0 = f2_mul(x0[0], x0[0]), sq1 = f2_mul(x1[0], x1[0]);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sq[e] = fmaf(x0[e], x0[e], x1[e] * x1[e]);
-    float ss = ((sq[0] + sq[1]) + (sq[2] + sq[3])) + ((sq[4] + sq[5]) + (sq[6] + sq[7]));
+    for (int e = 1; e < 4; ++e) {
+        sq0 = f2_fma(x0[e], x0[e], sq0);
+        sq1 = f2_fma(x1[e], x1[e], sq1);
+    }
+    const float2 sq = f2_split(f2_add(sq0, sq1));
+    float ss = sq.x + sq.y;
 #pragma unroll
     for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
     const float m = fmaf(ss, 1.f / D, eps);
-    const float r = 1.f / sqrtf(m);
-    const float mr = m * r, mr_lo = fmaf(m, r, -mr);
-    const float rest = fmaf(-mr, r, 1.f) - mr_lo * r;              // 1 - m r^2
-    float r_lo = 0.5f * r * rest;
-    if (!(fabsf(r_lo) < r)) r_lo = 0.f;                            // m = 0 or not finite: r alone
+    const float r = kExact ? 1.f / sqrtf(m) : rsqrtf(m);
+    const uint64_t r2 = f2_make(r, r);
+    uint64_t w0[4], w1[4];                   // the chunks' weights, from shared memory at wa and wb
+    {
+        Raw8<float> f;
+        f.w[0] = lds128(wa), f.w[1] = lds128(wa + 16);
+        widen8(f, w0);
+        f.w[0] = lds128(wb), f.w[1] = lds128(wb + 16);
+        widen8(f, w1);
+    }
+    if constexpr (kExact) {
+        const float mr = m * r, mr_lo = fmaf(m, r, -mr);
+        float r_lo = 0.5f * r * (fmaf(-mr, r, 1.f) - mr_lo * r);   // r (1 - m r^2) / 2
+        if (!(fabsf(r_lo) < r)) r_lo = 0.f;                        // m = 0 or not finite: r alone
+        const uint64_t lo2 = f2_make(r_lo, r_lo), nr2 = f2_make(-r, -r);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float p0 = x0[e] * r, p1 = x1[e] * r;
-        const float q0 = fmaf(x0[e], r_lo, fmaf(x0[e], r, -p0)), q1 = fmaf(x1[e], r_lo, fmaf(x1[e], r, -p1));
-        x0[e] = fmaf(p0, w0[e], q0 * w0[e]);
-        x1[e] = fmaf(p1, w1[e], q1 * w1[e]);
+        for (int e = 0; e < 4; ++e) {
+            const uint64_t p0 = f2_mul(x0[e], r2), p1 = f2_mul(x1[e], r2);
+            const uint64_t q0 = f2_fma(x0[e], lo2, f2_fma(x0[e], r2, f2_mul(x0[e], nr2)));
+            const uint64_t q1 = f2_fma(x1[e], lo2, f2_fma(x1[e], r2, f2_mul(x1[e], nr2)));
+            x0[e] = f2_fma(p0, w0[e], f2_mul(q0, w0[e]));
+            x1[e] = f2_fma(p1, w1[e], f2_mul(q1, w1[e]));
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            x0[e] = f2_mul(f2_mul(x0[e], r2), w0[e]);
+            x1[e] = f2_mul(f2_mul(x1[e], r2), w1[e]);
+        }
     }
 }
 
-// (a, b) -> (a cos - b sin, b cos + a sin), with the remainders of the products
-// that are rounded first.
-__device__ __forceinline__ void rotate(float& a, float& b, float2 cs) {
-    const float bs = b * cs.y, as = a * cs.y;
-    const float x = fmaf(a, cs.x, -bs) - fmaf(b, cs.y, -bs);
-    b = fmaf(b, cs.x, as) + fmaf(a, cs.y, -as);
-    a = x;
+// A lane's eight (cos, sin) pairs, two to a register pair, and -sin.
+struct Turn {
+    uint64_t c[4], s[4], n[4];
+    __device__ __forceinline__ void set(int e, uint4 f) {
+        c[e] = f2_make(__uint_as_float(f.x), __uint_as_float(f.z));
+        s[e] = f2_make(__uint_as_float(f.y), __uint_as_float(f.w));
+        n[e] = f2_make(-__uint_as_float(f.y), -__uint_as_float(f.w));
+    }
+};
+
+// a c + b r, kExact with what the product b r rounds away (nr = -r).
+template <bool kExact>
+__device__ __forceinline__ uint64_t fma_rest(uint64_t a, uint64_t c, uint64_t b, uint64_t r, uint64_t nr) {
+    const uint64_t x = f2_fma(a, c, f2_mul(b, r));
+    if constexpr (kExact) return f2_add(x, f2_fma(b, r, f2_mul(b, nr)));
+    else return x;
+}
+template <bool kExact>
+__device__ __forceinline__ float fma_rest(float a, float c, float b, float r) {
+    const float br = b * r, x = fmaf(a, c, br);
+    if constexpr (kExact) return x + fmaf(b, r, -br);
+    else return x;
 }
 
-// Codes and scale of one row (two 8-element chunks a lane, kLanes lanes a row),
-// by the append's rule: s = fp16(min(amax / qmax, 65504)), code = x / s rounded to
-// nearest even and clamped.
+// (a, b) -> (a cos - b sin, b cos + a sin) of a lane's eight pairs.
+template <bool kExact>
+__device__ __forceinline__ void rotate(uint64_t (&x0)[4], uint64_t (&x1)[4], const Turn& t, bool interleaved) {
+    if (interleaved) {
+        auto one = [&](uint64_t& x, float c, float s) {
+            const float2 v = f2_split(x);
+            x = f2_make(fma_rest<kExact>(v.x, c, v.y, -s), fma_rest<kExact>(v.y, c, v.x, s));
+        };
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {        // pairs 0 .. 3 are chunk 0's, 4 .. 7 chunk 1's
+            const float2 c = f2_split(t.c[e / 2]), s = f2_split(t.s[e / 2]);
+            const float2 d = f2_split(t.c[2 + e / 2]), u = f2_split(t.s[2 + e / 2]);
+            one(x0[e], e % 2 ? c.y : c.x, e % 2 ? s.y : s.x);
+            one(x1[e], e % 2 ? d.y : d.x, e % 2 ? u.y : u.x);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint64_t a = x0[e], b = x1[e];
+            x0[e] = fma_rest<kExact>(a, t.c[e], b, t.n[e], t.s[e]);
+            x1[e] = fma_rest<kExact>(b, t.c[e], a, t.s[e], t.n[e]);
+        }
+    }
+}
+
+// Codes and scale of one row (two 8-element chunks a lane, kLanes lanes a row), by the
+// append's rule: s = fp16(min(amax / qmax, 65504)), code = x / s rounded to nearest
+// even and clamped. The quotient is the correctly rounded one: with y = RN(1/s), once
+// a row, q = RN(x y) and the exact remainder x - q s, RN(q + (x - q s) y) is RN(x / s)
+// (Markstein's theorem; s has 11 significant bits, so its mantissa is not all ones,
+// and no step leaves fp32's range where the code is not zero), at three instructions
+// instead of a division. A row with an infinity divides.
 template <int kOut, int kLanes>
-__device__ __forceinline__ void quantise_store(const float (&x0)[8], const float (&x1)[8], bool live, uint8_t* row,
+__device__ __forceinline__ void quantise_store(const uint64_t (&x0)[4], const uint64_t (&x1)[4], bool live, uint8_t* row,
                                                int c0, int c1, __half* scale, bool first) {
     constexpr float kQmax = kOut == kOutFp8 ? 448.0f : kOut == kOutI4 ? 7.0f : 127.0f;
     float amax = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fmaxf(fabsf(x0[e]), fabsf(x1[e])));
+    for (int e = 0; e < 4; ++e) {
+        const float2 a = f2_split(x0[e]), b = f2_split(x1[e]);
+        amax = fmaxf(amax, fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(b.x), fabsf(b.y))));
+    }
 #pragma unroll
     for (int o = kLanes / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
     const __half sh = __float2half_rn(fminf(__fdiv_rn(amax, kQmax), 65504.0f));
     const float sf = __half2float(sh);
     if (!live) return;
+    const float y = __fdiv_rn(1.f, sf);
+    const uint64_t y2 = f2_make(y, y), ns2 = f2_make(-sf, -sf);
+    const bool finite = amax < INFINITY;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         uint32_t w[2] = {0u, 0u};
+        if (sf != 0.f) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            uint32_t code = 0;
-            if (sf != 0.f) {
-                const float t = __fdiv_rn(h ? x1[e] : x0[e], sf);
+            for (int e = 0; e < 4; ++e) {
+                const uint64_t x = h ? x1[e] : x0[e];
+                const uint64_t q = f2_mul(x, y2);
+                float2 t = f2_split(f2_fma(f2_fma(q, ns2, x), y2, q));
+                if (!finite) {
+                    const float2 xs = f2_split(x);
+                    t = make_float2(__fdiv_rn(xs.x, sf), __fdiv_rn(xs.y, sf));
+                }
                 if constexpr (kOut == kOutFp8) {
-                    code = (uint32_t)__nv_cvt_float_to_fp8(t, __NV_SATFINITE, __NV_E4M3);
+                    const uint32_t two = __nv_cvt_float2_to_fp8x2(t, __NV_SATFINITE, __NV_E4M3);
+                    w[e / 2] |= two << (16 * (e % 2));
                 } else {
                     constexpr int qm = (int)kQmax;
-                    code = (uint32_t)max(-qm, min(qm, __float2int_rn(t)));
+                    const uint32_t a = (uint32_t)max(-qm, min(qm, __float2int_rn(t.x)));
+                    const uint32_t b = (uint32_t)max(-qm, min(qm, __float2int_rn(t.y)));
+                    if constexpr (kOut == kOutI4) w[0] |= ((a & 0xFu) | ((b & 0xFu) << 4)) << (8 * e);
+                    else w[e / 2] |= ((a & 0xFFu) | ((b & 0xFFu) << 8)) << (16 * (e % 2));
                 }
             }
-            if constexpr (kOut == kOutI4) w[0] |= (code & 0xFu) << (4 * e);
-            else w[e / 4] |= (code & 0xFFu) << (8 * (e % 4));
         }
         const int c = h ? c1 : c0;
         if constexpr (kOut == kOutI4) *reinterpret_cast<uint32_t*>(row + 4 * c) = w[0];
@@ -258,15 +349,27 @@ struct Place {
 };
 
 template <typename T, int D, int kOut>
-__global__ void __launch_bounds__(kRopeWarps * 32) norm_rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kRopeWarps * 32, RopeCfg<T>::kCtas) norm_rope_kernel(const RopeArgs a) {
     using C = RopeCfg<T>;
     constexpr int kLanes = D / 16;                 // lanes per row
     constexpr int kRows = 32 / kLanes;             // rows per warp step
     constexpr bool kCached = kOut != kOutDense;
+    constexpr bool kCoded = kOut > kOutCache;      // rows are quantised
     extern __shared__ __align__(16) uint8_t smem_raw[];
     grid_dependency_wait();
     launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // the weights as fp32, q's then k's
+    const uint32_t weights = smem_addr(smem_raw) + C::kWeights;
+    for (int i = threadIdx.x; i < 2 * D; i += kRopeWarps * 32) {
+        const void* w = i < D ? a.q_weight : a.k_weight;
+        if (w != nullptr)
+            reinterpret_cast<float*>(smem_raw + C::kWeights)[i] =
+                a.weight_dtype == GQA_DTYPE_F32    ? static_cast<const float*>(w)[i % D]
+                : a.weight_dtype == GQA_DTYPE_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(w)[i % D])
+                                                   : __half2float(static_cast<const __half*>(w)[i % D]);
+    }
+    __syncthreads();
     const int unit = (int)blockIdx.x * kRopeWarps + warp;
     const int part = unit % a.parts;
     const long long t_lo = (long long)(unit / a.parts) * a.run;
@@ -282,33 +385,36 @@ __global__ void __launch_bounds__(kRopeWarps * 32) norm_rope_kernel(const RopeAr
         c1 = li + half;
     }
     const bool is_q = part < a.q_parts;
-    // head of this lane's row in step u, -1: none. Steps of a K/V part: kKvSteps of
-    // K, then the same heads' V.
-    auto head = [&](int u) {
-        const int h = is_q ? (part * kRopeSteps + u) * kRows + grp
-                           : ((part - a.q_parts) * kKvSteps + u % kKvSteps) * kRows + grp;
-        const bool in = is_q ? u < kRopeSteps && h < a.H : u < (kCached ? 2 : 1) * kKvSteps && h < a.K;
-        return in ? h : -1;
-    };
-    const uint32_t ring = smem_addr(smem_raw) + warp * (C::kStages * C::kStage) + lane * 16;
+    const bool normed = (is_q ? a.q_weight : a.k_weight) != nullptr;
+    const uint32_t wbase = weights + (is_q ? 0 : D * 4);
+    const uint32_t ring = smem_addr(smem_raw) + warp * (C::kStages * C::kStage);
+    // rows of step u lie u * kRows heads past this lane's first one, of step 0
+    const int h0 = (is_q ? part * kRopeSteps : (part - a.q_parts) * kKvSteps) * kRows + grp;
+    const T* src0 = static_cast<const T*>(is_q ? a.q : a.k) + t_lo * (is_q ? a.q_stride : a.k_stride) + (long long)h0 * D;
+    const T* vsrc0 = is_q || !kCached ? nullptr : static_cast<const T*>(a.v) + t_lo * a.v_stride + (long long)h0 * D;
+    const long long src_step = is_q ? a.q_stride : a.k_stride;
+    bool in[kMost];                                // this lane has a row in step u
+#pragma unroll
+    for (int u = 0; u < kMost; ++u) {
+        const int h = h0 + (is_q ? u : u % kKvSteps) * kRows;
+        in[u] = is_q ? u < kRopeSteps && h < a.H : u < (kCached ? 2 : 1) * kKvSteps && h < a.K;
+    }
 
     // ---- fetch: everything token t needs, into stage s
     int b = 0, left = 0, pos = 0;                  // its sequence, tokens after it in there, its position
     auto fetch = [&](int j, int s) -> Place {
         const long long t = t_lo + j;
         const uint32_t st = ring + s * C::kStage;
+        const T* row = src0 + j * src_step;
+        const T* vrow = vsrc0 + (kCached ? j * a.v_stride : 0);
 #pragma unroll
         for (int u = 0; u < kMost; ++u) {
-            const int h = head(u);
-            if (h < 0) continue;
-            const T* src = is_q           ? static_cast<const T*>(a.q) + t * a.q_stride
-                           : u < kKvSteps ? static_cast<const T*>(a.k) + t * a.k_stride
-                                          : static_cast<const T*>(a.v) + t * a.v_stride;
-            src += h * D;
+            if (!in[u]) continue;
+            const T* src = is_q ? row + u * kRows * D : u < kKvSteps ? row + u * kRows * D : vrow + (u - kKvSteps) * kRows * D;
 #pragma unroll
             for (int i = 0; i < C::kPieces; ++i) {
-                async16(st + ((2 * u) * C::kPieces + i) * 512, reinterpret_cast<const uint4*>(src + 8 * c0) + i);
-                async16(st + ((2 * u + 1) * C::kPieces + i) * 512, reinterpret_cast<const uint4*>(src + 8 * c1) + i);
+                async16(st + ((2 * u) * C::kPieces + i) * 512 + lane * 16, reinterpret_cast<const uint4*>(src + 8 * c0) + i);
+                async16(st + ((2 * u + 1) * C::kPieces + i) * 512 + lane * 16, reinterpret_cast<const uint4*>(src + 8 * c1) + i);
             }
         }
         Place p{0, 0, true, true};
@@ -337,40 +443,23 @@ __global__ void __launch_bounds__(kRopeWarps * 32) norm_rope_kernel(const RopeAr
             if (p.turn < 0 || p.turn >= a.rope_rows) {
                 if (lane == 0 && part == 0) flag_error(a.err, GQA_DEVERR_POSITION);
                 p.live = false;
-            } else if (turns) {
-                const uint4* src = reinterpret_cast<const uint4*>(a.rope + (long long)p.turn * (a.rotary_dim / 2) + 8 * li);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) async16(st + (C::kRowSlots + e) * 512, src + e);
+            } else if (lane < 4 * half) {          // 16 bytes a lane: the row once for the warp
+                async16(st + C::kTable + lane * 16,
+                        reinterpret_cast<const uint4*>(a.rope + (long long)p.turn * (a.rotary_dim / 2)) + lane);
             }
         }
         if constexpr (kCached) {
             if (p.live && !is_q) {
                 p.slot = pos >= 0 && pos < a.max_blocks * kBlock;
-                if (p.slot)
-                    async4(st + (C::kRowSlots + 4) * 512 - lane * 12,
-                           a.block_tables + (long long)b * a.max_blocks + pos / kBlock);
-                else if (lane == 0 && part == a.q_parts)
-                    flag_error(a.err, GQA_DEVERR_POSITION);
+                if (!p.slot) {
+                    if (lane == 0 && part == a.q_parts) flag_error(a.err, GQA_DEVERR_POSITION);
+                } else if (lane == 0) {
+                    async4(st + C::kEntry, a.block_tables + (long long)b * a.max_blocks + pos / kBlock);
+                }
             }
         }
         return p;
     };
-
-    // ---- this lane's weights
-    const void* wp = is_q ? a.q_weight : a.k_weight;
-    float w0[8], w1[8];
-    if (wp != nullptr) {
-        if (a.weight_dtype == GQA_DTYPE_F32) {
-            widen8(load8(static_cast<const float*>(wp) + 8 * c0), w0);
-            widen8(load8(static_cast<const float*>(wp) + 8 * c1), w1);
-        } else if (a.weight_dtype == GQA_DTYPE_BF16) {
-            widen8(load8(static_cast<const __nv_bfloat16*>(wp) + 8 * c0), w0);
-            widen8(load8(static_cast<const __nv_bfloat16*>(wp) + 8 * c1), w1);
-        } else {
-            widen8(load8(static_cast<const __half*>(wp) + 8 * c0), w0);
-            widen8(load8(static_cast<const __half*>(wp) + 8 * c1), w1);
-        }
-    }
 
     // ---- norm, rotation and store of token t from stage s
     auto finish = [&](const Place& p, int j, int s) {
@@ -381,7 +470,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32) norm_rope_kernel(const RopeAr
         if constexpr (kCached) {
             if (!is_q) {
                 if (!p.slot) return;
-                const int ph = (int)lds32(st + (C::kRowSlots + 4) * 512 - lane * 12);
+                const int ph = (int)lds32(st + C::kEntry);
                 if (ph < 0 || ph >= a.num_blocks) {
                     if (lane == 0 && part == a.q_parts) flag_error(a.err, GQA_DEVERR_BLOCK_INDEX);
                     return;
@@ -390,64 +479,52 @@ __global__ void __launch_bounds__(kRopeWarps * 32) norm_rope_kernel(const RopeAr
                 sidx = (long long)ph * a.K * kBlock + p.pos % kBlock;
             }
         }
-        float2 cs[8];
+        Turn turn;
         if (turns) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint4 f = lds128(st + (C::kRowSlots + e) * 512);
-                cs[2 * e] = make_float2(__uint_as_float(f.x), __uint_as_float(f.y));
-                cs[2 * e + 1] = make_float2(__uint_as_float(f.z), __uint_as_float(f.w));
-            }
+            for (int e = 0; e < 4; ++e) turn.set(e, lds128(st + C::kTable + (4 * li + e) * 16));
         }
 #pragma unroll
         for (int u = 0; u < kMost; ++u) {
             const bool is_v = !is_q && u >= kKvSteps;
             if (is_v && !kCached) break;
-            const int h = head(u);
-            const bool live = h >= 0;
-            if (!__any_sync(kFull, live)) continue;
+            if (!__any_sync(kFull, in[u])) continue;
             Raw8<T> r0, r1;
 #pragma unroll
-            for (int i = 0; i < C::kPieces; ++i) {
-                r0.w[i] = live ? lds128(st + ((2 * u) * C::kPieces + i) * 512) : make_uint4(0u, 0u, 0u, 0u);
-                r1.w[i] = live ? lds128(st + ((2 * u + 1) * C::kPieces + i) * 512) : make_uint4(0u, 0u, 0u, 0u);
+            for (int i = 0; i < C::kPieces; ++i) {       // (a lane without a row works on what the slot holds)
+                r0.w[i] = lds128(st + ((2 * u) * C::kPieces + i) * 512 + lane * 16);
+                r1.w[i] = lds128(st + ((2 * u + 1) * C::kPieces + i) * 512 + lane * 16);
             }
-            float x0[8], x1[8];
+            uint64_t x0[4], x1[4];
             widen8(r0, x0);
             widen8(r1, x1);
             if (!is_v) {
-                if (wp != nullptr) norm_row<kLanes, D>(x0, x1, w0, w1, a.eps);
-                if (turns) {
-                    if (a.interleaved) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            rotate(x0[2 * e], x0[2 * e + 1], cs[e]);
-                            rotate(x1[2 * e], x1[2 * e + 1], cs[4 + e]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) rotate(x0[e], x1[e], cs[e]);
-                    }
-                }
+                auto work = [&](auto exact) {
+                    constexpr bool kExact = decltype(exact)::value;
+                    if (normed) norm_row<kExact, kLanes, D>(x0, x1, wbase + 32 * c0, wbase + 32 * c1, a.eps);
+                    if (turns) rotate<kExact>(x0, x1, turn, a.interleaved != 0);
+                };
+                if (sizeof(T) == 4 || (kCoded && !is_q)) work(std::true_type{});
+                else work(std::false_type{});
             }
+            const int h = h0 + (is_q ? u : u % kKvSteps) * kRows;
             if (is_q || kOut == kOutDense) {
-                if (live) {
-                    T* out = is_q ? static_cast<T*>(a.q_out) + (t * a.H + h) * D
-                                  : static_cast<T*>(a.k_out) + (t * a.K + h) * D;
+                if (in[u]) {
+                    T* out = is_q ? static_cast<T*>(a.q_out) + (t * a.H + h) * D : static_cast<T*>(a.k_out) + (t * a.K + h) * D;
                     store8r(out + 8 * c0, narrow8<T>(x0));
                     store8r(out + 8 * c1, narrow8<T>(x1));
                 }
             } else if constexpr (kOut == kOutCache) {
-                if (live) {
+                if (in[u]) {
                     T* out = static_cast<T*>(is_v ? a.v_cache : a.k_cache) + dst + (long long)h * a.sh;
                     store8r(out + 8 * c0, is_v ? r0 : narrow8<T>(x0));
                     store8r(out + 8 * c1, is_v ? r1 : narrow8<T>(x1));
                 }
             } else if constexpr (kCached) {
-                const long long off = dst + (long long)max(h, 0) * a.sh;
+                const long long off = dst + (long long)h * a.sh;
                 uint8_t* out = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + (kOut == kOutI4 ? off / 2 : off);
-                __half* sc = (is_v ? a.v_scale : a.k_scale) + sidx + (long long)max(h, 0) * kBlock;
-                quantise_store<kOut, kLanes>(x0, x1, live, out, c0, c1, sc, li == 0);
+                __half* sc = (is_v ? a.v_scale : a.k_scale) + sidx + (long long)h * kBlock;
+                quantise_store<kOut, kLanes>(x0, x1, in[u], out, c0, c1, sc, li == 0);
             }
         }
     };
@@ -466,9 +543,11 @@ __global__ void __launch_bounds__(kRopeWarps * 32) norm_rope_kernel(const RopeAr
         int s_next = s + kAhead;
         if (s_next >= C::kStages) s_next -= C::kStages;
         q[kAhead] = Place{0, 0, false, false};
+        __syncwarp();                              // the warp has read the stage's table row and entry
         if (j + kAhead < n) q[kAhead] = fetch(j + kAhead, s_next);
         async_commit();
-        async_wait<kAhead>();                      // this lane's copies of token j have landed
+        async_wait<kAhead>();                      // this lane's copies of token j have landed,
+        __syncwarp();                              // and the other lanes'
         finish(q[0], j, s);
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) q[i] = q[i + 1];
