@@ -41,6 +41,8 @@ BLOCK_SIZE = 16
 DTYPE_CODE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2, torch.int8: 3,
               torch.float8_e4m3fn: 4}
 
+_DEV_DTYPES = frozenset(DTYPE_CODE) | {torch.uint8}
+
 GQA_DEVERR_BLOCK_INDEX = 1
 GQA_DEVERR_CONTEXT_LEN = 2
 GQA_DEVERR_POSITION = 4
@@ -259,6 +261,8 @@ def _dev(t: Optional[torch.Tensor], name: str, index: bool = False, optional: bo
         if optional:
             return None
         raise ValueError(f"{name} is required")
+    if t.is_cuda and t.is_contiguous() and (t.dtype is torch.int32 if index else t.dtype in _DEV_DTYPES):
+        return t.data_ptr()
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous (the library reads it as a packed array)")
     if index and t.dtype != torch.int32:
@@ -367,9 +371,10 @@ def _scratch(cache: dict, need: int, idx: int, stream, zero: bool) -> torch.Tens
            torch.cuda.current_stream(torch.device("cuda", idx)).cuda_stream)
     buf = None if capturing else cache.get(key)
     if buf is None or buf.numel() < need:
-        make = torch.zeros if zero else torch.empty
         with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(torch.device("cuda", idx))):
-            buf = make(need, dtype=torch.uint8, device=torch.device("cuda", idx))
+            buf = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", idx))
+            if zero:                           # a captured call zeroes at every replay: the counter's header alone
+                (buf[:256] if capturing else buf).zero_()
         if not capturing:
             cache[key] = buf
     return buf
@@ -503,14 +508,23 @@ def rope_table(positions: int, rotary_dim: int, base: float = 10000.0, device="c
     return table
 
 
+_ROW_DTYPES = frozenset((torch.float32, torch.float16, torch.bfloat16))
+
+
 def _token_rows(t: torch.Tensor, name: str, like: torch.Tensor, heads: Optional[int] = None):
     """(pointer, elements between tokens) of rows [..., heads, d] whose heads are
     contiguous and whose tokens are evenly spaced (a view into a fused projection)."""
+    if t.dim() == 3 and like.dim() == 3:               # the usual case: [tokens, heads, d]
+        n, H, d = t.shape
+        sn, sh, sd = t.stride()
+        if (n == like.shape[0] and d == like.shape[2] and t.dtype is like.dtype and t.dtype in _ROW_DTYPES and sd == 1
+                and sh == d and sn >= H * d and (heads is None or H == heads) and t.is_cuda):
+            return t.data_ptr(), sn
     if t.dim() not in (3, 4) or tuple(t.shape[:-2]) != tuple(like.shape[:-2]) or t.shape[-1] != like.shape[-1]:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, which does not go with q's {tuple(like.shape)}")
     if heads is not None and t.shape[-2] != heads:
         raise ValueError(f"{name} has {t.shape[-2]} heads, not {heads}")
-    if t.dtype not in (torch.float32, torch.float16, torch.bfloat16) or t.dtype != like.dtype:
+    if t.dtype not in _ROW_DTYPES or t.dtype != like.dtype:
         raise ValueError(f"{name} must have q's dtype, one of float32, float16, bfloat16, not {t.dtype}")
     H, d = int(t.shape[-2]), int(t.shape[-1])
     st = t.stride()
@@ -533,24 +547,25 @@ def _token_rows(t: torch.Tensor, name: str, like: torch.Tensor, heads: Optional[
 
 
 def _norm_rope_desc(q, rope, q_weight, k_weight, eps, interleaved) -> NormRopeDesc:
-    d = int(q.shape[-1])
-    desc = NormRopeDesc(None, None, None, 0, float(eps), 0, 0, int(bool(interleaved)), 0)
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+    d = q.shape[-1]
+    pointers, code = [None, None], 0
+    for i, w in enumerate((q_weight, k_weight)):
         if w is None:
             continue
-        if tuple(w.shape) != (d,):
+        name = ("q_weight", "k_weight")[i]
+        if w.dim() != 1 or w.shape[0] != d:
             raise ValueError(f"{name} must be [{d}], not {tuple(w.shape)}")
-        if w.dtype not in (torch.float32, torch.float16, torch.bfloat16):
+        if w.dtype not in _ROW_DTYPES:
             raise ValueError(f"{name} has unsupported dtype {w.dtype}")
-        setattr(desc, name, _dev(w, name))
-        desc.weight_dtype = DTYPE_CODE[w.dtype]
+        pointers[i], code = _dev(w, name), DTYPE_CODE[w.dtype]
     if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
         raise ValueError("q_weight and k_weight must have one dtype")
+    table, rows, rotary = None, 0, 0
     if rope is not None:
         if rope.dim() != 3 or rope.shape[2] != 2 or rope.dtype != torch.float32:
             raise ValueError(f"rope must be float32 [positions, rotary_dim/2, 2], not {rope.dtype} {tuple(rope.shape)}")
-        desc.rope, desc.rope_rows, desc.rotary_dim = _dev(rope, "rope"), int(rope.shape[0]), 2 * int(rope.shape[1])
-    return desc
+        table, rows, rotary = _dev(rope, "rope"), rope.shape[0], 2 * rope.shape[1]
+    return NormRopeDesc(pointers[0], pointers[1], table, code, eps, rows, rotary, 1 if interleaved else 0, 0)
 
 
 def _same_or_apart(out: torch.Tensor, src: torch.Tensor, name: str):
@@ -757,8 +772,10 @@ def kv_pages_fork(ref_counts: torch.Tensor, block_tables: torch.Tensor, context_
     _check_pool(ref_counts, block_tables, context_lens, src_rows=src_rows, dst_rows=dst_rows, err=err,
                 workspace=workspace)
     if copies is None:
-        buf = torch.empty((2 * n + 1, 2), dtype=torch.int32, device=ref_counts.device)
-        copies = PageCopies(buf[:n], buf[2 * n, :1], buf[n:2 * n])
+        dev = ref_counts.device
+        copies = PageCopies(torch.empty((n, 2), dtype=torch.int32, device=dev),
+                            torch.empty(1, dtype=torch.int32, device=dev),
+                            torch.empty((n, 2), dtype=torch.int32, device=dev))
     elif copies.rows is None or copies.pairs.shape[0] < n or copies.rows.shape[0] != n:
         raise ValueError(f"copies must have room for {n} pairs and exactly {n} rows")
     else:
@@ -825,8 +842,8 @@ def kv_pages_compact(ref_counts: torch.Tensor, block_tables: torch.Tensor, max_c
         n = nb // 2 if max_copies is None else int(max_copies)
         if n < 0:
             raise ValueError(f"max_copies must not be negative: {n}")
-        buf = torch.empty((n + 1, 2), dtype=torch.int32, device=ref_counts.device)
-        copies = PageCopies(buf[:n], buf[n])
+        copies = PageCopies(torch.empty((n, 2), dtype=torch.int32, device=ref_counts.device),
+                            torch.empty(2, dtype=torch.int32, device=ref_counts.device))
     else:
         _check_copies(copies, ref_counts.device)
         n = int(copies.pairs.shape[0]) if max_copies is None else int(max_copies)

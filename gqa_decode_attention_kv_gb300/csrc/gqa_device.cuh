@@ -239,41 +239,6 @@ __device__ __forceinline__ float2 unpack2(uint32_t v) {
     }
 }
 
-// Packed fp32 pairs (one 64-bit register pair): add, subtract, multiply and
-// multiply-add of both halves in one instruction, each half rounded to nearest
-// like the scalar operation. They halve the arithmetic instructions of code that
-// is bound by issue (the prefill's softmax, the norm and rotation of heads).
-__device__ __forceinline__ uint64_t f2_make(float x, float y) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-    return r;
-}
-__device__ __forceinline__ float2 f2_split(uint64_t v) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t f2_sub(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-
 // Four int8 codes (one 32-bit word, byte i = element i) -> two packed f16 pairs,
 // exact: each byte is biased to u = x + 128, placed as the mantissa of
 // 1024 + u (fp16 0x6400 | u), and 1152 is subtracted.

@@ -71,14 +71,14 @@ struct RopeArgs {
     int32_t* err;
     long long tokens;
     int H, K, q_parts, parts;                 // warps per token: q_parts, then K/V parts
-    int run;                                  // consecutive tokens a warp serves
+    int runs, run, longer;                    // runs of `run` consecutive tokens, the first `longer` of one more
 };
 
 // Stages of a warp's ring, and their layout: the rows of kMost steps in 16-byte
 // slots of 32 lanes, then the table row (64 bytes a lane of a row), then the page
-// entry. Two stages and at most 102 registers let five CTAs share an SM: the kernel
-// waits on its own instruction latencies more than on memory (measured on 16384
-// tokens of 32 + 8 heads, d = 128: KERNEL_FIGURES).
+// entry. Two stages, so that four or five CTAs share an SM: the kernel waits on its own
+// instruction latencies more than on memory (three stages and three CTAs: 81 us where
+// this takes 67).
 template <typename T>
 struct RopeCfg {
     static constexpr int kPieces = sizeof(T) / 2;                 // 16-byte pieces per chunk
@@ -86,13 +86,31 @@ struct RopeCfg {
     static constexpr int kTable = kRowSlots * 512, kEntry = kTable + 512;
     static constexpr int kStage = kEntry + 16;
     static constexpr int kStages = 2;
-    static constexpr int kWeights = kRopeWarps * kStages * kStage;   // fp32, q then k
-    static constexpr int kSmem = kWeights + 2 * 128 * 4;
-    static constexpr int kCtas = sizeof(T) == 4 ? 3 : 5;
+    static constexpr int kSmem = kRopeWarps * kStages * kStage;
 };
 
+// Rows a lane works on at a time, and CTAs per SM the registers are cut for. Two rows
+// overlap their shuffles and roots but need 128 registers (4 CTAs); rows that are
+// quantised one by one fit 5. Measured, 16384 tokens of 32 + 8 bf16 heads, d = 128, one
+// row at 5 / two at 4 / two at 5 CTAs: 69.3 / 67.3 / 70 us; 13.7k ragged tokens of
+// 24 + 8 heads, d = 64, onto an FP8 cache: 43 / 48 / 65 us.
+template <typename T, int kOut>
+struct RopeShape {
+    static constexpr bool kTwo = sizeof(T) == 2 && kOut <= kOutCache;
+    static constexpr int kPair = kTwo ? 2 : 1;
+    static constexpr int kCtas = sizeof(T) == 4 ? 3 : kTwo ? 4 : 5;
+};
+
+template <int kDst, int kSrc>
 __device__ __forceinline__ void async16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0+%2], [%1+%3], 16;" ::"r"(dst), "l"(src), "n"(kDst), "n"(kSrc) : "memory");
+}
+template <int kBegin, int kEnd, class F>
+__device__ __forceinline__ void static_for(F&& f) {
+    if constexpr (kBegin < kEnd) {
+        f(std::integral_constant<int, kBegin>{});
+        static_for<kBegin + 1, kEnd>(f);
+    }
 }
 __device__ __forceinline__ void async4(uint32_t dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
@@ -120,37 +138,35 @@ __device__ __forceinline__ void store8r(T* p, const Raw8<T>& r) {
 #pragma unroll
     for (int i = 0; i < (int)(sizeof(T) / 2); ++i) reinterpret_cast<uint4*>(p)[i] = r.w[i];
 }
-// Eight elements as four packed fp32 pairs.
 template <typename T>
-__device__ __forceinline__ void widen8(const Raw8<T>& r, uint64_t (&x)[4]) {
+__device__ __forceinline__ void widen8(const Raw8<T>& r, float (&x)[8]) {
     const uint4 w = r.w[0];
     if constexpr (sizeof(T) == 4) {
         const uint4 v = r.w[sizeof(T) / 2 - 1];
-        x[0] = f2_make(__uint_as_float(w.x), __uint_as_float(w.y));
-        x[1] = f2_make(__uint_as_float(w.z), __uint_as_float(w.w));
-        x[2] = f2_make(__uint_as_float(v.x), __uint_as_float(v.y));
-        x[3] = f2_make(__uint_as_float(v.z), __uint_as_float(v.w));
+        const uint32_t u[8] = {w.x, w.y, w.z, w.w, v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(u[i]);
     } else {
         constexpr bool kB = std::is_same<T, __nv_bfloat16>::value;
         const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float2 f = unpack2<kB>(u[i]);
-            x[i] = f2_make(f.x, f.y);
+            x[2 * i] = f.x;
+            x[2 * i + 1] = f.y;
         }
     }
 }
 template <typename T>
-__device__ __forceinline__ Raw8<T> narrow8(const uint64_t (&x)[4]) {
+__device__ __forceinline__ Raw8<T> narrow8(const float (&x)[8]) {
     Raw8<T> r;
-    const float2 a = f2_split(x[0]), b = f2_split(x[1]), c = f2_split(x[2]), d = f2_split(x[3]);
     if constexpr (sizeof(T) == 4) {
-        r.w[0] = make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
+        r.w[0] = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
         r.w[sizeof(T) / 2 - 1] =
-            make_uint4(__float_as_uint(c.x), __float_as_uint(c.y), __float_as_uint(d.x), __float_as_uint(d.y));
+            make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7]));
     } else {
         constexpr bool kB = std::is_same<T, __nv_bfloat16>::value;
-        r.w[0] = make_uint4(pack2<kB>(a.x, a.y), pack2<kB>(b.x, b.y), pack2<kB>(c.x, c.y), pack2<kB>(d.x, d.y));
+        r.w[0] = make_uint4(pack2<kB>(x[0], x[1]), pack2<kB>(x[2], x[3]), pack2<kB>(x[4], x[5]), pack2<kB>(x[6], x[7]));
     }
     return r;
 }
@@ -183,105 +199,74 @@ __device__ __forceinline__ bool sequence_of(const RopeArgs& a, long long tok, in
     return i < cnt;
 }
 
-// The norm of a row held by kLanes lanes, x <- x / sqrt(mean(x^2) + eps) * w, two
-// elements an instruction. kExact carries what fp32 products round away (the inverse
-// root's low part by one Newton step, the products' remainders), to about half a step
-// of fp32: for rows that stay fp32 or are quantised next, where a code next to a
-// border, or a scale next to one of fp16, then falls where the exact value puts it.
-// Rows rounded to 16 bits do not need it, and the kernel is bound by issue as much as
-// by memory (carried everywhere it took 16384 tokens from 72 to 95 us).
-template <bool kExact, int kLanes, int D>
-__device__ __forceinline__ void norm_row(uint64_t (&x0)[4], uint64_t (&x1)[4], uint32_t wa, uint32_t wb, float eps) {
-    uint64_t sq0 = f2_mul(x0[0], x0[0]), sq1 = f2_mul(x1[0], x1[0]);
+// The norm of kN rows, each held by kLanes lanes, x <- x / sqrt(mean(x^2) + eps) * w;
+// the rows' shuffles and roots go by together, which hides their latency. kExact
+// carries what fp32 products round away (the inverse root's low part by one Newton
+// step, the products' remainders), to about half a step of fp32: for rows that stay
+// fp32 or are quantised next, where a code next to a border, or a scale next to one of
+// fp16, then falls where the exact value puts it. Rows rounded to 16 bits do not need
+// it, and the kernel is bound by issue as much as by memory (carried everywhere it took
+// 16384 tokens from 72 to 95 us). Packed fp32x2 instructions do not pay here: the moves
+// that pair the operands made it 913 instructions per warp and token, against 667.
+template <bool kExact, int kLanes, int D, int kN>
+__device__ __forceinline__ void norm_rows(float (&x0)[kN][8], float (&x1)[kN][8], const float (&w0)[8],
+                                          const float (&w1)[8], float eps) {
+    float ss[kN];
 #pragma unroll
-    for (int e = 1; e < 4; ++e) {
-        sq0 = f2_fma(x0[e], x0[e], sq0);
-        sq1 = f2_fma(x1[e], x1[e], sq1);
-    }
-    const float2 sq = f2_split(f2_add(sq0, sq1));
-    float ss = sq.x + sq.y;
+    for (int u = 0; u < kN; ++u) {
+        float sa = x0[u][0] * x0[u][0], sb = x1[u][0] * x1[u][0], sc = x0[u][1] * x0[u][1], sd = x1[u][1] * x1[u][1];
 #pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
-    const float m = fmaf(ss, 1.f / D, eps);
-    const float r = kExact ? 1.f / sqrtf(m) : rsqrtf(m);
-    const uint64_t r2 = f2_make(r, r);
-    uint64_t w0[4], w1[4];                   // the chunks' weights, from shared memory at wa and wb
-    {
-        Raw8<float> f;
-        f.w[0] = lds128(wa), f.w[1] = lds128(wa + 16);
-        widen8(f, w0);
-        f.w[0] = lds128(wb), f.w[1] = lds128(wb + 16);
-        widen8(f, w1);
+        for (int e = 2; e < 8; e += 2) {
+            sa = fmaf(x0[u][e], x0[u][e], sa);
+            sb = fmaf(x1[u][e], x1[u][e], sb);
+            sc = fmaf(x0[u][e + 1], x0[u][e + 1], sc);
+            sd = fmaf(x1[u][e + 1], x1[u][e + 1], sd);
+        }
+        ss[u] = (sa + sb) + (sc + sd);
     }
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int u = 0; u < kN; ++u) ss[u] += __shfl_xor_sync(kFull, ss[u], o);
+#pragma unroll
+    for (int u = 0; u < kN; ++u) {
+        const float m = fmaf(ss[u], 1.f / D, eps);
+        if constexpr (kExact) {
+            const float r = 1.f / sqrtf(m);
+            const float mr = m * r, mr_lo = fmaf(m, r, -mr);
+            float r_lo = 0.5f * r * (fmaf(-mr, r, 1.f) - mr_lo * r);   // r (1 - m r^2) / 2
+            if (!(fabsf(r_lo) < r)) r_lo = 0.f;                        // m = 0 or not finite: r alone
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float p0 = x0[u][e] * r, p1 = x1[u][e] * r;
+                const float q0 = fmaf(x0[u][e], r_lo, fmaf(x0[u][e], r, -p0));
+                const float q1 = fmaf(x1[u][e], r_lo, fmaf(x1[u][e], r, -p1));
+                x0[u][e] = fmaf(p0, w0[e], q0 * w0[e]);
+                x1[u][e] = fmaf(p1, w1[e], q1 * w1[e]);
+            }
+        } else {
+            const float r = rsqrtf(m);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                x0[u][e] = x0[u][e] * r * w0[e];
+                x1[u][e] = x1[u][e] * r * w1[e];
+            }
+        }
+    }
+}
+
+// (a, b) -> (a cos - b sin, b cos + a sin), kExact with what the products that are
+// rounded first lose.
+template <bool kExact>
+__device__ __forceinline__ void rotate(float& a, float& b, float c, float s) {
+    const float bs = b * s, as = a * s;
+    float x = fmaf(a, c, -bs), y = fmaf(b, c, as);
     if constexpr (kExact) {
-        const float mr = m * r, mr_lo = fmaf(m, r, -mr);
-        float r_lo = 0.5f * r * (fmaf(-mr, r, 1.f) - mr_lo * r);   // r (1 - m r^2) / 2
-        if (!(fabsf(r_lo) < r)) r_lo = 0.f;                        // m = 0 or not finite: r alone
-        const uint64_t lo2 = f2_make(r_lo, r_lo), nr2 = f2_make(-r, -r);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint64_t p0 = f2_mul(x0[e], r2), p1 = f2_mul(x1[e], r2);
-            const uint64_t q0 = f2_fma(x0[e], lo2, f2_fma(x0[e], r2, f2_mul(x0[e], nr2)));
-            const uint64_t q1 = f2_fma(x1[e], lo2, f2_fma(x1[e], r2, f2_mul(x1[e], nr2)));
-            x0[e] = f2_fma(p0, w0[e], f2_mul(q0, w0[e]));
-            x1[e] = f2_fma(p1, w1[e], f2_mul(q1, w1[e]));
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            x0[e] = f2_mul(f2_mul(x0[e], r2), w0[e]);
-            x1[e] = f2_mul(f2_mul(x1[e], r2), w1[e]);
-        }
+        x -= fmaf(b, s, -bs);
+        y += fmaf(a, s, -as);
     }
-}
-
-// A lane's eight (cos, sin) pairs, two to a register pair, and -sin.
-struct Turn {
-    uint64_t c[4], s[4], n[4];
-    __device__ __forceinline__ void set(int e, uint4 f) {
-        c[e] = f2_make(__uint_as_float(f.x), __uint_as_float(f.z));
-        s[e] = f2_make(__uint_as_float(f.y), __uint_as_float(f.w));
-        n[e] = f2_make(-__uint_as_float(f.y), -__uint_as_float(f.w));
-    }
-};
-
-// a c + b r, kExact with what the product b r rounds away (nr = -r).
-template <bool kExact>
-__device__ __forceinline__ uint64_t fma_rest(uint64_t a, uint64_t c, uint64_t b, uint64_t r, uint64_t nr) {
-    const uint64_t x = f2_fma(a, c, f2_mul(b, r));
-    if constexpr (kExact) return f2_add(x, f2_fma(b, r, f2_mul(b, nr)));
-    else return x;
-}
-template <bool kExact>
-__device__ __forceinline__ float fma_rest(float a, float c, float b, float r) {
-    const float br = b * r, x = fmaf(a, c, br);
-    if constexpr (kExact) return x + fmaf(b, r, -br);
-    else return x;
-}
-
-// (a, b) -> (a cos - b sin, b cos + a sin) of a lane's eight pairs.
-template <bool kExact>
-__device__ __forceinline__ void rotate(uint64_t (&x0)[4], uint64_t (&x1)[4], const Turn& t, bool interleaved) {
-    if (interleaved) {
-        auto one = [&](uint64_t& x, float c, float s) {
-            const float2 v = f2_split(x);
-            x = f2_make(fma_rest<kExact>(v.x, c, v.y, -s), fma_rest<kExact>(v.y, c, v.x, s));
-        };
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {        // pairs 0 .. 3 are chunk 0's, 4 .. 7 chunk 1's
-            const float2 c = f2_split(t.c[e / 2]), s = f2_split(t.s[e / 2]);
-            const float2 d = f2_split(t.c[2 + e / 2]), u = f2_split(t.s[2 + e / 2]);
-            one(x0[e], e % 2 ? c.y : c.x, e % 2 ? s.y : s.x);
-            one(x1[e], e % 2 ? d.y : d.x, e % 2 ? u.y : u.x);
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint64_t a = x0[e], b = x1[e];
-            x0[e] = fma_rest<kExact>(a, t.c[e], b, t.n[e], t.s[e]);
-            x1[e] = fma_rest<kExact>(b, t.c[e], a, t.s[e], t.n[e]);
-        }
-    }
+    a = x;
+    b = y;
 }
 
 // Codes and scale of one row (two 8-element chunks a lane, kLanes lanes a row), by the
@@ -292,45 +277,39 @@ __device__ __forceinline__ void rotate(uint64_t (&x0)[4], uint64_t (&x1)[4], con
 // and no step leaves fp32's range where the code is not zero), at three instructions
 // instead of a division. A row with an infinity divides.
 template <int kOut, int kLanes>
-__device__ __forceinline__ void quantise_store(const uint64_t (&x0)[4], const uint64_t (&x1)[4], bool live, uint8_t* row,
+__device__ __forceinline__ void quantise_store(const float (&x0)[8], const float (&x1)[8], bool live, uint8_t* row,
                                                int c0, int c1, __half* scale, bool first) {
     constexpr float kQmax = kOut == kOutFp8 ? 448.0f : kOut == kOutI4 ? 7.0f : 127.0f;
     float amax = 0.f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const float2 a = f2_split(x0[e]), b = f2_split(x1[e]);
-        amax = fmaxf(amax, fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(b.x), fabsf(b.y))));
-    }
+    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fmaxf(fabsf(x0[e]), fabsf(x1[e])));
 #pragma unroll
     for (int o = kLanes / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
     const __half sh = __float2half_rn(fminf(__fdiv_rn(amax, kQmax), 65504.0f));
     const float sf = __half2float(sh);
     if (!live) return;
     const float y = __fdiv_rn(1.f, sf);
-    const uint64_t y2 = f2_make(y, y), ns2 = f2_make(-sf, -sf);
     const bool finite = amax < INFINITY;
+    auto quotient = [&](float x) {
+        const float q = x * y;
+        return finite ? fmaf(fmaf(-q, sf, x), y, q) : __fdiv_rn(x, sf);
+    };
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         uint32_t w[2] = {0u, 0u};
         if (sf != 0.f) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint64_t x = h ? x1[e] : x0[e];
-                const uint64_t q = f2_mul(x, y2);
-                float2 t = f2_split(f2_fma(f2_fma(q, ns2, x), y2, q));
-                if (!finite) {
-                    const float2 xs = f2_split(x);
-                    t = make_float2(__fdiv_rn(xs.x, sf), __fdiv_rn(xs.y, sf));
-                }
+            for (int e = 0; e < 8; e += 2) {
+                const float t0 = quotient(h ? x1[e] : x0[e]), t1 = quotient(h ? x1[e + 1] : x0[e + 1]);
                 if constexpr (kOut == kOutFp8) {
-                    const uint32_t two = __nv_cvt_float2_to_fp8x2(t, __NV_SATFINITE, __NV_E4M3);
-                    w[e / 2] |= two << (16 * (e % 2));
+                    const uint32_t two = __nv_cvt_float2_to_fp8x2(make_float2(t0, t1), __NV_SATFINITE, __NV_E4M3);
+                    w[e / 4] |= two << (16 * (e / 2 % 2));
                 } else {
                     constexpr int qm = (int)kQmax;
-                    const uint32_t a = (uint32_t)max(-qm, min(qm, __float2int_rn(t.x)));
-                    const uint32_t b = (uint32_t)max(-qm, min(qm, __float2int_rn(t.y)));
-                    if constexpr (kOut == kOutI4) w[0] |= ((a & 0xFu) | ((b & 0xFu) << 4)) << (8 * e);
-                    else w[e / 2] |= ((a & 0xFFu) | ((b & 0xFFu) << 8)) << (16 * (e % 2));
+                    const uint32_t a = (uint32_t)max(-qm, min(qm, __float2int_rn(t0)));
+                    const uint32_t b = (uint32_t)max(-qm, min(qm, __float2int_rn(t1)));
+                    if constexpr (kOut == kOutI4) w[0] |= ((a & 0xFu) | ((b & 0xFu) << 4)) << (4 * e);
+                    else w[e / 4] |= ((a & 0xFFu) | ((b & 0xFFu) << 8)) << (16 * (e / 2 % 2));
                 }
             }
         }
@@ -349,7 +328,7 @@ struct Place {
 };
 
 template <typename T, int D, int kOut>
-__global__ void __launch_bounds__(kRopeWarps * 32, RopeCfg<T>::kCtas) norm_rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kRopeWarps * 32, RopeShape<T, kOut>::kCtas) norm_rope_kernel(const RopeArgs a) {
     using C = RopeCfg<T>;
     constexpr int kLanes = D / 16;                 // lanes per row
     constexpr int kRows = 32 / kLanes;             // rows per warp step
@@ -359,22 +338,12 @@ __global__ void __launch_bounds__(kRopeWarps * 32, RopeCfg<T>::kCtas) norm_rope_
     grid_dependency_wait();
     launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    // the weights as fp32, q's then k's
-    const uint32_t weights = smem_addr(smem_raw) + C::kWeights;
-    for (int i = threadIdx.x; i < 2 * D; i += kRopeWarps * 32) {
-        const void* w = i < D ? a.q_weight : a.k_weight;
-        if (w != nullptr)
-            reinterpret_cast<float*>(smem_raw + C::kWeights)[i] =
-                a.weight_dtype == GQA_DTYPE_F32    ? static_cast<const float*>(w)[i % D]
-                : a.weight_dtype == GQA_DTYPE_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(w)[i % D])
-                                                   : __half2float(static_cast<const __half*>(w)[i % D]);
-    }
-    __syncthreads();
     const int unit = (int)blockIdx.x * kRopeWarps + warp;
     const int part = unit % a.parts;
-    const long long t_lo = (long long)(unit / a.parts) * a.run;
-    if (t_lo >= a.tokens) return;                  // uniform per warp
-    const int n = (int)min((long long)a.run, a.tokens - t_lo);
+    const int r = unit / a.parts;                  // run r: a.run tokens, the first a.longer one more
+    if (r >= a.runs) return;                       // uniform per warp
+    const long long t_lo = (long long)r * a.run + min(r, a.longer);
+    const int n = a.run + (r < a.longer ? 1 : 0);
     const int li = lane % kLanes, grp = lane / kLanes;
     const int half = a.rotary_dim / 16;            // lanes of a row that rotate
     const bool turns = li < half;
@@ -385,38 +354,44 @@ __global__ void __launch_bounds__(kRopeWarps * 32, RopeCfg<T>::kCtas) norm_rope_
         c1 = li + half;
     }
     const bool is_q = part < a.q_parts;
-    const bool normed = (is_q ? a.q_weight : a.k_weight) != nullptr;
-    const uint32_t wbase = weights + (is_q ? 0 : D * 4);
+    // this warp's first row, and its steps: query rows, or K rows and as many V rows
+    const int hw = is_q ? part * kRopeSteps * kRows : (part - a.q_parts) * kKvSteps * kRows;
+    const int rows = is_q ? min(kRopeSteps * kRows, a.H - hw) : min(kKvSteps * kRows, a.K - hw);
+    const int h0 = hw + grp;                       // this lane's row of step 0; of step u: h0 + u kRows
     const uint32_t ring = smem_addr(smem_raw) + warp * (C::kStages * C::kStage);
-    // rows of step u lie u * kRows heads past this lane's first one, of step 0
-    const int h0 = (is_q ? part * kRopeSteps : (part - a.q_parts) * kKvSteps) * kRows + grp;
-    const T* src0 = static_cast<const T*>(is_q ? a.q : a.k) + t_lo * (is_q ? a.q_stride : a.k_stride) + (long long)h0 * D;
-    const T* vsrc0 = is_q || !kCached ? nullptr : static_cast<const T*>(a.v) + t_lo * a.v_stride + (long long)h0 * D;
-    const long long src_step = is_q ? a.q_stride : a.k_stride;
-    bool in[kMost];                                // this lane has a row in step u
-#pragma unroll
-    for (int u = 0; u < kMost; ++u) {
-        const int h = h0 + (is_q ? u : u % kKvSteps) * kRows;
-        in[u] = is_q ? u < kRopeSteps && h < a.H : u < (kCached ? 2 : 1) * kKvSteps && h < a.K;
-    }
+    const int c01 = 8 * (c1 - c0);                 // elements between the chunks
 
-    // ---- fetch: everything token t needs, into stage s
+    // ---- fetch: everything the run's next token needs, into stage s
+    const T* src = static_cast<const T*>(is_q ? a.q : a.k) + t_lo * (is_q ? a.q_stride : a.k_stride) + (long long)h0 * D + 8 * c0;
+    const T* vsrc = is_q || !kCached ? src : static_cast<const T*>(a.v) + t_lo * a.v_stride + (long long)h0 * D + 8 * c0;
+    const long long src_step = is_q ? a.q_stride : a.k_stride;
     int b = 0, left = 0, pos = 0;                  // its sequence, tokens after it in there, its position
     auto fetch = [&](int j, int s) -> Place {
         const long long t = t_lo + j;
         const uint32_t st = ring + s * C::kStage;
-        const T* row = src0 + j * src_step;
-        const T* vrow = vsrc0 + (kCached ? j * a.v_stride : 0);
-#pragma unroll
-        for (int u = 0; u < kMost; ++u) {
-            if (!in[u]) continue;
-            const T* src = is_q ? row + u * kRows * D : u < kKvSteps ? row + u * kRows * D : vrow + (u - kKvSteps) * kRows * D;
-#pragma unroll
-            for (int i = 0; i < C::kPieces; ++i) {
-                async16(st + ((2 * u) * C::kPieces + i) * 512 + lane * 16, reinterpret_cast<const uint4*>(src + 8 * c0) + i);
-                async16(st + ((2 * u + 1) * C::kPieces + i) * 512 + lane * 16, reinterpret_cast<const uint4*>(src + 8 * c1) + i);
+        auto rows_in = [&](auto first, auto steps, const T* from) {
+            static_for<0, decltype(steps)::value>([&](auto u) {
+                constexpr int kSlot = 2 * C::kPieces * (decltype(first)::value + decltype(u)::value) * 512;
+                constexpr int kFrom = decltype(u)::value * kRows * D * (int)sizeof(T);
+                if (u * kRows + grp < rows) {
+                    static_for<0, C::kPieces>([&](auto i) {
+                        async16<kSlot + i * 512, kFrom + i * 16>(st + lane * 16, from);
+                        async16<kSlot + (C::kPieces + i) * 512, kFrom + i * 16>(st + lane * 16, from + c01);
+                    });
+                }
+            });
+        };
+        using std::integral_constant;
+        if (is_q) {
+            rows_in(integral_constant<int, 0>{}, integral_constant<int, kRopeSteps>{}, src);
+        } else {
+            rows_in(integral_constant<int, 0>{}, integral_constant<int, kKvSteps>{}, src);
+            if constexpr (kCached) {
+                rows_in(integral_constant<int, kKvSteps>{}, integral_constant<int, kKvSteps>{}, vsrc);
+                vsrc += a.v_stride;
             }
         }
+        src += src_step;
         Place p{0, 0, true, true};
         if constexpr (kCached) {
             if (left > 0) {                        // the token after the last one, same sequence
@@ -444,8 +419,8 @@ __global__ void __launch_bounds__(kRopeWarps * 32, RopeCfg<T>::kCtas) norm_rope_
                 if (lane == 0 && part == 0) flag_error(a.err, GQA_DEVERR_POSITION);
                 p.live = false;
             } else if (lane < 4 * half) {          // 16 bytes a lane: the row once for the warp
-                async16(st + C::kTable + lane * 16,
-                        reinterpret_cast<const uint4*>(a.rope + (long long)p.turn * (a.rotary_dim / 2)) + lane);
+                async16<C::kTable, 0>(st + lane * 16,
+                                      reinterpret_cast<const uint4*>(a.rope + (long long)p.turn * (a.rotary_dim / 2)) + lane);
             }
         }
         if constexpr (kCached) {
@@ -461,70 +436,134 @@ __global__ void __launch_bounds__(kRopeWarps * 32, RopeCfg<T>::kCtas) norm_rope_
         return p;
     };
 
-    // ---- norm, rotation and store of token t from stage s
+    // ---- this lane's weights
+    const void* wp = is_q ? a.q_weight : a.k_weight;
+    float w0[8], w1[8];
+    if (wp != nullptr) {
+        if (a.weight_dtype == GQA_DTYPE_F32) {
+            widen8(load8(static_cast<const float*>(wp) + 8 * c0), w0);
+            widen8(load8(static_cast<const float*>(wp) + 8 * c1), w1);
+        } else if (a.weight_dtype == GQA_DTYPE_BF16) {
+            widen8(load8(static_cast<const __nv_bfloat16*>(wp) + 8 * c0), w0);
+            widen8(load8(static_cast<const __nv_bfloat16*>(wp) + 8 * c1), w1);
+        } else {
+            widen8(load8(static_cast<const __half*>(wp) + 8 * c0), w0);
+            widen8(load8(static_cast<const __half*>(wp) + 8 * c1), w1);
+        }
+    }
+
+    // ---- norm, rotation and store of the run's token j from stage s
     auto finish = [&](const Place& p, int j, int s) {
         if (!p.live) return;                       // uniform per warp
         const long long t = t_lo + j;
-        const uint32_t st = ring + s * C::kStage;
-        long long dst = 0, sidx = 0;               // element offset of kv-head 0's slot; its scale
-        if constexpr (kCached) {
-            if (!is_q) {
-                if (!p.slot) return;
-                const int ph = (int)lds32(st + C::kEntry);
-                if (ph < 0 || ph >= a.num_blocks) {
-                    if (lane == 0 && part == a.q_parts) flag_error(a.err, GQA_DEVERR_BLOCK_INDEX);
-                    return;
-                }
-                dst = (long long)ph * a.sb + (long long)(p.pos % kBlock) * a.st;
-                sidx = (long long)ph * a.K * kBlock + p.pos % kBlock;
-            }
-        }
-        Turn turn;
+        const uint32_t st = ring + s * C::kStage, mine = st + lane * 16;
+        float cs[8], sn[8];
         if (turns) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) turn.set(e, lds128(st + C::kTable + (4 * li + e) * 16));
+            for (int e = 0; e < 4; ++e) {
+                const uint4 f = lds128(st + C::kTable + (4 * li + e) * 16);
+                cs[2 * e] = __uint_as_float(f.x);
+                sn[2 * e] = __uint_as_float(f.y);
+                cs[2 * e + 1] = __uint_as_float(f.z);
+                sn[2 * e + 1] = __uint_as_float(f.w);
+            }
         }
+        // row of slot u: raw, and normed and turned
+        auto row_of = [&](int u, Raw8<T>& r0, Raw8<T>& r1) {
 #pragma unroll
-        for (int u = 0; u < kMost; ++u) {
-            const bool is_v = !is_q && u >= kKvSteps;
-            if (is_v && !kCached) break;
-            if (!__any_sync(kFull, in[u])) continue;
-            Raw8<T> r0, r1;
+            for (int i = 0; i < C::kPieces; ++i) {
+                r0.w[i] = lds128(mine + (2 * C::kPieces * u + i) * 512);
+                r1.w[i] = lds128(mine + (2 * C::kPieces * u + C::kPieces + i) * 512);
+            }
+        };
+        // rows of steps u .. u + kN - 1, normed and turned
+        auto turned = [&](auto exact, auto steps, int u0, float (&x0)[decltype(steps)::value][8],
+                          float (&x1)[decltype(steps)::value][8]) {
+            constexpr bool kExact = decltype(exact)::value;
+            constexpr int kN = decltype(steps)::value;
 #pragma unroll
-            for (int i = 0; i < C::kPieces; ++i) {       // (a lane without a row works on what the slot holds)
-                r0.w[i] = lds128(st + ((2 * u) * C::kPieces + i) * 512 + lane * 16);
-                r1.w[i] = lds128(st + ((2 * u + 1) * C::kPieces + i) * 512 + lane * 16);
+            for (int u = 0; u < kN; ++u) {
+                Raw8<T> r0, r1;
+                row_of(u0 + u, r0, r1);
+                widen8(r0, x0[u]);
+                widen8(r1, x1[u]);
             }
-            uint64_t x0[4], x1[4];
-            widen8(r0, x0);
-            widen8(r1, x1);
-            if (!is_v) {
-                auto work = [&](auto exact) {
-                    constexpr bool kExact = decltype(exact)::value;
-                    if (normed) norm_row<kExact, kLanes, D>(x0, x1, wbase + 32 * c0, wbase + 32 * c1, a.eps);
-                    if (turns) rotate<kExact>(x0, x1, turn, a.interleaved != 0);
-                };
-                if (sizeof(T) == 4 || (kCoded && !is_q)) work(std::true_type{});
-                else work(std::false_type{});
+            if (wp != nullptr) norm_rows<kExact, kLanes, D>(x0, x1, w0, w1, a.eps);
+            if (turns) {
+#pragma unroll
+                for (int u = 0; u < kN; ++u) {
+                    if (a.interleaved) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            rotate<kExact>(x0[u][2 * e], x0[u][2 * e + 1], cs[e], sn[e]);
+                            rotate<kExact>(x1[u][2 * e], x1[u][2 * e + 1], cs[4 + e], sn[4 + e]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) rotate<kExact>(x0[u][e], x1[u][e], cs[e], sn[e]);
+                    }
+                }
             }
-            const int h = h0 + (is_q ? u : u % kKvSteps) * kRows;
-            if (is_q || kOut == kOutDense) {
-                if (in[u]) {
-                    T* out = is_q ? static_cast<T*>(a.q_out) + (t * a.H + h) * D : static_cast<T*>(a.k_out) + (t * a.K + h) * D;
-                    store8r(out + 8 * c0, narrow8<T>(x0));
-                    store8r(out + 8 * c1, narrow8<T>(x1));
+        };
+        constexpr int kPair = RopeShape<T, kOut>::kPair;
+        using Pair = std::integral_constant<int, kPair>;
+        static_assert(kMost % 2 == 0 && kKvSteps % 2 == 0, "steps come in pairs");
+        if (is_q || kOut == kOutDense) {           // rows of a dense output
+            T* out = (is_q ? static_cast<T*>(a.q_out) + t * a.H * D : static_cast<T*>(a.k_out) + t * a.K * D) + h0 * D + 8 * c0;
+#pragma unroll
+            for (int u = 0; u < kMost; u += kPair) {
+                if (u * kRows >= rows) break;      // uniform; a lane without a row works on what its slot holds
+                float x0[kPair][8], x1[kPair][8];
+                turned(std::integral_constant<bool, sizeof(T) == 4>{}, Pair{}, u, x0, x1);
+#pragma unroll
+                for (int v = 0; v < kPair; ++v) {
+                    if ((u + v) * kRows + grp >= rows) continue;
+                    store8r(out + (u + v) * kRows * D, narrow8<T>(x0[v]));
+                    store8r(out + (u + v) * kRows * D + c01, narrow8<T>(x1[v]));
                 }
-            } else if constexpr (kOut == kOutCache) {
-                if (in[u]) {
-                    T* out = static_cast<T*>(is_v ? a.v_cache : a.k_cache) + dst + (long long)h * a.sh;
-                    store8r(out + 8 * c0, is_v ? r0 : narrow8<T>(x0));
-                    store8r(out + 8 * c1, is_v ? r1 : narrow8<T>(x1));
+            }
+            return;
+        }
+        if constexpr (kCached) {                   // K and V rows of the cache
+            if (!p.slot) return;
+            const int ph = (int)lds32(st + C::kEntry);
+            if (ph < 0 || ph >= a.num_blocks) {
+                if (lane == 0 && part == a.q_parts) flag_error(a.err, GQA_DEVERR_BLOCK_INDEX);
+                return;
+            }
+            // element offset of this lane's row of step 0, and of its scale
+            long long off = (long long)ph * a.sb + (long long)(p.pos % kBlock) * a.st + (long long)h0 * a.sh;
+            long long sidx = ((long long)ph * a.K + h0) * kBlock + p.pos % kBlock;
+#pragma unroll
+            for (int u = 0; u < kKvSteps; u += kPair) {
+                if (u * kRows >= rows) break;
+                float x0[kPair][8], x1[kPair][8];
+                turned(std::integral_constant<bool, sizeof(T) == 4 || kCoded>{}, Pair{}, u, x0, x1);
+#pragma unroll
+                for (int v = 0; v < kPair; ++v, off += kRows * a.sh, sidx += kRows * kBlock) {
+                    const bool in = (u + v) * kRows + grp < rows;
+                    if constexpr (kCoded) {
+                        if ((u + v) * kRows >= rows) break;
+                        const long long at = kOut == kOutI4 ? off / 2 : off;
+                        quantise_store<kOut, kLanes>(x0[v], x1[v], in, static_cast<uint8_t*>(a.k_cache) + at, c0, c1,
+                                                     a.k_scale + sidx, li == 0);
+                        Raw8<T> r0, r1;
+                        row_of(kKvSteps + u + v, r0, r1);
+                        widen8(r0, x0[v]);
+                        widen8(r1, x1[v]);
+                        quantise_store<kOut, kLanes>(x0[v], x1[v], in, static_cast<uint8_t*>(a.v_cache) + at, c0, c1,
+                                                     a.v_scale + sidx, li == 0);
+                    } else if (in) {
+                        T* ko = static_cast<T*>(a.k_cache) + off + 8 * c0;
+                        store8r(ko, narrow8<T>(x0[v]));
+                        store8r(ko + c01, narrow8<T>(x1[v]));
+                        Raw8<T> r0, r1;
+                        row_of(kKvSteps + u + v, r0, r1);
+                        T* vo = static_cast<T*>(a.v_cache) + off + 8 * c0;
+                        store8r(vo, r0);
+                        store8r(vo + c01, r1);
+                    }
                 }
-            } else if constexpr (kCached) {
-                const long long off = dst + (long long)h * a.sh;
-                uint8_t* out = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + (kOut == kOutI4 ? off / 2 : off);
-                __half* sc = (is_v ? a.v_scale : a.k_scale) + sidx + (long long)h * kBlock;
-                quantise_store<kOut, kLanes>(x0, x1, in[u], out, c0, c1, sc, li == 0);
             }
         }
     };
@@ -658,12 +697,14 @@ cudaError_t launch_norm_rope(const NormRopeLaunch& L) {
     const int sms = device_sms(-1), per_sm = ctas_per_sm(fn, kRopeWarps * 32, smem);
     if (sms < 1 || per_sm < 1) return cudaErrorInvalidConfiguration;
     if (a.tokens == 0) return cudaSuccess;
-    // one wave of warps: each serves as many consecutive tokens as it takes
-    const long long runs = std::max<long long>(1, (long long)sms * per_sm * kRopeWarps / a.parts);
-    const long long run = (a.tokens + runs - 1) / runs;
-    if (run > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    a.run = (int)run;
-    const long long units = (a.tokens + run - 1) / run * a.parts;
+    // one wave of warps, each with an even share of consecutive tokens
+    const long long runs =
+        std::min(a.tokens, std::max<long long>(1, (long long)sms * per_sm * kRopeWarps / a.parts));
+    if (a.tokens / runs >= 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    a.runs = (int)runs;
+    a.run = (int)(a.tokens / runs);
+    a.longer = (int)(a.tokens % runs);
+    const long long units = runs * a.parts;
     if (units > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     void* args[] = {&a};
     return launch_pdl(fn, dim3((unsigned)((units + kRopeWarps - 1) / kRopeWarps)), kRopeWarps * 32, smem, L.stream, args);
