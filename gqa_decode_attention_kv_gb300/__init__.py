@@ -137,7 +137,7 @@ def load() -> ctypes.CDLL:
             lib.gqa_prefill.argtypes = [ctypes.POINTER(KVCacheDesc), vp, i32, i32, vp, i32, vp, i32, vp,
                                         i32, ctypes.c_float, i32, vp, i32, i32, vp, vp]
             lib.gqa_prefill.restype = ctypes.c_int
-            lib.gqa_prefill_sinks.argtypes = [*lib.gqa_prefill.argtypes[:12], i32, *lib.gqa_prefill.argtypes[12:]]
+            lib.gqa_prefill_sinks.argtypes = [*lib.gqa_prefill.argtypes[:12], i32, i64, *lib.gqa_prefill.argtypes[12:]]
             lib.gqa_prefill_sinks.restype = ctypes.c_int
             lib.gqa_kv_pages_workspace_size.argtypes = [i64, i32]
             lib.gqa_kv_pages_workspace_size.restype = ctypes.c_size_t
@@ -908,7 +908,7 @@ def gqa_prefill(cache: PagedKVCache, q: torch.Tensor, q_start: torch.Tensor, max
     st = load().gqa_prefill_sinks(ctypes.byref(desc), args[0], DTYPE_CODE[q.dtype], int(q.shape[1]),
                                   args[1], int(max_new_tokens), args[2],
                                   int(block_tables.shape[1]), args[3], B, float(scale), int(window),
-                                  int(sinks), op, DTYPE_CODE[out.dtype], int(kernel), args[4],
+                                  int(sinks), int(q.shape[0]), op, DTYPE_CODE[out.dtype], int(kernel), args[4],
                                   _stream_ptr(stream))
     _check(st, "gqa_prefill")
     return out

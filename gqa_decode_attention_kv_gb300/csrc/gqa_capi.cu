@@ -622,16 +622,16 @@ int gqa_prefill(const gqa_kv_cache_t* cache, const void* q, int32_t q_dtype, int
                 int32_t sliding_window, void* out, int32_t out_dtype, int32_t kernel, int32_t* err_flag,
                 void* stream) {
     return gqa_prefill_sinks(cache, q, q_dtype, num_heads, q_start, max_new_tokens, block_tables, max_blocks_per_seq,
-                             context_lens, batch, scale, sliding_window, 0, out, out_dtype, kernel, err_flag, stream);
+                             context_lens, batch, scale, sliding_window, 0, 0, out, out_dtype, kernel, err_flag, stream);
 }
 
 int gqa_prefill_sinks(const gqa_kv_cache_t* cache, const void* q, int32_t q_dtype, int32_t num_heads,
                       const int32_t* q_start, int32_t max_new_tokens, const int32_t* block_tables,
                       int32_t max_blocks_per_seq, const int32_t* context_lens, int32_t batch, float scale,
-                      int32_t sliding_window, int32_t sink_tokens, void* out, int32_t out_dtype, int32_t kernel,
-                      int32_t* err_flag, void* stream) {
+                      int32_t sliding_window, int32_t sink_tokens, int64_t total_new_tokens, void* out,
+                      int32_t out_dtype, int32_t kernel, int32_t* err_flag, void* stream) {
     int st = check_cache(cache);
-    if (sink_tokens < 0) return GQA_ERR_INVALID;
+    if (sink_tokens < 0 || total_new_tokens < 0) return GQA_ERR_INVALID;
     if (kernel < 0 || kernel > GQA_PREFILL_TCGEN05_PAIRED) return GQA_ERR_INVALID;
     if (st != GQA_OK) return st;
     if (batch < 0 || num_heads <= 0 || max_blocks_per_seq <= 0 || max_new_tokens < 0 || sliding_window < 0)
@@ -659,6 +659,7 @@ int gqa_prefill_sinks(const gqa_kv_cache_t* cache, const void* q, int32_t q_dtyp
     L.scale = scale;
     L.window = sliding_window;
     L.sinks = sink_tokens;
+    L.total_new_tokens = total_new_tokens;
     L.out = out;
     L.out_dtype = out_dtype;
     L.kernel = kernel;

@@ -117,6 +117,7 @@ struct PrefillLaunch {
     float scale;
     int window;
     int sinks;                  // first tokens that stay visible beside the window
+    long long total_new_tokens; // rows of q, 0: not known
     void* out;
     int out_dtype;
     int kernel;                 // GQA_PREFILL_* (0 = tcgen05)

@@ -1003,13 +1003,14 @@ constexpr uint32_t kW2ColO = 128;                //         O at 256t + 128
 // are persistent: each walks its share of the (query tile, kv-head, sequence)
 // items, and the next item's Q load and first S products run while the softmax
 // warps store the last item's output.
-template <int kTiles>
+template <int kTiles, int kDim = 128>
 struct W2Cfg {
-    static constexpr int D = 128;
+    static constexpr int D = kDim;
+    static constexpr int kHalves = D / 64;               // 128-byte column halves of a row
     static constexpr int kRows = kTiles * kTcRows;       // query rows per CTA
     static constexpr int kSoftWarps = 4 * kTiles;
     static constexpr int kThreads = kRows + 32 * kTiles + 64;   // + an MMA warp per tile, K and V copy warps
-    static constexpr int kStages = kTiles == 2 ? 4 : 2;  // K and V stages
+    static constexpr int kStages = kTiles == 2 || D == 64 ? 4 : 2;  // K and V stages
     static constexpr int kCtasPerSm = kTiles == 2 ? 1 : 2;
     static constexpr uint32_t kTmemCols = 256u * kTiles;
     static constexpr int kQt = kTcRows * D * 2;          // one Q tile: 2 halves x 128 rows x 128 B
@@ -1023,11 +1024,11 @@ struct W2Cfg {
     static_assert(kSmem * kCtasPerSm <= 227 * 1024, "CTAs per SM fit the shared memory");
 };
 
-template <typename T, int kTiles, bool kSinks>
-__global__ void __launch_bounds__(W2Cfg<kTiles>::kThreads, W2Cfg<kTiles>::kCtasPerSm)
+template <typename T, int kTiles, int kDim, bool kSinks>
+__global__ void __launch_bounds__(W2Cfg<kTiles, kDim>::kThreads, W2Cfg<kTiles, kDim>::kCtasPerSm)
 prefill_tc2_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                    const __grid_constant__ CUtensorMap omap, const PrefillArgs a) {
-    using C = W2Cfg<kTiles>;
+    using C = W2Cfg<kTiles, kDim>;
     constexpr int kS = C::kStages;
     constexpr int D = C::D;
     constexpr bool kB = std::is_same<T, __nv_bfloat16>::value;
@@ -1210,21 +1211,26 @@ prefill_tc2_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 fence_proxy_async_smem();          // earlier generic writes to the stage come first
                 __syncwarp();
                 if (!k_warp) {
-                    // V: one box per page (the page map lands it as [half][slot][128 B])
+                    // V: one box per page (head_dim 128: the page map lands it as
+                    // [half][slot][128 B])
                     if (lane < kW2Blocks) {
                         int pq = ph[0];
 #pragma unroll
                         for (int i = 1; i < kW2Blocks; ++i)
                             if (lane == i) pq = ph[i];
                         if (pq >= 0) {
-                            auto coord = [&](int which) { return which == 1 ? it.g : pq; };
-                            tma_load_5d(sV + stage(G) * C::kVc + lane * C::kVb, &vmap, 0, 0, 0,
-                                        coord(a.page_perm[0]), coord(a.page_perm[1]), bar, pol);
+                            const uint32_t dst = sV + stage(G) * C::kVc + lane * C::kVb;
+                            auto coord = [&](int which) { return which == 0 ? 0 : (which == 1 ? it.g : pq); };
+                            if constexpr (C::kHalves == 2)
+                                tma_load_5d(dst, &vmap, 0, 0, 0, coord(a.page_perm[0]), coord(a.page_perm[1]), bar, pol);
+                            else
+                                tma_load_4d(dst, &vmap, 0, coord(a.map_perm[0]), coord(a.map_perm[1]),
+                                            coord(a.map_perm[2]), bar, pol);
                         }
                     }
-                } else if (lane < 2 * kW2Blocks) {
+                } else if (lane < C::kHalves * kW2Blocks) {
                     // K: one lane per (block, 64-element half) box
-                    const int q = lane >> 1, h = lane & 1;
+                    const int q = lane / C::kHalves, h = lane % C::kHalves;
                     int pq = ph[0];
 #pragma unroll
                     for (int i = 1; i < kW2Blocks; ++i)
@@ -1240,8 +1246,8 @@ prefill_tc2_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                     if (seen != ~0ull) {
                         ok = __all_sync(kFull, mbar_wait(bar_z, z_par));
                         z_par ^= 1u;
-                        for (int i = lane; ok && i < kW2Chunk * 16; i += 32) {
-                            const int t = i / 16, h = (i / 8) % 2, ck = i % 8;
+                        for (int i = lane; ok && i < kW2Chunk * C::kHalves * 8; i += 32) {
+                            const int t = i / (C::kHalves * 8), h = (i / 8) % C::kHalves, ck = i % 8;
                             if (!((seen >> t) & 1u))
                                 sts128(sV + stage(G) * C::kVc + (t / kBlock) * C::kVb + h * (kBlock * 128) + (t % kBlock) * 128 + ck * 16,
                                        make_uint4(0u, 0u, 0u, 0u));
@@ -1497,8 +1503,8 @@ prefill_tc2_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 if (!kSinks && (bm != (1u << kW2Blocks) - 1u || cpos + kW2Chunk > it.L)) {
                     ok = __all_sync(kFull, mbar_wait(bar_v(G), par_st(G)));
                     const uint32_t vb = sV + stage(G) * C::kVc;
-                    for (int i = tid & (kTcRows - 1); i < kW2Chunk * 2 * 8; i += kTcRows) {
-                        const int tk2 = i / 16, h = (i / 8) % 2, ck = i % 8;
+                    for (int i = tid & (kTcRows - 1); i < kW2Chunk * C::kHalves * 8; i += kTcRows) {
+                        const int tk2 = i / (C::kHalves * 8), h = (i / 8) % C::kHalves, ck = i % 8;
                         if (((bm >> (tk2 / kBlock)) & 1u) && cpos + tk2 < it.L) continue;
                         sts128(vb + (tk2 / kBlock) * C::kVb + h * (kBlock * 128) + (tk2 % kBlock) * 128 + ck * 16,
                                make_uint4(0u, 0u, 0u, 0u));
@@ -1601,8 +1607,8 @@ prefill_tc2_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
 
 template <typename T, int kTiles>
 const void* prefill_tc2_fn(bool sinks) {
-    return sinks ? reinterpret_cast<const void*>(&prefill_tc2_kernel<T, kTiles, true>)
-                 : reinterpret_cast<const void*>(&prefill_tc2_kernel<T, kTiles, false>);
+    return sinks ? reinterpret_cast<const void*>(&prefill_tc2_kernel<T, kTiles, 128, true>)
+                 : reinterpret_cast<const void*>(&prefill_tc2_kernel<T, kTiles, 128, false>);
 }
 
 template <typename T, int D>
@@ -1629,13 +1635,28 @@ int launch_prefill(const PrefillLaunch& L) {
     const bool sinks = L.window > 0 && L.sinks > 0;
     // the 64-token-chunk tcgen05 forms serve head_dim 128: two query tiles per
     // CTA (one CTA per SM) or one (two CTAs per SM)
-    const bool wide2 = tc && D == 128 && (L.kernel == GQA_PREFILL_AUTO || L.kernel == GQA_PREFILL_TCGEN05_WIDE);
-    const bool wide1 = tc && D == 128 && L.kernel == GQA_PREFILL_TCGEN05_PAIRED;
-    const bool wide = wide1 || wide2;
-    const int rows_per_cta = wide2 ? W2Cfg<2>::kRows : wide1 ? W2Cfg<1>::kRows : tc ? kTcRows : kPfRows;
+    const int sms = device_sms(-1);
+    if (sms <= 0) return GQA_ERR_CUDA;
+    // With sinks AUTO goes by size. Up to two 256-row items per SM, one-tile CTAs
+    // spread the tiles better (one chunk of 64 tokens, 24 + 8 heads: 25 against 33 us;
+    // six ragged chunks, 288 items: 58 against 66), above that two tiles share K/V
+    // (16 ragged chunks, 1536 items: 241 against 266 us). head_dim 64 has a one-tile
+    // form of its own (8 x 2048 tokens: 275 us, the 32-token form 382).
+    const long long items2 = ((long long)L.max_new_tokens * G + W2Cfg<2>::kRows - 1) / W2Cfg<2>::kRows * K * L.batch;
+    const bool few = sinks && L.kernel == GQA_PREFILL_AUTO && items2 <= 2LL * sms;
+    const bool wide2 = tc && D == 128 && !few && (L.kernel == GQA_PREFILL_AUTO || L.kernel == GQA_PREFILL_TCGEN05_WIDE);
+    const bool wide1 = tc && D == 128 && (few || L.kernel == GQA_PREFILL_TCGEN05_PAIRED);
+    const bool wide64 = tc && D == 64 && sinks && L.kernel == GQA_PREFILL_AUTO;
+    const bool wide = wide1 || wide2 || wide64;
+    const int rows_per_cta = wide2 ? W2Cfg<2>::kRows : wide1 || wide64 ? W2Cfg<1>::kRows : tc ? kTcRows : kPfRows;
     const void* fn = nullptr;
     int smem = 0;
-    if (wide) {
+    if (wide64) {
+        if (c.dtype != GQA_DTYPE_BF16 && c.dtype != GQA_DTYPE_F16) return GQA_ERR_UNSUPPORTED;
+        fn = c.dtype == GQA_DTYPE_BF16 ? reinterpret_cast<const void*>(&prefill_tc2_kernel<__nv_bfloat16, 1, 64, true>)
+                                       : reinterpret_cast<const void*>(&prefill_tc2_kernel<__half, 1, 64, true>);
+        smem = W2Cfg<1, 64>::kSmem;
+    } else if (wide) {
         if (c.dtype != GQA_DTYPE_BF16 && c.dtype != GQA_DTYPE_F16) return GQA_ERR_UNSUPPORTED;
         const bool bf = c.dtype == GQA_DTYPE_BF16;
         fn = wide2 ? (bf ? prefill_tc2_fn<__nv_bfloat16, 2>(sinks) : prefill_tc2_fn<__half, 2>(sinks))
@@ -1667,7 +1688,7 @@ int launch_prefill(const PrefillLaunch& L) {
     int page_perm[2] = {1, 2};
     if (tc && D == 128 && !encode_page_map(&vmap, c, c.v, page_perm))   // V a page per box
         return GQA_ERR_UNSUPPORTED;
-    const int threads = wide2 ? W2Cfg<2>::kThreads : wide1 ? W2Cfg<1>::kThreads : tc ? kTcThreads : kPfWarps * 32;
+    const int threads = wide2 ? W2Cfg<2>::kThreads : wide1 || wide64 ? W2Cfg<1>::kThreads : tc ? kTcThreads : kPfWarps * 32;
     if (ctas_per_sm(fn, threads, smem) < 1) return GQA_ERR_CUDA;
 
     PrefillArgs a;
@@ -1700,7 +1721,7 @@ int launch_prefill(const PrefillLaunch& L) {
     CUtensorMap omap;
     memset(&omap, 0, sizeof(omap));
     a.out_tma = 0;
-    if (wide && L.out_dtype == GQA_DTYPE_F32 && (32 % G == 0 || G % 32 == 0))
+    if (wide && D == 128 && L.out_dtype == GQA_DTYPE_F32 && (32 % G == 0 || G % 32 == 0))
         a.out_tma = encode_out_map(&omap, L.out, L.num_heads, G, (long long)L.max_new_tokens * L.batch) ? 1 : 0;
 
     cudaLaunchAttribute pdl[1];
@@ -1710,10 +1731,14 @@ int launch_prefill(const PrefillLaunch& L) {
     if (wide) {
         // persistent CTAs: as many as fit at once, each walking its items
         const long long items = (long long)a.tiles_per_seq * K * L.batch;
-        const int sms = device_sms(-1);
-        if (items > INT32_MAX || sms <= 0) return GQA_ERR_UNSUPPORTED;
+        if (items > INT32_MAX) return GQA_ERR_UNSUPPORTED;
         const long long fit = (long long)sms * (wide2 ? W2Cfg<2>::kCtasPerSm : W2Cfg<1>::kCtasPerSm);
-        cfg.gridDim = dim3((unsigned)(items < fit ? items : fit));
+        // With sinks, a batch whose sequences leave over a tenth of the tiles empty gets
+        // a CTA per item: the hardware's order evens out what the fixed deal cannot (16
+        // chunks of 300 to 1024 tokens: 241 against 304 us; even prompts lose 8%).
+        const bool ragged = sinks && L.total_new_tokens > 0 &&
+                            (double)L.total_new_tokens < 0.9 * (double)L.max_new_tokens * L.batch;
+        cfg.gridDim = dim3((unsigned)(ragged || items < fit ? items : fit));
     } else {
         cfg.gridDim = dim3((unsigned)a.tiles_per_seq, (unsigned)K, (unsigned)L.batch);
     }

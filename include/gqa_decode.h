@@ -455,12 +455,16 @@ GQA_API int gqa_prefill(const gqa_kv_cache_t *cache, const void *q, int32_t q_dt
  * never read (their table entries may hold anything). S = 0, or W = 0 (full
  * attention), is gqa_prefill. sink_tokens < 0 is GQA_ERR_INVALID; an S beyond the
  * context makes every position up to p visible.
+ *  total_new_tokens  rows of q (q_start[batch]) as the host knows them, 0 where it does
+ *                    not: it picks the schedule of ragged batches and changes no result.
+ *  kernel            GQA_PREFILL_AUTO goes by size (one- or two-tile CTAs at head_dim
+ *                    128, a 64-token-chunk form at head_dim 64).
  */
 GQA_API int gqa_prefill_sinks(const gqa_kv_cache_t *cache, const void *q, int32_t q_dtype, int32_t num_heads,
                 const int32_t *q_start, int32_t max_new_tokens, const int32_t *block_tables,
                 int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t batch, float scale,
-                int32_t sliding_window, int32_t sink_tokens, void *out, int32_t out_dtype, int32_t kernel,
-                int32_t *err_flag, void *stream);
+                int32_t sliding_window, int32_t sink_tokens, int64_t total_new_tokens, void *out,
+                int32_t out_dtype, int32_t kernel, int32_t *err_flag, void *stream);
 
 /*
  * Bytes of device workspace gqa_decode needs for this shape (tokens_per_seq as

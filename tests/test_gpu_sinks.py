@@ -142,6 +142,33 @@ def test_captured_decode_replays_on_new_inputs(gq):
         case.context_lens -= 17                          # the graph reads the lengths on the device
 
 
+def test_graphs_captured_on_one_stream_do_not_share_a_workspace(gq):
+    """Two graphs without a workspace of the caller's, the second replayed first and then
+    both at once on streams of their own."""
+    side = torch.cuda.Stream()
+    made = []
+    for seed, lens in ((51, [900, 3000]), (52, [2500, 40])):
+        case = gi.make_case(2, 16, 4, 128, lens, "bf16", seed=seed, device="cuda")
+        cache, out = gq.cache_from_case(case), torch.full(case.q.shape, float("nan"), device="cuda")
+        gq.load()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            gq.gqa_decode(cache, case.q, case.block_table, case.context_lens, case.scale, out=out, window=600, sinks=4)
+        made.append((graph, case, cache, out, attend_case(case, 600, 4)))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    made[1][0].replay()
+    torch.cuda.synchronize()
+    assert max_abs_err(made[1][3], made[1][4]) <= TOL
+    for _ in range(20):
+        for s, (graph, *_rest) in zip(streams, made):
+            with torch.cuda.stream(s):
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, _, _, out, ref in made:
+        assert max_abs_err(out, ref) <= TOL
+
+
 def test_noalloc_gives_the_same_bits(gq):
     case = gi.make_case(len(LENS), 32, 8, 128, LENS, "bf16", seed=38, device="cuda")
     a = _decode(gq, case, window=40, sinks=4)
@@ -205,8 +232,23 @@ def test_prefill_group_sizes_and_types(gq, H, K, d, dtype, kernel):
     assert max_abs_err(_prefill(gq, case, q, start, news, window=50, sinks=6, kernel=kernel), ref) <= TOL
 
 
-@pytest.mark.parametrize("kernel", [3, 4])
-def test_prefill_many_items_per_cta(gq, kernel):
+@pytest.mark.parametrize("window,sinks", [(1, 1), (16, 4), (37, 20), (37, 100), (200, 64), (200, 65), (64, 5000)])
+@pytest.mark.parametrize("H,K,dtype", [(12, 4, "f16"), (8, 2, "bf16")])
+def test_prefill_of_64_element_heads(gq, H, K, dtype, window, sinks):
+    news = [3, 64, 129, 300, 0, 1]
+    prior = [10, 0, 77, 456, 20, 391]
+    lens = [n + p for n, p in zip(news, prior)]
+    case, q, start = _prefill_case(lens, news, H, K, 64, dtype, seed=47)
+    ref = _prefill_reference(case, q, news, window, sinks)
+    table = _poisoned(case, window, sinks, news)
+    for out_dtype in (torch.float32, gi.DTYPES[dtype]):
+        out = _prefill(gq, case, q, start, news, table, window=window, sinks=sinks, out_dtype=out_dtype)
+        ulp = 0.0 if out_dtype == torch.float32 else torch.finfo(out_dtype).eps / 2
+        assert np.all(np.abs(out.double().cpu().numpy() - ref) <= TOL + ulp * np.abs(ref))
+
+
+@pytest.mark.parametrize("kernel,d", [(3, 128), (4, 128), (0, 64)])
+def test_prefill_many_items_per_cta(gq, kernel, d):
     """More (tile, kv-head, sequence) items than CTAs: the walk over the sinks and
     the window starts anew for every item a CTA takes."""
     rng = np.random.default_rng(43)
@@ -214,16 +256,16 @@ def test_prefill_many_items_per_cta(gq, kernel):
     news[3] = 120
     prior = rng.integers(0, 150, size=40).tolist()
     lens = [n + p for n, p in zip(news, prior)]
-    case, q, start = _prefill_case(lens, news, 32, 8, 128, "bf16", seed=44)
+    case, q, start = _prefill_case(lens, news, 32, 8, d, "bf16", seed=44)
     ref = _prefill_reference(case, q, news, 33, 17)
     assert max_abs_err(_prefill(gq, case, q, start, news, window=33, sinks=17, kernel=kernel), ref) <= TOL
 
 
-@pytest.mark.parametrize("kernel", [0, 1, 2, 4])
-def test_prefill_hidden_tokens_may_hold_anything(gq, kernel):
+@pytest.mark.parametrize("kernel,d", [(0, 128), (1, 128), (2, 128), (4, 128), (0, 64), (1, 64)])
+def test_prefill_hidden_tokens_may_hold_anything(gq, kernel, d):
     W, S = 21, 5
     news, lens = [9, 16], [120, 333]
-    case, q, start = _prefill_case(lens, news, 8, 2, 128, "bf16", seed=45)
+    case, q, start = _prefill_case(lens, news, 8, 2, d, "bf16", seed=45)
     ref = _prefill_reference(case, q, news, W, S)
     for b, (L, n) in enumerate(zip(lens, news)):
         first = L - n + 1 - W

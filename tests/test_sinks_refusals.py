@@ -28,7 +28,7 @@ def test_negative_sinks_are_refused(lib, sinks, batch, expect):
     assert lib.gqa_decode_sinks(ctypes.byref(d), 0x30000, 2, 32, 0x40000, 8, 0x50000, batch, 0.1, 0x60000, 0, 0x70000,
                                 1 << 20, ctypes.byref(opts), sinks, None, None) == expect
     assert lib.gqa_prefill_sinks(ctypes.byref(d), 0x30000, 2, 32, 0x40000, 16, 0x50000, 8, 0x60000, batch, 0.1, 32,
-                                 sinks, 0x70000, 0, 0, None, None) == expect
+                                 sinks, 0, 0x70000, 0, 0, None, None) == expect
 
 
 def test_the_calls_keep_the_checks_of_the_plain_ones(lib):
@@ -37,4 +37,6 @@ def test_the_calls_keep_the_checks_of_the_plain_ones(lib):
     assert lib.gqa_decode_sinks(ctypes.byref(d), 0x30000, 2, 32, 0x40000, 8, 0x50000, 4, 0.1, 0x60000, 0, 0x70000,
                                 1 << 20, ctypes.byref(opts), 4, None, None) == INVALID
     assert lib.gqa_prefill_sinks(ctypes.byref(d), 0x30000, 2, 32, 0x40000, 16, 0x50000, 8, 0x60000, 4, 0.1, -1, 4,
-                                 0x70000, 0, 0, None, None) == INVALID
+                                 0, 0x70000, 0, 0, None, None) == INVALID
+    assert lib.gqa_prefill_sinks(ctypes.byref(d), 0x30000, 2, 32, 0x40000, 16, 0x50000, 8, 0x60000, 4, 0.1, 32, 4,
+                                 -1, 0x70000, 0, 0, None, None) == INVALID
