@@ -189,12 +189,14 @@ def _prefill_case(lens, news, H, K, d, dtype, seed):
     return case, q, start
 
 
-def _prefill_reference(case, q, news, window, sinks):
+def _prefill_reference(case, q, news, window, sinks, magnitude=False):
+    """Output rows, or with ``magnitude`` the same weights over |v|."""
     qh = q.double().cpu().numpy()
     out, row = [], 0
     for b, n in enumerate(news):
         if n:
-            out.append(attend(qh[row:row + n], cached_rows(case, "k", b), cached_rows(case, "v", b), case.scale, window,
+            v = cached_rows(case, "v", b)
+            out.append(attend(qh[row:row + n], cached_rows(case, "k", b), np.abs(v) if magnitude else v, case.scale, window,
                               sinks))
         row += n
     return np.concatenate(out)
@@ -241,10 +243,13 @@ def test_prefill_of_64_element_heads(gq, H, K, dtype, window, sinks):
     case, q, start = _prefill_case(lens, news, H, K, 64, dtype, seed=47)
     ref = _prefill_reference(case, q, news, window, sinks)
     table = _poisoned(case, window, sinks, news)
+    # a 16-bit output takes the weights rounded to the cache's type, each off by half a
+    # step of itself: the output by half a step of sum w |v| at most, and of itself
+    spread = _prefill_reference(case, q, news, window, sinks, magnitude=True)
     for out_dtype in (torch.float32, gi.DTYPES[dtype]):
         out = _prefill(gq, case, q, start, news, table, window=window, sinks=sinks, out_dtype=out_dtype)
-        ulp = 0.0 if out_dtype == torch.float32 else torch.finfo(out_dtype).eps / 2
-        assert np.all(np.abs(out.double().cpu().numpy() - ref) <= TOL + ulp * np.abs(ref))
+        step = 0.0 if out_dtype == torch.float32 else torch.finfo(out_dtype).eps / 2
+        assert np.all(np.abs(out.double().cpu().numpy() - ref) <= TOL + step * (np.abs(ref) + spread))
 
 
 @pytest.mark.parametrize("kernel,d", [(3, 128), (4, 128), (0, 64)])
@@ -274,6 +279,32 @@ def test_prefill_hidden_tokens_may_hold_anything(gq, kernel, d):
             case.k_cache[p, :, t % 16] = float("nan")
             case.v_cache[p, :, t % 16] = float("inf")
     assert max_abs_err(_prefill(gq, case, q, start, news, window=W, sinks=S, kernel=kernel), ref) <= TOL
+
+
+@pytest.mark.parametrize("dtype,out_dtype", [("bf16", torch.bfloat16), ("f16", torch.float16), ("f16", torch.bfloat16)])
+@pytest.mark.parametrize("kernel", [0, 3, 4, 1])
+def test_prefill_half_outputs(gq, dtype, out_dtype, kernel):
+    """Weights rounded once to the cache's type (see the 64-element heads above)."""
+    news, prior = [70, 1, 200, 33], [100, 300, 0, 555]
+    lens = [n + p for n, p in zip(news, prior)]
+    case, q, start = _prefill_case(lens, news, 16, 4, 128, dtype, seed=48)
+    ref = _prefill_reference(case, q, news, 90, 7)
+    spread = _prefill_reference(case, q, news, 90, 7, magnitude=True)
+    out = _prefill(gq, case, q, start, news, window=90, sinks=7, out_dtype=out_dtype, kernel=kernel)
+    allowed = TOL + torch.finfo(out_dtype).eps / 2 * np.abs(ref) + torch.finfo(gi.DTYPES[dtype]).eps / 2 * spread
+    assert np.all(np.abs(out.double().cpu().numpy() - ref) <= allowed)
+
+
+@pytest.mark.parametrize("dtype", ["i8", "fp8", "i4", "i4kc"])
+@pytest.mark.parametrize("T", [1, 3])
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float16])
+def test_decode_half_outputs_of_code_caches(gq, dtype, T, out_dtype):
+    """The fp32 output's bound and half a step of the output's own type."""
+    lens = [1, 16, 40, 257, 0, 600]
+    case = gi.make_case(len(lens), 32, 4, 128, lens, dtype, seed=39, device="cuda", queries=T)
+    ref = attend_case(case, 50, 6)
+    out = _decode(gq, case, window=50, sinks=6, out_dtype=out_dtype).double().cpu().numpy()
+    assert np.all(np.abs(out - ref) <= TOL + torch.finfo(out_dtype).eps / 2 * np.abs(ref))
 
 
 def test_prefill_last_token_is_the_decode(gq):
