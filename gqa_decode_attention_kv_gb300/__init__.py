@@ -251,6 +251,15 @@ def _stream_ptr(stream) -> Optional[int]:
     return torch.cuda.current_stream().cuda_stream
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """A result of a call on ``stream``, allocated there: memory another stream just
+    freed may still be in use on that one."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _dev(t: Optional[torch.Tensor], name: str, index: bool = False, optional: bool = False):
     """Device pointer of a tensor the library reads or writes as a packed array.
 
@@ -420,7 +429,7 @@ def gqa_decode(cache: PagedKVCache, q: torch.Tensor, block_tables: torch.Tensor,
     _on_cache_device(cache, q=q, block_tables=block_tables, context_lens=context_lens, out=out,
                      workspace=workspace, err=err)
     if out is None:
-        out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
+        out = _empty(q.shape, out_dtype, q.device, stream)
     if workspace is None:
         workspace = workspace_for(B, H, cache.num_kv_heads, d, q.device, T, stream)
     op, wp = _dev(out, "out"), _dev(workspace, "workspace")
@@ -456,7 +465,7 @@ def gqa_decode_noalloc(cache: PagedKVCache, q: torch.Tensor, block_tables: torch
     _check_out(q, out)
     _on_cache_device(cache, q=q, block_tables=block_tables, context_lens=context_lens, out=out, err=err)
     if out is None:
-        out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
+        out = _empty(q.shape, out_dtype, q.device, stream)
     op = _dev(out, "out")
     opts = DecodeOpts(T, window, kernel, 0, 0, 0, None, None)
     desc = cache.desc()
@@ -579,9 +588,9 @@ def _same_or_apart(out: torch.Tensor, src: torch.Tensor, name: str):
         raise ValueError(f"{name} overlaps its input without being it")
 
 
-def _q_out(q: torch.Tensor, q_out: Optional[torch.Tensor], name: str) -> torch.Tensor:
+def _q_out(q: torch.Tensor, q_out: Optional[torch.Tensor], name: str, stream) -> torch.Tensor:
     if q_out is None:
-        return torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        return _empty(q.shape, q.dtype, q.device, stream)
     if tuple(q_out.shape) != tuple(q.shape) or q_out.dtype != q.dtype:
         raise ValueError(f"{name} must have the input's shape and dtype, not {tuple(q_out.shape)} {q_out.dtype}")
     _dev(q_out, name)
@@ -618,7 +627,7 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: Optional[torch.Ten
     ep = _dev(err, "err", True, True)
     _on_one_device(q=q, k=k, positions=positions, rope=rope, q_weight=q_weight, k_weight=k_weight, q_out=q_out,
                    k_out=k_out, err=err)
-    q_out, k_out = _q_out(q, q_out, "q_out"), _q_out(k, k_out, "k_out")
+    q_out, k_out = _q_out(q, q_out, "q_out", stream), _q_out(k, k_out, "k_out", stream)
     st = load().gqa_qk_norm_rope(ctypes.byref(desc), qp, qs, q_out.data_ptr(), int(q.shape[-2]), kp, ks,
                                  k_out.data_ptr(), int(k.shape[-2]), int(q.shape[-1]), DTYPE_CODE[q.dtype], tokens, pp,
                                  ep, _stream_ptr(stream))
@@ -667,7 +676,7 @@ def qk_norm_rope_append(cache: PagedKVCache, q: torch.Tensor, k: torch.Tensor, v
     _on_cache_device(cache, q=q, k=k, v=v, block_tables=block_tables, positions=positions, rope=rope,
                      q_weight=q_weight, k_weight=k_weight, token_start=token_start, rope_positions=rope_positions,
                      q_out=q_out, err=err)
-    q_out = _q_out(q, q_out, "q_out")
+    q_out = _q_out(q, q_out, "q_out", stream)
     if tokens == 0 or T == 0:
         return q_out
     cdesc = cache.desc()
@@ -773,9 +782,7 @@ def kv_pages_fork(ref_counts: torch.Tensor, block_tables: torch.Tensor, context_
                 workspace=workspace)
     if copies is None:
         dev = ref_counts.device
-        copies = PageCopies(torch.empty((n, 2), dtype=torch.int32, device=dev),
-                            torch.empty(1, dtype=torch.int32, device=dev),
-                            torch.empty((n, 2), dtype=torch.int32, device=dev))
+        copies = PageCopies(*(_empty(shape, torch.int32, dev, stream) for shape in ((n, 2), (1,), (n, 2))))
     elif copies.rows is None or copies.pairs.shape[0] < n or copies.rows.shape[0] != n:
         raise ValueError(f"copies must have room for {n} pairs and exactly {n} rows")
     else:
@@ -842,8 +849,7 @@ def kv_pages_compact(ref_counts: torch.Tensor, block_tables: torch.Tensor, max_c
         n = nb // 2 if max_copies is None else int(max_copies)
         if n < 0:
             raise ValueError(f"max_copies must not be negative: {n}")
-        copies = PageCopies(torch.empty((n, 2), dtype=torch.int32, device=ref_counts.device),
-                            torch.empty(2, dtype=torch.int32, device=ref_counts.device))
+        copies = PageCopies(*(_empty(shape, torch.int32, ref_counts.device, stream) for shape in ((n, 2), (2,))))
     else:
         _check_copies(copies, ref_counts.device)
         n = int(copies.pairs.shape[0]) if max_copies is None else int(max_copies)
@@ -902,7 +908,7 @@ def gqa_prefill(cache: PagedKVCache, q: torch.Tensor, q_start: torch.Tensor, max
     _on_cache_device(cache, q=q, q_start=q_start, block_tables=block_tables,
                      context_lens=context_lens, out=out, err=err)
     if out is None:
-        out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
+        out = _empty(q.shape, out_dtype, q.device, stream)
     op = _dev(out, "out")
     desc = cache.desc()
     st = load().gqa_prefill_sinks(ctypes.byref(desc), args[0], DTYPE_CODE[q.dtype], int(q.shape[1]),

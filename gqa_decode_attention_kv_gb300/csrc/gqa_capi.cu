@@ -307,7 +307,7 @@ const char* gqa_status_string(int status) {
     }
 }
 
-int gqa_version(void) { return 300; }
+int gqa_version(void) { return 400; }
 
 int64_t gqa_kv_pool_elements(int64_t num_blocks, int32_t num_kv_heads, int32_t head_dim) {
     if (num_blocks < 0 || num_kv_heads < 0 || head_dim < 0) return -1;

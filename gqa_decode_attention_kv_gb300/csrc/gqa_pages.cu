@@ -329,7 +329,8 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const PageArgs 
             const int s = a.src[i], d = a.dst[i];
             // a parent is no child of this call, a child has one parent and is empty
             const bool rows_ok = s >= 0 && s < a.table_rows && d >= 0 && d < a.table_rows;
-            if (!rows_ok || claim[d] != i || claim[s] != INT_MAX || a.lens[d] != 0) {
+            if (!rows_ok || claim[d] != i || claim[s] != INT_MAX || a.lens[d] != 0 ||
+                a.tables[(long long)d * a.max_blocks] >= 0) {
                 flag_error(a.err, GQA_DEVERR_ROW);
             } else {
                 const int L = a.lens[s];

@@ -346,7 +346,7 @@ GQA_API int gqa_kv_pages_reserve(int32_t *ref_counts, int64_t num_blocks, int32_
  * last page (L % 16 != 0) is copied to a fresh one, so each sequence may append. One
  * parent may have many children. Fork i is refused, and its row left alone, with
  * GQA_DEVERR_ROW if a row index is outside the table, the destination is named by an
- * earlier fork or is not empty (context_lens != 0; its entries must be empty too: free
+ * earlier fork or is not empty (context_lens != 0, or its first entry holds a page: free
  * it first), or the parent is some fork's destination;
  * GQA_DEVERR_NO_PAGES if no page is left for it; GQA_DEVERR_BLOCK_INDEX if the parent's
  * last entry is no page; GQA_DEVERR_CONTEXT_LEN if the parent's length is out of range.

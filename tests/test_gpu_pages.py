@@ -91,7 +91,7 @@ class Pool:
         for i, (s, d) in enumerate(zip(src, dst)):
             rows.append((-1, -1))
             if not (0 <= s < len(self.table) and 0 <= d < len(self.table)) or claimed[d] != i or s in claimed \
-                    or self.lens[d] != 0:
+                    or self.lens[d] != 0 or self.table[d][0] >= 0:
                 flag |= 16
                 continue
             L = self.lens[s]
@@ -279,6 +279,18 @@ def test_fork_refusals_leave_their_rows_alone(gq):
     same(pool, refs, tab, lens)
     assert c.pairs[:int(c.count[0])].tolist() == [list(p) for p in pairs]
     assert c.rows.tolist() == [list(r) for r in rows]
+
+
+def test_fork_into_an_empty_row_with_reserved_pages_is_refused(gq):
+    """Its pages would be nobody's afterwards."""
+    pool = Pool([1, 0, 0], [[0, -1], [-1, -1]], [5, 0])
+    refs, table, lens, err = on_gpu(pool)
+    pool.reserve([1, 1])
+    gq.kv_pages_reserve(refs, table, lens, 1)
+    flag, _, rows = pool.fork([0], [1])
+    c = gq.kv_pages_fork(refs, table, lens, cuda([0]), cuda([1]), err=err)
+    assert int(err.item()) == flag == gq.GQA_DEVERR_ROW and c.rows.tolist() == [[-1, -1]] and int(c.count[0]) == 0
+    same(pool, refs, table, lens)
 
 
 def test_fork_without_pages(gq):
