@@ -120,16 +120,23 @@ __device__ __forceinline__ int warp_before(int x, int lane) {     // exclusive p
     return incl - x;
 }
 
+// The first round's masks of find_free: loaded before anything else in the kernel, so
+// that their latency goes by with the rows'.
+__device__ __forceinline__ uint32_t first_held(const PageArgs& a) {
+    const int base = (threadIdx.x >> 5) * kChunk;
+    return base < a.num_blocks ? held_mask(a.refs, base, a.num_blocks, threadIdx.x & 31) : 0u;
+}
+
 // The `want` lowest free pages, in order, into list; returns how many there are
-// (CTA-uniform). Rounds of 32 chunks until enough are found.
-__device__ int find_free(const PageArgs& a, int want, int32_t* list, int* tmp) {
+// (CTA-uniform). Rounds of 32 chunks until enough are found; `held` is first_held().
+__device__ int find_free(const PageArgs& a, uint32_t held, int want, int32_t* list, int* tmp) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int found = 0;
     for (int round = 0; round < a.num_blocks && found < want; round += kPlanWarps * kChunk) {
         const int base = round + warp * kChunk;
         uint32_t free_m = 0;
         if (base < a.num_blocks) {
-            free_m = ~held_mask(a.refs, base, a.num_blocks, lane);
+            free_m = ~(round == 0 ? held : held_mask(a.refs, base, a.num_blocks, lane));
             // pages past the pool are none
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
@@ -199,6 +206,7 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_plan_kernel(const PageAr
     grid_dependency_wait();
     launch_dependents();
     const int lane = threadIdx.x & 31;
+    const uint32_t held = first_held(a);
     int carry = 0;
     for (int base = 0; base < a.n; base += kPlanThreads) {
         const int b = base + threadIdx.x;
@@ -224,7 +232,7 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_plan_kernel(const PageAr
         carry += total;
     }
     if (threadIdx.x == 0) a.ws_rows[a.n] = carry;
-    const int found = find_free(a, carry, a.ws_list, tmp);
+    const int found = find_free(a, held, carry, a.ws_list, tmp);
     if (threadIdx.x == 0) a.ws_hdr[0] = found;
     if constexpr (kAll) {
         for (int b = threadIdx.x; b < a.n; b += kPlanThreads) {
@@ -314,6 +322,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const PageArgs 
     __shared__ int tmp[kPlanWarps + 1];
     grid_dependency_wait();
     launch_dependents();
+    const uint32_t held = first_held(a);
     for (int r = threadIdx.x; r < a.table_rows; r += kPlanThreads) claim[r] = INT_MAX;
     __syncthreads();
     for (int i = threadIdx.x; i < a.n; i += kPlanThreads) {
@@ -350,7 +359,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const PageArgs 
         if (i < a.n) a.ws_rows[i] = kind == 0 ? rank : kind;
         carry += total;
     }
-    const int found = find_free(a, carry, a.ws_list, tmp);
+    const int found = find_free(a, held, carry, a.ws_list, tmp);
     for (int i = threadIdx.x; i < a.n; i += kPlanThreads) {
         int kind = a.ws_rows[i];
         if (kind >= found) {                 // (found <= the number of ranks)
