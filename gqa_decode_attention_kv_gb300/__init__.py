@@ -577,24 +577,26 @@ def _norm_rope_desc(q, rope, q_weight, k_weight, eps, interleaved) -> NormRopeDe
     return NormRopeDesc(pointers[0], pointers[1], table, code, eps, rows, rotary, 1 if interleaved else 0, 0)
 
 
-def _same_or_apart(out: torch.Tensor, src: torch.Tensor, name: str):
-    """out may be src itself (dense) or memory that src does not touch."""
-    if out.untyped_storage().data_ptr() != src.untyped_storage().data_ptr() or not out.numel():
+def _same_or_apart(out: torch.Tensor, src: torch.Tensor, name: str, same: bool = True):
+    """out may be memory that src does not touch or, with ``same``, src itself (dense)."""
+    if out.untyped_storage().data_ptr() != src.untyped_storage().data_ptr() or not out.numel() or not src.numel():
         return
-    if out.data_ptr() == src.data_ptr() and src.is_contiguous():
+    if same and out.data_ptr() == src.data_ptr() and src.is_contiguous():
         return
     end = lambda t: t.data_ptr() + (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * t.element_size()  # noqa: E731
     if out.data_ptr() < end(src) and src.data_ptr() < end(out):
-        raise ValueError(f"{name} overlaps its input without being it")
+        raise ValueError(f"{name} overlaps an input without being its own")
 
 
-def _q_out(q: torch.Tensor, q_out: Optional[torch.Tensor], name: str, stream) -> torch.Tensor:
+def _q_out(q: torch.Tensor, q_out: Optional[torch.Tensor], name: str, stream, *others: torch.Tensor) -> torch.Tensor:
     if q_out is None:
         return _empty(q.shape, q.dtype, q.device, stream)
     if tuple(q_out.shape) != tuple(q.shape) or q_out.dtype != q.dtype:
         raise ValueError(f"{name} must have the input's shape and dtype, not {tuple(q_out.shape)} {q_out.dtype}")
     _dev(q_out, name)
     _same_or_apart(q_out, q, name)
+    for t in others:
+        _same_or_apart(q_out, t, name, False)
     return q_out
 
 
@@ -627,7 +629,8 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: Optional[torch.Ten
     ep = _dev(err, "err", True, True)
     _on_one_device(q=q, k=k, positions=positions, rope=rope, q_weight=q_weight, k_weight=k_weight, q_out=q_out,
                    k_out=k_out, err=err)
-    q_out, k_out = _q_out(q, q_out, "q_out", stream), _q_out(k, k_out, "k_out", stream)
+    q_out, k_out = _q_out(q, q_out, "q_out", stream, k), _q_out(k, k_out, "k_out", stream, q)
+    _same_or_apart(k_out, q_out, "k_out", False)
     st = load().gqa_qk_norm_rope(ctypes.byref(desc), qp, qs, q_out.data_ptr(), int(q.shape[-2]), kp, ks,
                                  k_out.data_ptr(), int(k.shape[-2]), int(q.shape[-1]), DTYPE_CODE[q.dtype], tokens, pp,
                                  ep, _stream_ptr(stream))
@@ -676,7 +679,7 @@ def qk_norm_rope_append(cache: PagedKVCache, q: torch.Tensor, k: torch.Tensor, v
     _on_cache_device(cache, q=q, k=k, v=v, block_tables=block_tables, positions=positions, rope=rope,
                      q_weight=q_weight, k_weight=k_weight, token_start=token_start, rope_positions=rope_positions,
                      q_out=q_out, err=err)
-    q_out = _q_out(q, q_out, "q_out", stream)
+    q_out = _q_out(q, q_out, "q_out", stream, k, v)
     if tokens == 0 or T == 0:
         return q_out
     cdesc = cache.desc()

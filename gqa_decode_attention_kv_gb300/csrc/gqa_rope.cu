@@ -275,7 +275,8 @@ __device__ __forceinline__ void rotate(float& a, float& b, float c, float s) {
 // a row, q = RN(x y) and the exact remainder x - q s, RN(q + (x - q s) y) is RN(x / s)
 // (Markstein's theorem; s has 11 significant bits, so its mantissa is not all ones,
 // and no step leaves fp32's range where the code is not zero), at three instructions
-// instead of a division. A row with an infinity divides.
+// instead of a division; amax / qmax goes the same way (an infinite amax ends at 65504
+// as its quotient would). A row with an infinity divides.
 template <int kOut, int kLanes>
 __device__ __forceinline__ void quantise_store(const float (&x0)[8], const float (&x1)[8], bool live, uint8_t* row,
                                                int c0, int c1, __half* scale, bool first) {
@@ -285,10 +286,12 @@ __device__ __forceinline__ void quantise_store(const float (&x0)[8], const float
     for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fmaxf(fabsf(x0[e]), fabsf(x1[e])));
 #pragma unroll
     for (int o = kLanes / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
-    const __half sh = __float2half_rn(fminf(__fdiv_rn(amax, kQmax), 65504.0f));
+    constexpr float kInv = 1.0f / kQmax;     // RN(1 / qmax), folded by the compiler
+    const float s0 = amax * kInv;
+    const __half sh = __float2half_rn(fminf(fmaf(fmaf(-s0, kQmax, amax), kInv, s0), 65504.0f));
     const float sf = __half2float(sh);
     if (!live) return;
-    const float y = __fdiv_rn(1.f, sf);
+    const float y = __frcp_rn(sf);
     const bool finite = amax < INFINITY;
     auto quotient = [&](float x) {
         const float q = x * y;

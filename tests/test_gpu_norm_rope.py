@@ -195,6 +195,33 @@ def test_append_to_coded_caches(gq, cache_dtype, dtype, d):
     assert bool(((deq - ref).abs() <= allowed).all())
 
 
+@pytest.mark.parametrize("cache_dtype", ["i8", "fp8", "i4"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_codes_and_scales_are_the_appends_at_every_magnitude(gq, cache_dtype, d):
+    """Rows from 2^-140 to 2^120, ties (multiples of half a code), infinities and NaN: the
+    reciprocal with its correction gives the append's divisions bit for bit."""
+    K, n = 4, 1024
+    g = torch.Generator().manual_seed(81)
+    x = torch.randn((n, K, d), generator=g)
+    x *= torch.exp2(torch.randint(-140, 120, (n, K, 1), generator=g).float())
+    x[::7] = torch.randint(-254, 255, (len(range(0, n, 7)), K, d), generator=g).float() / 2   # halves of an int8 code
+    x[::7, :, 0] = 127.0
+    x[3, 0, 5], x[4, 1, 6], x[5, 2, 7] = float("inf"), float("-inf"), float("nan")
+    x[6] = 0
+    x = x.cuda()
+    kind = "int4" if cache_dtype == "i4" else gi.DTYPES[cache_dtype]
+    a, b = (gq.PagedKVCache.allocate(n // 16, K, d, kind) for _ in range(2))
+    table = torch.arange(n // 16, dtype=torch.int32, device="cuda").reshape(1, -1)
+    pos, start = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    q = torch.zeros((n, K, d), device="cuda")
+    gq.qk_norm_rope_append(a, q, x, x, table, pos, token_start=start, max_new_tokens=n)   # no norm, no rotation
+    gq.kv_append_varlen(b, x, x, start, n, table, pos)
+    torch.cuda.synchronize()
+    for name in ("k", "v"):
+        assert torch.equal(getattr(a, name + "_scale").view(torch.int16), getattr(b, name + "_scale").view(torch.int16))
+        assert torch.equal(getattr(a, name).view(torch.uint8), getattr(b, name).view(torch.uint8)), name
+
+
 @pytest.mark.parametrize("T", [1, 3])
 def test_uniform_tokens_match_the_ragged_call(gq, T):
     B, H, K, d = 5, 8, 2, 128

@@ -126,3 +126,6 @@ def test_binding_checks_the_description():
         base = torch.zeros(5, 4, 64)
         gq._same_or_apart(base[:4], base[1:], "q_out")
     gq._same_or_apart(q, q, "q_out")
+    with pytest.raises(ValueError, match="overlaps"):
+        gq._same_or_apart(q, q, "q_out", False)             # another input's memory
+    gq._same_or_apart(base[:2], base[2:], "q_out", False)
