@@ -13,12 +13,14 @@
 //
 // Bound: memory. Per token (H + 2K) d elements are read and written and one
 // table row is read; the arithmetic is ~10 flops an element. Layout: a lane
-// holds two 8-element chunks of a row, (c, c + rotary_dim/16) for split pairs and
-// (2c, 2c + 1) for interleaved ones, so both elements of every pair are in one
-// lane, the eight table pairs a lane needs are 64 contiguous bytes, and the norm
-// takes log2(d/16) shuffles; a warp step covers 512/d rows. A warp serves one part
-// of a token (kRopeSteps query steps, or kKvSteps steps of K and of V) for a run of
-// consecutive tokens, so the sequence is looked up once a run. The rows, the table
+// holds two 8-element chunks of a row, lane l's first ones lying side by side over the
+// lanes and its second ones too (adjacent chunks in one lane leave half of every
+// sector to another instruction: 94 against 70 us where 16384 tokens are only moved).
+// For split pairs the second chunk holds the first one's partners, so both elements of
+// every pair are in one lane; the norm takes log2(d/16) shuffles; a warp step covers
+// 512/d rows. A warp serves one part of a token (kRopeSteps query steps, or kKvSteps
+// steps of K and of V) for a run of consecutive tokens, so the sequence is looked up
+// once a run. The rows, the table
 // row and the page entry of the next tokens are in flight while one is worked on:
 // each lane copies the row pieces that it will read itself into a ring of stages
 // with cp.async (the table row and the page entry once for the warp), which needs no
@@ -37,12 +39,14 @@ namespace {
 
 constexpr int kRopeWarps = 4;     // warps per CTA
 constexpr int kRopeSteps = 4;     // query row steps one warp holds
-constexpr int kKvSteps = 2;       // K steps (and as many V steps) one warp holds
 constexpr int kMost = 4;          // steps a stage holds
-static_assert(kRopeSteps <= kMost && 2 * kKvSteps <= kMost, "a stage holds a part");
 
 // Where K (and V) rows go.
 enum KvOut : int { kOutDense = 0, kOutCache = 1, kOutI8 = 2, kOutFp8 = 3, kOutI4 = 4 };
+
+// K steps (and as many V steps) one warp holds
+constexpr int kv_steps(int out) { return out > kOutCache ? 1 : 2; }
+static_assert(kRopeSteps <= kMost && 2 * kv_steps(0) <= kMost, "a stage holds a part");
 
 struct RopeArgs {
     const void* q;
@@ -76,9 +80,9 @@ struct RopeArgs {
 
 // Stages of a warp's ring, and their layout: the rows of kMost steps in 16-byte
 // slots of 32 lanes, then the table row (64 bytes a lane of a row), then the page
-// entry. Two stages, so that four or five CTAs share an SM: the kernel waits on its own
-// instruction latencies more than on memory (three stages and three CTAs: 81 us where
-// this takes 67).
+// entry. Two stages, so that four CTAs share an SM: the kernel waits on its own
+// instruction latencies more than on memory (in one wave of 16384 tokens three stages and
+// three CTAs took 81 us, these 67).
 template <typename T>
 struct RopeCfg {
     static constexpr int kPieces = sizeof(T) / 2;                 // 16-byte pieces per chunk
@@ -89,16 +93,20 @@ struct RopeCfg {
     static constexpr int kSmem = kRopeWarps * kStages * kStage;
 };
 
-// Rows a lane works on at a time, and CTAs per SM the registers are cut for. Two rows
-// overlap their shuffles and roots but need 128 registers (4 CTAs); rows that are
-// quantised one by one fit 5. Measured, 16384 tokens of 32 + 8 bf16 heads, d = 128, one
-// row at 5 / two at 4 / two at 5 CTAs: 69.3 / 67.3 / 70 us; 13.7k ragged tokens of
-// 24 + 8 heads, d = 64, onto an FP8 cache: 43 / 48 / 65 us.
+// Rows a lane works on at a time, CTAs per SM the registers are cut for, and K (and V)
+// steps of a warp. Two rows overlap their shuffles and roots and need 128 registers (4
+// CTAs); quantised rows go one by one, their compensated arithmetic taking the registers.
+// Measured, 16384 tokens of 32 + 8 bf16 heads, d = 128, one row at 5 / two at 4 / two at
+// 5 CTAs: 69.3 / 67.3 / 70 us; 13.7k ragged tokens of 24 + 8 heads, d = 64, onto an FP8
+// cache, one row at 5 / 4 / 3 CTAs, two at 4: 40.5 / 33.5 / 35.1 / 44.8 us. A quantised
+// step of K and V takes a warp about as long as four query steps, so its warp holds one:
+// two made it the last to finish (16384 tokens, d = 128, FP8: 110 against 81 us).
 template <typename T, int kOut>
 struct RopeShape {
     static constexpr bool kTwo = sizeof(T) == 2 && kOut <= kOutCache;
     static constexpr int kPair = kTwo ? 2 : 1;
-    static constexpr int kCtas = sizeof(T) == 4 ? 3 : kTwo ? 4 : 5;
+    static constexpr int kCtas = sizeof(T) == 4 ? 3 : 4;
+    static constexpr int kKvSteps = kv_steps(kOut);
 };
 
 template <int kDst, int kSrc>
@@ -337,6 +345,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, RopeShape<T, kOut>::kCtas) no
     constexpr int kRows = 32 / kLanes;             // rows per warp step
     constexpr bool kCached = kOut != kOutDense;
     constexpr bool kCoded = kOut > kOutCache;      // rows are quantised
+    constexpr int kKvSteps = RopeShape<T, kOut>::kKvSteps;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     grid_dependency_wait();
     launch_dependents();
@@ -349,12 +358,14 @@ __global__ void __launch_bounds__(kRopeWarps * 32, RopeShape<T, kOut>::kCtas) no
     const int n = a.run + (r < a.longer ? 1 : 0);
     const int li = lane % kLanes, grp = lane / kLanes;
     const int half = a.rotary_dim / 16;            // lanes of a row that rotate
-    const bool turns = li < half;
-    // this lane's chunks of a row
-    int c0 = 2 * li, c1 = 2 * li + 1;
-    if (!a.interleaved && turns) {
-        c0 = li;
-        c1 = li + half;
+    // this lane's chunks of a row, and whether they turn: split pairs, l and its partner
+    // l + half, then the elements behind them; interleaved ones, l and l + kLanes
+    int c0 = li, c1 = li + kLanes;
+    bool turns0 = c0 < 2 * half, turns1 = c1 < 2 * half;
+    if (!a.interleaved) {
+        turns0 = turns1 = li < half;
+        if (turns0) c1 = li + half;
+        else c0 = li + half;
     }
     const bool is_q = part < a.q_parts;
     // this warp's first row, and its steps: query rows, or K rows and as many V rows
@@ -369,6 +380,8 @@ __global__ void __launch_bounds__(kRopeWarps * 32, RopeShape<T, kOut>::kCtas) no
     const T* vsrc = is_q || !kCached ? src : static_cast<const T*>(a.v) + t_lo * a.v_stride + (long long)h0 * D + 8 * c0;
     const long long src_step = is_q ? a.q_stride : a.k_stride;
     int b = 0, left = 0, pos = 0;                  // its sequence, tokens after it in there, its position
+    // table row of the run's next token where it is given: loaded a token ahead
+    int given = a.rope_positions != nullptr ? a.rope_positions[t_lo] : 0;
     auto fetch = [&](int j, int s) -> Place {
         const long long t = t_lo + j;
         const uint32_t st = ring + s * C::kStage;
@@ -417,7 +430,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, RopeShape<T, kOut>::kCtas) no
         }
         p.turn = pos;
         if (p.live && half > 0) {
-            if (a.rope_positions != nullptr) p.turn = a.rope_positions[t];
+            if (a.rope_positions != nullptr) p.turn = given;
             if (p.turn < 0 || p.turn >= a.rope_rows) {
                 if (lane == 0 && part == 0) flag_error(a.err, GQA_DEVERR_POSITION);
                 p.live = false;
@@ -426,6 +439,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, RopeShape<T, kOut>::kCtas) no
                                       reinterpret_cast<const uint4*>(a.rope + (long long)p.turn * (a.rotary_dim / 2)) + lane);
             }
         }
+        if (a.rope_positions != nullptr && j + 1 < n) given = a.rope_positions[t + 1];
         if constexpr (kCached) {
             if (p.live && !is_q) {
                 p.slot = pos >= 0 && pos < a.max_blocks * kBlock;
@@ -461,10 +475,12 @@ __global__ void __launch_bounds__(kRopeWarps * 32, RopeShape<T, kOut>::kCtas) no
         const long long t = t_lo + j;
         const uint32_t st = ring + s * C::kStage, mine = st + lane * 16;
         float cs[8], sn[8];
-        if (turns) {
+        if (turns0) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint4 f = lds128(st + C::kTable + (4 * li + e) * 16);
+            for (int e = 0; e < 4; ++e) {          // pairs 8 li .., or 4 c0 .. and 4 c1 ..
+                if (a.interleaved && e >= 2 && !turns1) break;
+                const int at = a.interleaved ? 2 * (e < 2 ? c0 : c1) + e % 2 : 4 * li + e;
+                const uint4 f = lds128(st + C::kTable + at * 16);
                 cs[2 * e] = __uint_as_float(f.x);
                 sn[2 * e] = __uint_as_float(f.y);
                 cs[2 * e + 1] = __uint_as_float(f.z);
@@ -492,15 +508,15 @@ __global__ void __launch_bounds__(kRopeWarps * 32, RopeShape<T, kOut>::kCtas) no
                 widen8(r1, x1[u]);
             }
             if (wp != nullptr) norm_rows<kExact, kLanes, D>(x0, x1, w0, w1, a.eps);
-            if (turns) {
+            if (turns0) {
 #pragma unroll
                 for (int u = 0; u < kN; ++u) {
                     if (a.interleaved) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            rotate<kExact>(x0[u][2 * e], x0[u][2 * e + 1], cs[e], sn[e]);
-                            rotate<kExact>(x1[u][2 * e], x1[u][2 * e + 1], cs[4 + e], sn[4 + e]);
-                        }
+                        for (int e = 0; e < 4; ++e) rotate<kExact>(x0[u][2 * e], x0[u][2 * e + 1], cs[e], sn[e]);
+                        if (!turns1) continue;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) rotate<kExact>(x1[u][2 * e], x1[u][2 * e + 1], cs[4 + e], sn[4 + e]);
                     } else {
 #pragma unroll
                         for (int e = 0; e < 8; ++e) rotate<kExact>(x0[u][e], x1[u][e], cs[e], sn[e]);
@@ -510,7 +526,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, RopeShape<T, kOut>::kCtas) no
         };
         constexpr int kPair = RopeShape<T, kOut>::kPair;
         using Pair = std::integral_constant<int, kPair>;
-        static_assert(kMost % 2 == 0 && kKvSteps % 2 == 0, "steps come in pairs");
+        static_assert(kMost % kPair == 0 && kKvSteps % kPair == 0, "steps come in whole groups");
         if (is_q || kOut == kOutDense) {           // rows of a dense output
             T* out = (is_q ? static_cast<T*>(a.q_out) + t * a.H * D : static_cast<T*>(a.k_out) + t * a.K * D) + h0 * D + 8 * c0;
 #pragma unroll
@@ -692,7 +708,7 @@ cudaError_t launch_norm_rope(const NormRopeLaunch& L) {
     }
     const int rows = 512 / L.head_dim;                             // rows per warp step
     a.q_parts = (a.H + rows * kRopeSteps - 1) / (rows * kRopeSteps);
-    a.parts = a.q_parts + (a.K + rows * kKvSteps - 1) / (rows * kKvSteps);
+    a.parts = a.q_parts + (a.K + rows * kv_steps(out) - 1) / (rows * kv_steps(out));
     const void* fn = L.dtype == GQA_DTYPE_F32   ? rope_fn_d<float>(L.head_dim, out)
                      : L.dtype == GQA_DTYPE_F16 ? rope_fn_d<__half>(L.head_dim, out)
                                                 : rope_fn_d<__nv_bfloat16>(L.head_dim, out);
@@ -700,9 +716,20 @@ cudaError_t launch_norm_rope(const NormRopeLaunch& L) {
     const int sms = device_sms(-1), per_sm = ctas_per_sm(fn, kRopeWarps * 32, smem);
     if (sms < 1 || per_sm < 1) return cudaErrorInvalidConfiguration;
     if (a.tokens == 0) return cudaSuccess;
-    // one wave of warps, each with an even share of consecutive tokens
+    // One wave of warps, each with an even share of consecutive tokens. Calls that stream
+    // from DRAM (twice the L2's 129 MB read and written) take eight: shorter runs keep the
+    // warps of the moment on fewer stretches of memory and even out parts of unequal work.
+    // Not where most of the warps' rows are empty, nor for quantised rows: these are bound
+    // by issue, and a run's start costs them more. Measured, one / eight waves, 32 + 8
+    // heads, d = 128: 73.8 / 63.5 us for 400 MB, 37.3 / 36.3 for 200, 14.4 / 17.7 for 98;
+    // 8 + 1 heads (31% of the rows), 334 MB: 83.9 / 88.7; FP8 cache, 370 MB, one / two /
+    // four: 81 / 84 / 86.
+    const int esize = L.dtype == GQA_DTYPE_F32 ? 4 : 2;
+    const bool streams = 2 * a.tokens * (a.H + 2 * a.K) * L.head_dim * esize >= (256LL << 20);
+    const bool filled = 2 * (a.H + 2 * a.K) >= a.parts * rows * kRopeSteps;
+    const int waves = streams && filled && out <= kOutCache ? 8 : 1;
     const long long runs =
-        std::min(a.tokens, std::max<long long>(1, (long long)sms * per_sm * kRopeWarps / a.parts));
+        std::min(a.tokens, std::max<long long>(1, (long long)waves * sms * per_sm * kRopeWarps / a.parts));
     if (a.tokens / runs >= 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     a.runs = (int)runs;
     a.run = (int)(a.tokens / runs);
