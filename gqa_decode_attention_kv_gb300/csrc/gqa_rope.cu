@@ -677,7 +677,7 @@ cudaError_t launch_norm_rope(const NormRopeLaunch& L) {
     a.rope_rows = r.rope_rows;
     a.rotary_dim = r.rope != nullptr ? r.rotary_dim : 0;
     a.interleaved = r.interleaved;
-    a.rope_positions = L.rope_positions;
+    a.rope_positions = r.rope != nullptr ? L.rope_positions : nullptr;   // read only where rows turn
     a.q_out = L.q_out;
     a.k_out = L.k_out;
     a.err = L.err;

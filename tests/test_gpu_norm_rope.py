@@ -302,6 +302,60 @@ def test_pages_past_32_bit_offsets(gq):
     assert torch.equal(cache.k[pages - 1, :, 3], k[0]) and torch.equal(cache.v[pages - 2, :, 15], v[1])
 
 
+@pytest.mark.parametrize("dtype,H,K,d,interleaved,lens", [("bf16", 32, 8, 128, False, [7001, 1, 3050, 2300]),
+                                                          ("f16", 24, 8, 64, True, [20001, 9007, 33]),
+                                                          ("bf16", 16, 8, 128, False, [16384, 0, 16])])
+def test_a_batch_that_streams_equals_its_parts(gq, dtype, H, K, d, interleaved, lens):
+    """Batches of over 256 MB read and written run in shorter runs of tokens; a row's
+    result does not depend on the run it is in, so the parts give the very same bits."""
+    t, total, B = TYPES[dtype], sum(lens), len(lens)
+    qkv = torch.randn((total, H + 2 * K, d), generator=torch.Generator("cuda").manual_seed(3), device="cuda").to(t)
+    q, k, v = qkv[:, :H], qkv[:, H:H + K], qkv[:, H + K:]
+    assert 2 * q.element_size() * qkv.numel() >= 256 << 20
+    rope, wq, wk = gq.rope_table(max(lens) + 9, d), randn((d,), t, 4), randn((d,), t, 5)
+    at = torch.randint(0, max(lens), (total,), generator=torch.Generator().manual_seed(6), dtype=torch.int32).cuda()
+    blocks = max(lens) // 16 + 2
+    table = torch.randperm(B * blocks, generator=torch.Generator().manual_seed(7)).to(torch.int32).view(B, blocks).cuda()
+    pos = torch.tensor([9, 0, 5, 1][:B], dtype=torch.int32, device="cuda")
+    start = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+    caches = []
+    for c in range(2):
+        caches.append(gq.PagedKVCache.allocate(B * blocks, K, d, t))
+        caches[c].k.zero_(), caches[c].v.zero_()
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    whole = gq.qk_norm_rope_append(caches[0], q, k, v, table, pos, rope, wq, wk, interleaved=interleaved,
+                                   token_start=start, max_new_tokens=max(lens), err=err)
+    dense = gq.qk_norm_rope(q, k, at, rope, wq, wk, interleaved=interleaved, err=err)
+    for b, n in enumerate(lens):
+        for lo in range(0, n, 4000):
+            i, m = int(start[b]) + lo, min(4000, n - lo)
+            one = torch.tensor([0, m], dtype=torch.int32, device="cuda")
+            part = gq.qk_norm_rope_append(caches[1], q[i:i + m], k[i:i + m], v[i:i + m], table[b:b + 1],
+                                          pos[b:b + 1] + lo, rope, wq, wk, interleaved=interleaved,
+                                          token_start=one, max_new_tokens=m, err=err)
+            assert torch.equal(whole[i:i + m], part)
+            for x, y in zip(dense, gq.qk_norm_rope(q[i:i + m], k[i:i + m], at[i:i + m], rope, wq, wk,
+                                                   interleaved=interleaved, err=err)):
+                assert torch.equal(x[i:i + m], y)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    assert torch.equal(caches[0].k, caches[1].k) and torch.equal(caches[0].v, caches[1].v)
+    few = torch.tensor([0, 1, 2, 3, total // 2, total - 2, total - 1])
+    check(dense[0][few], *turned(q[few], wq, 1e-6, rope, at[few], interleaved), t)
+    check(dense[1][few], *turned(k[few], wk, 1e-6, rope, at[few], interleaved), t)
+
+
+def test_positions_without_a_table_change_nothing(gq):
+    q, k = randn((9, 8, 128), torch.bfloat16, 1), randn((9, 2, 128), torch.bfloat16, 2)
+    w = randn((128,), torch.bfloat16, 3)
+    far = torch.full((9,), 2 ** 31 - 1, dtype=torch.int32, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    a, b = gq.qk_norm_rope(q, k, far, None, w, w, err=err)
+    c, e = gq.qk_norm_rope(q, k, None, None, w, w, err=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0 and torch.equal(a, c) and torch.equal(b, e)
+
+
 def test_other_stream_and_captured_replay(gq):
     B, H, K, d = 3, 8, 2, 128
     case, cache, start, positions, seq, at = _setup(gq, [1] * B, [3, 20, 9], K, d, "bf16", 61, extra=40)
