@@ -168,7 +168,19 @@ int launch_decode(const DecodeLaunch& L, int num_sms) {
     // the unit count, which must stay below 2^31.)
     int nrg = 1;
     bool ok = false;
-    if (GT <= kHeadsPerWarp) {
+    const int min_units = L.min_blocks_per_warp > 0 ? L.min_blocks_per_warp : 4;
+    // 9 to 16 rows of a coded cache with sinks: one warp per pair and 16 rows, where the
+    // workspace has room for its workers (the size asked for has; a fixed one may not)
+    bool rows16 = false;
+    if (sinks && kind == kKernelMma && L.row_layout == 0 && GT > kHeadsPerWarp && GT <= kMma16Rows &&
+        pick_sinks(c.dtype, kKernelMma16, D, 1, v)) {
+        const int P = workers_of(v, L.batch, num_sms);
+        rows16 = P > 0 && ws_layout(L.batch, K, GT, D, max_slots(L.batch, K, P, L.max_blocks, min_units, v.tail_chunks))
+                                  .total <= L.workspace_bytes;
+    }
+    if (rows16) {
+        ok = true;
+    } else if (GT <= kHeadsPerWarp) {
         ok = pick(1);
     } else {
         const int groups = row_groups(GT);
@@ -211,7 +223,7 @@ int launch_decode(const DecodeLaunch& L, int num_sms) {
         // the workspace is sized from the other flavours' workers alone, so that
         // its size does not depend on the options
         Variant g{};
-        if (pick_general(c.dtype, kind, D, nrg > 1 || GT <= kHeadsPerWarp ? 1 : warps_for_rows(GT), g))
+        if (pick_general(c.dtype, kind, D, rows16 || nrg > 1 || GT <= kHeadsPerWarp ? 1 : warps_for_rows(GT), g))
             workers = std::min(workers, workers_of(g, L.batch, num_sms));
     }
     if (workers < 1) return GQA_ERR_UNSUPPORTED;
@@ -221,7 +233,6 @@ int launch_decode(const DecodeLaunch& L, int num_sms) {
         grid = std::min(grid, std::max(1, (L.max_warps + v.workers_per_cta - 1) / v.workers_per_cta));
     const int P = grid * v.workers_per_cta;   // split-KV workers (KV splits per pass)
 
-    const int min_units = L.min_blocks_per_warp > 0 ? L.min_blocks_per_warp : 4;
     const WsLayout wl =
         ws_layout(L.batch, Kv, RS, D, max_slots(L.batch, Kv, P, L.max_blocks, min_units, v.tail_chunks));
     if (L.workspace == nullptr || L.workspace_bytes < wl.total) return GQA_ERR_WORKSPACE;

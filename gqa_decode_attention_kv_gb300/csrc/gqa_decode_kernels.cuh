@@ -117,6 +117,14 @@ struct DecodeArgs {
 // Measured on the T = 4, G = 16 and G = 64 workloads at 12 warps per SM with
 // the copy warp: 32 KB (four bf16 stages) beats 24 KB by 2-4% and ties 40 KB;
 // 16 KB loses 5%.
+// The 16-row kernel: 235 to 249 registers a thread, so two CTAs of four warps (at three
+// CTAs it spills and takes 83 us where it takes 44 as it is, FP8, 48 sequences, below).
+#ifndef GQA_MIN_CTAS_PER_SM_R16
+#define GQA_MIN_CTAS_PER_SM_R16 2
+#endif
+#ifndef GQA_RING_BYTES_PER_WARP_R16
+#define GQA_RING_BYTES_PER_WARP_R16 20480
+#endif
 #ifndef GQA_SHARED_RING_BYTES
 #define GQA_SHARED_RING_BYTES 32768
 #endif
@@ -139,6 +147,16 @@ constexpr int kMaxTailChunks = GQA_MAX_TAIL_CHUNKS;
 constexpr int kMinChunk = 4;
 
 constexpr int kHeadsPerWarp = 8;   // query heads one warp serves (the MMA N dimension)
+
+// Kernel kind next to those of KernelKind: tensor cores with 16 query rows a warp (the
+// MMA's M dimension), for coded caches of the sink flavour. Bound by issue and latency
+// like the other coded kernels, of whose ~450 instructions per block and warp half widen
+// codes: here a block is widened once for 16 rows, where two warps of 8 rows each widen
+// it all. Measured, shared ring with two row warps / this: 48 sequences of 300 to 8192
+// tokens, W = 1000, S = 20, T = 2, G = 8: FP8 53.9 / 43.8 us, int8 52.9 / 43.5, int4
+// 51.9 / 41.8; 9 rows (T = 1) 50.6 / 42.0; 16 sequences 28.7 / 28.8; one 16.0 / 16.8.
+constexpr int kKernelMma16 = 3;
+constexpr int kMma16Rows = 16;
 
 // kHeadWarps == 1: every warp is an independent split-KV worker with its own
 // ring and serves all (<= 8) heads of its group. kHeadWarps > 1: the CTA is one
@@ -172,8 +190,11 @@ struct Cfg {
     // rows) takes the 64-byte swizzle (16-byte chunk ^= (row >> 1) & 3), which
     // spreads its V reads over twice the banks. The CUDA-core kernel reads rows
     // whole and needs none.
-    static constexpr bool kSwizzle = (kKind == kKernelMma) && !kI4;
-    static constexpr int kSwizzleBytes = kKind != kKernelMma ? 0 : kI4 ? 64 : 128;
+    static constexpr bool kMma = kKind != kKernelFma;               // on the tensor cores
+    static constexpr bool kRows16 = kKind == kKernelMma16;
+    static_assert(!kRows16 || (kCoded && !kKc && kSinks && D == 128 && kHeadWarps == 1), "the 16-row kernel's cases");
+    static constexpr bool kSwizzle = kMma && !kI4;
+    static constexpr int kSwizzleBytes = !kMma ? 0 : kI4 ? 64 : 128;
     static constexpr int kStageAlign = kSwizzleBytes == 128 ? 1024 : kSwizzleBytes == 64 ? 512 : 128;
     static constexpr int kStage = ((2 * kTile + kScaleBytes + kStageAlign - 1) / kStageAlign) * kStageAlign;
     static constexpr int kNw = kHeadWarps;
@@ -190,7 +211,8 @@ struct Cfg {
     static constexpr bool kNarrowI4 =                // the one-token INT4 kernel with per-token scales
         kI4 && !kKc && !kGen && kHeadWarps == 1 && kKind == kKernelMma && D == 128;
     static constexpr int kMinCtas =
-        kNarrowI4 ? GQA_MIN_CTAS_PER_SM_I4
+        kRows16 ? GQA_MIN_CTAS_PER_SM_R16
+        : kNarrowI4 ? GQA_MIN_CTAS_PER_SM_I4
         : (kHeadWarps == 1 && kKind == kKernelMma && D == 128) ? (kCoded ? GQA_MIN_CTAS_PER_SM_I8 : 2)
         : (kHeadWarps > 1 && kKind == kKernelMma) ? std::max(1, GQA_SHARED_MIN_WARPS_PER_SM / kWarps)
                                                   : 1;
@@ -199,10 +221,11 @@ struct Cfg {
     // the benchmark workloads, so kernels short of registers load them when
     // the pair starts instead.
     static constexpr bool kPrefetchQ =
-        !(kCoded && kMinCtas >= 4) && !(kHeadWarps > 1 && kWarps * kMinCtas >= 12);
+        !kRows16 && !(kCoded && kMinCtas >= 4) && !(kHeadWarps > 1 && kWarps * kMinCtas >= 12);
     static constexpr int kRings = kHeadWarps == 1 ? kWarps : 1;
     static constexpr int kStages = std::max(
-        2, std::min(8, (kNarrowI4 ? GQA_RING_BYTES_PER_WARP_I4
+        2, std::min(8, (kRows16 ? GQA_RING_BYTES_PER_WARP_R16
+                        : kNarrowI4 ? GQA_RING_BYTES_PER_WARP_I4
                         : kHeadWarps == 1 ? GQA_RING_BYTES_PER_WARP : GQA_SHARED_RING_BYTES) / kStage));
     static constexpr int kBoxInner = kSwizzle ? 128 / kEs : kRowBytes / kEs;   // elements per box row
     static constexpr int kNumBox = kSwizzle ? kRowBytes / 128 : 1;
@@ -558,21 +581,11 @@ __device__ __forceinline__ void mma_t(float (&d)[4], uint32_t a0, uint32_t a1, u
 }
 
 
-// Gather one block's operands from shared memory (all reads of the slot).
-template <class C, int D>
-__device__ __forceinline__ void mma_load(MmaFrags<C, D>& f, uint32_t stage, int lane, int r, int c) {
-    const uint32_t sk = stage, sv = stage + C::kTile;
+// Gather one block's K and V codes from shared memory.
+template <class C, int D, class F>
+__device__ __forceinline__ void load_codes(F& f, uint32_t sk, uint32_t sv, int lane, int r, int c) {
     const int mi = lane >> 3, rr = lane & 7;
-    if constexpr (!C::kCoded) {
-        // K: matrices (toks 0-7 | 8-15) x (dims 16t..+7 | +8..+15) = a0, a1, a2, a3
-#pragma unroll
-        for (int t = 0; t < D / 16; ++t)
-            ldsm_x4(swz(sk, rr + 8 * (mi & 1), 2 * t + (mi >> 1)), f.k[t]);
-        // V^T: transposed matrices (dims 16j..+7 | +8..+15) x (toks 0-7 | 8-15)
-#pragma unroll
-        for (int j = 0; j < C::kMt; ++j)
-            ldsm_x4_t(swz(sv, rr + 8 * (mi >> 1), 2 * j + (mi & 1)), f.v[j]);
-    } else if constexpr (C::kI4) {
+    if constexpr (C::kI4) {
         // K: 16 bytes (32 codes) of tokens r and r+8 at chunk c; V: 8 bytes
         // (dims 16r..16r+15) of tokens 2c, 2c+1, 2c+8, 2c+9. 64-byte rows with
         // the 64-byte swizzle (chunk ^ (row >> 1) & 3): K touches each bank once
@@ -602,6 +615,25 @@ __device__ __forceinline__ void mma_load(MmaFrags<C, D>& f, uint32_t stage, int 
             f.v[i][0] = raw.x; f.v[i][1] = raw.y; f.v[i][2] = raw.z; f.v[i][3] = raw.w;
         }
     }
+}
+
+// Gather one block's operands from shared memory (all reads of the slot).
+template <class C, int D>
+__device__ __forceinline__ void mma_load(MmaFrags<C, D>& f, uint32_t stage, int lane, int r, int c) {
+    const uint32_t sk = stage, sv = stage + C::kTile;
+    const int mi = lane >> 3, rr = lane & 7;
+    if constexpr (!C::kCoded) {
+        // K: matrices (toks 0-7 | 8-15) x (dims 16t..+7 | +8..+15) = a0, a1, a2, a3
+#pragma unroll
+        for (int t = 0; t < D / 16; ++t)
+            ldsm_x4(swz(sk, rr + 8 * (mi & 1), 2 * t + (mi >> 1)), f.k[t]);
+        // V^T: transposed matrices (dims 16j..+7 | +8..+15) x (toks 0-7 | 8-15)
+#pragma unroll
+        for (int j = 0; j < C::kMt; ++j)
+            ldsm_x4_t(swz(sv, rr + 8 * (mi >> 1), 2 * j + (mi & 1)), f.v[j]);
+    } else {
+        load_codes<C, D>(f, sk, sv, lane, r, c);
+    }
     if constexpr (C::kCoded) {
         const uint32_t sc = stage + 2 * C::kTile;
         unsigned short h2, h3;
@@ -625,7 +657,81 @@ __device__ __forceinline__ void mma_load(MmaFrags<C, D>& f, uint32_t stage, int 
     }
 }
 
-// Which tokens of a block the two query rows of a lane (2c, 2c+1) attend:
+// V codes v[i][w] (token i of 2c, 2c+1, 2c+8, 2c+9; dims 16r + 4w .. +3, one byte each)
+// widened: put(j, a0, a1, a2, a3) gets dims 16r + 2j (a0, a2) and 16r + 2j + 1 (a1, a3) of
+// tokens 2c, 2c+1 (a0, a1) and 2c+8, 2c+9 (a2, a3), j = 0 .. 7.
+template <class C, class F>
+__device__ __forceinline__ void widen_v(const uint32_t (*v)[4], F&& put) {
+    if constexpr (C::kFp8) {
+        // pair (x.b[k], y.b[k]) straight from the two tokens' words, with
+        // the sign bytes, then widened as 2^-8 x (undone at the flush)
+#pragma unroll
+        for (int wd = 0; wd < 4; ++wd) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const uint32_t s0 = e ? 0xE6A2u : 0xC480u, s1 = e ? 0xF7B3u : 0xD591u;
+                const uint32_t a0 = e4m3x2_to_f16x2_scaled(v[0][wd], v[1][wd], s0);
+                const uint32_t a1 = e4m3x2_to_f16x2_scaled(v[0][wd], v[1][wd], s1);
+                const uint32_t a2 = e4m3x2_to_f16x2_scaled(v[2][wd], v[3][wd], s0);
+                const uint32_t a3 = e4m3x2_to_f16x2_scaled(v[2][wd], v[3][wd], s1);
+                const int j = 2 * wd + e;
+                put(j, a0, a1, a2, a3);
+            }
+        }
+        return;
+    }
+    if constexpr (C::kI4) {
+        // byte j of a token's 8 bytes holds dims 16r + 2j (low nibble, row r
+        // of m-tile j) and 16r + 2j + 1 (high nibble, row r+8). Pair the bytes
+        // of tokens (2c, 2c+1) and (2c+8, 2c+9): (x.bj, x.bj+1, y.bj, y.bj+1).
+#pragma unroll
+        for (int wd = 0; wd < 2; ++wd) {
+            const uint32_t t0 = __byte_perm(v[0][wd], v[1][wd], 0x5410);
+            const uint32_t t1 = __byte_perm(v[0][wd], v[1][wd], 0x7632);
+            const uint32_t u0 = __byte_perm(v[2][wd], v[3][wd], 0x5410);
+            const uint32_t u1 = __byte_perm(v[2][wd], v[3][wd], 0x7632);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t tx = (e < 2 ? t0 : t1) >> (8 * (e & 1));
+                const uint32_t ux = (e < 2 ? u0 : u1) >> (8 * (e & 1));
+                const uint32_t a0 = i4_lo_pair(tx), a1 = i4_hi_pair(tx);
+                const uint32_t a2 = i4_lo_pair(ux), a3 = i4_hi_pair(ux);
+                const int j = 4 * wd + e;
+                put(j, a0, a1, a2, a3);
+            }
+        }
+        return;
+    }
+    // A fragment of m-tile j = 2w + e (dims 16r + 4w + 2e, +1) for the token
+    // pair (x, y): interleave the two tokens' bytes, then widen each byte to
+    // f16 exactly (1024 + (code ^ 0x80) - 1152).
+    const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+    auto widen = [&](uint32_t t, uint32_t sel) -> uint32_t {
+        const uint32_t hv = __byte_perm(t, 0x64646464u, sel);
+        __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&hv), bias);
+        return as_u32(h);
+    };
+    const uint32_t flip = 0x80808080u;
+#pragma unroll
+    for (int wd = 0; wd < 4; ++wd) {
+        const uint32_t x0 = v[0][wd] ^ flip, y0 = v[1][wd] ^ flip;
+        const uint32_t x1 = v[2][wd] ^ flip, y1 = v[3][wd] ^ flip;
+        // bytes (x.b0, y.b0, x.b1, y.b1) and (x.b2, y.b2, x.b3, y.b3)
+        const uint32_t lo0 = __byte_perm(x0, y0, 0x5140), hi0 = __byte_perm(x0, y0, 0x7362);
+        const uint32_t lo1 = __byte_perm(x1, y1, 0x5140), hi1 = __byte_perm(x1, y1, 0x7362);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const uint32_t t0 = e ? hi0 : lo0, t1 = e ? hi1 : lo1;
+            // rows r (dim 4wd + 2e) and r+8 (dim 4wd + 2e + 1): tokens (2c, 2c+1)
+            const uint32_t a0 = widen(t0, 0x4140), a1 = widen(t0, 0x4342);
+            const uint32_t a2 = widen(t1, 0x4140), a3 = widen(t1, 0x4342);
+            const int j = 2 * wd + e;
+            put(j, a0, a1, a2, a3);
+        }
+    }
+}
+
+// Which tokens of a block the two query rows of a lane (2c, 2c+1; 16-row kernel: r, r+8) attend:
 // lo <= token < hi, block-relative, and with sinks also the tokens below
 // min(sink, hi). `partial` is false when every row of the pair attends the whole
 // block (the masks are then skipped, and the block lies wholly inside the
@@ -820,76 +926,10 @@ __device__ __forceinline__ void mma_compute(MmaState<C, D>& st, MmaFrags<C, D>& 
                 if (C::kSinks ? !((bm.seen >> tok) & 1u) : tok >= nvalid) f.v[i][0] = f.v[i][1] = f.v[i][2] = f.v[i][3] = 0u;
             }
         }
-        if constexpr (C::kFp8) {
-            // pair (x.b[k], y.b[k]) straight from the two tokens' words, with
-            // the sign bytes, then widened as 2^-8 x (undone at the flush)
-#pragma unroll
-            for (int wd = 0; wd < 4; ++wd) {
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const uint32_t s0 = e ? 0xE6A2u : 0xC480u, s1 = e ? 0xF7B3u : 0xD591u;
-                    const uint32_t a0 = e4m3x2_to_f16x2_scaled(f.v[0][wd], f.v[1][wd], s0);
-                    const uint32_t a1 = e4m3x2_to_f16x2_scaled(f.v[0][wd], f.v[1][wd], s1);
-                    const uint32_t a2 = e4m3x2_to_f16x2_scaled(f.v[2][wd], f.v[3][wd], s0);
-                    const uint32_t a3 = e4m3x2_to_f16x2_scaled(f.v[2][wd], f.v[3][wd], s1);
-                    const int j = 2 * wd + e;
-                    mma_f16(st.acc[j], a0, a1, a2, a3, bh0, bh1);
-                    mma_f16(st.acc[j], a0, a1, a2, a3, bl0, bl1);
-                }
-            }
-            return;
-        }
-        if constexpr (C::kI4) {
-            // byte j of a token's 8 bytes holds dims 16r + 2j (low nibble, row r
-            // of m-tile j) and 16r + 2j + 1 (high nibble, row r+8). Pair the bytes
-            // of tokens (2c, 2c+1) and (2c+8, 2c+9): (x.bj, x.bj+1, y.bj, y.bj+1).
-#pragma unroll
-            for (int wd = 0; wd < 2; ++wd) {
-                const uint32_t t0 = __byte_perm(f.v[0][wd], f.v[1][wd], 0x5410);
-                const uint32_t t1 = __byte_perm(f.v[0][wd], f.v[1][wd], 0x7632);
-                const uint32_t u0 = __byte_perm(f.v[2][wd], f.v[3][wd], 0x5410);
-                const uint32_t u1 = __byte_perm(f.v[2][wd], f.v[3][wd], 0x7632);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t tx = (e < 2 ? t0 : t1) >> (8 * (e & 1));
-                    const uint32_t ux = (e < 2 ? u0 : u1) >> (8 * (e & 1));
-                    const uint32_t a0 = i4_lo_pair(tx), a1 = i4_hi_pair(tx);
-                    const uint32_t a2 = i4_lo_pair(ux), a3 = i4_hi_pair(ux);
-                    const int j = 4 * wd + e;
-                    mma_f16(st.acc[j], a0, a1, a2, a3, bh0, bh1);
-                    mma_f16(st.acc[j], a0, a1, a2, a3, bl0, bl1);
-                }
-            }
-            return;
-        }
-        // A fragment of m-tile j = 2w + e (dims 16r + 4w + 2e, +1) for the token
-        // pair (x, y): interleave the two tokens' bytes, then widen each byte to
-        // f16 exactly (1024 + (code ^ 0x80) - 1152).
-        const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
-        auto widen = [&](uint32_t t, uint32_t sel) -> uint32_t {
-            const uint32_t hv = __byte_perm(t, 0x64646464u, sel);
-            __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&hv), bias);
-            return as_u32(h);
-        };
-        const uint32_t flip = 0x80808080u;
-#pragma unroll
-        for (int wd = 0; wd < 4; ++wd) {
-            const uint32_t x0 = f.v[0][wd] ^ flip, y0 = f.v[1][wd] ^ flip;
-            const uint32_t x1 = f.v[2][wd] ^ flip, y1 = f.v[3][wd] ^ flip;
-            // bytes (x.b0, y.b0, x.b1, y.b1) and (x.b2, y.b2, x.b3, y.b3)
-            const uint32_t lo0 = __byte_perm(x0, y0, 0x5140), hi0 = __byte_perm(x0, y0, 0x7362);
-            const uint32_t lo1 = __byte_perm(x1, y1, 0x5140), hi1 = __byte_perm(x1, y1, 0x7362);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const uint32_t t0 = e ? hi0 : lo0, t1 = e ? hi1 : lo1;
-                // rows r (dim 4wd + 2e) and r+8 (dim 4wd + 2e + 1): tokens (2c, 2c+1)
-                const uint32_t a0 = widen(t0, 0x4140), a1 = widen(t0, 0x4342);
-                const uint32_t a2 = widen(t1, 0x4140), a3 = widen(t1, 0x4342);
-                const int j = 2 * wd + e;
-                mma_f16(st.acc[j], a0, a1, a2, a3, bh0, bh1);
-                mma_f16(st.acc[j], a0, a1, a2, a3, bl0, bl1);
-            }
-        }
+        widen_v<C>(f.v, [&](int j, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+            mma_f16(st.acc[j], a0, a1, a2, a3, bh0, bh1);
+            mma_f16(st.acc[j], a0, a1, a2, a3, bl0, bl1);
+        });
     }
 }
 
@@ -925,6 +965,173 @@ __device__ __forceinline__ void mma_flush(const DecodeArgs& a, MmaState<C, D>& s
             }
         }
         if (!whole && r == 0) a.ws_ml[slot * a.RS + hh - row0] = make_float2(st.m[e], lsum);
+    }
+}
+
+// ------------------------------------------------------------------ tensor-core state, 16 rows
+//
+// S[row][token] = Q . K^T with Q as the A operand and the block's codes as B, so P is in
+// the A layout of O += P . V as it is (no transposes), and V's codes are B again. A lane
+// holds rows r and r + 8; of the output, dims 32c .. 32c+31 of both.
+
+template <class C, int D>
+struct Mma16State {
+    float m[2], l[2];          // rows r, r+8 (log2 units)
+    float acc[D / 8][4];       // n-tile t, column n: dim 16n + t
+    uint2 qf[2][D / 16];       // load_q_frags of rows r and r+8
+
+    __device__ __forceinline__ void reset() {
+        m[0] = m[1] = -INFINITY;
+        l[0] = l[1] = 0.f;
+#pragma unroll
+        for (int t = 0; t < D / 8; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
+    }
+};
+
+template <class C, int D>
+struct Frags16 {
+    uint32_t k[D / 32][4], v[4][4];   // as MmaFrags
+    float2 ks[2], vs[2];              // scales of tokens 2c, 2c+1 and 2c+8, 2c+9
+};
+
+template <class C, int D>
+__device__ __forceinline__ void mma16_load(Frags16<C, D>& f, uint32_t stage, int lane, int r, int c) {
+    load_codes<C, D>(f, stage, stage + C::kTile, lane, r, c);
+    const uint32_t sc = stage + 2 * C::kTile + 4 * c;
+    f.ks[0] = unpack2<false>(lds32(sc));
+    f.ks[1] = unpack2<false>(lds32(sc + 16));
+    f.vs[0] = unpack2<false>(lds32(sc + C::kVsOff));
+    f.vs[1] = unpack2<false>(lds32(sc + C::kVsOff + 16));
+}
+
+// One 16-token block. Masks and V's zeroing as in mma_compute; bm.lo0, hi0 are row r's,
+// lo1, hi1 row r+8's.
+template <class C, int D>
+__device__ __forceinline__ void mma16_compute(Mma16State<C, D>& st, Frags16<C, D>& f, const BlockMask& bm, int c,
+                                              float scale_log2) {
+    // ---- scores of tokens 0-7 and 8-15, even and odd k-steps apart (short chains)
+    float s0[2][4] = {}, s1[2][4] = {};
+    auto step = [&](int t, uint32_t l0, uint32_t l1, uint32_t h0, uint32_t h1) {
+        const uint2 x = st.qf[0][t], y = st.qf[1][t];
+        mma_f16(s0[t & 1], x.x, y.x, x.y, y.y, l0, h0);
+        mma_f16(s1[t & 1], x.x, y.x, x.y, y.y, l1, h1);
+    };
+#pragma unroll
+    for (int t = 0; t < D / 32; ++t) {
+        if constexpr (C::kI4) {
+            const uint32_t w = f.k[0][t], w8 = f.k[1][t];
+            step(2 * t, i4_lo_pair(w), i4_lo_pair(w8), i4_hi_pair(w), i4_hi_pair(w8));
+            step(2 * t + 1, i4_lo_pair(w >> 8), i4_lo_pair(w8 >> 8), i4_hi_pair(w >> 8), i4_hi_pair(w8 >> 8));
+        } else {
+            uint32_t l[4], h[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (C::kFp8) {
+                    l[i] = e4m3x2_to_f16x2_scaled(f.k[t][i], 0u, 0x9180u);   // as 2^-8 x, elements 0, 1
+                    h[i] = e4m3x2_to_f16x2_scaled(f.k[t][i], 0u, 0xB3A2u);   // elements 2, 3
+                } else {
+                    i8x4_to_f16x4(f.k[t][i], l[i], h[i]);
+                }
+            }
+            step(2 * t, l[0], l[1], h[0], h[1]);
+            step(2 * t + 1, l[2], l[3], h[2], h[3]);
+        }
+    }
+    // s[0..3] of row r: tokens 2c, 2c+1, 2c+8, 2c+9; s[4..7] of row r+8
+    const float k = (C::kFp8 ? 256.f : 1.f) * scale_log2;
+    const float ks[4] = {f.ks[0].x * k, f.ks[0].y * k, f.ks[1].x * k, f.ks[1].y * k};
+    float vs[4] = {f.vs[0].x, f.vs[0].y, f.vs[1].x, f.vs[1].y};
+    float s[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int e = (i & 1) + 2 * (i >> 2);
+        s[i] = (i & 2 ? s1[0][e] + s1[1][e] : s0[0][e] + s0[1][e]) * ks[i & 3];
+    }
+    if (bm.partial) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int tok = 2 * c + (i & 1) + 8 * (i >> 1);
+            if (!((bm.seen >> tok) & 1u)) {        // arbitrary codes and scales
+                vs[i] = 0.f;
+                f.v[i][0] = f.v[i][1] = f.v[i][2] = f.v[i][3] = 0u;
+            }
+            if ((tok < bm.lo0 && tok >= bm.sink) || tok >= bm.hi0) s[i] = -INFINITY;
+            if ((tok < bm.lo1 && tok >= bm.sink) || tok >= bm.hi1) s[4 + i] = -INFINITY;
+        }
+    }
+
+    // ---- online softmax (per row, over the 16 tokens of this block)
+    float mx0 = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])), mx1 = fmaxf(fmaxf(s[4], s[5]), fmaxf(s[6], s[7]));
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+        mx0 = fmaxf(mx0, __shfl_xor_sync(kFull, mx0, o));
+        mx1 = fmaxf(mx1, __shfl_xor_sync(kFull, mx1, o));
+    }
+    const bool up0 = mx0 > st.m[0], up1 = mx1 > st.m[1];
+    if (__any_sync(kFull, up0 || up1)) {
+        const float n0 = up0 ? mx0 : st.m[0], n1 = up1 ? mx1 : st.m[1];
+        const float a0 = up0 ? fast_exp2(st.m[0] - n0) : 1.f;
+        const float a1 = up1 ? fast_exp2(st.m[1] - n1) : 1.f;
+        st.m[0] = n0; st.m[1] = n1;
+        st.l[0] *= a0; st.l[1] *= a1;
+#pragma unroll
+        for (int t = 0; t < D / 8; ++t) {
+            st.acc[t][0] *= a0; st.acc[t][1] *= a0; st.acc[t][2] *= a1; st.acc[t][3] *= a1;
+        }
+    }
+    // a row that has attended nothing yet keeps m = -inf; its p must be 0, not NaN
+    const float mu0 = bm.partial && st.m[0] == -INFINITY ? 0.f : st.m[0];
+    const float mu1 = bm.partial && st.m[1] == -INFINITY ? 0.f : st.m[1];
+
+    // ---- P times V's scales -> f16 high + low parts, already the A operand
+    float w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float p = fast_exp2(s[i] - (i < 4 ? mu0 : mu1));
+        st.l[i >> 2] += p;
+        w[i] = p * vs[i & 3];
+    }
+    uint32_t hi[4], lo[4];                         // rows r, r+8 of tokens 2c, 2c+1; then of 2c+8, 2c+9
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int e = 4 * (i & 1) + 2 * (i >> 1);
+        hi[i] = pack2<false>(w[e], w[e + 1]);
+        const float2 x = unpack2<false>(hi[i]);
+        lo[i] = pack2<false>(w[e] - x.x, w[e + 1] - x.y);
+    }
+
+    // ---- O[row][dim] += P . V (high part, then low part); tiles 2j and 2j+1
+    auto put = [&](int j, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+        mma_f16(st.acc[2 * j], hi[0], hi[1], hi[2], hi[3], a0, a2);
+        mma_f16(st.acc[2 * j + 1], hi[0], hi[1], hi[2], hi[3], a1, a3);
+        mma_f16(st.acc[2 * j], lo[0], lo[1], lo[2], lo[3], a0, a2);
+        mma_f16(st.acc[2 * j + 1], lo[0], lo[1], lo[2], lo[3], a1, a3);
+    };
+    widen_v<C>(f.v, put);
+}
+
+template <class C, int D>
+__device__ __forceinline__ void mma16_flush(const DecodeArgs& a, Mma16State<C, D>& st, int b, int gv, bool whole,
+                                            int w, int r, int c) {
+    const long long slot = (long long)b * a.Kv + gv + w;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        float lsum = st.l[e];
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) lsum += __shfl_xor_sync(kFull, lsum, o);
+        const int hh = r + 8 * e;                  // row of the pair
+        if (hh >= a.GT) continue;
+        const float fix = C::kFp8 ? 256.f : 1.f;
+        const float mul = whole ? (lsum > 0.f ? fix / lsum : 0.f) : fix;
+        const long long base = (whole ? q_row<C::kGen>(a, b, gv, hh) : slot * a.RS + hh) * D + 32 * c;
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {              // dims 32c + 8h ..
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = st.acc[8 * (h & 1) + i][2 * e + (h >> 1)];
+            store8(whole ? a.out : a.ws_o, whole ? a.out_dtype : GQA_DTYPE_F32, base + 8 * h, v, mul);
+        }
+        if (!whole && c == 0) a.ws_ml[slot * a.RS + hh] = make_float2(st.m[e], lsum);
     }
 }
 
@@ -1150,6 +1357,7 @@ split_kv_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
     // segment runs out, and that chunk's block-table entries are fetched as soon
     // as its id is known, so switching segments costs no round trip.
     constexpr int kLookahead = 2;
+    constexpr bool kPooled = !C::kRows16;                  // else no pool: its code would only take registers
     const unsigned long long pool = (unsigned long long)pt.P * pt.cpw;
     int iss_u = 0, iss_hi = 0, iss_seg = -1, n_issued = 0;
     int nxt_lo = 0, nxt_hi = 0, nxt_seg = -1;
@@ -1171,12 +1379,12 @@ split_kv_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
         }
     };
     auto request = [&]() {
-        if (pend_out || exhausted) return;
+        if (!kPooled || pend_out || exhausted) return;
         if (lane == 0) pend = atomicAdd(a.ws_ctr, 1ull);
         pend_out = true;
     };
     auto resolve = [&]() {                 // the in-flight ticket -> the next segment
-        while (pend_out) {
+        while (kPooled && pend_out) {
             const unsigned long long cidx = __shfl_sync(kFull, pend, 0);
             pend_out = false;
             if (cidx >= pool) {
@@ -1215,7 +1423,7 @@ split_kv_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
                 request();
                 resolve();
             }
-            if (!nxt_ok) {
+            if (!kPooled || !nxt_ok) {
                 iss_done = true;
                 if (lane == 0) {
                     meta[4 * s] = kSlotEnd;
@@ -1274,7 +1482,7 @@ split_kv_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
         if (iss_hi - iss_u == kLookahead) request();
         if (iss_u == iss_hi) {             // segment issued: learn the next one, prefetch its table
             resolve();
-            if (nxt_ok) refill(nxt_lo);
+            if (kPooled && nxt_ok) refill(nxt_lo);
         }
     };
     // Bounded waits whose verdict is warp-uniform, so a timeout never splits a warp.
@@ -1318,7 +1526,9 @@ split_kv_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
 
     // ---- consumer: walk the units as they arrive
     const int r = lane >> 2, c = lane & 3;
-    using State = typename std::conditional<kKind == kKernelMma, MmaState<C, D>, FmaState<C, D>>::type;
+    using State = typename std::conditional<
+        kKind == kKernelMma, MmaState<C, D>,
+        typename std::conditional<C::kRows16, Mma16State<C, D>, FmaState<C, D>>::type>::type;
     State st;
     int cb = 0, cg = 0, cj = 0, cnb = 1, clen = 0, first_j = 0, cu_pair = 0;
     int nb_b = 0, nb_g = 0, next_u = -1;
@@ -1367,6 +1577,9 @@ split_kv_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
                         load_q_frags<C, D>(a, nb_b, nb_g / a.NRG,
                                            kShared ? hbase : (nb_g % a.NRG) * kHeadsPerWarp, r, c, st.qn);
                 }
+            } else if constexpr (C::kRows16) {
+                load_q_frags<C, D>(a, cb, cg, 0, r, c, st.qf[0]);
+                load_q_frags<C, D>(a, cb, cg, 8, r, c, st.qf[1]);
             } else {
                 fma_load_q<C, D>(a, st, cb, cg / a.NRG, hbase, lane);
             }
@@ -1387,10 +1600,13 @@ split_kv_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
             }
         }
         const bool unit_ok = kind == kSlotData;
-        if constexpr (kKind == kKernelMma) {
+        if constexpr (C::kMma) {
             // read the whole slot, hand it back to TMA, then compute from registers
-            MmaFrags<C, D> fr;
-            if (unit_ok) mma_load<C, D>(fr, ring + s * C::kStage, lane, r, c);
+            typename std::conditional<C::kRows16, Frags16<C, D>, MmaFrags<C, D>>::type fr;
+            if (unit_ok) {
+                if constexpr (C::kRows16) mma16_load<C, D>(fr, ring + s * C::kStage, lane, r, c);
+                else mma_load<C, D>(fr, ring + s * C::kStage, lane, r, c);
+            }
             if (!release_and_refill(k, s)) {
                 bail(k + 1);
                 return;
@@ -1404,11 +1620,14 @@ split_kv_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
                 bm.seen = ((0xffffu << lo) | below) & ((1u << nvalid) - 1u);
             }
             if (C::kGen && partial) {
-                row_range(a, clen, hbase + 2 * c, bm.lo0, bm.hi0);
-                row_range(a, clen, hbase + 2 * c + 1, bm.lo1, bm.hi1);
+                row_range(a, clen, C::kRows16 ? r : hbase + 2 * c, bm.lo0, bm.hi0);
+                row_range(a, clen, C::kRows16 ? r + 8 : hbase + 2 * c + 1, bm.lo1, bm.hi1);
                 bm.lo0 -= bpos; bm.hi0 -= bpos; bm.lo1 -= bpos; bm.hi1 -= bpos;
             }
-            if (unit_ok) mma_compute<C, D>(st, fr, nvalid, bm, r, c, a.scale_log2);
+            if (unit_ok) {
+                if constexpr (C::kRows16) mma16_compute<C, D>(st, fr, bm, c, a.scale_log2);
+                else mma_compute<C, D>(st, fr, nvalid, bm, r, c, a.scale_log2);
+            }
         } else {
             if (unit_ok) fma_block<C, D, T>(a, st, ring + s * C::kStage, nvalid, partial, bpos, clen, hbase, lane);
             if (!release_and_refill(k, s)) {
@@ -1424,6 +1643,7 @@ split_kv_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
             const bool whole = (first_j == 0) && last_of_pair;
             const int row0 = kShared ? 0 : hbase;
             if constexpr (kKind == kKernelMma) mma_flush<C, D>(a, st, cb, cg, hbase, row0, whole, seg, r, c);
+            else if constexpr (C::kRows16) mma16_flush<C, D>(a, st, cb, cg, whole, seg, r, c);
             else fma_flush<C, D>(a, st, cb, cg, hbase, row0, whole, seg, lane);
             if (last_of_seg) {
                 next_u = -1;                   // the next unit starts a new segment
@@ -1450,6 +1670,9 @@ split_kv_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
                 } else {
                     load_q_frags<C, D>(a, cb, cg / a.NRG, hbase, r, c, st.qf);
                 }
+            } else if constexpr (C::kRows16) {
+                load_q_frags<C, D>(a, cb, cg, 0, r, c, st.qf[0]);
+                load_q_frags<C, D>(a, cb, cg, 8, r, c, st.qf[1]);
             } else {
                 fma_load_q<C, D>(a, st, cb, cg / a.NRG, hbase, lane);
             }
@@ -1617,6 +1840,15 @@ Variant pick_width(int nw) {
 
 template <typename T, int D, bool kGen, bool kSinks>
 bool pick_kind(int kind, int nw, Variant& v) {
+    if (kind == kKernelMma16) {
+        if constexpr (kSinks && D == 128 && (std::is_same<T, int8_t>::value || std::is_same<T, __nv_fp8_e4m3>::value ||
+                                             std::is_same<T, int4x2>::value)) {
+            if (nw == 1) v = make_variant<kKernelMma16, T, D, 1, kGen, kSinks>();
+            return nw == 1;
+        } else {
+            return false;
+        }
+    }
     if (kind == kKernelMma) {
         if constexpr (std::is_same<T, float>::value ||
                       ((std::is_same<T, int8_t>::value || std::is_same<T, __nv_fp8_e4m3>::value ||

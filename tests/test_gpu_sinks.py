@@ -73,6 +73,52 @@ def test_several_new_tokens(gq, H, K, T, dtype, d, layout):
         assert max_abs_err(out, ref) <= TOL, (window, sinks)
 
 
+@pytest.mark.parametrize("H,K,T", [(36, 4, 1), (16, 1, 1), (20, 4, 3), (16, 2, 2), (2, 2, 11), (80, 8, 1)])
+@pytest.mark.parametrize("dtype", ["i8", "fp8", "i4"])
+def test_nine_to_sixteen_rows_of_coded_caches(gq, dtype, H, K, T):
+    """One warp serves the 16 rows of a pair: every layout, few and many splits, tokens
+    that nobody sees behind NaN scales, rows past G T, empty sequences."""
+    lens = [1, T, 15, 16, 17, 40, 257, 0, 601, 90]
+    case = gi.make_case(len(lens), H, K, 128, lens, dtype, seed=40 + H, device="cuda", queries=T)
+    for window, sinks in ((1, 1), (7, 3), (33, 20), (100, 16), (40, 2000)):
+        ref = attend_case(case, window, sinks)
+        table = _poisoned(case, window, sinks, [T] * len(lens))
+        for kw in (dict(), dict(max_warps=3, min_blocks_per_warp=1), dict(min_blocks_per_warp=1), dict(row_layout=2)):
+            out = _decode(gq, case, table, window=window, sinks=sinks, **kw)
+            assert max_abs_err(out, ref) <= TOL, (window, sinks, kw)
+    W, S = 21, 5
+    ref = attend_case(case, W, S)
+    for b, L in enumerate(lens):
+        seen_from = L - T + 1 - W
+        for t in range(S, max(0, seen_from)):
+            p = int(case.block_table[b, t // 16])
+            case.k_scale[p, :, t % 16] = float("nan")
+            case.v_scale[p, :, t % 16] = float("nan")
+        for t in range(L, -(-L // 16) * 16):
+            p = int(case.block_table[b, t // 16])
+            case.k_scale[p, :, t % 16] = float("nan")
+            case.v_scale[p, :, t % 16] = float("nan")
+    assert max_abs_err(_decode(gq, case, window=W, sinks=S), ref) <= TOL
+    for t, eps in ((torch.bfloat16, 2.0 ** -8), (torch.float16, 2.0 ** -11)):
+        got = _decode(gq, case, window=W, sinks=S, out_dtype=t).double().cpu().numpy()
+        assert np.all(np.abs(got - ref) <= TOL + np.abs(ref) * eps)
+
+
+def test_a_scratch_without_room_for_the_sixteen_row_workers(gq):
+    """880 x 8 pairs of 16 rows and 1216 workers exceed the 64 MB scratch, 608 do not."""
+    lens = [5 + b % 60 for b in range(880)]
+    case = gi.make_case(len(lens), 64, 8, 128, lens, "fp8", seed=39, device="cuda", queries=2)
+    want = _decode(gq, case, window=30, sinks=4)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = gq.gqa_decode_noalloc(gq.cache_from_case(case), case.q, case.block_table, case.context_lens, case.scale,
+                                window=30, sinks=4, err=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0 and float((got - want).abs().max()) <= TOL
+    part = [0, 1, 30, 59, 879]
+    ref = attend_case(case, 30, 4)
+    assert max(float(np.abs(got[b].double().cpu().numpy() - ref[b]).max()) for b in part) <= TOL
+
+
 def test_no_sinks_and_no_window_are_the_calls_without(gq):
     case = gi.make_case(len(LENS), 32, 8, 128, LENS, "bf16", seed=33, device="cuda")
     assert torch.equal(_decode(gq, case, window=40, sinks=0), _decode(gq, case, window=40))
