@@ -277,58 +277,71 @@ __device__ __forceinline__ void rotate(float& a, float& b, float c, float s) {
     b = y;
 }
 
-// Codes and scale of one row (two 8-element chunks a lane, kLanes lanes a row), by the
+// Codes and scales of kN rows (two 8-element chunks a lane, kLanes lanes a row), by the
 // append's rule: s = fp16(min(amax / qmax, 65504)), code = x / s rounded to nearest
 // even and clamped. The quotient is the correctly rounded one: with y = RN(1/s), once
 // a row, q = RN(x y) and the exact remainder x - q s, RN(q + (x - q s) y) is RN(x / s)
 // (Markstein's theorem; s has 11 significant bits, so its mantissa is not all ones,
 // and no step leaves fp32's range where the code is not zero), at three instructions
 // instead of a division; amax / qmax goes the same way (an infinite amax ends at 65504
-// as its quotient would). A row with an infinity divides.
-template <int kOut, int kLanes>
-__device__ __forceinline__ void quantise_store(const float (&x0)[8], const float (&x1)[8], bool live, uint8_t* row,
-                                               int c0, int c1, __half* scale, bool first) {
+// as its quotient would); an infinity and a NaN are their own quotients. The rows' maxima
+// and reciprocals go by together, which hides their latency.
+template <int kOut, int kLanes, int kN>
+__device__ __forceinline__ void quantise_store(const float (&x0)[kN][8], const float (&x1)[kN][8], bool live,
+                                               uint8_t* const (&row)[kN], int c0, int c1, __half* const (&scale)[kN],
+                                               bool first) {
     constexpr float kQmax = kOut == kOutFp8 ? 448.0f : kOut == kOutI4 ? 7.0f : 127.0f;
-    float amax = 0.f;
+    float amax[kN] = {};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fmaxf(fabsf(x0[e]), fabsf(x1[e])));
+    for (int u = 0; u < kN; ++u)
 #pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
-    constexpr float kInv = 1.0f / kQmax;     // RN(1 / qmax), folded by the compiler
-    const float s0 = amax * kInv;
-    const __half sh = __float2half_rn(fminf(fmaf(fmaf(-s0, kQmax, amax), kInv, s0), 65504.0f));
-    const float sf = __half2float(sh);
+        for (int e = 0; e < 8; ++e) amax[u] = fmaxf(amax[u], fmaxf(fabsf(x0[u][e]), fabsf(x1[u][e])));
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int u = 0; u < kN; ++u) amax[u] = fmaxf(amax[u], __shfl_xor_sync(kFull, amax[u], o));
     if (!live) return;
-    const float y = __frcp_rn(sf);
-    const bool finite = amax < INFINITY;
-    auto quotient = [&](float x) {
-        const float q = x * y;
-        return finite ? fmaf(fmaf(-q, sf, x), y, q) : __fdiv_rn(x, sf);
-    };
+    __half sh[kN];
+    float sf[kN], y[kN];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        uint32_t w[2] = {0u, 0u};
-        if (sf != 0.f) {
+    for (int u = 0; u < kN; ++u) {
+        constexpr float kInv = 1.0f / kQmax;     // RN(1 / qmax), folded by the compiler
+        const float s0 = amax[u] * kInv;
+        sh[u] = __float2half_rn(fminf(fmaf(fmaf(-s0, kQmax, amax[u]), kInv, s0), 65504.0f));
+        sf[u] = __half2float(sh[u]);
+        y[u] = __frcp_rn(sf[u]);
+    }
 #pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-                const float t0 = quotient(h ? x1[e] : x0[e]), t1 = quotient(h ? x1[e + 1] : x0[e + 1]);
-                if constexpr (kOut == kOutFp8) {
-                    const uint32_t two = __nv_cvt_float2_to_fp8x2(make_float2(t0, t1), __NV_SATFINITE, __NV_E4M3);
-                    w[e / 4] |= two << (16 * (e / 2 % 2));
-                } else {
-                    constexpr int qm = (int)kQmax;
-                    const uint32_t a = (uint32_t)max(-qm, min(qm, __float2int_rn(t0)));
-                    const uint32_t b = (uint32_t)max(-qm, min(qm, __float2int_rn(t1)));
-                    if constexpr (kOut == kOutI4) w[0] |= ((a & 0xFu) | ((b & 0xFu) << 4)) << (4 * e);
-                    else w[e / 4] |= ((a & 0xFFu) | ((b & 0xFFu) << 8)) << (16 * (e / 2 % 2));
+    for (int u = 0; u < kN; ++u) {
+        auto quotient = [&](float x) {
+            const float q = x * y[u];
+            return fabsf(x) < INFINITY ? fmaf(fmaf(-q, sf[u], x), y[u], q) : x;
+        };
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t w[2] = {0u, 0u};
+            if (sf[u] != 0.f) {
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) {
+                    const float t0 = quotient(h ? x1[u][e] : x0[u][e]), t1 = quotient(h ? x1[u][e + 1] : x0[u][e + 1]);
+                    if constexpr (kOut == kOutFp8) {
+                        const uint32_t two = __nv_cvt_float2_to_fp8x2(make_float2(t0, t1), __NV_SATFINITE, __NV_E4M3);
+                        w[e / 4] |= two << (16 * (e / 2 % 2));
+                    } else {
+                        constexpr int qm = (int)kQmax;
+                        const uint32_t a = (uint32_t)max(-qm, min(qm, __float2int_rn(t0)));
+                        const uint32_t b = (uint32_t)max(-qm, min(qm, __float2int_rn(t1)));
+                        if constexpr (kOut == kOutI4) w[0] |= ((a & 0xFu) | ((b & 0xFu) << 4)) << (4 * e);
+                        else w[e / 4] |= ((a & 0xFFu) | ((b & 0xFFu) << 8)) << (16 * (e / 2 % 2));
+                    }
                 }
             }
+            const int c = h ? c1 : c0;
+            if constexpr (kOut == kOutI4) *reinterpret_cast<uint32_t*>(row[u] + 4 * c) = w[0];
+            else *reinterpret_cast<uint2*>(row[u] + 8 * c) = make_uint2(w[0], w[1]);
         }
-        const int c = h ? c1 : c0;
-        if constexpr (kOut == kOutI4) *reinterpret_cast<uint32_t*>(row + 4 * c) = w[0];
-        else *reinterpret_cast<uint2*>(row + 8 * c) = make_uint2(w[0], w[1]);
+        if (first) *scale[u] = sh[u];
     }
-    if (first) *scale = sh;
 }
 
 // Where a token goes: its cache position and table row, or why it goes nowhere.
@@ -564,14 +577,19 @@ __global__ void __launch_bounds__(kRopeWarps * 32, RopeShape<T, kOut>::kCtas) no
                     if constexpr (kCoded) {
                         if ((u + v) * kRows >= rows) break;
                         const long long at = kOut == kOutI4 ? off / 2 : off;
-                        quantise_store<kOut, kLanes>(x0[v], x1[v], in, static_cast<uint8_t*>(a.k_cache) + at, c0, c1,
-                                                     a.k_scale + sidx, li == 0);
+                        float y0[2][8], y1[2][8];        // the K row and the V row
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            y0[0][e] = x0[v][e];
+                            y1[0][e] = x1[v][e];
+                        }
                         Raw8<T> r0, r1;
                         row_of(kKvSteps + u + v, r0, r1);
-                        widen8(r0, x0[v]);
-                        widen8(r1, x1[v]);
-                        quantise_store<kOut, kLanes>(x0[v], x1[v], in, static_cast<uint8_t*>(a.v_cache) + at, c0, c1,
-                                                     a.v_scale + sidx, li == 0);
+                        widen8(r0, y0[1]);
+                        widen8(r1, y1[1]);
+                        uint8_t* const to[2] = {static_cast<uint8_t*>(a.k_cache) + at, static_cast<uint8_t*>(a.v_cache) + at};
+                        __half* const scale[2] = {a.k_scale + sidx, a.v_scale + sidx};
+                        quantise_store<kOut, kLanes, 2>(y0, y1, in, to, c0, c1, scale, li == 0);
                     } else if (in) {
                         T* ko = static_cast<T*>(a.k_cache) + off + 8 * c0;
                         store8r(ko, narrow8<T>(x0[v]));
