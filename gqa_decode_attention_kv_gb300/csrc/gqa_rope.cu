@@ -97,10 +97,10 @@ struct RopeCfg {
 // steps of a warp. Two rows overlap their shuffles and roots and need 128 registers (4
 // CTAs); quantised rows go one by one, their compensated arithmetic taking the registers.
 // Measured, 16384 tokens of 32 + 8 bf16 heads, d = 128, one row at 5 / two at 4 / two at
-// 5 CTAs: 69.3 / 67.3 / 70 us; 13.7k ragged tokens of 24 + 8 heads, d = 64, onto an FP8
-// cache, one row at 5 / 4 / 3 CTAs, two at 4: 40.5 / 33.5 / 35.1 / 44.8 us. A quantised
-// step of K and V takes a warp about as long as four query steps, so its warp holds one:
-// two made it the last to finish (16384 tokens, d = 128, FP8: 110 against 81 us).
+// 5 CTAs: 69.3 / 67.3 / 70 us; 14.3k tokens of 24 + 8 heads, d = 64, onto an FP8
+// cache, one row at 5 / 4 CTAs, two at 4: 47.8 / 27.6 / 38.1 us. A
+// quantised step of K and V takes a warp longer than four query steps, so its warp holds
+// one: two make it the last to finish (16384 tokens, d = 128, FP8: 86.9 against 68.0 us).
 template <typename T, int kOut>
 struct RopeShape {
     static constexpr bool kTwo = sizeof(T) == 2 && kOut <= kOutCache;
@@ -240,7 +240,7 @@ __device__ __forceinline__ void norm_rows(float (&x0)[kN][8], float (&x1)[kN][8]
     for (int u = 0; u < kN; ++u) {
         const float m = fmaf(ss[u], 1.f / D, eps);
         if constexpr (kExact) {
-            const float r = 1.f / sqrtf(m);
+            const float r = rsqrtf(m);
             const float mr = m * r, mr_lo = fmaf(m, r, -mr);
             float r_lo = 0.5f * r * (fmaf(-mr, r, 1.f) - mr_lo * r);   // r (1 - m r^2) / 2
             if (!(fabsf(r_lo) < r)) r_lo = 0.f;                        // m = 0 or not finite: r alone
@@ -740,8 +740,7 @@ cudaError_t launch_norm_rope(const NormRopeLaunch& L) {
     // Not where most of the warps' rows are empty, nor for quantised rows: these are bound
     // by issue, and a run's start costs them more. Measured, one / eight waves, 32 + 8
     // heads, d = 128: 73.8 / 63.5 us for 400 MB, 37.3 / 36.3 for 200, 14.4 / 17.7 for 98;
-    // 8 + 1 heads (31% of the rows), 334 MB: 83.9 / 88.7; FP8 cache, 370 MB, one / two /
-    // four: 81 / 84 / 86.
+    // 8 + 1 heads (31% of the rows), 334 MB: 83.9 / 88.7; FP8 cache, 370 MB: 68.0 / 74.1.
     const int esize = L.dtype == GQA_DTYPE_F32 ? 4 : 2;
     const bool streams = 2 * a.tokens * (a.H + 2 * a.K) * L.head_dim * esize >= (256LL << 20);
     const bool filled = 2 * (a.H + 2 * a.K) >= a.parts * rows * kRopeSteps;
