@@ -950,8 +950,10 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 // (four 16 KB stages each). Per-chunk barriers (stages, S done, P ready, P.V done)
 // come in four copies taken in turn by chunk and the block masks in eight, so
 // that no parity wait can fall two phases behind (as in the 32-token kernel).
-// kParts: 16-bit parts P is kept in, 2, or 1 for the 16-bit outputs of the forms with
-// sinks (8 x 2048 tokens, W = 1024, S = 4, 32 + 8 heads of 128: 343 and 281 us).
+// P is kept in two 16-bit parts whatever the output's type: one part would save a third
+// of the MMAs (8 x 2048 tokens, W = 1024, S = 4, 32 + 8 heads of 128: 281 for 343 us),
+// but round every weight to the cache's type, for bf16 caches 8 times coarser than an
+// f16 output.
 // 16-byte cp.async into shared memory; src_bytes < 16 zero-fills the rest.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t src_bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
@@ -1026,7 +1028,7 @@ struct W2Cfg {
     static_assert(kSmem * kCtasPerSm <= 227 * 1024, "CTAs per SM fit the shared memory");
 };
 
-template <typename T, int kTiles, int kDim, bool kSinks, int kParts>
+template <typename T, int kTiles, int kDim, bool kSinks>
 __global__ void __launch_bounds__(W2Cfg<kTiles, kDim>::kThreads, W2Cfg<kTiles, kDim>::kCtasPerSm)
 prefill_tc2_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                    const __grid_constant__ CUtensorMap omap, const PrefillArgs a) {
@@ -1288,8 +1290,8 @@ prefill_tc2_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
 #pragma unroll
                 for (int jl = 0; jl < kW2Blocks; ++jl)
 #pragma unroll
-                    for (int part = 0; part < kParts; ++part)
-                        tc_mma_f16_ta(tmem + kW2ColTile * t + kW2ColO, pb + 8 * kParts * jl + 8 * part,
+                    for (int part = 0; part < 2; ++part)
+                        tc_mma_f16_ta(tmem + kW2ColTile * t + kW2ColO, pb + 16 * jl + 8 * part,
                                       smem_desc_sw128(vb + jl * C::kVb, kBlock * 128, 1024), kIdescO,
                                       !(first && jl == 0 && part == 0));
             };
@@ -1476,37 +1478,22 @@ prefill_tc2_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 const uint64_t mu2 = f2_make(mu, mu);
                 uint64_t ps2[2] = {f2_make(0.f, 0.f), f2_make(0.f, 0.f)};
                 // P over S: block jl's 16 tokens to columns [16jl, 16jl+16) of the
-                // buffer, 8 high then 8 low columns (kParts 1: to [8jl, 8jl+8))
-                if constexpr (kParts == 1) {
+                // buffer, 8 high then 8 low columns
 #pragma unroll
-                    for (int jl = 0; jl < kW2Blocks; jl += 2) {
-                        uint32_t w16[16];
+                for (int jl = 0; jl < kW2Blocks; ++jl) {
+                    uint32_t w16[16];
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const float2 d = f2_split(f2_sub(f2_make(sv[16 * jl + 2 * e], sv[16 * jl + 2 * e + 1]), mu2));
-                            const float x = fast_exp2(d.x), y = fast_exp2(d.y);
-                            ps2[e & 1] = f2_add(ps2[e & 1], f2_make(x, y));
-                            w16[e] = pack2<kB>(x, y);
-                        }
-                        tmem_st16(t_buf + 8 * jl, w16);
+                    for (int e = 0; e < 8; ++e) {
+                        const float2 d = f2_split(f2_sub(f2_make(sv[16 * jl + 2 * e], sv[16 * jl + 2 * e + 1]), mu2));
+                        const float x = fast_exp2(d.x), y = fast_exp2(d.y);
+                        const uint64_t xy = f2_make(x, y);
+                        ps2[e & 1] = f2_add(ps2[e & 1], xy);
+                        w16[e] = pack2<kB>(x, y);
+                        const float2 f = unpack2<kB>(w16[e]);
+                        const float2 r = f2_split(f2_sub(xy, f2_make(f.x, f.y)));
+                        w16[8 + e] = pack2<kB>(r.x, r.y);
                     }
-                } else {
-#pragma unroll
-                    for (int jl = 0; jl < kW2Blocks; ++jl) {
-                        uint32_t w16[16];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float2 d = f2_split(f2_sub(f2_make(sv[16 * jl + 2 * e], sv[16 * jl + 2 * e + 1]), mu2));
-                            const float x = fast_exp2(d.x), y = fast_exp2(d.y);
-                            const uint64_t xy = f2_make(x, y);
-                            ps2[e & 1] = f2_add(ps2[e & 1], xy);
-                            w16[e] = pack2<kB>(x, y);
-                            const float2 f = unpack2<kB>(w16[e]);
-                            const float2 r = f2_split(f2_sub(xy, f2_make(f.x, f.y)));
-                            w16[8 + e] = pack2<kB>(r.x, r.y);
-                        }
-                        tmem_st16(t_buf + 16 * jl, w16);
-                    }
+                    tmem_st16(t_buf + 16 * jl, w16);
                 }
                 tmem_wait_st();
                 {
@@ -1622,17 +1609,14 @@ prefill_tc2_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     if (warp == 0) tmem_dealloc(tmem, C::kTmemCols);
 }
 
-// one_part: sinks and a 16-bit output
 template <typename T, int kTiles>
-const void* prefill_tc2_fn(bool sinks, bool one_part) {
-    return one_part ? reinterpret_cast<const void*>(&prefill_tc2_kernel<T, kTiles, 128, true, 1>)
-           : sinks  ? reinterpret_cast<const void*>(&prefill_tc2_kernel<T, kTiles, 128, true, 2>)
-                    : reinterpret_cast<const void*>(&prefill_tc2_kernel<T, kTiles, 128, false, 2>);
+const void* prefill_tc2_fn(bool sinks) {
+    return sinks ? reinterpret_cast<const void*>(&prefill_tc2_kernel<T, kTiles, 128, true>)
+                 : reinterpret_cast<const void*>(&prefill_tc2_kernel<T, kTiles, 128, false>);
 }
 template <typename T>
-const void* prefill_tc2_64_fn(bool one_part) {
-    return one_part ? reinterpret_cast<const void*>(&prefill_tc2_kernel<T, 1, 64, true, 1>)
-                    : reinterpret_cast<const void*>(&prefill_tc2_kernel<T, 1, 64, true, 2>);
+const void* prefill_tc2_64_fn() {
+    return reinterpret_cast<const void*>(&prefill_tc2_kernel<T, 1, 64, true>);
 }
 
 template <typename T, int D>
@@ -1672,23 +1656,18 @@ int launch_prefill(const PrefillLaunch& L) {
     const bool wide1 = tc && D == 128 && (few || L.kernel == GQA_PREFILL_TCGEN05_PAIRED);
     const bool wide64 = tc && D == 64 && sinks && L.kernel == GQA_PREFILL_AUTO;
     const bool wide = wide1 || wide2 || wide64;
-    // A 16-bit output takes P as one 16-bit part: each weight is off by half a step of
-    // the cache's type at most (2^-8 bf16, 2^-11 fp16), as the output's rounding is;
-    // the row sums stay fp32 sums of the unrounded weights. It saves a third of the MMAs
-    // and the softmax warps' second rounding. fp32 outputs keep both parts.
-    const bool one_part = sinks && L.out_dtype != GQA_DTYPE_F32;
     const int rows_per_cta = wide2 ? W2Cfg<2>::kRows : wide1 || wide64 ? W2Cfg<1>::kRows : tc ? kTcRows : kPfRows;
     const void* fn = nullptr;
     int smem = 0;
     if (wide64) {
         if (c.dtype != GQA_DTYPE_BF16 && c.dtype != GQA_DTYPE_F16) return GQA_ERR_UNSUPPORTED;
-        fn = c.dtype == GQA_DTYPE_BF16 ? prefill_tc2_64_fn<__nv_bfloat16>(one_part) : prefill_tc2_64_fn<__half>(one_part);
+        fn = c.dtype == GQA_DTYPE_BF16 ? prefill_tc2_64_fn<__nv_bfloat16>() : prefill_tc2_64_fn<__half>();
         smem = W2Cfg<1, 64>::kSmem;
     } else if (wide) {
         if (c.dtype != GQA_DTYPE_BF16 && c.dtype != GQA_DTYPE_F16) return GQA_ERR_UNSUPPORTED;
         const bool bf = c.dtype == GQA_DTYPE_BF16;
-        fn = wide2 ? (bf ? prefill_tc2_fn<__nv_bfloat16, 2>(sinks, one_part) : prefill_tc2_fn<__half, 2>(sinks, one_part))
-                   : (bf ? prefill_tc2_fn<__nv_bfloat16, 1>(sinks, one_part) : prefill_tc2_fn<__half, 1>(sinks, one_part));
+        fn = wide2 ? (bf ? prefill_tc2_fn<__nv_bfloat16, 2>(sinks) : prefill_tc2_fn<__half, 2>(sinks))
+                   : (bf ? prefill_tc2_fn<__nv_bfloat16, 1>(sinks) : prefill_tc2_fn<__half, 1>(sinks));
         smem = wide2 ? W2Cfg<2>::kSmem : W2Cfg<1>::kSmem;
     } else if (c.dtype == GQA_DTYPE_BF16) {
         if (tc) {

@@ -459,8 +459,6 @@ GQA_API int gqa_prefill(const gqa_kv_cache_t *cache, const void *q, int32_t q_dt
  *                    not: it picks the schedule of ragged batches and changes no result.
  *  kernel            GQA_PREFILL_AUTO goes by size (one- or two-tile CTAs at head_dim
  *                    128, a 64-token-chunk form at head_dim 64).
- *  out_dtype         BF16 and F16 outputs of those forms take the softmax weights
- *                    rounded once to the cache's type (F32: as two parts of it).
  */
 GQA_API int gqa_prefill_sinks(const gqa_kv_cache_t *cache, const void *q, int32_t q_dtype, int32_t num_heads,
                 const int32_t *q_start, int32_t max_new_tokens, const int32_t *block_tables,
