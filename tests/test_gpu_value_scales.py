@@ -3,9 +3,11 @@ weights times V's scales go through 16-bit parts, which must not depend on how l
 
 Bound. A score errs by at most d 2^-24 sum |q_i k_i| scale (fp32 sums) and 2^-22 of itself;
 what q loses as fp16 below 2^-14, and with K's channel scales as two parts, is 2^-25 of an
-element of K's row or of its codes (at most 7 each); exp2 errs by 2^-22, the row's sum by n
-2^-24; a weight times its scale is kept as two fp16 parts, 2^-21 of itself, or 2^-33 of the
-largest scale where it is that small. Weights off by e move the output by e (sum w |v| +
+element of K's row or of its codes (at most 7 each); exp2 errs by 2^-22 and its argument, below
+27 + 8 for scales of 2^-24 and a maximum 2^8 times the one of the last rescale, by 2^-19, the
+row's sum by n 2^-24; a weight times its scale is kept as two fp16 parts, 2^-21 of itself, or,
+the largest scale being put above 2^3 and half the low part's step being 2^-25, 2^-28 of that
+one. Weights off by e move the output by e (sum w |v| +
 |out|), the sums of P.V and over the splits by n 2^-24 sum w |v|."""
 import numpy as np
 import pytest
@@ -55,9 +57,10 @@ def _reference(case, window, sinks):
         s_abs = max(float((np.abs(qb[:, h]) @ np.abs(k[:, h // G]).T).max()) for h in range(H)) * case.scale
         k_abs = float(np.abs(k).sum(-1).max()) + 7 * d
         seen = L if window == 0 else min(L, window + sinks + 16)
-        e = s_abs * (d * 2.0 ** -24 + 2.0 ** -22) + k_abs * case.scale * 2.0 ** -25 + 2.0 ** -22 + seen * 2.0 ** -24 + 2.0 ** -21
+        e = s_abs * (d * 2.0 ** -24 + 2.0 ** -22) + k_abs * case.scale * 2.0 ** -25 + 2.0 ** -19 + 2.0 ** -22 + seen * 2.0 ** -24 \
+            + 2.0 ** -21
         ref[b, T - n:] = out
-        bound[b, T - n:] = 1.01 * e * (spread + np.abs(out)) + seen * (2.0 ** -24 * spread + 2.0 ** -33 * np.abs(v).max()) \
+        bound[b, T - n:] = 1.01 * e * (spread + np.abs(out)) + seen * (2.0 ** -24 * spread + 2.0 ** -28 * np.abs(v).max()) \
             + 2.0 ** -140
     return ref, bound
 
