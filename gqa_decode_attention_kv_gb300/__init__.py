@@ -361,7 +361,19 @@ def decode_workspace_size(batch: int, num_heads: int, num_kv_heads: int, head_di
 
 
 _workspace_size_of = functools.lru_cache(maxsize=256)(decode_workspace_size)   # a shape's size does not change
-_ws_cache: dict = {}
+
+
+class _ThreadScratch(threading.local):
+    """Workspaces of the calls of one host thread, per (device, stream). A call queues
+    kernels that hand their results on through its workspace, and the interpreter may
+    change threads between two of them: threads on one stream must not share it."""
+
+    def __init__(self):
+        self.decode: dict = {}
+        self.pages: dict = {}
+
+
+_thread_scratch = _ThreadScratch()
 
 
 def _capturing(stream) -> bool:
@@ -372,8 +384,8 @@ def _capturing(stream) -> bool:
 
 
 def _scratch(cache: dict, need: int, idx: int, stream, zero: bool) -> torch.Tensor:
-    """``need`` bytes of device scratch: cached per (device, stream), or a captured
-    call's own."""
+    """``need`` bytes of device scratch: kept in the thread's ``cache`` per (device,
+    stream), or a captured call's own."""
     capturing = _capturing(stream)
     key = (idx, stream.cuda_stream if stream is not None else
            _raw_stream(idx) if _raw_stream is not None else
@@ -392,8 +404,9 @@ def _scratch(cache: dict, need: int, idx: int, stream, zero: bool) -> torch.Tens
 def workspace_for(batch: int, num_heads: int, num_kv_heads: int, head_dim: int,
                   device: torch.device, tokens_per_seq: int = 1, stream=None) -> torch.Tensor:
     """A cached, zero-initialised device workspace large enough for this shape,
-    one per (device, stream): calls on one stream run in order, so they may
-    share it; calls on different streams get different workspaces. The buffer
+    one per (host thread, device, stream): a thread's calls on one stream run in
+    order, so they may share it; calls of other threads or on other streams get
+    others. The buffer
     is allocated on that stream, so a larger one replacing it is ordered after
     the calls already queued there. A call that is being captured gets one of its
     own from the graph's memory, zeroed by the graph: graphs captured on one
@@ -404,7 +417,7 @@ def workspace_for(batch: int, num_heads: int, num_kv_heads: int, head_dim: int,
     if need == 0:
         raise ValueError("no workspace size for this shape")
     # zero-filled once: the library keeps its run-time work counter at zero between calls
-    return _scratch(_ws_cache, need, idx, stream, zero=True)
+    return _scratch(_thread_scratch.decode, need, idx, stream, zero=True)
 
 
 def gqa_decode(cache: PagedKVCache, q: torch.Tensor, block_tables: torch.Tensor,
@@ -700,23 +713,20 @@ class PageCopies:
     rows: Optional[torch.Tensor] = None
 
 
-_pages_ws_cache: dict = {}
-
-
 @functools.lru_cache(maxsize=256)
 def _pages_workspace_size(num_blocks: int, rows: int) -> int:
     return int(load().gqa_kv_pages_workspace_size(num_blocks, rows))
 
 
 def _pages_workspace(num_blocks: int, rows: int, device: torch.device, workspace, stream) -> torch.Tensor:
-    """The caller's workspace, or one per (device, stream) as ``workspace_for`` keeps."""
+    """The caller's workspace, or one per (host thread, device, stream) as ``workspace_for`` keeps."""
     if workspace is not None:
         _dev(workspace, "workspace")
         return workspace
     need = _pages_workspace_size(num_blocks, rows)
     if need == 0:
         raise ValueError(f"no workspace size for {num_blocks} pages and {rows} rows")
-    return _scratch(_pages_ws_cache, need, device.index, stream, zero=False)
+    return _scratch(_thread_scratch.pages, need, device.index, stream, zero=False)
 
 
 def _check_pool(ref_counts: torch.Tensor, block_tables: torch.Tensor, lens: Optional[torch.Tensor], **more):
