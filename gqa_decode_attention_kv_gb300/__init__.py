@@ -854,7 +854,9 @@ def kv_pages_compact(ref_counts: torch.Tensor, block_tables: torch.Tensor, max_c
     """Moves the highest live pages into the lowest holes until the live pages are the
     pool's first ones, ``max_copies`` of them at most (default: as many as it takes).
     ``kv_copy_pages`` applies the list returned; its count[1] is the number of live
-    pages. ``block_tables`` must hold every entry that names a page of the pool."""
+    pages. ``block_tables`` must hold every entry that names a page of the pool.
+    ``rows`` that an earlier fork left in a list given as ``copies`` become (-1, -1):
+    a compaction moves no table rows."""
     ep = _dev(err, "err", True, True)
     _check_pool(ref_counts, block_tables, None, err=err, workspace=workspace)
     nb = int(ref_counts.shape[0])
@@ -868,6 +870,9 @@ def kv_pages_compact(ref_counts: torch.Tensor, block_tables: torch.Tensor, max_c
         n = int(copies.pairs.shape[0]) if max_copies is None else int(max_copies)
         if not 0 <= n <= copies.pairs.shape[0] or copies.count.numel() < 2:
             raise ValueError(f"copies must have room for {n} pairs and two counts")
+        if copies.rows is not None:
+            with torch.cuda.stream(stream):              # (None: the current one)
+                copies.rows.fill_(-1)
     ws = _pages_workspace(nb, 0, ref_counts.device, workspace, stream)
     st = load().gqa_kv_pages_compact(ref_counts.data_ptr(), nb, block_tables.data_ptr(), int(block_tables.shape[0]),
                                      int(block_tables.shape[1]), copies.pairs.data_ptr(), n, copies.count.data_ptr(),
