@@ -378,6 +378,8 @@ int gqa_kv_pages_reserve(int32_t* ref_counts, int64_t num_blocks, int32_t* block
     if (!new_tokens && tokens_per_seq < 0) return GQA_ERR_INVALID;
     if (batch == 0 || (!new_tokens && tokens_per_seq == 0)) return GQA_OK;
     if (!context_lens) return GQA_ERR_INVALID;
+    // the ranks of the pages asked for are 32-bit sums over the rows
+    if ((long long)batch * max_blocks_per_seq > 0x7fffffffLL) return GQA_ERR_UNSUPPORTED;
     if ((st = check_pages_ws(workspace, workspace_bytes, num_blocks, batch)) != GQA_OK) return st;
     PagesLaunch L = {};
     L.ref_counts = ref_counts;

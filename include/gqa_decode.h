@@ -334,6 +334,7 @@ GQA_API size_t gqa_kv_pages_workspace_size(int64_t num_blocks, int32_t rows);
  * A row that the free pages do not cover whole gets none, and neither do the rows
  * after it that need any (GQA_DEVERR_NO_PAGES); a row with L < 0, n < 0 or L + n beyond its table
  * gets none (GQA_DEVERR_POSITION). batch <= table_rows; context_lens is not changed.
+ * GQA_ERR_UNSUPPORTED for tables of 2^31 entries or more (batch * max_blocks_per_seq).
  */
 GQA_API int gqa_kv_pages_reserve(int32_t *ref_counts, int64_t num_blocks, int32_t *block_tables,
                   int32_t max_blocks_per_seq, const int32_t *context_lens, const int32_t *new_tokens,
