@@ -541,7 +541,7 @@ def _token_rows(t: torch.Tensor, name: str, like: torch.Tensor, heads: Optional[
         sn, sh, sd = t.stride()
         if (n == like.shape[0] and d == like.shape[2] and t.dtype is like.dtype and t.dtype in _ROW_DTYPES and sd == 1
                 and sh == d and sn >= H * d and (heads is None or H == heads) and t.is_cuda):
-            return t.data_ptr(), sn
+            return t.data_ptr(), sn if n > 1 else H * d          # one token has no next one
     if t.dim() not in (3, 4) or tuple(t.shape[:-2]) != tuple(like.shape[:-2]) or t.shape[-1] != like.shape[-1]:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, which does not go with q's {tuple(like.shape)}")
     if heads is not None and t.shape[-2] != heads:
