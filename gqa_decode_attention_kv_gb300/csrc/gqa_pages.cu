@@ -650,7 +650,9 @@ cudaError_t launch_pdl(const void* fn, unsigned grid, int threads, int smem, cud
 
 cudaError_t launch_pages(void (*fn)(PageArgs), long long threads_wanted, int threads, int smem, const PageArgs& a,
                          cudaStream_t stream) {
-    const long long most = 152LL * 8;
+    const int sms = device_sms(-1);
+    if (sms < 1) return cudaErrorInvalidDevice;
+    const long long most = sms * 8LL;
     const long long grid = std::min(most, std::max(1LL, (threads_wanted + threads - 1) / threads));
     void* args[] = {const_cast<PageArgs*>(&a)};
     return launch_pdl(reinterpret_cast<const void*>(fn), (unsigned)grid, threads, smem, stream, args);
