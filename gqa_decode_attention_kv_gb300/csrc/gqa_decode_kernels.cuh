@@ -103,21 +103,18 @@ struct DecodeArgs {
 #define GQA_MIN_CTAS_PER_SM_I8 3
 #endif
 // The one-token INT4 tensor-core kernel (per-token scales) fits 128 registers
-// without spilling, so it runs 4 CTAs (16 warps) per SM, with a ring of five
-// 2.5 KB stages per warp so that four CTAs fit in shared memory. Measured on
-// the B=128 ragged INT4 workload: 2852 against 2647 GB/s at 3 CTAs and six
-// stages; four stages 2807. int8, FP8 and the KIVI-style cache spill at 128.
+// but for four spilled words, so it runs 4 CTAs (16 warps) per SM, with a ring
+// of five 2.5 KB stages per warp so that four CTAs fit in shared memory.
+// Measured on the B=128 ragged INT4 workload, before the weights' lift: 2852
+// against 2647 GB/s at 3 CTAs and six stages; four stages 2807. int8, FP8 and
+// the KIVI-style cache spill more at 128.
 #ifndef GQA_MIN_CTAS_PER_SM_I4
 #define GQA_MIN_CTAS_PER_SM_I4 4
 #endif
 #ifndef GQA_RING_BYTES_PER_WARP_I4
 #define GQA_RING_BYTES_PER_WARP_I4 12800
 #endif
-// Ring bytes of a CTA whose warps share one ring (groups of more than 8 heads).
-// Measured on the T = 4, G = 16 and G = 64 workloads at 12 warps per SM with
-// the copy warp: 32 KB (four bf16 stages) beats 24 KB by 2-4% and ties 40 KB;
-// 16 KB loses 5%.
-// The 16-row kernel: 235 to 249 registers a thread, so two CTAs of four warps (at three
+// The 16-row kernel: 234 to 251 registers a thread, so two CTAs of four warps (at three
 // CTAs it spills and takes 83 us where it takes 44 as it is, FP8, 48 sequences, below).
 #ifndef GQA_MIN_CTAS_PER_SM_R16
 #define GQA_MIN_CTAS_PER_SM_R16 2
@@ -125,6 +122,10 @@ struct DecodeArgs {
 #ifndef GQA_RING_BYTES_PER_WARP_R16
 #define GQA_RING_BYTES_PER_WARP_R16 20480
 #endif
+// Ring bytes of a CTA whose warps share one ring (groups of more than 8 heads).
+// Measured on the T = 4, G = 16 and G = 64 workloads at 12 warps per SM with
+// the copy warp: 32 KB (four bf16 stages) beats 24 KB by 2-4% and ties 40 KB;
+// 16 KB loses 5%.
 #ifndef GQA_SHARED_RING_BYTES
 #define GQA_SHARED_RING_BYTES 32768
 #endif
@@ -153,8 +154,10 @@ constexpr int kHeadsPerWarp = 8;   // query heads one warp serves (the MMA N dim
 // like the other coded kernels, of whose ~450 instructions per block and warp half widen
 // codes: here a block is widened once for 16 rows, where two warps of 8 rows each widen
 // it all. Measured, shared ring with two row warps / this: 48 sequences of 300 to 8192
-// tokens, W = 1000, S = 20, T = 2, G = 8: FP8 53.9 / 43.8 us, int8 52.9 / 43.5, int4
-// 51.9 / 41.8; 9 rows (T = 1) 50.6 / 42.0; 16 sequences 28.7 / 28.8; one 16.0 / 16.8.
+// tokens, W = 1000, S = 20, T = 2, G = 8: FP8 53.2 / 43.6 us, int8 52.7 / 42.7, int4
+// 51.8 / 41.1; 9 rows (T = 1) 50.2 / 41.8; 200 sequences 179.7 / 143.7; one with a window
+// of 20000 30.7 / 27.0. Few short windows are the exception, by a microsecond: 16
+// sequences 28.7 / 29.1, four 18.0 / 17.3, one 16.1 / 17.3.
 constexpr int kKernelMma16 = 3;
 constexpr int kMma16Rows = 16;
 

@@ -28,7 +28,7 @@
 // end with its last block (missing blocks pad the first chunk, and the diagonal
 // stays in as few chunks as without sinks), a row's mask is built a block at a time
 // as bits, and the V copy warp zeroes its rows as they land instead of the softmax
-// warps (8 x 2048-token prompts, 32 + 8 heads of 128, W = 1024, S = 4: 445 us before, 343
+// warps (8 x 2048-token prompts, 32 + 8 heads of 128, W = 1024, S = 4: 445 us before, 344
 // with all three, 341 without sinks).
 #include <algorithm>
 #include <cstring>
@@ -951,7 +951,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 // come in four copies taken in turn by chunk and the block masks in eight, so
 // that no parity wait can fall two phases behind (as in the 32-token kernel).
 // P is kept in two 16-bit parts whatever the output's type: one part would save a third
-// of the MMAs (8 x 2048 tokens, W = 1024, S = 4, 32 + 8 heads of 128: 281 for 343 us),
+// of the MMAs (8 x 2048 tokens, W = 1024, S = 4, 32 + 8 heads of 128: 279 for 344 us),
 // but round every weight to the cache's type, for bf16 caches 8 times coarser than an
 // f16 output.
 // 16-byte cp.async into shared memory; src_bytes < 16 zero-fills the rest.
@@ -1646,10 +1646,10 @@ int launch_prefill(const PrefillLaunch& L) {
     const int sms = device_sms(-1);
     if (sms <= 0) return GQA_ERR_CUDA;
     // With sinks AUTO goes by size. Up to two 256-row items per SM, one-tile CTAs
-    // spread the tiles better (one chunk of 64 tokens, 24 + 8 heads: 25 against 33 us;
-    // six ragged chunks, 288 items: 58 against 66), above that two tiles share K/V
-    // (16 ragged chunks, 1536 items: 241 against 266 us). head_dim 64 has a one-tile
-    // form of its own (8 x 2048 tokens: 275 us, the 32-token form 382).
+    // spread the tiles better (one chunk of 64 tokens, 24 + 8 heads: 27 against 35 us;
+    // six ragged chunks, 288 items: 54 against 58), above that two tiles share K/V
+    // (16 ragged chunks, 1536 items: 243 against 260 us). head_dim 64 has a one-tile
+    // form of its own (8 x 2048 tokens: 280 us, the 32-token form 388).
     const long long items2 = ((long long)L.max_new_tokens * G + W2Cfg<2>::kRows - 1) / W2Cfg<2>::kRows * K * L.batch;
     const bool few = sinks && L.kernel == GQA_PREFILL_AUTO && items2 <= 2LL * sms;
     const bool wide2 = tc && D == 128 && !few && (L.kernel == GQA_PREFILL_AUTO || L.kernel == GQA_PREFILL_TCGEN05_WIDE);
@@ -1742,7 +1742,7 @@ int launch_prefill(const PrefillLaunch& L) {
         const long long fit = (long long)sms * (wide2 ? W2Cfg<2>::kCtasPerSm : W2Cfg<1>::kCtasPerSm);
         // With sinks, a batch whose sequences leave over a tenth of the tiles empty gets
         // a CTA per item: the hardware's order evens out what the fixed deal cannot (16
-        // chunks of 300 to 1024 tokens: 241 against 304 us; even prompts lose 8%).
+        // chunks of 300 to 1024 tokens: 243 against 283 us; even prompts lose 8%).
         const bool ragged = sinks && L.total_new_tokens > 0 &&
                             (double)L.total_new_tokens < 0.9 * (double)L.max_new_tokens * L.batch;
         cfg.gridDim = dim3((unsigned)(ragged || items < fit ? items : fit));

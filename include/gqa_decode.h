@@ -454,7 +454,7 @@ GQA_API int gqa_prefill(const gqa_kv_cache_t *cache, const void *q, int32_t q_dt
  * the first S tokens of a sequence stay visible however far its window has moved.
  * Blocks that lie wholly behind the sinks and before every query's window are
  * never read (their table entries may hold anything). S = 0, or W = 0 (full
- * attention), is gqa_prefill. sink_tokens < 0 is GQA_ERR_INVALID; an S beyond the
+ * attention), is gqa_prefill, whose GQA_PREFILL_AUTO does not go by size. sink_tokens < 0 is GQA_ERR_INVALID; an S beyond the
  * context makes every position up to p visible.
  *  total_new_tokens  rows of q (q_start[batch]) as the host knows them, 0 where it does
  *                    not: it picks the schedule of ragged batches and changes no result.
