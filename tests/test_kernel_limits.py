@@ -9,8 +9,19 @@ from gqa_decode_attention_kv_gb300 import build as gbuild
 
 PROGRAM = r"""
 #include <cstdio>
+#include <cstdlib>
 #include <map>
+#include <new>
 #include "gqa_limits.h"
+static bool no_memory = false;
+void* operator new(std::size_t n) {
+    if (no_memory) throw std::bad_alloc();
+    void* p = std::malloc(n);
+    if (!p) throw std::bad_alloc();
+    return p;
+}
+void operator delete(void* p) noexcept { std::free(p); }
+void operator delete(void* p, std::size_t) noexcept { std::free(p); }
 int main() {
     const int kernels = 1000;
     static char fns[kernels];
@@ -39,6 +50,14 @@ int main() {
     int tries = 0;
     for (int r = 0; r < 2; ++r) failed += limits.raise(0, &fns[0], 20000, [&](int) { ++tries; return false; });
     for (int r = 0; r < 2; ++r) failed += limits.ctas(0, &fns[0], 1, 7, [&] { ++tries; return 0; }) != 0;
+    // without memory for an entry: no limit is set that would be forgotten, no exception
+    static char other;
+    no_memory = true;
+    failed += limits.raise(0, &other, 5000, [&](int) { ++lowered; return true; });
+    failed += limits.ctas(0, &other, 128, 5000, [] { return 3; }) != 3;
+    failed += !limits.raise(0, &fns[0], 9000, [&](int) { ++lowered; return true; });
+    no_memory = false;
+    failed += !limits.raise(0, &other, 5000, [](int) { return true; });
     std::printf("%d %d %d %d %d\n", sets, asks, lowered, failed, tries);
     return 0;
 }
