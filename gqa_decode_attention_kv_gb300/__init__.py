@@ -787,7 +787,8 @@ def kv_pages_fork(ref_counts: torch.Tensor, block_tables: torch.Tensor, context_
     """Sequences ``dst_rows[i]`` (empty rows) continue ``src_rows[i]``: full pages are
     shared, an unfinished last page gets a fresh one, to be filled by
     ``kv_copy_pages`` with the list returned, in every layer's cache, before the
-    sequences are read or written."""
+    sequences are read or written. A sequence taken back into a shared page may not
+    append there."""
     sp, dp = _row_list(src_rows, "src_rows"), _row_list(dst_rows, "dst_rows")
     if src_rows.shape != dst_rows.shape:
         raise ValueError(f"src_rows and dst_rows differ in length: {tuple(src_rows.shape)}, {tuple(dst_rows.shape)}")

@@ -344,8 +344,9 @@ GQA_API int gqa_kv_pages_reserve(int32_t *ref_counts, int64_t num_blocks, int32_
 /*
  * Forks: row dst_rows[i] becomes a copy of row src_rows[i], i < n. It shares the
  * parent's full pages (their counts rise; empty entries stay empty); an unfinished
- * last page (L % 16 != 0) is copied to a fresh one, so each sequence may append. One
- * parent may have many children. Fork i is refused, and its row left alone, with
+ * last page (L % 16 != 0) is copied to a fresh one, so each sequence may append. (A row
+ * whose length is lowered into a page that others share may not append there: the others
+ * would read it.) One parent may have many children. Fork i is refused, and its row left alone, with
  * GQA_DEVERR_ROW if a row index is outside the table, the destination is named by an
  * earlier fork or is not empty (context_lens != 0, or its first entry holds a page: free
  * it first), or the parent is some fork's destination;
