@@ -14,11 +14,14 @@ would repeat the module name):
                               (one or T causal new tokens per sequence, optional
                               sliding window)
 * ``kv_append_varlen``     -- the same for a different number of new tokens per sequence
+* ``kv_read``              -- cached rows back as dense K and V, from any cache type
+* ``gqa_decode_shared``    -- ``gqa_decode`` for rows that share long prefixes, each attended once
 * ``rope_table``           -- (cos, sin) of every position and pair, for the two calls below
 * ``qk_norm_rope``         -- per-head norm of queries and keys and their rotation, one pass
 * ``qk_norm_rope_append``  -- the same with K and V written into the paged cache
 * ``kv_pages_reserve``, ``kv_pages_fork``, ``kv_pages_free``, ``kv_pages_trim``,
   ``kv_pages_compact``     -- the pages of a pool: counts and block tables kept in step on the device
+* ``kv_pages_groups``      -- which rows share their first pages (the plan of ``gqa_decode_shared``)
 * ``kv_copy_pages``        -- the page copies a fork or compaction asks for, in every layer's cache
 * ``gqa_prefill``          -- causal attention of prompts (any length) over the paged cache
 * ``decode_workspace_size``-- workspace bytes ``gqa_decode`` needs
@@ -151,6 +154,17 @@ def load() -> ctypes.CDLL:
             for f in (lib.gqa_kv_pages_reserve, lib.gqa_kv_pages_fork, lib.gqa_kv_pages_free, lib.gqa_kv_pages_trim,
                       lib.gqa_kv_pages_compact, lib.gqa_kv_copy_pages):
                 f.restype = ctypes.c_int
+            lib.gqa_kv_read.argtypes = [ctypes.POINTER(KVCacheDesc), vp, vp, i32, i64, vp, i32, vp, i32, vp, i32, vp, vp]
+            lib.gqa_kv_read.restype = ctypes.c_int
+            lib.gqa_kv_pages_groups_size.argtypes = [i32]
+            lib.gqa_kv_pages_groups_size.restype = ctypes.c_size_t
+            lib.gqa_kv_pages_groups.argtypes = [vp, i32, vp, i32, i32, vp, ctypes.c_size_t, vp, vp]
+            lib.gqa_kv_pages_groups.restype = ctypes.c_int
+            lib.gqa_decode_shared_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32]
+            lib.gqa_decode_shared_workspace_size.restype = ctypes.c_size_t
+            lib.gqa_decode_shared.argtypes = [ctypes.POINTER(KVCacheDesc), vp, i32, i32, vp, i32, vp, i32, i32,
+                                              ctypes.c_float, vp, i32, vp, i32, vp, ctypes.c_size_t, vp, vp]
+            lib.gqa_decode_shared.restype = ctypes.c_int
             lib.gqa_rope_table.argtypes = [vp, i32, i32, ctypes.c_double, vp]
             lib.gqa_rope_table.restype = ctypes.c_int
             lib.gqa_qk_norm_rope.argtypes = [ctypes.POINTER(NormRopeDesc), vp, i64, vp, i32, vp, i64, vp, i32, i32,
@@ -460,6 +474,122 @@ def gqa_decode(cache: PagedKVCache, q: torch.Tensor, block_tables: torch.Tensor,
     return out
 
 
+@dataclasses.dataclass
+class PrefixGroups:
+    """Which rows of a batch share their first pages, as ``kv_pages_groups`` finds it:
+    int32 arrays, views of ``plan``. Group i holds ``rows[start[i]:start[i+1]]`` and shares
+    ``blocks[i]`` pages; ``slot`` and ``group`` of a row are -1 where it shares nothing."""
+    plan: torch.Tensor
+    batch: int
+
+    def _part(self, first: int, n: int) -> torch.Tensor:
+        return self.plan[first:first + n]
+
+    @property
+    def count(self) -> torch.Tensor:           # groups, rows in groups
+        return self._part(0, 2)
+
+    @property
+    def start(self) -> torch.Tensor:
+        return self._part(2, self.batch + 1)
+
+    @property
+    def blocks(self) -> torch.Tensor:
+        return self._part(3 + self.batch, self.batch)
+
+    @property
+    def rows(self) -> torch.Tensor:
+        return self._part(3 + 2 * self.batch, self.batch)
+
+    @property
+    def slot(self) -> torch.Tensor:
+        return self._part(3 + 3 * self.batch, self.batch)
+
+    @property
+    def group(self) -> torch.Tensor:
+        return self._part(3 + 4 * self.batch, self.batch)
+
+
+def kv_pages_groups(block_tables: torch.Tensor, context_lens: torch.Tensor, min_blocks: int = 1,
+                    groups: Optional[PrefixGroups] = None, err: Optional[torch.Tensor] = None,
+                    stream=None) -> PrefixGroups:
+    """The rows of ``block_tables`` that begin with the same pages, for
+    ``gqa_decode_shared``: of the rows with one first page those that have at least P full
+    pages in common with the lowest of them, where P >= ``min_blocks`` saves most reads.
+    Made once, it serves every step while rows only append; rows freed, forked into,
+    trimmed or compacted need a new one (``groups`` takes the memory of an old one)."""
+    tp, lp = _dev(block_tables, "block_tables", True), _dev(context_lens, "context_lens", True)
+    ep = _dev(err, "err", True, True)
+    if block_tables.dim() != 2:
+        raise ValueError(f"block_tables must be [rows, max_blocks], not {tuple(block_tables.shape)}")
+    B = int(context_lens.shape[0]) if context_lens.dim() == 1 else -1
+    if B < 0 or block_tables.shape[0] < B:
+        raise ValueError(f"context_lens must be [B] with at most {int(block_tables.shape[0])} rows, "
+                         f"not {tuple(context_lens.shape)}")
+    _on_one_device(block_tables=block_tables, context_lens=context_lens, err=err,
+                   groups=None if groups is None else groups.plan)
+    need = int(load().gqa_kv_pages_groups_size(B))
+    if need == 0:
+        raise ValueError(f"no plan for {B} rows")
+    if groups is None:
+        groups = PrefixGroups(_empty((need // 4,), torch.int32, block_tables.device, stream), B)
+    else:
+        _dev(groups.plan, "groups.plan", True)
+        if groups.batch != B or groups.plan.dim() != 1 or groups.plan.numel() * 4 < need:
+            raise ValueError(f"groups was made for {groups.batch} rows, not {B}")
+    if B == 0:
+        groups.plan.zero_()
+        return groups
+    st = load().gqa_kv_pages_groups(tp, int(block_tables.shape[1]), lp, B, int(min_blocks), groups.plan.data_ptr(),
+                                    groups.plan.numel() * 4, ep, _stream_ptr(stream))
+    _check(st, "gqa_kv_pages_groups")
+    return groups
+
+
+def decode_shared_workspace_size(batch: int, num_heads: int, num_kv_heads: int, head_dim: int, device: int = -1,
+                                 tokens_per_seq: int = 1) -> int:
+    return int(load().gqa_decode_shared_workspace_size(batch, num_heads, num_kv_heads, head_dim, tokens_per_seq, device))
+
+
+_shared_workspace_size_of = functools.lru_cache(maxsize=256)(decode_shared_workspace_size)
+
+
+def gqa_decode_shared(cache: PagedKVCache, q: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
+                      scale: float, groups: PrefixGroups, out: Optional[torch.Tensor] = None,
+                      out_dtype: torch.dtype = torch.float32, workspace: Optional[torch.Tensor] = None,
+                      max_group: int = 0, err: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """``gqa_decode`` (full attention; q [B, H, d] or [B, T, H, d]) for rows that share
+    long prefixes: the pages a group of ``groups`` shares are read once for all of its
+    rows. ``max_group``, the rows of the largest group where the host knows them, picks
+    the kernel's form and changes no result."""
+    T = 1 if q.dim() == 3 else int(q.shape[1])
+    B, H, d = q.shape[0], q.shape[-2], q.shape[-1]
+    qp, tp, lp = _dev(q, "q"), _dev(block_tables, "block_tables", True), _dev(context_lens, "context_lens", True)
+    gp, ep = _dev(groups.plan, "groups.plan", True), _dev(err, "err", True, True)
+    _check_query(cache, q, (3, 4))
+    _check_table_and_lens(block_tables, context_lens, B, "context_lens", B)
+    if groups.batch != B or groups.plan.numel() < 3 + 5 * B:
+        raise ValueError(f"groups was made for {groups.batch} rows, q holds {B}")
+    _check_out(q, out)
+    _on_cache_device(cache, q=q, block_tables=block_tables, context_lens=context_lens, out=out, workspace=workspace,
+                     groups=groups.plan, err=err)
+    if out is None:
+        out = _empty(q.shape, out_dtype, q.device, stream)
+    if workspace is None:
+        idx = q.device.index
+        need = _shared_workspace_size_of(B, H, cache.num_kv_heads, d, idx, T)
+        if need == 0:
+            raise ValueError("no workspace size for this shape")
+        workspace = _scratch(_thread_scratch.decode, need, idx, stream, zero=True)
+    op, wp = _dev(out, "out"), _dev(workspace, "workspace")
+    desc = cache.desc()
+    st = load().gqa_decode_shared(ctypes.byref(desc), qp, DTYPE_CODE[q.dtype], H, tp, int(block_tables.shape[1]), lp, B,
+                                  T, float(scale), gp, int(max_group), op, DTYPE_CODE[out.dtype], wp,
+                                  workspace.numel() * workspace.element_size(), ep, _stream_ptr(stream))
+    _check(st, "gqa_decode_shared")
+    return out
+
+
 def gqa_decode_noalloc(cache: PagedKVCache, q: torch.Tensor, block_tables: torch.Tensor,
                        context_lens: torch.Tensor, scale: float, out: Optional[torch.Tensor] = None,
                        out_dtype: torch.dtype = torch.float32, kernel: int = KERNEL_AUTO,
@@ -516,6 +646,62 @@ def kv_append_varlen(cache: PagedKVCache, k_new: torch.Tensor, v_new: torch.Tens
                                      args[3], int(block_tables.shape[1]), args[4],
                                      int(positions.shape[0]), args[5], _stream_ptr(stream))
     _check(st, "gqa_kv_append_varlen")
+
+
+def kv_read(cache: PagedKVCache, block_tables: torch.Tensor, positions: torch.Tensor,
+            token_start: Optional[torch.Tensor] = None, max_tokens: int = 1, total_tokens: Optional[int] = None,
+            dtype: Optional[torch.dtype] = None, k_out: Optional[torch.Tensor] = None,
+            v_out: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None, stream=None):
+    """Cached rows back as dense (k, v): of every sequence the tokens at positions[b],
+    positions[b]+1, ... as rows token_start[b] .. token_start[b+1]-1 of [total_tokens, K, d]
+    (at most ``max_tokens`` of a sequence), or without ``token_start`` ``max_tokens`` of
+    every sequence as [B, max_tokens, K, d]. Codes become code * scale, rounded once to
+    ``dtype``: that of k_out, else the cache's own, float32 for a coded cache. Rows of no
+    token are not written."""
+    tp, pp = _dev(block_tables, "block_tables", True), _dev(positions, "positions", True)
+    sp, ep = _dev(token_start, "token_start", True, True), _dev(err, "err", True, True)
+    B = int(positions.shape[0]) if positions.dim() == 1 else -1
+    if B < 0:
+        raise ValueError("positions must be 1-D")
+    _check_table_and_lens(block_tables, positions, B, "positions", B)
+    n = int(max_tokens)
+    if n < 0:
+        raise ValueError(f"max_tokens must not be negative: {n}")
+    if token_start is None:
+        if total_tokens is not None and int(total_tokens) != B * n:
+            raise ValueError(f"without token_start total_tokens is B * max_tokens = {B * n}, not {total_tokens}")
+        shape = (B, n, cache.num_kv_heads, cache.head_dim)
+    else:
+        if token_start.dim() != 1 or token_start.numel() < B + 1:
+            raise ValueError(f"token_start must be 1-D with >= {B + 1} entries")
+        if total_tokens is None:
+            if k_out is None:
+                raise ValueError("total_tokens is required with token_start and no k_out")
+            total_tokens = int(k_out.shape[0])
+        if int(total_tokens) < 0:
+            raise ValueError(f"total_tokens must not be negative: {total_tokens}")
+        shape = (int(total_tokens), cache.num_kv_heads, cache.head_dim)
+    if dtype is None:
+        dtype = k_out.dtype if k_out is not None else cache.k.dtype if cache.k.dtype in _ROW_DTYPES else torch.float32
+    if dtype not in _ROW_DTYPES:
+        raise ValueError(f"rows are read back as float32, float16 or bfloat16, not {dtype}")
+    outs = []
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        if t is None:
+            t = _empty(shape, dtype, cache.k.device, stream)
+        elif tuple(t.shape) != shape or t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype} {shape}, not {t.dtype} {tuple(t.shape)}")
+        _dev(t, name)
+        outs.append(t)
+    _same_or_apart(outs[1], outs[0], "v_out", False)
+    _on_cache_device(cache, block_tables=block_tables, positions=positions, token_start=token_start, k_out=k_out,
+                     v_out=v_out, err=err)
+    total = outs[0].numel() // max(1, cache.num_kv_heads * cache.head_dim)
+    desc = cache.desc()
+    st = load().gqa_kv_read(ctypes.byref(desc), outs[0].data_ptr(), outs[1].data_ptr(), DTYPE_CODE[dtype], total, sp, n,
+                            tp, int(block_tables.shape[1]), pp, B, ep, _stream_ptr(stream))
+    _check(st, "gqa_kv_read")
+    return outs[0], outs[1]
 
 
 def rope_table(positions: int, rotary_dim: int, base: float = 10000.0, device="cuda", stream=None) -> torch.Tensor:

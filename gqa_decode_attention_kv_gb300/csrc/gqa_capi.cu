@@ -529,6 +529,46 @@ int gqa_kv_copy_pages(const gqa_kv_cache_t* caches, int32_t num_caches, const in
     return launch_copy_pages(L) == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
 }
 
+int gqa_kv_read(const gqa_kv_cache_t* cache, void* k_out, void* v_out, int32_t out_dtype, int64_t total_tokens,
+                const int32_t* token_start, int32_t max_tokens, const int32_t* block_tables,
+                int32_t max_blocks_per_seq, const int32_t* positions, int32_t batch, int32_t* err_flag, void* stream) {
+    const int st = check_cache(cache);
+    if (st != GQA_OK) return st;
+    if (batch < 0 || max_blocks_per_seq <= 0 || max_tokens < 0 || total_tokens < 0) return GQA_ERR_INVALID;
+    if (!plain_dtype(out_dtype)) return GQA_ERR_UNSUPPORTED;
+    if ((long long)max_blocks_per_seq * GQA_BLOCK_SIZE > 0x7fffffffLL) return GQA_ERR_INVALID;
+    if (!token_start && total_tokens != (long long)batch * max_tokens) return GQA_ERR_INVALID;
+    // pages a CTA grid is counted in, and the items of a page
+    if (((long long)max_tokens / GQA_BLOCK_SIZE + 2) * batch > 0x7fffffffLL || cache->num_kv_heads > 65536)
+        return GQA_ERR_UNSUPPORTED;
+    if (batch == 0 || max_tokens == 0 || total_tokens == 0) return GQA_OK;
+    if (!k_out || !v_out || !block_tables || !positions) return GQA_ERR_INVALID;
+    if (!aligned16(k_out) || !aligned16(v_out)) return GQA_ERR_INVALID;
+    const cudaError_t e = launch_kv_read(*cache, k_out, v_out, out_dtype, total_tokens, token_start, max_tokens,
+                                         block_tables, max_blocks_per_seq, positions, batch, err_flag,
+                                         static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
+}
+
+size_t gqa_kv_pages_groups_size(int32_t batch) {
+    if (batch < 0 || batch > kMaxGroupRows) return 0;
+    return (size_t)prefix_groups_ints(batch) * sizeof(int32_t);
+}
+
+int gqa_kv_pages_groups(const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* context_lens,
+                        int32_t batch, int32_t min_blocks, int32_t* groups, size_t groups_bytes, int32_t* err_flag,
+                        void* stream) {
+    if (batch < 0 || max_blocks_per_seq <= 0 || min_blocks < 0) return GQA_ERR_INVALID;
+    if ((long long)max_blocks_per_seq * GQA_BLOCK_SIZE > 0x7fffffffLL) return GQA_ERR_INVALID;
+    if (batch > kMaxGroupRows) return GQA_ERR_UNSUPPORTED;
+    if (batch == 0) return GQA_OK;
+    if (!block_tables || !context_lens || !groups || !aligned16(groups)) return GQA_ERR_INVALID;
+    if (groups_bytes < gqa_kv_pages_groups_size(batch)) return GQA_ERR_WORKSPACE;
+    const cudaError_t e = launch_pages_groups(block_tables, max_blocks_per_seq, context_lens, batch, min_blocks, groups,
+                                              err_flag, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
+}
+
 int gqa_rope_table(float* table, int32_t positions, int32_t rotary_dim, double base, void* stream) {
     if (positions < 0 || rotary_dim <= 0 || rotary_dim % 2 || !(base > 0.0) || !std::isfinite(base)) return GQA_ERR_INVALID;
     if ((long long)positions * (rotary_dim / 2) > 256LL * 0x7fffffffLL) return GQA_ERR_UNSUPPORTED;
@@ -749,6 +789,61 @@ int gqa_decode_sinks(const gqa_kv_cache_t* cache, const void* q, int32_t q_dtype
     L.ev_end = opts ? static_cast<cudaEvent_t>(opts->event_main_end) : nullptr;
     L.err = err_flag;
     L.stream = static_cast<cudaStream_t>(stream);
+    return launch_decode(L, sms);
+}
+
+size_t gqa_decode_shared_workspace_size(int32_t batch, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                                        int32_t tokens_per_seq, int32_t device) {
+    const size_t own = gqa_decode_workspace_size(batch, num_heads, num_kv_heads, head_dim, tokens_per_seq, device);
+    return own == 0 ? 0 : own + shared_prefix_bytes(batch, num_heads, head_dim, tokens_per_seq, num_sms_of(device));
+}
+
+int gqa_decode_shared(const gqa_kv_cache_t* cache, const void* q, int32_t q_dtype, int32_t num_heads,
+                      const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* context_lens,
+                      int32_t batch, int32_t tokens_per_seq, float scale, const int32_t* groups, int32_t max_group,
+                      void* out, int32_t out_dtype, void* workspace, size_t workspace_bytes, int32_t* err_flag,
+                      void* stream) {
+    const int st = check_cache(cache);
+    if (st != GQA_OK) return st;
+    if (batch < 0 || num_heads <= 0 || max_blocks_per_seq <= 0 || tokens_per_seq < 0 || max_group < 0)
+        return GQA_ERR_INVALID;
+    if (num_heads % cache->num_kv_heads) return GQA_ERR_INVALID;
+    if ((long long)max_blocks_per_seq * GQA_BLOCK_SIZE > 0x7fffffffLL) return GQA_ERR_INVALID;
+    const int T = std::max(1, (int)tokens_per_seq);
+    if ((long long)(num_heads / cache->num_kv_heads) * T > kMaxGroup) return GQA_ERR_UNSUPPORTED;
+    if ((long long)batch * T * num_heads >= 0x7fffffffLL) return GQA_ERR_UNSUPPORTED;
+    if (batch > kMaxBatch) return GQA_ERR_UNSUPPORTED;
+    if ((long long)batch * cache->num_kv_heads * max_blocks_per_seq >= 0x7fffffffLL) return GQA_ERR_UNSUPPORTED;
+    if (!shared_prefix_supported(cache->dtype)) return GQA_ERR_UNSUPPORTED;
+    const bool q_ok = dtype_coded(cache->dtype) ? q_dtype == GQA_DTYPE_BF16 || q_dtype == GQA_DTYPE_F16
+                                                : q_dtype == cache->dtype;
+    if (!q_ok || !plain_dtype(out_dtype)) return GQA_ERR_UNSUPPORTED;
+    if (!std::isfinite(scale)) return GQA_ERR_INVALID;
+    if (batch == 0) return GQA_OK;
+    if (!q || !block_tables || !context_lens || !groups || !out) return GQA_ERR_INVALID;
+    if (!aligned16(q) || !aligned16(out) || !aligned16(groups)) return GQA_ERR_INVALID;
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return GQA_ERR_INVALID;
+    const int sms = num_sms_of(-1);
+    if (sms <= 0) return GQA_ERR_CUDA;
+    const SharedPrefix shared = {groups, max_group};
+    DecodeLaunch L = {};
+    L.cache = cache;
+    L.q = q;
+    L.q_dtype = q_dtype;
+    L.num_heads = num_heads;
+    L.block_tables = block_tables;
+    L.max_blocks = max_blocks_per_seq;
+    L.context_lens = context_lens;
+    L.batch = batch;
+    L.scale = scale;
+    L.out = out;
+    L.out_dtype = out_dtype;
+    L.workspace = workspace;
+    L.workspace_bytes = workspace_bytes;
+    L.tokens_per_seq = T;
+    L.err = err_flag;
+    L.stream = static_cast<cudaStream_t>(stream);
+    L.shared = &shared;
     return launch_decode(L, sms);
 }
 

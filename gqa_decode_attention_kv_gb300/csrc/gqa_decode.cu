@@ -10,7 +10,7 @@ namespace gqa {
 namespace dec {
 
 bool pick_plain(int dtype, int kind, int d, int nw, Variant& v) {
-    return pick_variant<false, false>(dtype, kind, d, nw, v);
+    return pick_variant<false, false, false>(dtype, kind, d, nw, v);
 }
 
 }  // namespace dec
@@ -123,8 +123,10 @@ int launch_decode(const DecodeLaunch& L, int num_sms) {
     Variant v{};
     const bool general = T > 1 || L.window > 0;
     const bool sinks = L.window > 0 && L.sinks > 0;
+    const bool tail = L.shared != nullptr;
     auto pick = [&](int warps) {
-        return sinks     ? pick_sinks(c.dtype, kind, D, warps, v)
+        return tail      ? pick_tail(c.dtype, kind, D, warps, v)
+               : sinks   ? pick_sinks(c.dtype, kind, D, warps, v)
                : general ? pick_general(c.dtype, kind, D, warps, v)
                          : pick_plain(c.dtype, kind, D, warps, v);
     };
@@ -186,7 +188,7 @@ int launch_decode(const DecodeLaunch& L, int num_sms) {
 
     const int smem = v.smem(L.batch);
     int workers = workers_of(v, L.batch, num_sms);
-    if (sinks) {
+    if (sinks || tail) {
         // the workspace is sized from the other flavours' workers alone, so that
         // its size does not depend on the options
         Variant g{};
@@ -202,7 +204,8 @@ int launch_decode(const DecodeLaunch& L, int num_sms) {
 
     const WsLayout wl =
         ws_layout(L.batch, Kv, RS, D, max_slots(L.batch, Kv, P, L.max_blocks, min_units, v.tail_chunks));
-    if (L.workspace == nullptr || L.workspace_bytes < wl.total) return GQA_ERR_WORKSPACE;
+    const size_t need = wl.total + (tail ? shared_prefix_bytes(L.batch, L.num_heads, D, T, num_sms) : 0);
+    if (L.workspace == nullptr || L.workspace_bytes < need) return GQA_ERR_WORKSPACE;
 
     DecodeArgs a;
     a.q = L.q;
@@ -230,6 +233,7 @@ int launch_decode(const DecodeLaunch& L, int num_sms) {
     a.RS = RS;
     a.window = L.window;
     a.sinks = sinks ? (int)std::min<long long>(L.sinks, (long long)L.max_blocks * kBlock) : 0;
+    a.groups = tail ? L.shared->groups : nullptr;
     a.max_blocks = L.max_blocks;
     a.out_dtype = L.out_dtype;
     a.q_dtype = L.q_dtype;
@@ -260,6 +264,10 @@ int launch_decode(const DecodeLaunch& L, int num_sms) {
     cfg.attrs = pdl;
     cfg.numAttrs = timed ? 0 : 1;
     if (L.ev_begin && cudaEventRecord(L.ev_begin, L.stream) != cudaSuccess) return GQA_ERR_CUDA;
+    if (tail) {
+        const int st = launch_shared_prefix(L, ws + wl.total, num_sms);
+        if (st != GQA_OK) return st;
+    }
     void* args[] = {&kmap, &vmap, &a};
     e = cudaLaunchKernelExC(&cfg, v.fn, args);
     if (e != cudaSuccess) return GQA_ERR_CUDA;
@@ -272,6 +280,7 @@ int launch_decode(const DecodeLaunch& L, int num_sms) {
         return GQA_ERR_CUDA;
     };
     if (L.ev_end && cudaEventRecord(L.ev_end, L.stream) != cudaSuccess) return fail_after_split();
+    if (tail) return launch_shared_merge(a, L, ws + wl.total, num_sms) == GQA_OK ? GQA_OK : fail_after_split();
 
     // Combine width from the expected pieces per row (about 1.5 workers' worth
     // of segments per pair when lengths are even).

@@ -6,7 +6,7 @@ namespace gqa {
 namespace dec {
 
 bool pick_general(int dtype, int kind, int d, int nw, Variant& v) {
-    return pick_variant<true, false>(dtype, kind, d, nw, v);
+    return pick_variant<true, false, false>(dtype, kind, d, nw, v);
 }
 
 }  // namespace dec

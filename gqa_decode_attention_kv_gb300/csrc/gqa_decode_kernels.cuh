@@ -2,8 +2,9 @@
 // as templates, with the host-side variant table. Included by gqa_decode.cu
 // (the one-token, full-attention flavour and the combine kernels), by
 // gqa_decode_general.cu (the flavour for several queries per sequence or a
-// sliding window) and by gqa_decode_sinks.cu (a sliding window with sink
-// tokens), so the three sets of instantiations compile in parallel.
+// sliding window), by gqa_decode_sinks.cu (a sliding window with sink tokens) and
+// by gqa_decode_tail.cu (what lies behind a prefix that the rows of a group share),
+// so the four sets of instantiations compile in parallel.
 //
 // Split-KV grouped-query decode attention over a paged cache.
 //
@@ -51,6 +52,7 @@
 #include <type_traits>
 
 #include "gqa_device.cuh"
+#include "gqa_groups.cuh"
 #include "gqa_internal.h"
 
 namespace gqa {
@@ -77,6 +79,7 @@ struct DecodeArgs {
     int GT;              // query rows per (sequence, kv-head) pair: G * T
     int window;          // sliding window in tokens; 0 = full attention
     int sinks;           // sink flavour: first tokens that stay visible
+    const int32_t* groups;   // tail flavour: which rows share their first blocks
     // Unit space: Kv = K * NRG heads per sequence. NRG > 1 splits a pair's GT
     // rows into groups of 8 ("virtual kv-heads" gv = g * NRG + group), each an
     // independent unit stream that re-reads the pair's tiles (from L2, since
@@ -169,14 +172,19 @@ constexpr int kMma16Rows = 16;
 // cycles a block, which a row warp would add to the group's pace while the
 // others waited (measured; with eight row warps the ninth caps registers at 168
 // and still wins).
-template <int kKind, typename T, int D, int kHeadWarps = 1, bool kGeneral = false, bool kSinkTokens = false>
+template <int kKind, typename T, int D, int kHeadWarps = 1, bool kGeneral = false, bool kSinkTokens = false,
+          bool kTailPart = false>
 struct Cfg {
     // kGen: T > 1 queries per sequence or a sliding window (per-row ranges);
     // false compiles the one-token, full-attention step with no range logic.
     // kSinks (only with kGen): the window keeps the first a.sinks tokens visible.
     static constexpr bool kGen = kGeneral;
+    // kTail (only with kGen, no window): a row that shares its first blocks attends the
+    // others alone, and every pair leaves its state in its slots.
     static constexpr bool kSinks = kSinkTokens;
+    static constexpr bool kTail = kTailPart;
     static_assert(kGen || !kSinks, "sinks come with a window");
+    static_assert(!kTail || (kGen && !kSinks), "the tail flavour has no window");
     static constexpr bool kI8 = std::is_same<T, int8_t>::value;
     static constexpr bool kFp8 = std::is_same<T, __nv_fp8_e4m3>::value;
     static constexpr bool kKc = std::is_same<T, int4kc>::value;   // K scales per channel
@@ -251,8 +259,8 @@ struct Smem {
     static constexpr int kEmpty = kBars + C::kRings * C::kStages * 8;     // "empty" (shared ring)
     static constexpr int kMeta = kEmpty + C::kStages * 8;                 // 4 ints per stage
     static constexpr int kScan = kMeta + C::kRings * C::kStages * 16;     // 64 ints
-    static constexpr int kLens = kScan + 64 * 4;                          // B ints, then B+1 prefix
-    static int bytes(int B) { return 1024 + kLens + (2 * B + 1) * 4; }
+    static constexpr int kLens = kScan + 64 * 4;                          // B ints, then B+1 prefix (tail: B more)
+    static int bytes(int B) { return 1024 + kLens + ((C::kTail ? 3 : 2) * B + 1) * 4; }
 };
 
 // ------------------------------------------------------------------ prologue
@@ -308,9 +316,10 @@ __device__ __forceinline__ void row_range(const DecodeArgs& a, int L, int rr, in
 
 
 // Validated lengths into lens_s and the prefix pref[0..B] (pref[0] = 0) of the
-// blocks each sequence's query rows attend.
-template <bool kGen, bool kSinks>
-__device__ void block_prefix(const DecodeArgs& a, int* lens_s, int* pref, int* tmp) {
+// blocks each sequence's query rows attend. kTail: start_s gets the blocks that the
+// row's group attends for it, and the length counts from behind them.
+template <bool kGen, bool kSinks, bool kTail>
+__device__ void block_prefix(const DecodeArgs& a, int* lens_s, int* pref, int* tmp, int* start_s) {
     const int tid = threadIdx.x, nthr = blockDim.x, lane = tid & 31, wid = tid >> 5;
     const int nw = nthr >> 5;
     const int maxtok = a.max_blocks * kBlock;
@@ -323,6 +332,11 @@ __device__ void block_prefix(const DecodeArgs& a, int* lens_s, int* pref, int* t
             if (L < 0 || L > maxtok) {
                 if (blockIdx.x == 0) flag_error(a.err, GQA_DEVERR_CONTEXT_LEN);
                 L = 0;
+            }
+            if constexpr (kTail) {
+                const int shared = shared_blocks(PrefixGroups(a.groups, a.B), i, L, a.T, a.max_blocks);
+                start_s[i] = shared;
+                L -= shared * kBlock;
             }
             lens_s[i] = L;
         }
@@ -1328,12 +1342,9 @@ __device__ __forceinline__ Partition make_partition(const DecodeArgs& a, int U) 
     return pt;
 }
 
-template <int kKind, typename T, int D, int kHeadWarps, bool kGen, bool kSinks>
-__global__ void __launch_bounds__(Cfg<kKind, T, D, kHeadWarps, kGen, kSinks>::kWarps * 32,
-                                  Cfg<kKind, T, D, kHeadWarps, kGen, kSinks>::kMinCtas)
-split_kv_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                const DecodeArgs a) {
-    using C = Cfg<kKind, T, D, kHeadWarps, kGen, kSinks>;
+template <int kKind, typename T, int D, int kHeadWarps, bool kGen, bool kSinks, bool kTail>
+__device__ __forceinline__ void split_kv(const CUtensorMap& kmap, const CUtensorMap& vmap, const DecodeArgs& a) {
+    using C = Cfg<kKind, T, D, kHeadWarps, kGen, kSinks, kTail>;
     using S = Smem<C>;
     constexpr bool kShared = kHeadWarps > 1;     // one ring, one worker per CTA
     extern __shared__ uint8_t smem_raw[];
@@ -1349,8 +1360,8 @@ split_kv_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
         prefetch_tensormap(&vmap);
     }
     launch_dependents();                       // the combine kernel may take its place now
-    grid_dependency_wait();                    // inputs may come from the previous kernel
-    block_prefix<kGen, kSinks>(a, lens_s, pref, tmp);
+    if constexpr (!kTail) grid_dependency_wait();   // inputs may come from the previous kernel
+    block_prefix<kGen, kSinks, kTail>(a, lens_s, pref, tmp, pref + a.B + 1);
     const Partition pt = make_partition(a, a.Kv * pref[a.B]);
     if (blockIdx.x == 0) {
         for (int i = threadIdx.x; i <= a.B; i += blockDim.x) a.ws_pref[i] = pref[i];
@@ -1425,7 +1436,8 @@ split_kv_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
         if (u < pt.U) {
             int b, g, j;
             locate(u, pref, a.B, a.Kv, b, g, j);
-            const int ph = a.block_tables[(long long)b * a.max_blocks + logical_block<kGen, kSinks>(a, lens_s[b], j)];
+            const int first = kTail ? (pref + a.B + 1)[b] : 0;
+            const int ph = a.block_tables[(long long)b * a.max_blocks + first + logical_block<kGen, kSinks>(a, lens_s[b], j)];
             if (ph < 0 || ph >= a.num_blocks) flag_error(a.err, GQA_DEVERR_BLOCK_INDEX);
             else win_phys = ph;
             win_g = g / a.NRG;                 // the real kv-head
@@ -1693,7 +1705,7 @@ split_kv_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
         const bool last_of_seg = (u == seg_end - 1);
         next_u = u + 1;
         if (last_of_pair || last_of_seg) {
-            const bool whole = (first_j == 0) && last_of_pair;
+            const bool whole = !kTail && (first_j == 0) && last_of_pair;
             const int row0 = kShared ? 0 : hbase;
             if constexpr (kKind == kKernelMma) mma_flush<C, D>(a, st, cb, cg, hbase, row0, whole, seg, r, c);
             else if constexpr (C::kRows16) mma16_flush<C, D>(a, st, cb, cg, whole, seg, r, c);
@@ -1733,6 +1745,18 @@ split_kv_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
             ++cj;
         }
     }
+}
+
+// The tail flavour runs beside the kernel before it, which attends the shared blocks and
+// lets this one start only after its own wait for earlier work: nothing it reads is still
+// being written. It ends after that kernel, so that the merge behind it has both.
+template <int kKind, typename T, int D, int kHeadWarps, bool kGen, bool kSinks, bool kTail>
+__global__ void __launch_bounds__(Cfg<kKind, T, D, kHeadWarps, kGen, kSinks, kTail>::kWarps * 32,
+                                  Cfg<kKind, T, D, kHeadWarps, kGen, kSinks, kTail>::kMinCtas)
+split_kv_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                const DecodeArgs a) {
+    split_kv<kKind, T, D, kHeadWarps, kGen, kSinks, kTail>(kmap, vmap, a);
+    if constexpr (kTail) grid_dependency_wait();
 }
 
 // ------------------------------------------------------------------ combine
@@ -1876,27 +1900,27 @@ struct Variant {
     int (*smem)(int);
 };
 
-template <int kKind, typename T, int D, int NW, bool kGen, bool kSinks>
+template <int kKind, typename T, int D, int NW, bool kGen, bool kSinks, bool kTail>
 Variant make_variant() {
-    using C = Cfg<kKind, T, D, NW, kGen, kSinks>;
-    return Variant{reinterpret_cast<const void*>(&split_kv_kernel<kKind, T, D, NW, kGen, kSinks>), C::kTailChunks, C::kWarps,
+    using C = Cfg<kKind, T, D, NW, kGen, kSinks, kTail>;
+    return Variant{reinterpret_cast<const void*>(&split_kv_kernel<kKind, T, D, NW, kGen, kSinks, kTail>), C::kTailChunks, C::kWarps,
                    NW == 1 ? C::kWarps : 1, C::kBoxInner, C::kSwizzleBytes, &Smem<C>::bytes};
 }
 
-template <int kKind, typename T, int D, bool kGen, bool kSinks>
+template <int kKind, typename T, int D, bool kGen, bool kSinks, bool kTail>
 Variant pick_width(int nw) {
-    if (nw == 1) return make_variant<kKind, T, D, 1, kGen, kSinks>();
-    if (nw == 2) return make_variant<kKind, T, D, 2, kGen, kSinks>();
-    if (nw == 4) return make_variant<kKind, T, D, 4, kGen, kSinks>();
-    return make_variant<kKind, T, D, 8, kGen, kSinks>();
+    if (nw == 1) return make_variant<kKind, T, D, 1, kGen, kSinks, kTail>();
+    if (nw == 2) return make_variant<kKind, T, D, 2, kGen, kSinks, kTail>();
+    if (nw == 4) return make_variant<kKind, T, D, 4, kGen, kSinks, kTail>();
+    return make_variant<kKind, T, D, 8, kGen, kSinks, kTail>();
 }
 
-template <typename T, int D, bool kGen, bool kSinks>
+template <typename T, int D, bool kGen, bool kSinks, bool kTail>
 bool pick_kind(int kind, int nw, Variant& v) {
     if (kind == kKernelMma16) {
         if constexpr (kSinks && D == 128 && (std::is_same<T, int8_t>::value || std::is_same<T, __nv_fp8_e4m3>::value ||
                                              std::is_same<T, int4x2>::value)) {
-            if (nw == 1) v = make_variant<kKernelMma16, T, D, 1, kGen, kSinks>();
+            if (nw == 1) v = make_variant<kKernelMma16, T, D, 1, kGen, kSinks, kTail>();
             return nw == 1;
         } else {
             return false;
@@ -1908,49 +1932,54 @@ bool pick_kind(int kind, int nw, Variant& v) {
                         std::is_same<T, int4x2>::value || std::is_same<T, int4kc>::value) && D != 128)) {
             return false;
         } else {
-            v = pick_width<kKernelMma, T, D, kGen, kSinks>(nw);
+            v = pick_width<kKernelMma, T, D, kGen, kSinks, kTail>(nw);
             return true;
         }
     }
     if constexpr (std::is_same<T, float>::value) {
-        v = pick_width<kKernelFma, T, D, kGen, kSinks>(nw);
+        v = pick_width<kKernelFma, T, D, kGen, kSinks, kTail>(nw);
         return true;
     } else {
         // the CUDA-core kernel serves fp32 caches, and <= 8-head groups of the others
         if (nw > 1) return false;
-        v = make_variant<kKernelFma, T, D, 1, kGen, kSinks>();
+        v = make_variant<kKernelFma, T, D, 1, kGen, kSinks, kTail>();
         return true;
     }
 }
 
-template <typename T, bool kGen, bool kSinks>
+template <typename T, bool kGen, bool kSinks, bool kTail>
 bool pick_dim(int kind, int d, int nw, Variant& v) {
-    if (d == 64) return pick_kind<T, 64, kGen, kSinks>(kind, nw, v);
-    if (d == 128) return pick_kind<T, 128, kGen, kSinks>(kind, nw, v);
+    if (d == 64) return pick_kind<T, 64, kGen, kSinks, kTail>(kind, nw, v);
+    if (d == 128) return pick_kind<T, 128, kGen, kSinks, kTail>(kind, nw, v);
     return false;
 }
 
 // The split-KV kernel for a cache dtype, kernel kind, head_dim and warps per
-// pair, in its plain (one token, full attention), general or sink flavour.
-template <bool kGen, bool kSinks>
+// pair, in its plain (one token, full attention), general, sink or tail flavour.
+template <bool kGen, bool kSinks, bool kTail>
 bool pick_variant(int dtype, int kind, int d, int nw, Variant& v) {
     switch (dtype) {
-        case GQA_DTYPE_F32: return pick_dim<float, kGen, kSinks>(kind, d, nw, v);
-        case GQA_DTYPE_F16: return pick_dim<__half, kGen, kSinks>(kind, d, nw, v);
-        case GQA_DTYPE_BF16: return pick_dim<__nv_bfloat16, kGen, kSinks>(kind, d, nw, v);
-        case GQA_DTYPE_I8: return pick_dim<int8_t, kGen, kSinks>(kind, d, nw, v);
-        case GQA_DTYPE_FP8_E4M3: return pick_dim<__nv_fp8_e4m3, kGen, kSinks>(kind, d, nw, v);
-        case GQA_DTYPE_I4: return pick_dim<int4x2, kGen, kSinks>(kind, d, nw, v);
-        case GQA_DTYPE_I4_KC: return pick_dim<int4kc, kGen, kSinks>(kind, d, nw, v);
+        case GQA_DTYPE_F32: return pick_dim<float, kGen, kSinks, kTail>(kind, d, nw, v);
+        case GQA_DTYPE_F16: return pick_dim<__half, kGen, kSinks, kTail>(kind, d, nw, v);
+        case GQA_DTYPE_BF16: return pick_dim<__nv_bfloat16, kGen, kSinks, kTail>(kind, d, nw, v);
+        case GQA_DTYPE_I8: return pick_dim<int8_t, kGen, kSinks, kTail>(kind, d, nw, v);
+        case GQA_DTYPE_FP8_E4M3: return pick_dim<__nv_fp8_e4m3, kGen, kSinks, kTail>(kind, d, nw, v);
+        case GQA_DTYPE_I4: return pick_dim<int4x2, kGen, kSinks, kTail>(kind, d, nw, v);
+        case GQA_DTYPE_I4_KC: return pick_dim<int4kc, kGen, kSinks, kTail>(kind, d, nw, v);
         default: return false;
     }
 }
 
-// Defined in gqa_decode.cu (plain), gqa_decode_general.cu (general) and
-// gqa_decode_sinks.cu (a window with sink tokens).
+// Defined in gqa_decode.cu (plain), gqa_decode_general.cu (general),
+// gqa_decode_sinks.cu (a window with sink tokens) and gqa_decode_tail.cu (tail).
 bool pick_plain(int dtype, int kind, int d, int nw, Variant& v);
 bool pick_general(int dtype, int kind, int d, int nw, Variant& v);
 bool pick_sinks(int dtype, int kind, int d, int nw, Variant& v);
+bool pick_tail(int dtype, int kind, int d, int nw, Variant& v);
+
+// Merge of a shared decode: the tail's pieces (a: the split-KV launch's arguments) and the
+// prefix's (gqa_shared.cu).
+int launch_shared_merge(const DecodeArgs& tail, const DecodeLaunch& L, uint8_t* ws, int num_sms);
 
 }  // namespace dec
 }  // namespace gqa

@@ -6,7 +6,7 @@ namespace gqa {
 namespace dec {
 
 bool pick_sinks(int dtype, int kind, int d, int nw, Variant& v) {
-    return pick_variant<true, true>(dtype, kind, d, nw, v);
+    return pick_variant<true, true, false>(dtype, kind, d, nw, v);
 }
 
 }  // namespace dec

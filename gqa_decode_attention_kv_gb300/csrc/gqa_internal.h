@@ -128,6 +128,24 @@ struct PrefillLaunch {
 // Validated launch; returns a gqa_status_t.
 int launch_prefill(const PrefillLaunch& L);
 
+// Reading the cache back: token_start NULL (max_tokens rows per sequence) or
+// [batch+1] row offsets; k_out and v_out hold `total` rows.
+cudaError_t launch_kv_read(const gqa_kv_cache_t& c, void* k_out, void* v_out, int out_dtype, long long total,
+                           const int32_t* token_start, int max_tokens, const int32_t* block_tables, int max_blocks,
+                           const int32_t* positions, int batch, int32_t* err, cudaStream_t stream);
+
+// Groups of rows that share their first pages; prefix_groups_ints: int32s of a plan.
+constexpr int kMaxGroupRows = 8192;                   // rows of a plan: the ranks of gqa_groups.cu
+long long prefix_groups_ints(int batch);
+cudaError_t launch_pages_groups(const int32_t* block_tables, int max_blocks, const int32_t* context_lens, int batch,
+                                int min_blocks, int32_t* plan, int32_t* err, cudaStream_t stream);
+
+// What a decode over shared prefixes takes next to a DecodeLaunch.
+struct SharedPrefix {
+    const int32_t* groups;      // a plan as gqa_kv_pages_groups makes it
+    int max_group;              // rows of the largest group, 0: not known
+};
+
 struct DecodeLaunch {
     const gqa_kv_cache_t* cache;
     const void* q;
@@ -152,7 +170,14 @@ struct DecodeLaunch {
     cudaEvent_t ev_begin, ev_end;
     int32_t* err;
     cudaStream_t stream;
+    const SharedPrefix* shared = nullptr;   // the groups whose shared blocks are attended once
 };
+
+// The shared part of such a decode (gqa_shared.cu): whether a cache type has it, its
+// workspace behind the split-KV one, and its launch. Returns a gqa_status_t.
+bool shared_prefix_supported(int dtype);
+size_t shared_prefix_bytes(int batch, int num_heads, int head_dim, int tokens_per_seq, int num_sms);
+int launch_shared_prefix(const DecodeLaunch& L, uint8_t* ws, int num_sms);
 
 // Resident CTAs per SM of kernel fn with `threads` threads and `smem` bytes of
 // dynamic shared memory on the current device (its shared-memory limit set to

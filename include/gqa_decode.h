@@ -234,6 +234,27 @@ GQA_API int gqa_kv_append_varlen(const gqa_kv_cache_t *cache, const void *k_new,
                   const int32_t *positions, int32_t batch, int32_t *err_flag, void *stream);
 
 /*
+ * Cached rows back as dense K and V, the inverse of the appends: row token_start[b] + i
+ * of k_out and v_out ([total_tokens, K, head_dim] of out_dtype: F32, F16 or BF16) is the
+ * cached token positions[b] + i of sequence b, i < token_start[b+1] - token_start[b]. A
+ * coded cache gives code * scale, rounded once to out_dtype; a cache of out_dtype itself
+ * its bits; another float cache its values, rounded.
+ *  token_start    device int32 [batch+1], non-decreasing, or NULL: max_tokens rows of
+ *                 every sequence, total_tokens = batch * max_tokens.
+ *  max_tokens     host bound on the rows of a sequence; one with more, with a negative
+ *                 count or with rows outside [0, total_tokens) is skipped and flagged
+ *                 (GQA_DEVERR_POSITION).
+ *  total_tokens   rows of k_out and v_out, 16-byte aligned.
+ *  A token whose position or block is out of range keeps what its rows held
+ *  (GQA_DEVERR_POSITION / _BLOCK_INDEX), and so do rows of no sequence. Tokens past a
+ *  sequence's end are read as the pages hold them. k_residual is not read.
+ */
+GQA_API int gqa_kv_read(const gqa_kv_cache_t *cache, void *k_out, void *v_out, int32_t out_dtype,
+                  int64_t total_tokens, const int32_t *token_start, int32_t max_tokens,
+                  const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *positions,
+                  int32_t batch, int32_t *err_flag, void *stream);
+
+/*
  * Norm and rotation of query and key heads. A head row x of d elements becomes
  *   y = x / sqrt(mean(x^2) + eps) * weight          (a NULL weight skips the norm)
  * and the pairs of its first rotary_dim elements turn by the angle of the token's
@@ -382,6 +403,34 @@ GQA_API int gqa_kv_pages_free(int32_t *ref_counts, int64_t num_blocks, int32_t *
 GQA_API int gqa_kv_pages_trim(int32_t *ref_counts, int64_t num_blocks, int32_t *block_tables,
                   int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t batch,
                   int32_t sliding_window, int32_t sink_tokens, int32_t *err_flag, void *stream);
+
+/*
+ * Which rows share their first pages: the plan of gqa_decode_shared. With n_b =
+ * context_lens[b] / 16 full pages, the leader of row b is the lowest row whose table
+ * begins with the same page, and m_b the number of leading entries, at most n_b and the
+ * leader's, that both have in common. Of the rows of a leader those with m_b >= P form a
+ * group that shares P pages, where P >= max(1, min_blocks) makes P * (rows - 1) largest
+ * (the larger P where two are equal); without a second row there is none. Groups are in
+ * the order of their leaders, rows of a group in ascending order, the leader first.
+ *  groups  device int32, 16-byte aligned, gqa_kv_pages_groups_size(batch) bytes, with
+ *          B = batch:
+ *            [0], [1]     groups, rows in groups
+ *            start  [B+1] group i holds rows[start[i]] .. rows[start[i+1] - 1]; entries
+ *                         past the last group: the number of rows in groups
+ *            blocks [B]   pages that group i shares, 0 past the last group
+ *            rows   [B]   the rows, group by group, -1 past the last
+ *            slot   [B]   where row b stands in rows, -1: in no group
+ *            group  [B]   its group, -1: in none
+ *          one behind the other, then scratch. A caller who knows the groups may write
+ *          the arrays.
+ *  A row whose length is out of range shares nothing (GQA_DEVERR_CONTEXT_LEN). batch <= 8192.
+ *  A plan stays right while its rows only append; rows that are freed, forked into,
+ *  trimmed or compacted need a new one.
+ */
+GQA_API size_t gqa_kv_pages_groups_size(int32_t batch);
+GQA_API int gqa_kv_pages_groups(const int32_t *block_tables, int32_t max_blocks_per_seq,
+                  const int32_t *context_lens, int32_t batch, int32_t min_blocks, int32_t *groups,
+                  size_t groups_bytes, int32_t *err_flag, void *stream);
 
 /*
  * Compaction: with N live pages, the i-th highest live page at or past index N moves to
@@ -535,6 +584,33 @@ GQA_API int gqa_decode_sinks(const gqa_kv_cache_t *cache, const void *q, int32_t
                const int32_t *context_lens, int32_t batch, float scale, void *out,
                int32_t out_dtype, void *workspace, size_t workspace_bytes,
                const gqa_decode_opts_t *opts, int32_t sink_tokens, int32_t *err_flag, void *stream);
+
+/*
+ * gqa_decode for a batch whose rows share long prefixes: the pages that a group of rows
+ * has in common are read once and attended for all of its queries, every row's others on
+ * their own, and the two joined by their log-sum-exp weights. The result is gqa_decode's,
+ * to fp32 rounding (full attention; no window).
+ *  tokens_per_seq  T, as in gqa_decode_opts_t (0 meaning 1).
+ *  groups          device, a plan of this batch as gqa_kv_pages_groups lays it out. The
+ *                  shared pages are read through the table row of a group's first row. A
+ *                  row of a group that is shorter than the shared pages and its T - 1
+ *                  first new tokens (an empty one, say) attends alone. Entries of a plan
+ *                  that point outside it or the tables share nothing; a plan that names
+ *                  pages rows do not share gives those rows another row's prefix.
+ *  max_group       rows of the largest group as the host knows them, 0 where it does not:
+ *                  it picks the kernel's form and changes no result.
+ *  workspace       device, >= gqa_decode_shared_workspace_size(...) bytes, otherwise as
+ *                  gqa_decode's (which it may be shared with).
+ *  Cache dtypes: F16, BF16; others are GQA_ERR_UNSUPPORTED. Other arguments and limits as
+ *  gqa_decode; batch <= 8191.
+ */
+GQA_API size_t gqa_decode_shared_workspace_size(int32_t batch, int32_t num_heads, int32_t num_kv_heads,
+                                 int32_t head_dim, int32_t tokens_per_seq, int32_t device);
+GQA_API int gqa_decode_shared(const gqa_kv_cache_t *cache, const void *q, int32_t q_dtype, int32_t num_heads,
+               const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *context_lens,
+               int32_t batch, int32_t tokens_per_seq, float scale, const int32_t *groups, int32_t max_group,
+               void *out, int32_t out_dtype, void *workspace, size_t workspace_bytes, int32_t *err_flag,
+               void *stream);
 
 /*
  * gqa_decode without a caller-supplied workspace. The pages have no

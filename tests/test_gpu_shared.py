@@ -1,0 +1,313 @@
+"""Decode attention over shared prefixes against the softmax written out in fp64.
+
+Bound of an fp32 output, relative to the largest |v|: a score of d <= 128 products that are
+exact in fp32 has an accumulation error of at most 128 * 2^-23 * sum |q_i k_i| * scale, with
+N(0,1) inputs below 8 * 128 * 2^-23 = 2^-13; it enters a weight and the sum of weights, so
+2^-12. Weights in two 16-bit parts add 2^-16 each, exp2 and the merges 2^-20. Together below
+2^-11. An output of a 16-bit type adds half its step."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import shared
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def gq():
+    from gqa_decode_attention_kv_gb300 import build
+    build.build()
+    import gqa_decode_attention_kv_gb300 as m
+    return m
+
+
+def run(gq, kind, K, G, d, T, groups, alone, seed=0, q_dtype=None, out=torch.float32, order="pktd", max_group=0,
+        columns=1, plan=None, tweak=None, amp=1.0, scale=None):
+    bt = shared.batch(groups, alone, seed, columns=columns)
+    cache, values = shared.pool(kind, bt.pages, K, d, seed + 1, gq, order=order, amp=amp)
+    if tweak:
+        tweak(bt, cache, values)
+    qt = q_dtype or shared.DTYPES.get(kind, torch.bfloat16)
+    q = torch.randn(len(bt.lens), T, K * G, d, generator=torch.Generator().manual_seed(seed + 2)).to(qt)
+    table, lens = torch.from_numpy(bt.table).cuda(), torch.from_numpy(bt.lens).cuda()
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    plan = gq.kv_pages_groups(table, lens, err=err) if plan is None else plan(table, lens)
+    scale = 1 / math.sqrt(d) if scale is None else scale
+    got = gq.gqa_decode_shared(cache, q.cuda() if T > 1 else q[:, 0].contiguous().cuda(), table, lens, scale, plan,
+                               out_dtype=out, max_group=max_group, err=err)
+    torch.cuda.synchronize()
+    want = shared.attend(q.double().numpy(), values, bt.table, bt.lens, scale)
+    return got.view(q.shape).double().cpu().numpy(), want, int(err), values, plan
+
+
+def check(got, want, values, out=torch.float32):
+    bound = np.nanmax(np.abs(values[1])) * 2.0 ** -11 + (
+        np.abs(want) * torch.finfo(out).eps / 2 if out != torch.float32 else 0)
+    assert np.isfinite(got).all()
+    assert (np.abs(got - want) <= bound).all(), float((np.abs(got - want) - bound).max())
+
+
+SHAPES = [
+    # K, G, d, T, groups (shared blocks, lengths), alone
+    (1, 1, 128, 1, [(1, [17, 16])], []),
+    (2, 4, 128, 1, [(3, [49, 50, 70])], [5, 0]),
+    (2, 4, 64, 1, [(4, [64, 65, 66, 100])], []),
+    (2, 3, 128, 2, [(5, [82, 99, 81])], [1, 2, 300]),
+    (8, 4, 128, 1, [(64, [1025, 1040, 1100, 1024])], [7]),
+    (4, 8, 64, 3, [(17, [275, 290, 300]), (2, [35, 60]), (40, [700, 650])], [0, 33]),
+    (1, 8, 128, 4, [(33, [532] * 9)], []),                       # 288 rows: more than a CTA's tiles
+    (2, 8, 128, 1, [(20, [321 + i for i in range(40)])], []),    # 320 rows
+    (1, 16, 64, 1, [(9, [150] * 9)], [3]),                       # 144 rows
+    (2, 2, 128, 16, [(6, [112, 130])], [40]),
+    (3, 5, 128, 1, [(7, [113, 120]), (7, [115, 200, 131])], []),
+]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("K,G,d,T,groups,alone", SHAPES)
+def test_against_fp64(gq, kind, K, G, d, T, groups, alone):
+    got, want, err, values, plan = run(gq, kind, K, G, d, T, groups, alone)
+    assert err == 0
+    assert plan.count.tolist()[0] == len(groups)
+    check(got, want, values)
+
+
+@pytest.mark.parametrize("max_group", [1, 4, 500])
+@pytest.mark.parametrize("out", [torch.float16, torch.bfloat16, torch.float32])
+def test_forms_and_outputs(gq, max_group, out):
+    """The hint picks one or two tiles per CTA whatever the groups are."""
+    got, want, err, values, _ = run(gq, "bf16", 2, 8, 128, 1, [(20, [321 + i for i in range(40)]), (9, [150, 151])], [11],
+                                    out=out, max_group=max_group)
+    assert err == 0
+    check(got, want, values, out)
+
+
+@pytest.mark.parametrize("order", ["ptkd", "kptd", "pktd"])
+def test_axis_orders(gq, order):
+    got, want, err, values, _ = run(gq, "f16", 4, 2, 128, 1, [(10, [161, 170, 200])], [30], order=order)
+    assert err == 0
+    check(got, want, values)
+
+
+def test_short_and_empty_rows_of_a_group(gq):
+    """Rows that went back behind the shared pages attend alone, with the plan they were in."""
+    for T in (1, 2):
+        bt = shared.batch([(10, [161, 170, 200, 165, 190, 177])], [], 0)
+        cache, values = shared.pool("bf16", bt.pages, 2, 128, 1, gq)
+        table, lens = torch.from_numpy(bt.table).cuda(), torch.from_numpy(bt.lens).cuda()
+        plan_ = gq.kv_pages_groups(table, lens)
+        now = bt.lens.copy()
+        now[0], now[2], now[3] = 0, 33, 160
+        lens.copy_(torch.from_numpy(now))
+        q = torch.randn(6, T, 8, 128, generator=torch.Generator().manual_seed(3)).bfloat16()
+        got = gq.gqa_decode_shared(cache, q.cuda(), table, lens, 0.09, plan_)
+        want = shared.attend(q.double().numpy(), values, bt.table, now, 0.09)
+        check(got.double().cpu().numpy(), want, values)
+        assert (got[0] == 0).all()
+
+
+def test_no_groups_and_one_row(gq):
+    got, want, err, values, plan = run(gq, "bf16", 2, 4, 128, 1, [], [100])
+    assert err == 0 and plan.count.tolist() == [0, 0]
+    check(got, want, values)
+
+
+def test_poison_behind_the_rows(gq):
+    """Slots behind a row's end and pages of no row hold NaN; nothing of them is seen."""
+    def tweak(bt, cache, values):
+        owned = np.zeros((bt.pages, 16), dtype=bool)
+        for b, L in enumerate(bt.lens):
+            for t in range(L):
+                owned[bt.table[b, t // 16], t % 16] = True
+        at = torch.from_numpy(~owned)
+        for t in (cache.k, cache.v):
+            x = t.cpu()                                             # [pages, K, 16, d]
+            x[at[:, None, :].expand(-1, x.shape[1], -1)] = float("nan")
+            t.copy_(x)
+
+    for d in (64, 128):
+        got, want, err, values, _ = run(gq, "bf16", 2, 4, d, 1, [(5, [81, 95, 90]), (6, [97, 98])], [3, 0, 18], tweak=tweak)
+        assert err == 0
+        check(got, want, values)
+
+
+def test_same_pages_elsewhere_in_the_tables(gq):
+    """A page that another row holds at another place is no shared prefix."""
+    def tweak(bt, cache, values):
+        bt.table[0, 3] = bt.table[1, 2]
+
+    got, want, err, values, plan = run(gq, "f16", 2, 2, 64, 1, [(2, [60, 64, 50])], [], tweak=tweak)
+    assert err == 0 and plan.blocks.tolist()[0] == 2
+    check(got, want, values)
+
+
+def test_large_and_small_scores(gq):
+    """Scores far apart: the running maximum is rescaled step by step."""
+    for amp, scale in ((4.0, 0.5), (1.0, 0.0), (1.0, -0.1)):
+        bt = shared.batch([(40, [641, 700, 655])], [], 5)
+        cache, values = shared.pool("bf16", bt.pages, 2, 128, 6, gq, amp=amp)
+        q = torch.randn(3, 1, 8, 128, generator=torch.Generator().manual_seed(7)).bfloat16()
+        table, lens = torch.from_numpy(bt.table).cuda(), torch.from_numpy(bt.lens).cuda()
+        got = gq.gqa_decode_shared(cache, q[:, 0].contiguous().cuda(), table, lens, scale, gq.kv_pages_groups(table, lens))
+        want = shared.attend(q.double().numpy(), values, bt.table, bt.lens, scale)
+        # scores up to amp * scale * sqrt(d) times larger than the bound above allows for
+        bound = np.abs(values[1]).max() * 2.0 ** -11 * max(1.0, amp * abs(scale) * math.sqrt(128))
+        assert (np.abs(got.view(q.shape).double().cpu().numpy() - want) <= bound).all()
+
+
+def test_equals_decode_and_shares_its_workspace(gq):
+    bt = shared.batch([(30, [500 + i for i in range(7)]), (11, [200, 300])], [40, 0], 8)
+    cache, values = shared.pool("bf16", bt.pages, 4, 128, 9, gq)
+    B = len(bt.lens)
+    q = torch.randn(B, 16, 128, generator=torch.Generator().manual_seed(10)).bfloat16().cuda()
+    table, lens = torch.from_numpy(bt.table).cuda(), torch.from_numpy(bt.lens).cuda()
+    plan = gq.kv_pages_groups(table, lens)
+    ws = torch.zeros(gq.decode_shared_workspace_size(B, 16, 4, 128), dtype=torch.uint8, device="cuda")
+    outs = []
+    for _ in range(3):
+        outs.append(gq.gqa_decode(cache, q, table, lens, 0.1, workspace=ws))
+        outs.append(gq.gqa_decode_shared(cache, q, table, lens, 0.1, plan, workspace=ws))
+    for a in outs[2:]:
+        assert torch.equal(a, outs[0]) or torch.equal(a, outs[1])
+    assert float((outs[0] - outs[1]).abs().max()) <= 2 * np.abs(values[1]).max() * 2.0 ** -11
+
+
+def test_streams_and_graphs(gq):
+    """Captured calls of one stream replayed on two, interleaved with eager ones."""
+    bt = shared.batch([(30, [500 + i for i in range(7)])], [40], 11)
+    cache, values = shared.pool("bf16", bt.pages, 4, 128, 12, gq)
+    B = len(bt.lens)
+    q = torch.randn(B, 1, 16, 128, generator=torch.Generator().manual_seed(13)).bfloat16()
+    table, lens = torch.from_numpy(bt.table).cuda(), torch.from_numpy(bt.lens).cuda()
+    want = shared.attend(q.double().numpy(), values, bt.table, bt.lens, 0.1)
+    q = q[:, 0].contiguous().cuda()
+    plan = gq.kv_pages_groups(table, lens)
+    gq.gqa_decode_shared(cache, q, table, lens, 0.1, plan)
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            p = gq.kv_pages_groups(table, lens)
+            outs.append(gq.gqa_decode_shared(cache, q, table, lens, 0.1, p))
+        graphs.append(g)
+    side = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        for s, g in zip(side, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+        eager = gq.gqa_decode_shared(cache, q, table, lens, 0.1, plan)
+        on = gq.gqa_decode_shared(cache, q, table, lens, 0.1, plan, stream=side[0])
+    torch.cuda.synchronize()
+    for o in (*outs, eager, on):
+        check(o.view(want.shape).double().cpu().numpy(), want, values)
+
+
+def test_bad_pages_are_flagged(gq):
+    """A shared entry that is no page: flagged, its tokens are not seen, nothing else changes."""
+    bt = shared.batch([(9, [150, 160])], [40], 14)
+    cache, values = shared.pool("bf16", bt.pages, 2, 128, 15, gq)
+    q = torch.randn(3, 1, 8, 128, generator=torch.Generator().manual_seed(16)).bfloat16()
+    table, lens = torch.from_numpy(bt.table).cuda(), torch.from_numpy(bt.lens).cuda()
+    plan = gq.kv_pages_groups(table, lens)
+    lead = plan.rows.tolist()[0]
+    for bad in (-1, bt.pages, 2 ** 31 - 1):
+        broken = table.clone()
+        broken[lead, 4] = bad
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        got = gq.gqa_decode_shared(cache, q[:, 0].contiguous().cuda(), broken, lens, 0.1, plan, err=err)
+        assert int(err) == gq.GQA_DEVERR_BLOCK_INDEX
+        assert torch.isfinite(got).all()
+        alone = [b for b in range(3) if b not in plan.rows.tolist()[:2]][0]
+        want = shared.attend(q.double().numpy(), values, bt.table, bt.lens, 0.1)
+        check(got.view(q.shape).double().cpu().numpy()[[alone]], want[[alone]], values)
+
+
+def test_lengths_out_of_range_are_flagged(gq):
+    bt = shared.batch([(9, [150, 160, 170])], [], 17)
+    cache, values = shared.pool("bf16", bt.pages, 2, 128, 18, gq)
+    q = torch.randn(3, 1, 8, 128, generator=torch.Generator().manual_seed(19)).bfloat16()
+    table, lens = torch.from_numpy(bt.table).cuda(), torch.from_numpy(bt.lens).cuda()
+    plan = gq.kv_pages_groups(table, lens)
+    want = shared.attend(q.double().numpy(), values, bt.table, bt.lens, 0.1)
+    for bad in (-5, 16 * bt.table.shape[1] + 1):
+        now = lens.clone()
+        now[1] = bad
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        got = gq.gqa_decode_shared(cache, q[:, 0].contiguous().cuda(), table, now, 0.1, plan, err=err)
+        assert int(err) == gq.GQA_DEVERR_CONTEXT_LEN
+        check(got.view(q.shape).double().cpu().numpy()[[0, 2]], want[[0, 2]], values)
+
+
+def test_plans_that_point_astray_share_nothing(gq):
+    """Entries outside the plan or the tables: every row attends alone, or as its entries say."""
+    bt = shared.batch([(9, [150, 160, 170])], [60], 20)
+    cache, values = shared.pool("bf16", bt.pages, 2, 128, 21, gq)
+    B = len(bt.lens)
+    q = torch.randn(B, 1, 8, 128, generator=torch.Generator().manual_seed(22)).bfloat16()
+    table, lens = torch.from_numpy(bt.table).cuda(), torch.from_numpy(bt.lens).cuda()
+    want = shared.attend(q.double().numpy(), values, bt.table, bt.lens, 0.1)
+    for part, value in (("count", 0), ("count", -3), ("start", -7), ("start", 10 ** 6), ("blocks", 0), ("blocks", -1),
+                        ("blocks", 10 ** 6), ("slot", -1), ("slot", 10 ** 6), ("group", 10 ** 6), ("group", -2),
+                        ("rows", 10 ** 6), ("rows", -9)):
+        plan = gq.kv_pages_groups(table, lens)
+        getattr(plan, part).fill_(value)
+        got = gq.gqa_decode_shared(cache, q[:, 0].contiguous().cuda(), table, lens, 0.1, plan)
+        check(got.view(q.shape).double().cpu().numpy(), want, values)
+
+
+def test_plan_written_by_the_caller(gq):
+    """Two of three rows that share pages, over fewer pages than they have in common."""
+    bt = shared.batch([(9, [150, 160, 170])], [60], 23)
+    cache, values = shared.pool("f16", bt.pages, 2, 64, 24, gq)
+    B = len(bt.lens)
+    q = torch.randn(B, 2, 8, 64, generator=torch.Generator().manual_seed(25)).half()
+    table, lens = torch.from_numpy(bt.table).cuda(), torch.from_numpy(bt.lens).cuda()
+    kin = sorted(plan_rows for plan_rows in gq.kv_pages_groups(table, lens).rows.tolist() if plan_rows >= 0)
+    a, b = kin[2], kin[0]
+    plan = gq.kv_pages_groups(table, lens)
+    plan.count.copy_(torch.tensor([1, 2]))
+    plan.start.fill_(2)
+    plan.start[0] = 0
+    plan.blocks.fill_(0)
+    plan.blocks[0] = 5
+    plan.rows.copy_(torch.tensor([a, b] + [-1] * (B - 2)))
+    plan.slot.fill_(-1)
+    plan.group.fill_(-1)
+    plan.slot[a], plan.slot[b] = 0, 1
+    plan.group[a], plan.group[b] = 0, 0
+    got = gq.gqa_decode_shared(cache, q.cuda(), table, lens, 0.1, plan)
+    want = shared.attend(q.double().numpy(), values, bt.table, bt.lens, 0.1)
+    check(got.double().cpu().numpy(), want, values)
+
+
+def test_steps_after_a_fork(gq):
+    """fork, the plan, then steps of append and shared decode, against plain decode."""
+    K, G, d, B = 2, 4, 128, 6
+    cache = gq.PagedKVCache.allocate(128, K, d, torch.bfloat16)
+    refs = torch.zeros(128, dtype=torch.int32, device="cuda")
+    table = torch.full((B, 24), -1, dtype=torch.int32, device="cuda")
+    lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(26)
+    rand = lambda *s: torch.randn(*s, generator=gen, device="cuda").bfloat16()  # noqa: E731
+    n = torch.tensor([203] + [0] * (B - 1), dtype=torch.int32, device="cuda")
+    gq.kv_pages_reserve(refs, table, lens, n)
+    gq.kv_append_varlen(cache, rand(203, K, d), rand(203, K, d),
+                        torch.tensor([0] + [203] * B, dtype=torch.int32, device="cuda"), 203, table, lens)
+    lens += n
+    child = torch.arange(1, B, dtype=torch.int32, device="cuda")
+    copies = gq.kv_pages_fork(refs, table, lens, torch.zeros_like(child), child)
+    gq.kv_copy_pages(cache, copies)
+    plan = gq.kv_pages_groups(table, lens)
+    assert plan.count.tolist() == [1, B] and plan.blocks.tolist()[0] == 203 // 16
+    for step in range(20):
+        gq.kv_pages_reserve(refs, table, lens, 1)
+        gq.kv_append(cache, rand(B, K, d), rand(B, K, d), table, lens)
+        lens += 1
+        q = rand(B, K * G, d)
+        a = gq.gqa_decode_shared(cache, q, table, lens, 0.09, plan)
+        b = gq.gqa_decode(cache, q, table, lens, 0.09)
+        assert float((a - b).abs().max()) <= 2 * 5 * 2.0 ** -11, step
