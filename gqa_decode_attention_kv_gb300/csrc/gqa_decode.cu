@@ -257,7 +257,7 @@ int launch_decode(const DecodeLaunch& L, int num_sms) {
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
     const bool timed = L.ev_begin || L.ev_end;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
+    cfg.gridDim = dim3(tail ? grid + 1 : grid);
     cfg.blockDim = dim3(v.warps * 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = L.stream;

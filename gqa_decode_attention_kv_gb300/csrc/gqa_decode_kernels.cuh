@@ -79,7 +79,6 @@ struct DecodeArgs {
     int GT;              // query rows per (sequence, kv-head) pair: G * T
     int window;          // sliding window in tokens; 0 = full attention
     int sinks;           // sink flavour: first tokens that stay visible
-    const int32_t* groups;   // tail flavour: which rows share their first blocks
     // Unit space: Kv = K * NRG heads per sequence. NRG > 1 splits a pair's GT
     // rows into groups of 8 ("virtual kv-heads" gv = g * NRG + group), each an
     // independent unit stream that re-reads the pair's tiles (from L2, since
@@ -91,6 +90,7 @@ struct DecodeArgs {
     int page_perm[2];    // page-map dims 3, 4 -> 1 kv-head, 2 block
     int max_tail_chunks; // pooled chunks per worker range (0 = static partition only)
     float scale_log2;    // scale * log2(e)
+    const int32_t* groups;   // tail flavour: which rows share their first blocks
 };
 
 // Warps per CTA and shared-memory ring bytes per warp of the split-KV kernel
@@ -1342,8 +1342,15 @@ __device__ __forceinline__ Partition make_partition(const DecodeArgs& a, int U) 
     return pt;
 }
 
+// The tail flavour runs beside the kernel before it, which attends the shared blocks and
+// lets this one start only after its own wait for earlier work: nothing that the workers
+// read is still being written. Its one CTA past the workers ends after that kernel, so that
+// the merge behind has both.
 template <int kKind, typename T, int D, int kHeadWarps, bool kGen, bool kSinks, bool kTail>
-__device__ __forceinline__ void split_kv(const CUtensorMap& kmap, const CUtensorMap& vmap, const DecodeArgs& a) {
+__global__ void __launch_bounds__(Cfg<kKind, T, D, kHeadWarps, kGen, kSinks, kTail>::kWarps * 32,
+                                  Cfg<kKind, T, D, kHeadWarps, kGen, kSinks, kTail>::kMinCtas)
+split_kv_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                const DecodeArgs a) {
     using C = Cfg<kKind, T, D, kHeadWarps, kGen, kSinks, kTail>;
     using S = Smem<C>;
     constexpr bool kShared = kHeadWarps > 1;     // one ring, one worker per CTA
@@ -1360,7 +1367,12 @@ __device__ __forceinline__ void split_kv(const CUtensorMap& kmap, const CUtensor
         prefetch_tensormap(&vmap);
     }
     launch_dependents();                       // the combine kernel may take its place now
-    if constexpr (!kTail) grid_dependency_wait();   // inputs may come from the previous kernel
+    if constexpr (!kTail) {
+        grid_dependency_wait();                // inputs may come from the previous kernel
+    } else if (blockIdx.x == gridDim.x - 1) {
+        grid_dependency_wait();
+        return;
+    }
     block_prefix<kGen, kSinks, kTail>(a, lens_s, pref, tmp, pref + a.B + 1);
     const Partition pt = make_partition(a, a.Kv * pref[a.B]);
     if (blockIdx.x == 0) {
@@ -1436,8 +1448,9 @@ __device__ __forceinline__ void split_kv(const CUtensorMap& kmap, const CUtensor
         if (u < pt.U) {
             int b, g, j;
             locate(u, pref, a.B, a.Kv, b, g, j);
-            const int first = kTail ? (pref + a.B + 1)[b] : 0;
-            const int ph = a.block_tables[(long long)b * a.max_blocks + first + logical_block<kGen, kSinks>(a, lens_s[b], j)];
+            int lb = logical_block<kGen, kSinks>(a, lens_s[b], j);
+            if constexpr (kTail) lb += pref[a.B + 1 + b];            // behind the shared blocks
+            const int ph = a.block_tables[(long long)b * a.max_blocks + lb];
             if (ph < 0 || ph >= a.num_blocks) flag_error(a.err, GQA_DEVERR_BLOCK_INDEX);
             else win_phys = ph;
             win_g = g / a.NRG;                 // the real kv-head
@@ -1745,18 +1758,6 @@ __device__ __forceinline__ void split_kv(const CUtensorMap& kmap, const CUtensor
             ++cj;
         }
     }
-}
-
-// The tail flavour runs beside the kernel before it, which attends the shared blocks and
-// lets this one start only after its own wait for earlier work: nothing it reads is still
-// being written. It ends after that kernel, so that the merge behind it has both.
-template <int kKind, typename T, int D, int kHeadWarps, bool kGen, bool kSinks, bool kTail>
-__global__ void __launch_bounds__(Cfg<kKind, T, D, kHeadWarps, kGen, kSinks, kTail>::kWarps * 32,
-                                  Cfg<kKind, T, D, kHeadWarps, kGen, kSinks, kTail>::kMinCtas)
-split_kv_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                const DecodeArgs a) {
-    split_kv<kKind, T, D, kHeadWarps, kGen, kSinks, kTail>(kmap, vmap, a);
-    if constexpr (kTail) grid_dependency_wait();
 }
 
 // ------------------------------------------------------------------ combine
