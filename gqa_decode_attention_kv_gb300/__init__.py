@@ -474,40 +474,22 @@ def gqa_decode(cache: PagedKVCache, q: torch.Tensor, block_tables: torch.Tensor,
     return out
 
 
-@dataclasses.dataclass
 class PrefixGroups:
     """Which rows of a batch share their first pages, as ``kv_pages_groups`` finds it:
     int32 arrays, views of ``plan``. Group i holds ``rows[start[i]:start[i+1]]`` and shares
-    ``blocks[i]`` pages; ``slot`` and ``group`` of a row are -1 where it shares nothing."""
-    plan: torch.Tensor
-    batch: int
+    ``blocks[i]`` pages; ``slot`` and ``group`` of a row are -1 where it shares nothing;
+    ``count`` holds the groups and the rows in groups."""
+    __slots__ = ("plan", "batch", "count", "start", "blocks", "rows", "slot", "group")
 
-    def _part(self, first: int, n: int) -> torch.Tensor:
-        return self.plan[first:first + n]
+    def __init__(self, plan: torch.Tensor, batch: int):
+        self.plan, self.batch = plan, batch
+        self.count, self.start, self.blocks, self.rows, self.slot, self.group = plan.split_with_sizes(
+            (2, batch + 1, batch, batch, batch, batch, plan.shape[0] - 3 - 5 * batch))[:6]
 
-    @property
-    def count(self) -> torch.Tensor:           # groups, rows in groups
-        return self._part(0, 2)
 
-    @property
-    def start(self) -> torch.Tensor:
-        return self._part(2, self.batch + 1)
-
-    @property
-    def blocks(self) -> torch.Tensor:
-        return self._part(3 + self.batch, self.batch)
-
-    @property
-    def rows(self) -> torch.Tensor:
-        return self._part(3 + 2 * self.batch, self.batch)
-
-    @property
-    def slot(self) -> torch.Tensor:
-        return self._part(3 + 3 * self.batch, self.batch)
-
-    @property
-    def group(self) -> torch.Tensor:
-        return self._part(3 + 4 * self.batch, self.batch)
+@functools.lru_cache(maxsize=256)
+def _groups_size_of(batch: int) -> int:
+    return int(load().gqa_kv_pages_groups_size(batch))
 
 
 def kv_pages_groups(block_tables: torch.Tensor, context_lens: torch.Tensor, min_blocks: int = 1,
@@ -528,7 +510,7 @@ def kv_pages_groups(block_tables: torch.Tensor, context_lens: torch.Tensor, min_
                          f"not {tuple(context_lens.shape)}")
     _on_one_device(block_tables=block_tables, context_lens=context_lens, err=err,
                    groups=None if groups is None else groups.plan)
-    need = int(load().gqa_kv_pages_groups_size(B))
+    need = _groups_size_of(B)
     if need == 0:
         raise ValueError(f"no plan for {B} rows")
     if groups is None:

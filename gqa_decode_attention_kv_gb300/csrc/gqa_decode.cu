@@ -202,8 +202,9 @@ int launch_decode(const DecodeLaunch& L, int num_sms) {
         grid = std::min(grid, std::max(1, (L.max_warps + v.workers_per_cta - 1) / v.workers_per_cta));
     const int P = grid * v.workers_per_cta;   // split-KV workers (KV splits per pass)
 
+    // (the tail flavour picks its workers on the device, so its ranges have no host bound)
     const WsLayout wl =
-        ws_layout(L.batch, Kv, RS, D, max_slots(L.batch, Kv, P, L.max_blocks, min_units, v.tail_chunks));
+        ws_layout(L.batch, Kv, RS, D, max_slots(L.batch, Kv, P, tail ? 0 : L.max_blocks, min_units, v.tail_chunks));
     const size_t need = wl.total + (tail ? shared_prefix_bytes(L.batch, L.num_heads, D, T, num_sms) : 0);
     if (L.workspace == nullptr || L.workspace_bytes < need) return GQA_ERR_WORKSPACE;
 
@@ -234,6 +235,8 @@ int launch_decode(const DecodeLaunch& L, int num_sms) {
     a.window = L.window;
     a.sinks = sinks ? (int)std::min<long long>(L.sinks, (long long)L.max_blocks * kBlock) : 0;
     a.groups = tail ? L.shared->groups : nullptr;
+    a.split = SplitModel{};
+    if (tail && !split_model(L, num_sms, a.split)) return GQA_ERR_UNSUPPORTED;
     a.max_blocks = L.max_blocks;
     a.out_dtype = L.out_dtype;
     a.q_dtype = L.q_dtype;

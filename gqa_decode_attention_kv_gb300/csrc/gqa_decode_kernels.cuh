@@ -91,6 +91,7 @@ struct DecodeArgs {
     int max_tail_chunks; // pooled chunks per worker range (0 = static partition only)
     float scale_log2;    // scale * log2(e)
     const int32_t* groups;   // tail flavour: which rows share their first blocks
+    SplitModel split;        //               and the GPU's division with the prefix kernel
 };
 
 // Warps per CTA and shared-memory ring bytes per warp of the split-KV kernel
@@ -1331,15 +1332,36 @@ struct Partition {
     }
 };
 
-__device__ __forceinline__ Partition make_partition(const DecodeArgs& a, int U) {
+__device__ __forceinline__ Partition make_partition(const DecodeArgs& a, int U, int P) {
     Partition pt;
     pt.U = U;
-    pt.P = max(a.P, 1);
+    pt.P = max(P, 1);
     pt.R = max((U + pt.P - 1) / pt.P, a.min_units);
     pt.Cz = max(kMinChunk, (pt.R + 31) / 32);
     pt.cpw = min(a.max_tail_chunks, pt.R / (8 * pt.Cz));
     pt.Rs = pt.R - pt.cpw * pt.Cz;
     return pt;
+}
+
+// Workers of the tail flavour: those of the SMs that the prefix kernel leaves (the CTAs
+// after them find no room before it ends, and then nothing to do). units: blocks of the
+// rows' own times kv-heads; tmp: 32 ints of shared memory.
+template <class C>
+__device__ int tail_workers(const DecodeArgs& a, int units, int* tmp) {
+    const PrefixGroups plan(a.groups, a.B);
+    const int n = plan.groups(), lane = threadIdx.x & 31;
+    int steps = 0;
+    for (int i = threadIdx.x; i < n; i += blockDim.x)
+        steps += problem_of(group_span(plan, i, a.max_blocks), a.K, a.GT, a.split.cta_rows).units;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) steps += __shfl_xor_sync(kFull, steps, o);
+    if (lane == 0) tmp[threadIdx.x >> 5] = steps;
+    __syncthreads();
+    steps = 0;
+    for (int i = 0; i < (int)blockDim.x / 32; ++i) steps += tmp[i];
+    const int per_cta = C::kNw == 1 ? C::kWarps : 1;
+    const int ctas = a.P / per_cta, left = a.split.sms - prefix_sms(a.split, steps, units);
+    return max(1, (int)((long long)ctas * left / a.split.sms)) * per_cta;
 }
 
 // The tail flavour runs beside the kernel before it, which attends the shared blocks and
@@ -1374,7 +1396,7 @@ split_kv_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
         return;
     }
     block_prefix<kGen, kSinks, kTail>(a, lens_s, pref, tmp, pref + a.B + 1);
-    const Partition pt = make_partition(a, a.Kv * pref[a.B]);
+    const Partition pt = make_partition(a, a.Kv * pref[a.B], kTail ? tail_workers<C>(a, pref[a.B] * a.K, tmp) : a.P);
     if (blockIdx.x == 0) {
         for (int i = threadIdx.x; i <= a.B; i += blockDim.x) a.ws_pref[i] = pref[i];
         if (threadIdx.x == 0) {
@@ -1980,6 +2002,7 @@ bool pick_tail(int dtype, int kind, int d, int nw, Variant& v);
 
 // Merge of a shared decode: the tail's pieces (a: the split-KV launch's arguments) and the
 // prefix's (gqa_shared.cu).
+bool split_model(const DecodeLaunch& L, int num_sms, SplitModel& m);
 int launch_shared_merge(const DecodeArgs& tail, const DecodeLaunch& L, uint8_t* ws, int num_sms);
 
 }  // namespace dec

@@ -3,14 +3,17 @@
 // With n_b the full pages of row b, its leader is the lowest row with the same first
 // page, and m_b the number of leading entries it has in common with the leader's. Of a
 // leader's rows a group takes P pages where P (c(P) - 1) is largest, c(P) the rows with
-// m_b >= P: the pages that attending them once saves reading. Three short kernels, each
-// with the whole GPU on it, because each needs all of the one before:
-//   runs    one CTA per row: the leader, then the common run, 512 entries a step
-//   counts  one warp per row: c(m_b) over all rows, the best P of each leader by one
-//           64-bit maximum (saving, then fewer rows, so the larger P at equal saving)
-//   places  one warp per row: groups in the order of their leaders, members by row
-// The tables are read once as far as rows agree (the leaders' rows come from L2). The
-// two passes over all pairs of rows are 8 bytes a pair from L2 or L1.
+// m_b >= P: the pages that attending them once saves reading. Each step needs all of the
+// one before:
+//   runs    the leader of a row, then the run they have in common
+//   counts  c(m_b) over all rows, the best P of each leader by one 64-bit maximum (the
+//           saving, then fewer rows, so the larger P at equal saving)
+//   places  groups in the order of their leaders, members by row
+// The tables are read once as far as rows agree (the leaders' rows come from L2), which is
+// a few microseconds at most: the steps' latencies bound this. Up to 128 rows one cluster
+// of eight CTAs does all three, a warp per row, with one cluster barrier; more rows take a
+// launch per step over the whole GPU, where the two passes over all pairs of rows run from
+// shared memory.
 #include "gqa_groups.cuh"
 #include "gqa_internal.h"
 
@@ -29,22 +32,74 @@ struct GroupsArgs {
 };
 
 constexpr int kRunThreads = 128, kRunUnroll = 4;
-constexpr int kPairThreads = 256;
+constexpr int kPairThreads = 512, kPairRows = kPairThreads / 32;   // a warp per row
+constexpr int kSmallCtas = 8, kSmallRows = kSmallCtas * kPairRows;
 constexpr int kRankBits = 14;
 constexpr unsigned kRankMask = (1u << kRankBits) - 1;
+
+// What a run of m pages that c > 1 rows share is worth, as a leader's best is kept.
+__device__ __forceinline__ unsigned long long worth(int m, int c) {
+    return ((unsigned long long)m * (unsigned)(c - 1) << kRankBits) | (kRankMask - (unsigned)c);
+}
+// The pages of a best, 0: no group.
+__device__ __forceinline__ int pages_of(unsigned long long best) {
+    if (best == 0ull) return 0;
+    return (int)((best >> kRankBits) / (kRankMask - (unsigned)(best & kRankMask) - 1u));
+}
+
+// Row b of B, by one warp: lead[r] is the leader of row r where it is a member of that
+// leader's group, else -1; shared: pages of b's own group.
+__device__ __forceinline__ void place_row(int32_t* plan, int B, const int* lead, int b, int shared, int lane) {
+    const int mine = lead[b];
+    int groups = 0, total = 0, before_groups = 0, before = 0;
+#pragma unroll 4
+    for (int r = lane; r < B; r += 32) {
+        const int w = lead[r];
+        total += w >= 0;
+        groups += w == r;
+        before_groups += w == r && r < mine;
+        before += w >= 0 && (w < mine || (w == mine && r < b));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        groups += __shfl_xor_sync(kFull, groups, o);
+        total += __shfl_xor_sync(kFull, total, o);
+        before_groups += __shfl_xor_sync(kFull, before_groups, o);
+        before += __shfl_xor_sync(kFull, before, o);
+    }
+    if (lane != 0) return;
+    const GroupsLayout l(B);
+    if (b == 0) {
+        plan[0] = groups;
+        plan[1] = total;
+        plan[l.start + B] = total;
+    }
+    plan[l.slot + b] = mine >= 0 ? before : -1;
+    plan[l.group + b] = mine >= 0 ? before_groups : -1;
+    if (mine >= 0) plan[l.rows + before] = b;
+    if (mine == b) {
+        plan[l.start + before_groups] = before;
+        plan[l.blocks + before_groups] = shared;
+    }
+    if (b >= total) plan[l.rows + b] = -1;
+    if (b >= groups) {
+        plan[l.start + b] = total;
+        plan[l.blocks + b] = 0;
+    }
+}
+
+__device__ __forceinline__ int full_pages(const GroupsArgs& a, int r) {   // -1: a length out of range
+    const int L = a.context_lens[r];
+    return L < 0 || L > a.max_blocks * kBlock ? -1 : L / kBlock;
+}
 
 __global__ void __launch_bounds__(kRunThreads) runs_kernel(const GroupsArgs a) {
     __shared__ int s_min;
     const int tid = threadIdx.x, b = blockIdx.x;
     launch_dependents();
     grid_dependency_wait();
-    auto full_pages = [&](int r) {
-        const int L = a.context_lens[r];
-        if (L < 0 || L > a.max_blocks * kBlock) return -1;
-        return L / kBlock;
-    };
     const int32_t* mine = a.block_tables + (long long)b * a.max_blocks;
-    const int n = full_pages(b);
+    const int n = full_pages(a, b);
     if (tid == 0 && n < 0) flag_error(a.err, GQA_DEVERR_CONTEXT_LEN);
     const int key = n > 0 ? *mine : -1;
     if (tid == 0) a.best[b] = 0ull;
@@ -62,7 +117,7 @@ __global__ void __launch_bounds__(kRunThreads) runs_kernel(const GroupsArgs a) {
         for (int i = 0; i < kRunUnroll; ++i) {
             const int r = base + i * kRunThreads + tid;
             first[i] = r < b ? a.block_tables[(long long)r * a.max_blocks] : -1;
-            len[i] = r < b ? full_pages(r) : 0;
+            len[i] = r < b ? full_pages(a, r) : 0;
         }
 #pragma unroll
         for (int i = kRunUnroll - 1; i >= 0; --i)
@@ -74,7 +129,7 @@ __global__ void __launch_bounds__(kRunThreads) runs_kernel(const GroupsArgs a) {
         if (leader < b) break;
     }
     const int32_t* lead = a.block_tables + (long long)leader * a.max_blocks;
-    const int most = min(n, full_pages(leader));
+    const int most = min(n, full_pages(a, leader));
     int run = most;
     for (int base = 0; base < most; base += kRunThreads * kRunUnroll) {
         if (tid == 0) s_min = most;
@@ -100,79 +155,116 @@ __global__ void __launch_bounds__(kRunThreads) runs_kernel(const GroupsArgs a) {
 }
 
 __global__ void __launch_bounds__(kPairThreads) counts_kernel(const GroupsArgs a) {
-    const int lane = threadIdx.x & 31, b = blockIdx.x * (kPairThreads / 32) + (threadIdx.x >> 5);
+    extern __shared__ int2 s_run[];            // [B]
+    const int lane = threadIdx.x & 31, b = blockIdx.x * kPairRows + (threadIdx.x >> 5);
     launch_dependents();
     grid_dependency_wait();
+    for (int r = threadIdx.x; r < a.B; r += kPairThreads) s_run[r] = a.run[r];
+    __syncthreads();
     if (b >= a.B) return;
-    const int2 me = a.run[b];
+    const int2 me = s_run[b];
     if (me.y < max(a.min_blocks, 1)) return;
     int c = 0;
 #pragma unroll 4
     for (int r = lane; r < a.B; r += 32) {
-        const int2 o = a.run[r];
+        const int2 o = s_run[r];
         c += o.x == me.x && o.y >= me.y;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(kFull, c, o);
-    if (lane == 0 && c > 1)
-        atomicMax(a.best + me.x, ((unsigned long long)me.y * (unsigned)(c - 1) << kRankBits) | (kRankMask - (unsigned)c));
+    if (lane == 0 && c > 1) atomicMax(a.best + me.x, worth(me.y, c));
 }
 
 __global__ void __launch_bounds__(kPairThreads) places_kernel(const GroupsArgs a) {
-    const int lane = threadIdx.x & 31, b = blockIdx.x * (kPairThreads / 32) + (threadIdx.x >> 5);
+    extern __shared__ int s_lead[];            // [B], then the leaders' pages [B]
+    int* s_pages = s_lead + a.B;
+    const int b = blockIdx.x * kPairRows + (threadIdx.x >> 5);
     launch_dependents();
     grid_dependency_wait();
-    if (b >= a.B) return;
-    // pages of a leader's group, 0: none
-    auto pages = [&](int leader) -> int {
-        const unsigned long long k = a.best[leader];
-        if (k == 0ull) return 0;
-        return (int)((k >> kRankBits) / (kRankMask - (unsigned)(k & kRankMask) - 1u));
-    };
-    const int2 me = a.run[b];
-    const int shared = pages(me.x);
-    const bool member = shared > 0 && me.y >= shared;
-    int groups = 0, total = 0, before_groups = 0, before = 0;
-#pragma unroll 4
-    for (int r = lane; r < a.B; r += 32) {
+    for (int r = threadIdx.x; r < a.B; r += kPairThreads) s_pages[r] = pages_of(a.best[r]);
+    __syncthreads();
+    for (int r = threadIdx.x; r < a.B; r += kPairThreads) {
         const int2 o = a.run[r];
-        const int p = pages(o.x);
-        if (p == 0 || o.y < p) continue;
-        const bool head = o.x == r;
-        ++total;
-        groups += head;
-        before_groups += head && r < me.x;
-        before += o.x < me.x || (o.x == me.x && r < b);
+        s_lead[r] = s_pages[o.x] > 0 && o.y >= s_pages[o.x] ? o.x : -1;
     }
+    __syncthreads();
+    if (b < a.B) place_row(a.plan, a.B, s_lead, b, s_pages[b], threadIdx.x & 31);
+}
+
+// All three steps for up to kSmallRows rows.
+__global__ void __cluster_dims__(kSmallCtas) __launch_bounds__(kPairThreads) small_kernel(const GroupsArgs a) {
+    __shared__ int2 s_run[kSmallRows];
+    __shared__ unsigned long long s_best[kSmallRows];
+    __shared__ int s_lead[kSmallRows];
+    const int tid = threadIdx.x, lane = tid & 31, b = blockIdx.x * kPairRows + (tid >> 5);
+    launch_dependents();
+    grid_dependency_wait();
+    if (b < a.B) {
+        const int32_t* mine = a.block_tables + (long long)b * a.max_blocks;
+        const int n = full_pages(a, b);
+        if (lane == 0 && n < 0) flag_error(a.err, GQA_DEVERR_CONTEXT_LEN);
+        const int key = n > 0 ? mine[0] : -1;
+        int leader = b, run = 0;
+        if (key >= 0) {                        // uniform per warp
+            int first = b;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        groups += __shfl_xor_sync(kFull, groups, o);
-        total += __shfl_xor_sync(kFull, total, o);
-        before_groups += __shfl_xor_sync(kFull, before_groups, o);
-        before += __shfl_xor_sync(kFull, before, o);
-    }
-    if (lane != 0) return;
-    const GroupsLayout l(a.B);
-    int32_t* plan = a.plan;
-    if (b == 0) {
-        plan[0] = groups;
-        plan[1] = total;
-        plan[l.start + a.B] = total;           // where every row leads a group: unused otherwise
-    }
-    plan[l.slot + b] = member ? before : -1;
-    plan[l.group + b] = member ? before_groups : -1;
-    if (member) {
-        plan[l.rows + before] = b;
-        if (me.x == b) {
-            plan[l.start + before_groups] = before;
-            plan[l.blocks + before_groups] = shared;
+            for (int i = kSmallRows / 32 - 1; i >= 0; --i) {
+                const int r = 32 * i + lane;
+                if (r < b && a.block_tables[(long long)r * a.max_blocks] == key && full_pages(a, r) > 0) first = r;
+            }
+            leader = __reduce_min_sync(kFull, first);
+            const int32_t* lead = a.block_tables + (long long)leader * a.max_blocks;
+            const int most = min(n, full_pages(a, leader));
+            run = most;
+            for (int base = 0; base < most && run == most; base += 32 * 2 * kRunUnroll) {
+                int x[2 * kRunUnroll], y[2 * kRunUnroll];
+#pragma unroll
+                for (int i = 0; i < 2 * kRunUnroll; ++i) {
+                    const int j = base + 32 * i + lane;
+                    x[i] = j < most ? mine[j] : 0;
+                    y[i] = j < most ? lead[j] : 0;
+                }
+                int at = most;
+#pragma unroll
+                for (int i = 2 * kRunUnroll - 1; i >= 0; --i)
+                    if (x[i] != y[i] || x[i] < 0) at = base + 32 * i + lane;
+                run = __reduce_min_sync(kFull, at);
+            }
         }
+        if (lane == 0) a.run[b] = make_int2(leader, run);
     }
-    if (b >= total) plan[l.rows + b] = -1;
-    if (b >= groups) {
-        plan[l.start + b] = total;
-        plan[l.blocks + b] = 0;
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    // every CTA counts for all rows, then places its own
+    for (int r = tid; r < a.B; r += kPairThreads) {
+        s_run[r] = __ldcg(a.run + r);
+        s_best[r] = 0ull;
     }
+    __syncthreads();
+    constexpr int kParts = kPairThreads / kSmallRows;          // threads of a row
+    static_assert(kParts == 4, "four neighbouring threads count for a row");
+    {
+        const int r = tid / kParts;
+        int c = 0;
+        int2 me = make_int2(0, 0);
+        if (r < a.B) {
+            me = s_run[r];
+            for (int o = tid % kParts; o < a.B; o += kParts) {
+                const int2 x = s_run[o];
+                c += x.x == me.x && x.y >= me.y;
+            }
+        }
+        c += __shfl_xor_sync(kFull, c, 1);
+        c += __shfl_xor_sync(kFull, c, 2);
+        if (tid % kParts == 0 && me.y >= max(a.min_blocks, 1) && c > 1) atomicMax(&s_best[me.x], worth(me.y, c));
+    }
+    __syncthreads();
+    for (int r = tid; r < a.B; r += kPairThreads) {
+        const int2 o = s_run[r];
+        const int pages = pages_of(s_best[o.x]);
+        s_lead[r] = pages > 0 && o.y >= pages ? o.x : -1;
+    }
+    __syncthreads();
+    if (b < a.B) place_row(a.plan, a.B, s_lead, b, pages_of(s_best[b]), lane);
 }
 
 }  // namespace
@@ -202,12 +294,21 @@ cudaError_t launch_pages_groups(const int32_t* block_tables, int max_blocks, con
     cfg.stream = stream;
     cfg.attrs = pdl;
     cfg.numAttrs = 1;
+    if (batch <= kSmallRows) {
+        cfg.gridDim = dim3(kSmallCtas);
+        cfg.blockDim = dim3(kPairThreads);
+        return cudaLaunchKernelEx(&cfg, small_kernel, a);
+    }
     cfg.gridDim = dim3(batch);
     cfg.blockDim = dim3(kRunThreads);
     cudaError_t e = cudaLaunchKernelEx(&cfg, runs_kernel, a);
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3((batch + kPairThreads / 32 - 1) / (kPairThreads / 32));
+    cfg.gridDim = dim3((batch + kPairRows - 1) / kPairRows);
     cfg.blockDim = dim3(kPairThreads);
+    cfg.dynamicSmemBytes = batch * sizeof(int2);               // both kernels: 8 bytes a row, 64 KB at most
+    if (ctas_per_sm(reinterpret_cast<const void*>(&counts_kernel), kPairThreads, cfg.dynamicSmemBytes) < 1 ||
+        ctas_per_sm(reinterpret_cast<const void*>(&places_kernel), kPairThreads, cfg.dynamicSmemBytes) < 1)
+        return cudaErrorInvalidConfiguration;
     if ((e = cudaLaunchKernelEx(&cfg, counts_kernel, a)) != cudaSuccess) return e;
     return cudaLaunchKernelEx(&cfg, places_kernel, a);
 }

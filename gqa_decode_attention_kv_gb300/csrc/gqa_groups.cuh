@@ -31,30 +31,69 @@ struct PrefixGroups {
 // Group i: its first slot, rows and shared blocks. A group whose entries lie outside the
 // plan or the tables has none, so that no plan leads a read astray.
 struct GroupSpan {
-    int first, rows, blocks, leader;
+    int first, rows, blocks;
 };
 __device__ __forceinline__ GroupSpan group_span(const PrefixGroups& p, int i, int max_blocks) {
-    GroupSpan s{0, 0, 0, 0};
     const int a = p.start[i], e = p.start[i + 1], n = p.blocks[i];
-    if (a < 0 || e <= a || e > p.B || n <= 0 || n > max_blocks) return s;
-    const int lead = p.rows[a];
-    if (lead < 0 || lead >= p.B) return s;
-    return GroupSpan{a, e - a, n, lead};
+    const bool good = a >= 0 && e > a && e <= p.B && n > 0 && n <= max_blocks;
+    return good ? GroupSpan{a, e - a, n} : GroupSpan{0, 0, 0};
 }
 
 // Blocks that its group attends for row b of length L (T new tokens included): all that
 // the group shares where every query of the row sees them whole, else none, and the row
-// attends its context alone. g and slot: its group and place in it.
+// attends its context alone. g and member: its group and place in it. (All loads before
+// the first branch: two trips to memory.)
 __device__ __forceinline__ int shared_blocks(const PrefixGroups& p, int b, int L, int T, int max_blocks, int* g = nullptr,
                                              int* member = nullptr) {
-    const int s = p.slot[b], i = p.group[b];
-    if (s < 0 || s >= p.B || i < 0 || i >= p.groups() || p.rows[s] != b) return 0;
-    const GroupSpan span = group_span(p, i, max_blocks);
-    if (s < span.first || s >= span.first + span.rows) return 0;
+    const int s = p.slot[b], i = p.group[b], n_groups = p.groups();
+    const int sc = min(max(s, 0), p.B - 1), ic = min(max(i, 0), p.B - 1);
+    const int row = p.rows[sc];
+    const GroupSpan span = group_span(p, ic, max_blocks);
+    if (s != sc || i != ic || i >= n_groups || row != b || s < span.first || s >= span.first + span.rows) return 0;
     if ((long long)span.blocks * kBlock + T - 1 > L) return 0;
     if (g) *g = i;
     if (member) *member = s - span.first;
     return span.blocks;
+}
+
+// ---- how the shared decode divides the GPU
+//
+// The kernel that attends the shared blocks and the one that attends the rows' own run side
+// by side: the first takes as many SMs as make both end together, as far as their work can
+// be told from the plan and the lengths. Times are per SM.
+constexpr int kStepTokens = 64;                   // tokens of a step of the prefix kernel
+struct SplitModel {
+    int sms, ctas_per_sm, cta_rows;               // of the prefix kernel
+    float step_us, prefix_us;                     // a step of an SM's CTAs, the kernel's start and end
+    float unit_us, tail_us;                       // a (block, kv-head) of the tail, its start
+};
+
+// One group's rows for one kv-head, and how its steps lie.
+struct Problem {
+    int rows, tiles, chunks, units;
+};
+__device__ __forceinline__ Problem problem_of(const GroupSpan& s, int K, int GT, int cta_rows) {
+    Problem p;
+    p.rows = s.rows * GT;
+    p.tiles = (p.rows + cta_rows - 1) / cta_rows;
+    p.chunks = (s.blocks * kBlock + kStepTokens - 1) / kStepTokens;
+    p.units = p.tiles * p.chunks * K;
+    return p;
+}
+
+// SMs for `steps` steps of the prefix beside `units` blocks of the tail: the fewest with
+// which the prefix ends no later than the tail on the others.
+__device__ __forceinline__ int prefix_sms(const SplitModel& m, int steps, int units) {
+    if (steps == 0) return 0;
+    if (units == 0) return m.sms;
+    const float wp = steps * m.step_us / m.ctas_per_sm, wt = units * m.unit_us;
+    int lo = 1, hi = m.sms - 1;                   // hi: the answer where nothing less does
+    while (lo < hi) {
+        const int x = (lo + hi) >> 1;
+        if (m.prefix_us + wp / x <= m.tail_us + wt / (m.sms - x)) hi = x;
+        else lo = x + 1;
+    }
+    return max(lo, 1);
 }
 
 }  // namespace gqa

@@ -2,10 +2,12 @@
 // cache type. Element i of a row is code * scale (exact in fp32: at most 8 x 11 bits),
 // rounded once to the output's type; rows of the output's own type are copied bit for bit.
 //
-// Bound by memory: codes and scales are read once and the rows written once. A thread
-// takes 8 elements of a row of one page (4 to 32 bytes in, 16 or 32 out), kUnroll of
-// them at a time; the lanes of a row and the rows of a page are adjacent, so a warp's
-// loads are whole lines of the page and its stores whole pieces of a token's row.
+// Bound by memory: codes and scales are read once and the rows written once. A warp takes
+// the 16 rows of one (page, K or V, kv-head) at a time, all of its loads in flight before
+// the first store; a lane holds 8 elements of every second or fourth row, so that a store
+// instruction writes whole 128- to 256-byte pieces of a token's row.
+#include <algorithm>
+
 #include "gqa_device.cuh"
 #include "gqa_internal.h"
 
@@ -25,7 +27,7 @@ struct ReadArgs {
     int batch, K, max_tokens, max_blocks, pages_per_cta, ctas_per_seq;
 };
 
-constexpr int kReadThreads = 256, kUnroll = 4, kElems = 8;
+constexpr int kReadThreads = 256, kElems = 8;
 
 // Cache formats as the kernel sees them.
 enum ReadKind : int { kReadF32, kReadF16, kReadBf16, kReadI8, kReadFp8, kReadI4, kReadI4Kc };
@@ -74,28 +76,51 @@ struct Raw {                      // 8 elements as they lie in the cache
     }
 };
 
+// 8 elements as they go out: 32-bit words, 4 of a 16-bit type, 8 of fp32.
 template <int kKind, int kOut>
-__device__ __forceinline__ void put(void* out, long long at, const Raw<kKind>& raw, const float (&f)[kElems]) {
-    if constexpr (kOut == kKind) {             // the same type: the same bits
-        uint4* p = reinterpret_cast<uint4*>(static_cast<uint8_t*>(out) + at * (Raw<kKind>::kBits / 8));
+struct Out {
+    static constexpr int kWords = kOut == kReadF32 ? 8 : 4;
+    uint32_t w[kWords];
+    __device__ __forceinline__ Out(const Raw<kKind>& raw, const float (&f)[kElems]) {
+        if constexpr (kOut == kKind) {         // the same type: the same bits
 #pragma unroll
-        for (int i = 0; i < Raw<kKind>::kBits / 16; ++i)
-            p[i] = make_uint4(raw.w[4 * i], raw.w[4 * i + 1], raw.w[4 * i + 2], raw.w[4 * i + 3]);
-    } else if constexpr (kOut == kReadF32) {
-        float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
-        p[0] = make_float4(f[0], f[1], f[2], f[3]);
-        p[1] = make_float4(f[4], f[5], f[6], f[7]);
-    } else {
-        constexpr bool kB = kOut == kReadBf16;
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at) =
-            make_uint4(pack2<kB>(f[0], f[1]), pack2<kB>(f[2], f[3]), pack2<kB>(f[4], f[5]), pack2<kB>(f[6], f[7]));
+            for (int i = 0; i < kWords; ++i) w[i] = raw.w[i];
+        } else if constexpr (kOut == kReadF32) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(f[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = pack2<kOut == kReadBf16>(f[2 * i], f[2 * i + 1]);
+        }
+        if constexpr (kWords == 8) {
+            // lanes 2i and 2i + 1 swap halves, so that each of their two stores writes 32
+            // bytes in a row, of the even lane's elements and then of the odd's
+            const bool odd = threadIdx.x & 1;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t got = __shfl_xor_sync(kFull, odd ? w[i] : w[4 + i], 1);
+                if (odd) w[i] = got;
+                else w[4 + i] = got;
+            }
+        }
     }
-}
+    // at: the lane's own first element
+    __device__ __forceinline__ void store(void* out, long long at) const {
+        if constexpr (kWords == 4) {
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+            uint32_t* p = static_cast<uint32_t*>(out) + at - 4 * (threadIdx.x & 1);
+            *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(p + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+    }
+};
 
 template <int kKind, int kOut, int D>
 __global__ void __launch_bounds__(kReadThreads) read_kernel(const ReadArgs a) {
-    constexpr int kLanes = D / kElems;         // threads of a row
+    constexpr int kLanes = D / kElems, kRowsPerStep = 32 / kLanes, kSteps = kBlock / kRowsPerStep;
     constexpr bool kCoded = kKind >= kReadI8;
+    constexpr int kBits = Raw<kKind>::kBits;
     launch_dependents();
     grid_dependency_wait();
     const int b = blockIdx.x / a.ctas_per_seq, part = blockIdx.x - b * a.ctas_per_seq;
@@ -106,69 +131,79 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const ReadArgs a) {
         return;
     }
     const long long pos0 = a.positions[b], end = pos0 + n;
-    // pages first .. last hold the rows; this CTA's are first + part * pages_per_cta ..
+    // pages (pos0 >> 4) .. (end - 1) >> 4 hold the rows; this CTA's are page0 ..
     const long long page0 = (pos0 >> 4) + (long long)part * a.pages_per_cta;
     const int pages = (int)min((long long)a.pages_per_cta, ((end + kBlock - 1) >> 4) - page0);
-    if (pages <= 0) return;
-    const int items = pages * 2 * a.K * kBlock * kLanes;
-    for (int base = 0; base < items; base += kReadThreads * kUnroll) {
-        Raw<kKind> raw[kUnroll];
-        float s[kUnroll];
-        uint4 kc[kUnroll];
-        long long at[kUnroll];                 // element of the output, -1: none
-        bool is_v[kUnroll];
-#pragma unroll
-        for (int i = 0; i < kUnroll; ++i) {
-            const int item = base + i * kReadThreads + threadIdx.x;
-            at[i] = -1;
-            is_v[i] = false;
-            s[i] = 1.f;
-            if (item >= items) continue;
-            const int e = (item % kLanes) * kElems, slot = item / kLanes % kBlock;
-            const int tile = item / (kLanes * kBlock), side = tile / a.K, g = tile - side * a.K;
-            is_v[i] = side & 1;
-            const long long page = page0 + (side >> 1), pos = page * kBlock + slot;
-            if (pos < pos0 || pos >= end) continue;
-            if (pos < 0 || page >= a.max_blocks) {
-                if (g == 0 && e == 0) flag_error(a.err, GQA_DEVERR_POSITION);
-                continue;
-            }
-            const int ph = a.block_tables[(long long)b * a.max_blocks + page];
-            if (ph < 0 || ph >= a.num_blocks) {
-                if (g == 0 && e == 0) flag_error(a.err, GQA_DEVERR_BLOCK_INDEX);
-                continue;
-            }
-            const long long off = ph * a.sb + g * a.sh + slot * a.st + e;
-            raw[i].load(static_cast<const uint8_t*>(is_v[i] ? a.v : a.k) + off * Raw<kKind>::kBits / 8);
-            if constexpr (kCoded) {
-                const long long tok = ((long long)ph * a.K + g) * kBlock + slot;
-                if (kKind == kReadI4Kc && !is_v[i])
-                    kc[i] = *reinterpret_cast<const uint4*>(a.k_scale + ((long long)ph * a.K + g) * D + e);
-                else
-                    s[i] = __half2float((is_v[i] ? a.v_scale : a.k_scale)[tok]);
-            }
-            at[i] = ((row0 + pos - pos0) * a.K + g) * D + e;
+    const int tiles = pages * 2 * a.K;         // (page, K or V, kv-head), kv-heads adjacent
+    const int lane = threadIdx.x & 31;
+    const int e = lane % kLanes * kElems, slot0 = lane / kLanes;
+    for (int tile = threadIdx.x >> 5; tile < tiles; tile += kReadThreads / 32) {
+        const int side = tile / a.K, g = tile - side * a.K;
+        const bool is_v = side & 1;
+        const long long page = page0 + (side >> 1);
+        // slots [lo, hi) of the page are asked for
+        const int lo = (int)max(0ll, pos0 - page * kBlock), hi = (int)min((long long)kBlock, end - page * kBlock);
+        if (page < 0 || page >= a.max_blocks) {
+            if (g == 0 && lane == 0) flag_error(a.err, GQA_DEVERR_POSITION);
+            continue;
         }
+        const int ph = a.block_tables[(long long)b * a.max_blocks + page];
+        if (ph < 0 || ph >= a.num_blocks) {
+            if (g == 0 && lane == 0) flag_error(a.err, GQA_DEVERR_BLOCK_INDEX);
+            continue;
+        }
+        const long long at = ph * a.sb + g * a.sh + slot0 * a.st + e;
+        const uint8_t* src = static_cast<const uint8_t*>(is_v ? a.v : a.k) + at * kBits / 8;
+        const long long step = kRowsPerStep * a.st * kBits / 8;
+        Raw<kKind> raw[kSteps];
 #pragma unroll
-        for (int i = 0; i < kUnroll; ++i) {
-            if (at[i] < 0) continue;
-            float f[kElems];
-            raw[i].values(f);
-            if constexpr (kCoded) {
-                if (kKind == kReadI4Kc && !is_v[i]) {
-                    const uint32_t w[4] = {kc[i].x, kc[i].y, kc[i].z, kc[i].w};
+        for (int i = 0; i < kSteps; ++i) {
+            const int slot = slot0 + i * kRowsPerStep;
+            if (slot >= lo && slot < hi) raw[i].load(src + i * step);
+        }
+        const bool channels = kKind == kReadI4Kc && !is_v;            // scales by channel, else by token
+        uint4 kc = make_uint4(0u, 0u, 0u, 0u);
+        float scale = 0.f;                     // lane t: token t's
+        if constexpr (kCoded) {
+            const long long head = (long long)ph * a.K + g;
+            if (channels) kc = *reinterpret_cast<const uint4*>(a.k_scale + head * D + e);
+            else if (lane < kBlock) scale = __half2float((is_v ? a.v_scale : a.k_scale)[head * kBlock + lane]);
+        }
+        // the row of slot s is row0 + 16 page + s - pos0
+        const long long out0 = ((row0 + page * kBlock - pos0 + slot0) * a.K + g) * D + e;
+        void* out = is_v ? a.v_out : a.k_out;
+        auto rows = [&](auto&& scaled) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 x = unpack2<false>(w[j]);
-                        f[2 * j] *= x.x;
-                        f[2 * j + 1] *= x.y;
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < kElems; ++j) f[j] *= s[i];
-                }
+            for (int i = 0; i < kSteps; ++i) {
+                const int slot = slot0 + i * kRowsPerStep;
+                float f[kElems];
+                raw[i].values(f);
+                scaled(f, i);
+                const Out<kKind, kOut> o(raw[i], f);
+                if (slot >= lo && slot < hi) o.store(out, out0 + (long long)i * kRowsPerStep * a.K * D);
             }
-            put<kKind, kOut>(is_v[i] ? a.v_out : a.k_out, at[i], raw[i], f);
+        };
+        if constexpr (!kCoded) {
+            rows([](float (&)[kElems], int) {});
+        } else if (channels) {
+            float c[kElems];
+            const uint32_t w[4] = {kc.x, kc.y, kc.z, kc.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 x = unpack2<false>(w[j]);
+                c[2 * j] = x.x;
+                c[2 * j + 1] = x.y;
+            }
+            rows([&](float (&f)[kElems], int) {
+#pragma unroll
+                for (int j = 0; j < kElems; ++j) f[j] *= c[j];
+            });
+        } else {
+            rows([&](float (&f)[kElems], int i) {
+                const float x = __shfl_sync(kFull, scale, slot0 + i * kRowsPerStep);
+#pragma unroll
+                for (int j = 0; j < kElems; ++j) f[j] *= x;
+            });
         }
     }
 }
@@ -220,11 +255,11 @@ cudaError_t launch_kv_read(const gqa_kv_cache_t& c, void* k_out, void* v_out, in
     a.K = c.num_kv_heads;
     a.max_tokens = max_tokens;
     a.max_blocks = max_blocks;
-    // a page of one kv-head is 2 * 16 * d / 8 items, 256 or 512: pages until a CTA's
-    // threads have kUnroll of them each, where there are pages enough
-    const int per_page = 2 * c.num_kv_heads * kBlock * c.head_dim / kElems;
-    a.pages_per_cta = max(1, kReadThreads * kUnroll / per_page);
+    // Four tiles a warp where that still fills the GPU, else fewer: a CTA first walks
+    // positions, table entry and data, one behind the other.
     const long long pages = ((long long)max_tokens + 2 * kBlock - 2) / kBlock;   // an unaligned run touches one more
+    a.pages_per_cta = std::max(1, 2 * kReadThreads / 32 / c.num_kv_heads);
+    while (a.pages_per_cta > 1 && pages * batch < 1216LL * a.pages_per_cta) a.pages_per_cta /= 2;
     a.ctas_per_seq = (int)((pages + a.pages_per_cta - 1) / a.pages_per_cta);
     const long long grid = (long long)a.ctas_per_seq * batch;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;

@@ -12,9 +12,9 @@
 // The prefix kernel works on the 5th-generation tensor cores, 128 query rows (the MMA's M)
 // a tile, the K/V of 64 tokens (4 pages) a step:
 //   S[128 x 64]  = Q K^T     Q and K in shared memory, S in tensor memory
-//   softmax                  one thread per row; the weights as a high and a low 16-bit
-//                            part over S (a 16-bit weight alone would round it to the
-//                            cache's type)
+//   softmax                  two threads per row, 32 of the step's tokens each; the weights
+//                            as a high and a low 16-bit part over S (a 16-bit weight alone
+//                            would round it to the cache's type)
 //   O[128 x d]  += P V       P from tensor memory, V from shared memory
 // The (group, kv-head, tile) problems are laid out one behind the other in steps and cut
 // into equal runs, one per CTA of a single resident wave, so a long prefix is split over
@@ -33,12 +33,43 @@ using dec::DecodeArgs;
 using dec::Partition;
 
 constexpr int kRows = 128;                       // query rows of a tile: the MMA's M, one TMEM lane each
-constexpr int kChunk = 64;                       // tokens of a step: N of S, K of P.V
+constexpr int kChunk = kStepTokens;              // tokens of a step: N of S, K of P.V
 constexpr int kChunkBlocks = kChunk / kBlock;
 constexpr int kBufs = 4;                         // per-step barrier copies (G & 3)
 constexpr uint32_t kColTile = 256;               // tile t: S buffers at columns 256t, 256t + 64,
 constexpr uint32_t kColO = 128;                  //         O at 256t + 128
+constexpr int kHalf = kChunk / 2;                // tokens of a step that a softmax thread takes
 constexpr float kSlackLog2 = 8.f;                // headroom before (m, l, O) are rescaled
+
+// Barrier of the two warps that share rows; pair_any: whether any of their threads says so.
+__device__ __forceinline__ void pair_sync(int id) { asm volatile("barrier.cta.sync.aligned %0, 64;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ bool pair_any(int id, bool mine) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\t"
+        "barrier.cta.red.or.aligned.pred q, %1, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(id), "r"((uint32_t)mine)
+        : "memory");
+    return r != 0;
+}
+
+// Two weights as a high and a low 16-bit part each. bf16's high part is the value cut
+// off, which takes no conversion (together 2^-16 of the weight; rounded 2^-17).
+template <bool kBf16>
+__device__ __forceinline__ void split2(float x, float y, uint64_t xy, uint32_t& hi, uint32_t& lo) {
+    float2 h;
+    if constexpr (kBf16) {
+        const uint32_t u = __float_as_uint(x), v = __float_as_uint(y);
+        hi = __byte_perm(u, v, 0x7632);
+        h = make_float2(__uint_as_float(u & 0xffff0000u), __uint_as_float(v & 0xffff0000u));
+    } else {
+        hi = pack2<false>(x, y);
+        h = unpack2<false>(hi);
+    }
+    const float2 r = f2_split(f2_sub(xy, f2_make(h.x, h.y)));
+    lo = pack2<kBf16>(r.x, r.y);
+}
 
 struct SharedArgs {
     const void* q;
@@ -50,24 +81,12 @@ struct SharedArgs {
     int B, H, K, G, T, GT, max_blocks, min_units;
     int map_perm[3], page_perm[2];
     float scale_log2;
+    SplitModel split;
     int32_t* hdr;        // [0] steps per CTA, [1] all steps, [2] rows of a CTA
     int32_t* first_unit; // [groups] first step of each group
     float2 *ml_a, *ml_b; // (m, l) of a problem's first piece by row, and of CTA j's continued one
     float *o_a, *o_b;    // their un-normalised outputs
 };
-
-// Rows of group g's problem for one kv-head, and how its steps lie.
-struct Problem {
-    int rows, tiles, chunks, units;
-};
-__device__ __forceinline__ Problem problem_of(const GroupSpan& s, int K, int GT, int rows_per_cta) {
-    Problem p;
-    p.rows = s.rows * GT;
-    p.tiles = (p.rows + rows_per_cta - 1) / rows_per_cta;
-    p.chunks = (s.blocks + kChunkBlocks - 1) / kChunkBlocks;
-    p.units = p.tiles * p.chunks * K;
-    return p;
-}
 
 // kTiles query tiles per CTA: two (one CTA per SM, all 512 tensor-memory columns, K/V read
 // once for 256 rows) or one (two CTAs per SM).
@@ -75,8 +94,8 @@ template <int kTiles, int D>
 struct SharedCfg {
     static constexpr int kHalves = D / 64;               // 128-byte column halves of a row
     static constexpr int kCtaRows = kTiles * kRows;
-    static constexpr int kSoftWarps = 4 * kTiles;
-    static constexpr int kThreads = kCtaRows + 32 * kTiles + 64;   // + an MMA warp per tile, K and V copy warps
+    static constexpr int kSoftWarps = 8 * kTiles;        // four for each half of a step's tokens
+    static constexpr int kThreads = 32 * (kSoftWarps + kTiles + 2);   // + an MMA warp per tile, K and V copy warps
     static constexpr int kStages = kTiles == 2 || D == 64 ? 4 : 2;  // K and V stages
     static constexpr int kCtasPerSm = kTiles == 2 ? 1 : 2;
     static constexpr uint32_t kTmemCols = 256u * kTiles;
@@ -85,7 +104,8 @@ struct SharedCfg {
     static constexpr int kVb = kBlock * D * 2;           // one V page
     static constexpr int kVc = kChunkBlocks * kVb;
     static constexpr int kOffK = kTiles * kQt, kOffV = kOffK + kStages * kKc, kOffBar = kOffV + kStages * kVc;
-    static constexpr int kSmem = 1024 + kOffBar + 768;
+    static constexpr int kOffEx = kOffBar + 1024;        // [tile][half][row]: maxima, then sums
+    static constexpr int kSmem = 1024 + kOffEx + kCtaRows * 8;
     static_assert((kSmem + 1024) * kCtasPerSm <= 228 * 1024, "CTAs per SM fit the shared memory");
 };
 
@@ -104,10 +124,9 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
     uint8_t* gb = smem_raw + (sb - raw);
     const uint32_t sQ = sb, sK = sb + C::kOffK, sV = sb + C::kOffV;
     // Barriers, 8 B each: K stages, V stages (stage G % kS), then per tile t "S_t(G)
-    // done", "P_t(G).V(G) done", "P_t(G) ready" (copy G & 3); the block-mask slots
-    // (G & 7), per tile "Q_t stored"; then the TMEM address, the masks and the scan's
-    // scratch. G counts the CTA's steps across its segments. Per-step barriers come in
-    // four copies, so that no parity wait can fall two phases behind.
+    // done", "P_t(G).V(G) done", "P_t(G) ready" (copy G & 3), "Q_t stored"; then the TMEM
+    // address and the scan's scratch. G counts the CTA's steps across its segments. Per-step
+    // barriers come in four copies, so that no parity wait can fall two phases behind.
     const uint32_t bar0 = sb + C::kOffBar;
     auto stage = [](int c) { return c % kS; };
     auto par_st = [](int c) { return (uint32_t)(c / kS) & 1u; };
@@ -116,18 +135,16 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
     auto bar_s = [&](int t, int c) { return bar0 + 64 + 96 * t + 8 * (c & 3); };
     auto bar_o = [&](int t, int c) { return bar0 + 96 + 96 * t + 8 * (c & 3); };
     auto bar_p = [&](int t, int c) { return bar0 + 128 + 96 * t + 8 * (c & 3); };
-    auto bar_m = [&](int c) { return bar0 + 256 + 8 * (c & 7); };
-    auto bar_q = [&](int t) { return bar0 + 320 + 8 * t; };
-    const uint32_t tslot = bar0 + 336;
-    volatile uint32_t* cmask = reinterpret_cast<volatile uint32_t*>(gb + C::kOffBar + 352);   // [8]
-    int* scan = reinterpret_cast<int*>(gb + C::kOffBar + 384);                                // [64], then [2] the start
+    auto bar_q = [&](int t) { return bar0 + 256 + 8 * t; };
+    const uint32_t tslot = bar0 + 272;
+    int* scan = reinterpret_cast<int*>(gb + C::kOffBar + 288);      // [128] sums, then the run's group and where it begins
     auto par4 = [](int c) { return (uint32_t)(c >> 2) & 1u; };
-    auto par8 = [](int c) { return (uint32_t)(c >> 3) & 1u; };
 
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(kFull, tid >> 5, 0);               // uniform: addresses from it stay so
     const bool softmax = warp < C::kSoftWarps, loader = warp >= C::kSoftWarps + kTiles;
     const bool mma_warp = !softmax && !loader;
-    const int tt = warp >> 2;                                   // softmax warps: their tile
+    const int tt = warp >> 3, hf = (warp >> 2) & 1;             // softmax warps: their tile and half
     if (tid == 0) {
         prefetch_tensormap(&kmap);
         prefetch_tensormap(&vmap);
@@ -139,37 +156,54 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
             for (int i = 0; i < kBufs; ++i) {
                 mbar_init(bar_s(t, i), 1);
                 mbar_init(bar_o(t, i), 1);
-                mbar_init(bar_p(t, i), 4);     // one arrival per softmax warp of the tile
+                mbar_init(bar_p(t, i), 8);     // one arrival per softmax warp of the tile
             }
-            mbar_init(bar_q(t), 4);
+            mbar_init(bar_q(t), 8);
         }
-        for (int i = 0; i < 8; ++i) mbar_init(bar_m(i), 1);
         fence_mbar_init();
     }
+    if (warp == 0) tmem_alloc(tslot, C::kTmemCols);
     // The tail kernel behind this one does not wait for it: it may start only once
     // everything before this kernel has ended, which this wait makes sure of.
     grid_dependency_wait();
     launch_dependents();
 
-    // ---- the steps of all problems, and where this CTA's run of them begins
+    // ---- the steps of all problems and the rows' own blocks, from them the CTAs that take
+    // part, and where this CTA's run of steps begins. Each thread takes a group of a round;
+    // the first round's stay in registers.
     const PrefixGroups plan(a.groups, a.B);
     const int n_groups = plan.groups();
-    const int P = (int)gridDim.x, j = (int)blockIdx.x;
+    const int j = (int)blockIdx.x;
     constexpr int kWarps = C::kThreads / 32;
-    auto units_of = [&](int i) {
-        return i < n_groups ? problem_of(group_span(plan, i, a.max_blocks), a.K, a.GT, C::kCtaRows).units : 0;
-    };
-    int U = 0;
+    auto span_of = [&](int i) { return i < n_groups ? group_span(plan, i, a.max_blocks) : GroupSpan{0, 0, 0}; };
+    auto units_of = [&](const GroupSpan& x) { return problem_of(x, a.K, a.GT, C::kCtaRows).units; };
+    GroupSpan mine = span_of(tid);
+    int U = 0, own = 0;
     {
-        int mine = 0;
-        for (int i = tid; i < n_groups; i += C::kThreads) mine += units_of(i);
+        int sum = units_of(mine), rows_own = 0;
+        for (int i = tid + C::kThreads; i < n_groups; i += C::kThreads) sum += units_of(span_of(i));
+        for (int b = tid; b < a.B; b += C::kThreads) {
+            const int L = a.context_lens[b];
+            if (L > 0 && L <= a.max_blocks * kBlock)
+                rows_own += (L + kBlock - 1) / kBlock - shared_blocks(plan, b, L, a.T, a.max_blocks);
+        }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(kFull, mine, o);
-        if (lane == 0) scan[warp] = mine;
+        for (int o = 16; o > 0; o >>= 1) {
+            sum += __shfl_xor_sync(kFull, sum, o);
+            rows_own += __shfl_xor_sync(kFull, rows_own, o);
+        }
+        if (lane == 0) {
+            scan[warp] = sum;
+            scan[32 + warp] = rows_own;
+        }
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i) U += scan[i];
+        for (int i = 0; i < kWarps; ++i) {
+            U += scan[i];
+            own += scan[32 + i];
+        }
     }
+    const int P = max(1, prefix_sms(a.split, U, own * a.K) * C::kCtasPerSm);
     const int R = max((U + P - 1) / P, a.min_units);
     const int u_lo = (int)min((long long)U, (long long)j * R), u_hi = (int)min((long long)U, (long long)(j + 1) * R);
     if (j == 0 && tid == 0) {
@@ -179,35 +213,39 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
     }
     int carry = 0;
     for (int base = 0; base < n_groups; base += C::kThreads) {
-        const int x = units_of(base + tid);
+        if (base > 0) mine = span_of(base + tid);
+        const int x = units_of(mine);
         int y = x;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int z = __shfl_up_sync(kFull, y, o);
             if (lane >= o) y += z;
         }
-        __syncthreads();                       // scan[] of the round before has been read
-        if (lane == 31) scan[warp] = y;
+        if (base > 0) __syncthreads();         // the round before has been read
+        if (lane == 31) scan[64 + warp] = y;
         __syncthreads();
         int before = carry;
 #pragma unroll
         for (int i = 0; i < kWarps; ++i) {
-            if (i < warp) before += scan[i];
-            carry += scan[i];
+            if (i < warp) before += scan[64 + i];
+            carry += scan[64 + i];
         }
         const int first = before + y - x;
-        if (x > 0 && first <= u_lo && u_lo < first + x) {
-            scan[64] = base + tid;
-            scan[65] = first;
+        if (x > 0 && first <= u_lo && u_lo < first + x) {     // the group that the run begins in
+            scan[128] = base + tid;
+            scan[129] = first;
+            *reinterpret_cast<GroupSpan*>(scan + 130) = mine;
         }
         if (j == 0 && base + tid < n_groups) a.first_unit[base + tid] = first;
     }
-    if (u_lo >= u_hi) return;                  // uniform per CTA, before any allocation
-    if (warp == 0) tmem_alloc(tslot, C::kTmemCols);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gb + (tslot - sb));
+    const uint32_t tmem = __shfl_sync(kFull, *reinterpret_cast<volatile uint32_t*>(gb + (tslot - sb)), 0);
+    if (u_lo >= u_hi) {                        // uniform per CTA
+        if (warp == 0) tmem_dealloc(tmem, C::kTmemCols);
+        return;
+    }
     bool ok = true;
 
     // ---- the CTA's segments: runs of steps [c0, c1) of one (group, kv-head, tile)
@@ -215,18 +253,19 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
         GroupSpan span;
         int g, rows, row0, c0, c1;
     };
-    int w_group = scan[64], w_base = scan[65], w_u = u_lo;
+    int w_group = scan[128], w_base = scan[129], w_u = u_lo;
+    GroupSpan w_span = *reinterpret_cast<const GroupSpan*>(scan + 130);
     auto next_seg = [&](Seg& s) -> bool {
         if (w_u >= u_hi) return false;
         for (;;) {
-            s.span = group_span(plan, w_group, a.max_blocks);
-            const Problem p = problem_of(s.span, a.K, a.GT, C::kCtaRows);
+            const Problem p = problem_of(w_span, a.K, a.GT, C::kCtaRows);
             const int rel = w_u - w_base;
             if (rel >= p.units) {              // steps are left, so a group is
                 w_base += p.units;
-                ++w_group;
+                w_span = group_span(plan, ++w_group, a.max_blocks);
                 continue;
             }
+            s.span = w_span;
             const int pair = rel / p.chunks;
             s.c0 = rel - pair * p.chunks;
             s.g = pair / p.tiles;
@@ -242,13 +281,27 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
 
     if (loader) {
         // ================================================== copy warps: K, then V
+        // A block that is missing (behind the prefix's last, or an entry that is no page) is
+        // asked for at coordinate -1 and lands as zeros.
         const bool k_warp = warp == C::kSoftWarps + kTiles;
         const uint64_t once = l2_policy_evict_first(), again = l2_policy_evict_last();
         int issued = 0, G = 0;
         while (have && ok) {
             const uint64_t pol = it.rows > C::kCtaRows ? again : once;   // other tiles read the same pages
+            const int leader = min(max(plan.rows[it.span.first], 0), a.B - 1);
+            const int32_t* table = a.block_tables + (long long)leader * a.max_blocks;
             int win_base = -(1 << 30), win_phys = -1;
             for (int c = it.c0; c < it.c1 && ok; ++c, ++G) {
+                const int v0 = kChunkBlocks * c;
+                if (v0 - win_base >= 32 || v0 < win_base) {       // 32 entries: whole chunks
+                    win_base = v0;
+                    win_phys = -1;
+                    if (v0 + lane < it.span.blocks) {
+                        const int p = table[v0 + lane];
+                        if (p < 0 || p >= a.num_blocks) flag_error(a.err, GQA_DEVERR_BLOCK_INDEX);
+                        else win_phys = p;
+                    }
+                }
                 if (G >= kS) {
                     // K(G) once every tile's S(G-kS) has read K(G-kS); V(G) once
                     // every tile's P(G-kS).V(G-kS) has read V(G-kS)
@@ -259,56 +312,27 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
                     ok = __all_sync(kFull, w);
                     if (!ok) break;
                 }
-                const int v0 = kChunkBlocks * c;
-                if (v0 - win_base >= 32 || v0 < win_base) {       // 32 entries: whole chunks
-                    win_base = v0;
-                    win_phys = -1;
-                    if (v0 + lane < it.span.blocks) {
-                        const int p = a.block_tables[(long long)it.span.leader * a.max_blocks + v0 + lane];
-                        if (p < 0 || p >= a.num_blocks) flag_error(a.err, GQA_DEVERR_BLOCK_INDEX);
-                        else win_phys = p;
-                    }
-                }
-                int ph[kChunkBlocks];
-                uint32_t mask = 0;
-                int nval = 0;
-#pragma unroll
-                for (int q = 0; q < kChunkBlocks; ++q) {
-                    ph[q] = __shfl_sync(kFull, win_phys, v0 + q - win_base);
-                    if (ph[q] >= 0) mask |= 1u << q, ++nval;
-                }
                 const uint32_t bar = k_warp ? bar_k(G) : bar_v(G);
-                if (lane == 0) {
-                    if (k_warp) {
-                        cmask[G & 7] = mask;
-                        mbar_arrive(bar_m(G));     // publishes the mask (release)
-                    }
-                    mbar_arrive_expect_tx(bar, (uint32_t)(nval * C::kVb));
-                }
-                fence_proxy_async_smem();          // earlier generic writes to the stage come first
+                if (lane == 0) mbar_arrive_expect_tx(bar, C::kVc);
                 __syncwarp();
-                int pq = ph[0];
-                const int q = k_warp ? lane / C::kHalves : lane;
-#pragma unroll
-                for (int i = 1; i < kChunkBlocks; ++i)
-                    if (q == i) pq = ph[i];
+                // K: one lane per (block, 64-element half) box; V: one box per page
+                // (head_dim 128: the page map lands it as [half][slot][128 B])
+                const int boxes = k_warp ? C::kHalves : 1;
+                const int q = lane / boxes, h = lane - q * boxes;
+                const int pq = __shfl_sync(kFull, win_phys, (v0 - win_base + q) & 31);
                 auto coord = [&](int which) { return which == 0 ? 0 : (which == 1 ? it.g : pq); };
                 const int y = coord(a.map_perm[0]), z = coord(a.map_perm[1]), w = coord(a.map_perm[2]);
-                if (!k_warp) {
-                    // V: one box per page (head_dim 128: the page map lands it as
-                    // [half][slot][128 B])
-                    if (lane < kChunkBlocks && pq >= 0) {
-                        const uint32_t dst = sV + stage(G) * C::kVc + lane * C::kVb;
+                if (q < kChunkBlocks) {
+                    if (k_warp) {
+                        tma_load_4d(sK + stage(G) * C::kKc + h * (kChunk * 128) + q * (kBlock * 128), &kmap, h * 64, y, z,
+                                    w, bar, pol);
+                    } else {
+                        const uint32_t dst = sV + stage(G) * C::kVc + q * C::kVb;
                         if constexpr (C::kHalves == 2)
                             tma_load_5d(dst, &vmap, 0, 0, 0, coord(a.page_perm[0]), coord(a.page_perm[1]), bar, pol);
                         else
                             tma_load_4d(dst, &vmap, 0, y, z, w, bar, pol);
                     }
-                } else if (lane < C::kHalves * kChunkBlocks && pq >= 0) {
-                    // K: one lane per (block, 64-element half) box
-                    const int h = lane % C::kHalves;
-                    tma_load_4d(sK + stage(G) * C::kKc + h * (kChunk * 128) + q * (kBlock * 128), &kmap, h * 64, y, z, w,
-                                bar, pol);
                 }
                 ++issued;
             }
@@ -321,100 +345,108 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
                 mbar_wait(k_warp ? bar_k(c) : bar_v(c), par_st(c), kWaitLimitNs / 4);
         }
     } else if (mma_warp) {
-        // ================================================== MMA warps: one per tile (one lane issues)
+        // ================================================== MMA warps: one per tile
+        // The whole warp walks along and one elected lane issues: from a branch of one lane
+        // the operands go through vector registers, 144 cycles a P.V product for 38.
         const int t = warp - C::kSoftWarps;
-        if (lane == 0) {
-            auto issue_s = [&](int G) {            // S_t(G) = Q_t K(G)^T into buffer G & 1
-                const uint32_t kb = sK + stage(G) * C::kKc, qb = sQ + t * C::kQt;
+        auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(kFull, mbar_wait(bar, parity)); };
+        auto issue_s = [&](int G) {                // S_t(G) = Q_t K(G)^T into buffer G & 1
+            const uint32_t kb = sK + stage(G) * C::kKc, qb = sQ + t * C::kQt;
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    const uint64_t ad = smem_desc_sw128(qb + (ks >> 2) * (kRows * 128) + (ks & 3) * 32, 16, 1024);
-                    const uint64_t bd = smem_desc_sw128(kb + (ks >> 2) * (kChunk * 128) + (ks & 3) * 32, 16, 1024);
-                    tc_mma_f16(tmem + kColTile * t + kChunk * (G & 1), ad, bd, kIdescS, ks > 0);
-                }
-            };
-            auto issue_pv = [&](int G, bool first) {   // O_t (+)= P_t(G) V(G), high part then low part per block
-                const uint32_t vb = sV + stage(G) * C::kVc, pb = tmem + kColTile * t + kChunk * (G & 1);
+            for (int ks = 0; ks < D / 16; ++ks) {
+                const uint64_t ad = smem_desc_sw128(qb + (ks >> 2) * (kRows * 128) + (ks & 3) * 32, 16, 1024);
+                const uint64_t bd = smem_desc_sw128(kb + (ks >> 2) * (kChunk * 128) + (ks & 3) * 32, 16, 1024);
+                tc_mma_f16_elect(tmem + kColTile * t + kChunk * (G & 1), ad, bd, kIdescS, ks > 0);
+            }
+        };
+        auto issue_pv = [&](int G, bool first) {   // O_t (+)= P_t(G) V(G), high part then low part per block
+            const uint32_t vb = sV + stage(G) * C::kVc, pb = tmem + kColTile * t + kChunk * (G & 1);
 #pragma unroll
-                for (int jl = 0; jl < kChunkBlocks; ++jl)
+            for (int jl = 0; jl < kChunkBlocks; ++jl)
 #pragma unroll
-                    for (int part = 0; part < 2; ++part)
-                        tc_mma_f16_ta(tmem + kColTile * t + kColO, pb + 16 * jl + 8 * part,
-                                      smem_desc_sw128(vb + jl * C::kVb, kBlock * 128, 1024), kIdescO,
-                                      !(first && jl == 0 && part == 0));
-            };
-            int s_done = 0, o_done = 0, gc = 0, qi = 0;   // commits issued (failure path), steps, segments
-            while (have && ok) {
-                // a tile past the group's rows takes part in the barriers alone
-                const bool live = it.row0 + kRows * t < it.rows;
-                const int n = it.c1 - it.c0;
-                // Q_t of this segment stored; the last one's P.V done, so both S buffers
-                // are free (its commit covers every earlier product)
-                ok = mbar_wait(bar_q(t), (uint32_t)qi & 1u);
-                ++qi;
-                if (ok && gc > 0) ok = mbar_wait(bar_o(t, gc - 1), par4(gc - 1));
-                for (int c = 0; c < min(n, 2) && ok; ++c) {
-                    ok = mbar_wait(bar_k(gc + c), par_st(gc + c));
+                for (int part = 0; part < 2; ++part)
+                    tc_mma_f16_ta_elect(tmem + kColTile * t + kColO, pb + 16 * jl + 8 * part,
+                                        smem_desc_sw128(vb + jl * C::kVb, kBlock * 128, 1024), kIdescO,
+                                        !(first && jl == 0 && part == 0));
+        };
+        int s_done = 0, o_done = 0, gc = 0, qi = 0;   // commits issued (failure path), steps, segments
+        while (have && ok) {
+            // a tile past the group's rows takes part in the barriers alone
+            const bool live = it.row0 + kRows * t < it.rows;
+            const int n = it.c1 - it.c0;
+            // Q_t of this segment stored; the last one's P.V done, so both S buffers
+            // are free (its commit covers every earlier product)
+            ok = wait(bar_q(t), (uint32_t)qi & 1u);
+            ++qi;
+            if (ok && gc > 0) ok = wait(bar_o(t, gc - 1), par4(gc - 1));
+            for (int c = 0; c < min(n, 2) && ok; ++c) {
+                ok = wait(bar_k(gc + c), par_st(gc + c));
+                tc_fence_after();
+                if (!ok) break;
+                if (live) issue_s(gc + c);
+                tc_commit_elect(bar_s(t, gc + c));
+                ++s_done;
+            }
+            for (int c = 0; c < n && ok; ++c) {
+                const int G = gc + c;
+                // V(G) landed, P_t(G) written over S_t(G)
+                ok = wait(bar_v(G), par_st(G)) && wait(bar_p(t, G), par4(G));
+                tc_fence_after();
+                if (!ok) break;
+                if (live) issue_pv(G, c == 0);
+                tc_commit_elect(bar_o(t, G));
+                ++o_done;
+                if (c + 2 < n) {
+                    // S_t(G+2) overwrites P_t(G): wait until PV_t(G) has read it
+                    ok = wait(bar_k(G + 2), par_st(G + 2)) && wait(bar_o(t, G), par4(G));
                     tc_fence_after();
                     if (!ok) break;
-                    if (live) issue_s(gc + c);
-                    tc_commit(bar_s(t, gc + c));
+                    if (live) issue_s(G + 2);
+                    tc_commit_elect(bar_s(t, G + 2));
                     ++s_done;
                 }
-                for (int c = 0; c < n && ok; ++c) {
-                    const int G = gc + c;
-                    // P_t(G) written over S_t(G); V(G) rows of missing tokens zeroed by tile t's softmax
-                    ok = mbar_wait(bar_p(t, G), par4(G)) && mbar_wait(bar_v(G), par_st(G));
-                    tc_fence_after();
-                    if (!ok) break;
-                    if (live) issue_pv(G, c == 0);
-                    tc_commit(bar_o(t, G));
-                    ++o_done;
-                    if (c + 2 < n) {
-                        // S_t(G+2) overwrites P_t(G): wait until PV_t(G) has read it
-                        ok = mbar_wait(bar_o(t, G), par4(G)) && mbar_wait(bar_k(G + 2), par_st(G + 2));
-                        tc_fence_after();
-                        if (!ok) break;
-                        if (live) issue_s(G + 2);
-                        tc_commit(bar_s(t, G + 2));
-                        ++s_done;
-                    }
-                }
-                gc += n;
-                if (ok) have = next_seg(it);
             }
-            if (!ok) {
-                // let this tile's MMAs land before the tensor memory goes, each
-                // barrier's events in order
-                flag_error(a.err, GQA_DEVERR_TIMEOUT);
-                for (int k = max(0, s_done - kBufs); k < s_done; ++k) mbar_wait(bar_s(t, k), par4(k), kWaitLimitNs / 4);
-                for (int k = max(0, o_done - kBufs); k < o_done; ++k) mbar_wait(bar_o(t, k), par4(k), kWaitLimitNs / 4);
-            }
+            gc += n;
+            if (ok) have = next_seg(it);
+        }
+        if (!ok) {
+            // let this tile's MMAs land before the tensor memory goes, each
+            // barrier's events in order
+            if (lane == 0) flag_error(a.err, GQA_DEVERR_TIMEOUT);
+            for (int k = max(0, s_done - kBufs); k < s_done; ++k) mbar_wait(bar_s(t, k), par4(k), kWaitLimitNs / 4);
+            for (int k = max(0, o_done - kBufs); k < o_done; ++k) mbar_wait(bar_o(t, k), par4(k), kWaitLimitNs / 4);
         }
         __syncwarp();
     } else {
-        // ================================================== softmax warps: one row per thread
-        const uint32_t t_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kColTile * tt;
-        const uint32_t t_o = t_lane + kColO;
+        // ================================================== softmax warps: two threads per row
+        const int quad = warp & 3;                 // the tile's rows 32 quad .. +31, one a lane
+        const int row_t = 32 * quad + lane;
+        const uint32_t t_lane = tmem + ((uint32_t)(32 * quad) << 16) + kColTile * tt;
+        const uint32_t t_o = t_lane + kColO + hf * (D / 2);
         const uint32_t qt = sQ + tt * C::kQt;
-        // This warp's 32 Q rows of segment x into its tile's swizzled K-major layout by
+        float* ex = reinterpret_cast<float*>(gb + C::kOffEx) + tt * 2 * kRows;
+        const int pair_bar = 1 + 4 * tt + quad;    // the two warps that hold the same rows
+        // This warp's 16 Q rows of segment x into its tile's swizzled K-major layout by
         // cp.async (16 bytes a lane; rows past the group's are zero-filled), then "Q_t
-        // stored" once they have landed.
+        // stored" once they have landed. All of their places are looked up first.
         auto load_q = [&](const Seg& x) {
-            constexpr int kLanesPerRow = D / 8, kRowsPerStep = 32 / kLanesPerRow, kSteps = 32 / kRowsPerStep;
+            constexpr int kLanesPerRow = D / 8, kRowsPerStep = 32 / kLanesPerRow, kSteps = 16 / kRowsPerStep;
             const int c16 = lane % kLanesPerRow;
-            const int rl0 = 32 * (warp & 3) + lane / kLanesPerRow;
+            const int rl0 = 16 * (warp & 7) + lane / kLanesPerRow;
             const int rq0 = x.row0 + kRows * tt + rl0;
+            int src[kSteps];                       // rows of q
 #pragma unroll
             for (int i = 0; i < kSteps; ++i) {
-                const int rl = rl0 + i * kRowsPerStep, rq = rq0 + i * kRowsPerStep;
+                const int rq = rq0 + i * kRowsPerStep;
                 const int member = rq / a.GT, w = rq - member * a.GT, tok = w / a.G;
                 const int b = rq < x.rows ? plan.rows[x.span.first + member] : -1;
-                const bool in = b >= 0 && b < a.B;
-                const long long src =
-                    in ? (((long long)b * a.T + tok) * a.H + (long long)x.g * a.G + (w - tok * a.G)) * D + 8 * c16 : 0;
+                src[i] = b >= 0 && b < a.B ? (b * a.T + tok) * a.H + x.g * a.G + (w - tok * a.G) : -1;
+            }
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                const int rl = rl0 + i * kRowsPerStep;
                 cp_async16(qt + (c16 >> 3) * (kRows * 128) + rl * 128 + (((c16 & 7) ^ (rl & 7)) << 4),
-                           static_cast<const uint16_t*>(a.q) + src, in ? 16u : 0u);
+                           static_cast<const uint16_t*>(a.q) + (long long)max(src[i], 0) * D + 8 * c16, src[i] >= 0 ? 16u : 0u);
             }
         };
         auto q_stored = [&]() {
@@ -429,119 +461,101 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
         }
         int gc = 0;
         while (have && ok) {
-            Seg nx;
-            const bool have_nx = next_seg(nx);
             const int n = it.c1 - it.c0;
             const bool tile_live = it.row0 + kRows * tt < it.rows;
-            float m = -INFINITY, l = 0.f;
+            float m = -INFINITY, l = 0.f;      // the row's maximum, this half's sum
             for (int c = 0; c < n; ++c) {
                 const int G = gc + c;
                 ok = __all_sync(kFull, mbar_wait(bar_s(tt, G), par4(G)));   // S_t(G) done
-                ok = ok && __all_sync(kFull, mbar_wait(bar_m(G), par8(G)));
                 if (!ok) break;
                 tc_fence_after();
                 if (!tile_live) {
-                    if (c == n - 1 && have_nx) load_q(nx);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar_p(tt, G));
                     continue;
                 }
-                const uint32_t bm = cmask[G & 7];
-                const uint32_t t_buf = t_lane + kChunk * (G & 1);
-                float sv[kChunk];
+                const uint32_t t_buf = t_lane + kChunk * (G & 1) + kHalf * hf;
+                uint32_t r[kHalf / 16][16];
+#pragma unroll
+                for (int u = 0; u < kHalf / 16; ++u) tmem_ld16(t_buf + 16 * u, r[u]);
+                tmem_wait_ld();
+                float scl = a.scale_log2;
+                const int blocks = it.span.blocks - kChunkBlocks * (it.c0 + c);   // of this step and after
+                if (blocks < kChunkBlocks || !(scl > 0.f)) {      // the prefix's last step; or no positive scale
+#pragma unroll
+                    for (int u = 0; u < kHalf / 16; ++u) {
+                        const bool here = kHalf / kBlock * hf + u < blocks;
+#pragma unroll
+                        for (int q = 0; q < 16; ++q)
+                            r[u][q] = __float_as_uint(here ? __uint_as_float(r[u][q]) * scl : -INFINITY);
+                    }
+                    scl = 1.f;
+                }
+                float mx;
                 {
-                    uint32_t r[kChunk / 16][16];
+                    float mx2[kHalf / 16];                        // short chains of 3-input maxima
 #pragma unroll
-                    for (int u = 0; u < kChunk / 16; ++u) tmem_ld16(t_buf + 16 * u, r[u]);
-                    tmem_wait_ld();
-                    const uint64_t sc2 = f2_make(a.scale_log2, a.scale_log2);
+                    for (int u = 0; u < kHalf / 16; ++u) {
+                        float v0 = fmaxf(__uint_as_float(r[u][0]), __uint_as_float(r[u][1]));
+                        float v1 = fmaxf(__uint_as_float(r[u][2]), __uint_as_float(r[u][3]));
 #pragma unroll
-                    for (int u = 0; u < kChunk / 16; ++u)
-#pragma unroll
-                        for (int q = 0; q < 16; q += 2) {
-                            const float2 v = f2_split(f2_mul(f2_make(__uint_as_float(r[u][q]), __uint_as_float(r[u][q + 1])), sc2));
-                            sv[16 * u + q] = v.x;
-                            sv[16 * u + q + 1] = v.y;
+                        for (int q = 4; q < 16; q += 4) {
+                            v0 = fmax3(v0, __uint_as_float(r[u][q]), __uint_as_float(r[u][q + 1]));
+                            v1 = fmax3(v1, __uint_as_float(r[u][q + 2]), __uint_as_float(r[u][q + 3]));
                         }
+                        mx2[u] = fmaxf(v0, v1);
+                    }
+                    mx = fmaxf(mx2[0], mx2[1]) * scl;
                 }
-                // the segment's last S_t is in registers, and with it every S_t of it is
-                // done: Q_t's buffer is free for the next segment's rows
-                if (c == n - 1 && have_nx) load_q(nx);
-                const bool whole = bm == (1u << kChunkBlocks) - 1u;
-                if (!whole) {                  // the prefix's last step, or entries that are no page
-#pragma unroll
-                    for (int q = 0; q < kChunk; ++q)
-                        if (!((bm >> (q / kBlock)) & 1u)) sv[q] = -INFINITY;
-                }
-                float mx4[4];                                     // four short chains of 3-input maxima
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    float v = fmaxf(sv[16 * k], sv[16 * k + 15]);
-#pragma unroll
-                    for (int i = 1; i < 15; i += 2) v = fmax3(v, sv[16 * k + i], sv[16 * k + i + 1]);
-                    mx4[k] = v;
-                }
-                const float mx = fmax3(mx4[0], mx4[1], fmaxf(mx4[2], mx4[3]));
                 // lazy rescale: keep the stale maximum while the new one stays within 2^slack
-                const bool old_live = m != -INFINITY;
-                const bool resc = mx > m + kSlackLog2;
-                float alpha = 1.f;
-                if (resc) {
-                    alpha = old_live ? fast_exp2(m - mx) : 0.f;
-                    m = mx;
-                }
-                l *= alpha;
-                if (c > 0 && __any_sync(kFull, resc && old_live)) {       // O holds earlier steps: scale it
-                    // once P_t(G-1).V(G-1) has landed in it
-                    ok = __all_sync(kFull, mbar_wait(bar_o(tt, G - 1), par4(G - 1)));
-                    if (!ok) break;
-                    tc_fence_after();
-                    const float f = (resc && old_live) ? alpha : 1.f;
+                // of it for all rows of the two warps
+                if (pair_any(pair_bar, mx > m + kSlackLog2)) {
+                    ex[hf * kRows + row_t] = mx;
+                    pair_sync(pair_bar);
+                    mx = fmaxf(mx, ex[(hf ^ 1) * kRows + row_t]);
+                    const bool old_live = m != -INFINITY;
+                    const bool resc = mx > m + kSlackLog2;
+                    const float alpha = !resc ? 1.f : old_live ? fast_exp2(m - mx) : 0.f;
+                    if (resc) m = mx;
+                    l *= alpha;
+                    if (c > 0 && __any_sync(kFull, resc && old_live)) {       // O holds earlier steps: scale it
+                        // once P_t(G-1).V(G-1) has landed in it, this half its columns
+                        ok = __all_sync(kFull, mbar_wait(bar_o(tt, G - 1), par4(G - 1)));
+                        tc_fence_after();
+                        const float f = resc && old_live ? alpha : 1.f;
+#pragma unroll 1
+                        for (int q = 0; q < D / 32; ++q) {
+                            uint32_t r16[16];
+                            tmem_ld16(t_o + 16 * q, r16);
+                            tmem_wait_ld();
 #pragma unroll
-                    for (int q = 0; q < D / 16; ++q) {
-                        uint32_t r16[16];
-                        tmem_ld16(t_o + 16 * q, r16);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) r16[k] = __float_as_uint(__uint_as_float(r16[k]) * f);
-                        tmem_st16(t_o + 16 * q, r16);
+                            for (int k = 0; k < 16; ++k) r16[k] = __float_as_uint(__uint_as_float(r16[k]) * f);
+                            tmem_st16(t_o + 16 * q, r16);
+                        }
                     }
                 }
-                const float mu = m == -INFINITY ? 0.f : m;    // a row with nothing attended yet: p = 0
-                const uint64_t mu2 = f2_make(mu, mu);
+                const float mu = m == -INFINITY ? 0.f : -m;   // a row with nothing attended yet: p = 0
+                const uint64_t mu2 = f2_make(mu, mu), sc2 = f2_make(scl, scl);
                 uint64_t ps2[2] = {f2_make(0.f, 0.f), f2_make(0.f, 0.f)};
-                // P over S: block jl's 16 tokens to columns [16jl, 16jl+16) of the
-                // buffer, 8 high then 8 low columns
+                // P over S: a block's 16 tokens to its own columns, 8 high then 8 low ones
 #pragma unroll
-                for (int jl = 0; jl < kChunkBlocks; ++jl) {
+                for (int u = 0; u < kHalf / 16; ++u) {
                     uint32_t w16[16];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const float2 d = f2_split(f2_sub(f2_make(sv[16 * jl + 2 * e], sv[16 * jl + 2 * e + 1]), mu2));
+                        const float2 d = f2_split(
+                            f2_fma(f2_make(__uint_as_float(r[u][2 * e]), __uint_as_float(r[u][2 * e + 1])), sc2, mu2));
                         const float x = fast_exp2(d.x), y = fast_exp2(d.y);
                         const uint64_t xy = f2_make(x, y);
                         ps2[e & 1] = f2_add(ps2[e & 1], xy);
-                        w16[e] = pack2<kB>(x, y);
-                        const float2 f = unpack2<kB>(w16[e]);
-                        const float2 r = f2_split(f2_sub(xy, f2_make(f.x, f.y)));
-                        w16[8 + e] = pack2<kB>(r.x, r.y);
+                        split2<kB>(x, y, xy, w16[e], w16[8 + e]);
                     }
-                    tmem_st16(t_buf + 16 * jl, w16);
+                    tmem_st16(t_buf + 16 * u, w16);
                 }
                 tmem_wait_st();
                 {
                     const float2 p0 = f2_split(ps2[0]), p1 = f2_split(ps2[1]);
                     l += (p0.x + p1.x) + (p0.y + p1.y);
-                }
-                // V rows of missing blocks hold arbitrary bits: each tile zeroes them before
-                // its P(G) is ready (its MMA warp issues P_t(G).V(G) only then); both tiles
-                // write the same zeros
-                if (!whole) {
-                    ok = __all_sync(kFull, mbar_wait(bar_v(G), par_st(G)));
-                    const uint32_t vb = sV + stage(G) * C::kVc;
-                    for (int i = tid & (kRows - 1); i < kChunkBlocks * C::kVb / 16; i += kRows)
-                        if (!((bm >> (i / (C::kVb / 16))) & 1u)) sts128(vb + 16 * i, make_uint4(0u, 0u, 0u, 0u));
-                    fence_proxy_async_smem();      // zeroed V visible to the tensor core
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -549,8 +563,14 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
                 if (!ok) break;
             }
             if (!ok) break;
-            // the next segment's Q_t has landed: its MMA warp may start on it
-            if (have_nx) q_stored();
+            // every S_t of the segment is done, so Q_t's buffer is free: with the next one's
+            // rows in it, its MMA warp may start on it
+            Seg nx;
+            const bool have_nx = next_seg(nx);
+            if (have_nx) {
+                load_q(nx);
+                q_stored();
+            }
             // ---- wait for this tile's last P.V, then leave the row's state: a problem's
             // first piece by its row, a continued one (only a CTA's first can be) by CTA
             const int G_last = gc + n - 1;
@@ -558,24 +578,38 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
             if (!ok) break;
             tc_fence_after();
             if (tile_live) {
-                const int row = it.row0 + tid;     // tid = 128 t + row of tile t
-                const bool first = it.c0 == 0, live = row < it.rows;
-                const long long at = first ? (long long)it.span.first * a.GT * a.K + (long long)it.g * it.rows + row
-                                           : (long long)j * C::kCtaRows + tid;
-                float4* dst = reinterpret_cast<float4*>((first ? a.o_a : a.o_b) + at * D);
+                const int row = it.row0 + kRows * tt + row_t;
+                const bool first = it.c0 == 0;
+                const long long base = first ? (long long)it.span.first * a.GT * a.K + (long long)it.g * it.rows
+                                             : (long long)j * C::kCtaRows - it.row0;
+                ex[hf * kRows + row_t] = l;
+                // Lanes 2i and 2i + 1 swap quarters of their rows, so that together they
+                // write whole 32-byte pieces, of the even lane's row and then of the odd's.
+                const int odd = lane & 1, row_e = row - odd;
+                float* dst = (first ? a.o_a : a.o_b) + (base + row_e) * D + hf * (D / 2) + 4 * odd;
 #pragma unroll
-                for (int q = 0; q < D / 16; ++q) {
+                for (int q = 0; q < D / 32; ++q) {
                     uint32_t r16[16];
                     tmem_ld16(t_o + 16 * q, r16);
                     tmem_wait_ld();
-                    if (live) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            dst[4 * q + k] = make_float4(__uint_as_float(r16[4 * k]), __uint_as_float(r16[4 * k + 1]),
-                                                         __uint_as_float(r16[4 * k + 2]), __uint_as_float(r16[4 * k + 3]));
+                    for (int k = 0; k < 16; k += 8) {
+                        float x[4], y[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t got = __shfl_xor_sync(kFull, odd ? r16[k + i] : r16[k + 4 + i], 1);
+                            x[i] = __uint_as_float(odd ? got : r16[k + i]);         // of the even row
+                            y[i] = __uint_as_float(odd ? r16[k + 4 + i] : got);     // of the odd row
+                        }
+                        float* to = dst + 16 * q + k;
+                        if (row_e < it.rows) *reinterpret_cast<float4*>(to) = make_float4(x[0], x[1], x[2], x[3]);
+                        if (row_e + 1 < it.rows) *reinterpret_cast<float4*>(to + D) = make_float4(y[0], y[1], y[2], y[3]);
                     }
                 }
-                if (live) (first ? a.ml_a : a.ml_b)[at] = make_float2(m, l);
+                pair_sync(pair_bar);
+                if (hf == 0 && row < it.rows)
+                    (first ? a.ml_a : a.ml_b)[base + row] = make_float2(m, l + ex[kRows + row_t]);
+                pair_sync(pair_bar);               // ex has been read
             }
             gc += n;
             it = nx;
@@ -597,61 +631,57 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
 // an even share of the pieces. A piece that saw nothing holds m = -inf and o = 0.
 template <int D, int kRowWarps, int kCtaRows>
 __global__ void __launch_bounds__(kRowWarps * kCtaRows * 32) shared_merge_kernel(const DecodeArgs a, const SharedArgs p) {
-    static_assert(kRowWarps == 1 || kCtaRows == 1, "rows of several warps need a CTA each");
-    __shared__ float s_m[kRowWarps], s_l[kRowWarps];
-    __shared__ float s_acc[kRowWarps > 1 ? kRowWarps : 1][kRowWarps > 1 ? D : 1];
+    __shared__ float s_m[kCtaRows][kRowWarps], s_l[kCtaRows][kRowWarps];
+    __shared__ float s_acc[kRowWarps > 1 ? kCtaRows : 1][kRowWarps > 1 ? kRowWarps : 1][kRowWarps > 1 ? D : 4];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int sub = warp % kRowWarps;
     const int bh = (int)blockIdx.x * kCtaRows + warp / kRowWarps;   // rows < 2^31 (host-checked)
     launch_dependents();
-    grid_dependency_wait();                    // the tail kernel, which ends after the prefix kernel
-    if (blockIdx.x == 0 && tid == 0) *a.ws_ctr = 0ull;
     const int TH = a.T * a.H;
-    if (bh >= a.B * TH) return;                // uniform per warp, and per CTA where warps share a row
-    const int b = bh / TH, ih = bh - b * TH;
+    const int b = min(bh / TH, a.B - 1), ih = bh - b * TH;
     const int i = ih / a.H, h = ih - i * a.H, g = h / a.G;
     const int rr = i * a.G + (h - g * a.G);                           // row of the pair
     const int rg = a.NRG > 1 ? rr / dec::kHeadsPerWarp : 0;
     const int gv = g * a.NRG + rg, hh = rr - rg * dec::kHeadsPerWarp;
     const long long orow = (long long)bh * D;
-
-    // the tail's pieces
+    // what the earlier kernels read too needs no wait (this one starts once they have begun)
+    const PrefixGroups plan(p.groups, a.B);
+    const int len = a.context_lens[b];
+    int grp = 0, member = 0;
+    const int shared = len < 0 || len > a.max_blocks * kBlock ? 0 : shared_blocks(plan, b, len, a.T, a.max_blocks, &grp, &member);
+    const GroupSpan span = group_span(plan, grp, a.max_blocks);
+    grid_dependency_wait();                    // the tail kernel, which ends after the prefix kernel
+    if (blockIdx.x == 0 && tid == 0) *a.ws_ctr = 0ull;
+    if (bh >= a.B * TH) return;                // uniform per warp, and per CTA where warps share a row
     const int p0 = a.ws_pref[b], nb = a.ws_pref[b + 1] - p0;
+    const int R = p.hdr[0], cta_rows = p.hdr[2], unit0 = p.first_unit[grp];
+    Partition pt;
+    pt.R = a.ws_hdr[0];
+    pt.U = a.ws_hdr[1];
+    pt.Rs = a.ws_hdr[2];
+    pt.Cz = a.ws_hdr[3];
+    pt.P = a.ws_hdr[4];
+    pt.cpw = a.ws_hdr[5];
+
+    // the tail's pieces, then the prefix's
     long long first = 0;
     int n1 = 0;
     if (nb > 0) {
-        Partition pt;
-        pt.R = a.ws_hdr[0];
-        pt.U = a.ws_hdr[1];
-        pt.Rs = a.ws_hdr[2];
-        pt.Cz = a.ws_hdr[3];
-        pt.P = a.ws_hdr[4];
-        pt.cpw = a.ws_hdr[5];
         const int u0 = a.Kv * p0 + gv * nb, s0 = pt.segment_of(u0);
         n1 = pt.segment_of(u0 + nb - 1) - s0 + 1;
         first = (long long)b * a.Kv + gv + s0;
     }
-    // the prefix's
     int n2 = 0, j0 = 0, in_tile = 0;
     long long row_a = 0;
-    {
-        const PrefixGroups plan(p.groups, a.B);
-        const int L = a.context_lens[b];
-        int grp = 0, member = 0;
-        const int shared = L < 0 || L > a.max_blocks * kBlock ? 0 : shared_blocks(plan, b, L, a.T, a.max_blocks, &grp, &member);
-        if (shared > 0) {
-            const int cta_rows = p.hdr[2], R = p.hdr[0];
-            const GroupSpan span = group_span(plan, grp, a.max_blocks);
-            const Problem pr = problem_of(span, a.K, a.GT, cta_rows);
-            const int row = member * a.GT + rr, tile = row / cta_rows;
-            in_tile = row - tile * cta_rows;
-            row_a = (long long)span.first * a.GT * a.K + (long long)g * pr.rows + row;
-            const int u0 = p.first_unit[grp] + (g * pr.tiles + tile) * pr.chunks;
-            j0 = u0 / R;
-            n2 = (u0 + pr.chunks - 1) / R - j0 + 1;
-        }
+    if (shared > 0) {
+        const Problem pr = problem_of(span, a.K, a.GT, cta_rows);
+        const int row = member * a.GT + rr, tile = row / cta_rows;
+        in_tile = row - tile * cta_rows;
+        row_a = (long long)span.first * a.GT * a.K + (long long)g * pr.rows + row;
+        const int u0 = unit0 + (g * pr.tiles + tile) * pr.chunks;
+        j0 = u0 / R;
+        n2 = (u0 + pr.chunks - 1) / R - j0 + 1;
     }
-    const int cta_rows = n2 > 0 ? p.hdr[2] : 0;
     const int n = n1 + n2;
     auto piece_ml = [&](int x) -> const float2* {
         if (x < n1) return a.ws_ml + (first + x) * a.RS + hh;
@@ -696,24 +726,26 @@ __global__ void __launch_bounds__(kRowWarps * kCtaRows * 32) shared_merge_kernel
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(kFull, L, o);
     if constexpr (kRowWarps > 1) {
-        if (has_dims) *reinterpret_cast<float4*>(&s_acc[sub][4 * lane]) = acc;
+        const int rw = warp / kRowWarps;
+        if (has_dims) *reinterpret_cast<float4*>(&s_acc[rw][sub][4 * lane]) = acc;
         if (lane == 0) {
-            s_m[sub] = Mw;
-            s_l[sub] = L;
+            s_m[rw][sub] = Mw;
+            s_l[rw][sub] = L;
         }
-        __syncthreads();
-        float M = s_m[0];
+        // the row's warps alone: rows of a CTA may have left
+        asm volatile("barrier.cta.sync.aligned %0, %1;" ::"r"(1 + rw), "r"(32 * kRowWarps) : "memory");
+        float M = s_m[rw][0];
 #pragma unroll
-        for (int w = 1; w < kRowWarps; ++w) M = fmaxf(M, s_m[w]);
-        auto share = [&](int w) { return s_m[w] == -INFINITY ? 0.f : fast_exp2(s_m[w] - M); };
+        for (int w = 1; w < kRowWarps; ++w) M = fmaxf(M, s_m[rw][w]);
+        auto share = [&](int w) { return s_m[rw][w] == -INFINITY ? 0.f : fast_exp2(s_m[rw][w] - M); };
         float Lt = 0.f;
 #pragma unroll
-        for (int w = 0; w < kRowWarps; ++w) Lt += s_l[w] * share(w);
+        for (int w = 0; w < kRowWarps; ++w) Lt += s_l[rw][w] * share(w);
         const float inv = Lt > 0.f ? 1.f / Lt : 0.f;
-        for (int x = tid; x < D; x += blockDim.x) {
+        for (int x = tid % (32 * kRowWarps); x < D; x += 32 * kRowWarps) {
             float v = 0.f;
 #pragma unroll
-            for (int w = 0; w < kRowWarps; ++w) v += s_acc[w][x] * share(w);
+            for (int w = 0; w < kRowWarps; ++w) v += s_acc[rw][w][x] * share(w);
             dec::store1(a.out, a.out_dtype, orow + x, v * inv);
         }
     } else if (has_dims) {
@@ -775,7 +807,23 @@ PrefixWs prefix_ws(long long batch, long long rows, int d, int sms) {
     return w;
 }
 
-SharedArgs make_args(const DecodeLaunch& L, uint8_t* ws, int sms) {
+// The times behind the GPU's division, measured in the middle of long prefixes and tails of
+// 16-bit caches: a step of 256 rows takes an SM 1.05 us (of 128 rows in two CTAs 0.6), a
+// (block, kv-head) of the rows' own 32 bytes a nanosecond.
+SplitModel split_of(const DecodeLaunch& L, const Form& f, int sms) {
+    const gqa_kv_cache_t& c = *L.cache;
+    SplitModel m;
+    m.sms = sms;
+    m.ctas_per_sm = f.ctas_per_sm;
+    m.cta_rows = f.rows;
+    m.step_us = (f.rows > kRows ? 1.05f : 1.2f) * (c.head_dim == 128 ? 1.f : 0.7f);
+    m.prefix_us = 9.f;
+    m.unit_us = 2.f * kBlock * dtype_bytes(c.dtype, c.head_dim) / 40000.f;
+    m.tail_us = 4.f;
+    return m;
+}
+
+SharedArgs make_args(const DecodeLaunch& L, const Form& f, uint8_t* ws, int sms) {
     const gqa_kv_cache_t& c = *L.cache;
     const PrefixWs w = prefix_ws(L.batch, (long long)L.batch * L.tokens_per_seq * L.num_heads, c.head_dim, sms);
     SharedArgs a = {};
@@ -794,6 +842,7 @@ SharedArgs make_args(const DecodeLaunch& L, uint8_t* ws, int sms) {
     a.max_blocks = L.max_blocks;
     a.min_units = 2;
     a.scale_log2 = L.scale * dec::kLog2e;
+    a.split = split_of(L, f, sms);
     a.hdr = reinterpret_cast<int32_t*>(ws);
     a.first_unit = reinterpret_cast<int32_t*>(ws + w.first_unit);
     a.ml_a = reinterpret_cast<float2*>(ws + w.ml_a);
@@ -819,6 +868,13 @@ int launch_pdl(const void* fn, unsigned grid, int threads, int smem, cudaStream_
 
 }  // namespace
 
+bool dec::split_model(const DecodeLaunch& L, int num_sms, SplitModel& m) {
+    Form f;
+    if (!pick_form(L, f)) return false;
+    m = split_of(L, f, num_sms);
+    return true;
+}
+
 bool shared_prefix_supported(int dtype) { return dtype == GQA_DTYPE_F16 || dtype == GQA_DTYPE_BF16; }
 
 size_t shared_prefix_bytes(int batch, int num_heads, int head_dim, int tokens_per_seq, int num_sms) {
@@ -829,7 +885,7 @@ int launch_shared_prefix(const DecodeLaunch& L, uint8_t* ws, int num_sms) {
     const gqa_kv_cache_t& c = *L.cache;
     Form f;
     if (!pick_form(L, f)) return GQA_ERR_UNSUPPORTED;
-    SharedArgs a = make_args(L, ws, num_sms);
+    SharedArgs a = make_args(L, f, ws, num_sms);
     CUtensorMap kmap, vmap;
     if (!encode_cache_map(&kmap, c, c.k, 64, 128, a.map_perm) || !encode_cache_map(&vmap, c, c.v, 64, 128, a.map_perm))
         return GQA_ERR_UNSUPPORTED;
@@ -842,7 +898,7 @@ int launch_shared_prefix(const DecodeLaunch& L, uint8_t* ws, int num_sms) {
 int dec::launch_shared_merge(const DecodeArgs& tail, const DecodeLaunch& L, uint8_t* ws, int num_sms) {
     Form f;
     if (!pick_form(L, f)) return GQA_ERR_UNSUPPORTED;
-    SharedArgs p = make_args(L, ws, num_sms);
+    SharedArgs p = make_args(L, f, ws, num_sms);
     DecodeArgs a = tail;
     // Warps per row from the expected pieces: about 1.5 workers' worth of the tail's
     // segments per pair, and the prefix kernel's CTAs over one group's problems.
@@ -856,8 +912,9 @@ int dec::launch_shared_merge(const DecodeArgs& tail, const DecodeLaunch& L, uint
                  : reinterpret_cast<const void*>(&shared_merge_kernel<128, 1, 8>);
         per_cta = 8;
     } else if (est <= 64) {
-        fn = d64 ? reinterpret_cast<const void*>(&shared_merge_kernel<64, 8, 1>)
-                 : reinterpret_cast<const void*>(&shared_merge_kernel<128, 8, 1>);
+        fn = d64 ? reinterpret_cast<const void*>(&shared_merge_kernel<64, 4, 2>)
+                 : reinterpret_cast<const void*>(&shared_merge_kernel<128, 4, 2>);
+        per_cta = 2;
     } else {
         fn = d64 ? reinterpret_cast<const void*>(&shared_merge_kernel<64, 32, 1>)
                  : reinterpret_cast<const void*>(&shared_merge_kernel<128, 32, 1>);
