@@ -137,7 +137,7 @@ int launch_decode(const DecodeLaunch& L, int num_sms) {
     // the unit count, which must stay below 2^31.)
     int nrg = 1;
     bool ok = false;
-    const int min_units = L.min_blocks_per_warp > 0 ? L.min_blocks_per_warp : 4;
+    const int min_units = L.min_blocks_per_warp > 0 ? L.min_blocks_per_warp : tail ? 1 : 4;
     // 9 to 16 rows of a coded cache with sinks: one warp per pair and 16 rows, where the
     // workspace has room for its workers (the size asked for has; a fixed one may not)
     bool rows16 = false;

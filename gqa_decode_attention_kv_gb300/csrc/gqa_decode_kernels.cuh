@@ -329,15 +329,17 @@ __device__ void block_prefix(const DecodeArgs& a, int* lens_s, int* pref, int* t
         const int i = base + tid;
         int L = 0;
         if (i < a.B) {
-            L = a.context_lens[i];
-            if (L < 0 || L > maxtok) {
-                if (blockIdx.x == 0) flag_error(a.err, GQA_DEVERR_CONTEXT_LEN);
-                L = 0;
-            }
             if constexpr (kTail) {
-                const int shared = shared_blocks(PrefixGroups(a.groups, a.B), i, L, a.T, a.max_blocks);
-                start_s[i] = shared;
-                L -= shared * kBlock;
+                const SharedRow r = shared_row(PrefixGroups(a.groups, a.B), a.context_lens, i, a.T, a.max_blocks);
+                if (r.len < 0 && blockIdx.x == 0) flag_error(a.err, GQA_DEVERR_CONTEXT_LEN);
+                start_s[i] = r.blocks;
+                L = max(0, r.len) - r.blocks * kBlock;
+            } else {
+                L = a.context_lens[i];
+                if (L < 0 || L > maxtok) {
+                    if (blockIdx.x == 0) flag_error(a.err, GQA_DEVERR_CONTEXT_LEN);
+                    L = 0;
+                }
             }
             lens_s[i] = L;
         }

@@ -39,21 +39,29 @@ __device__ __forceinline__ GroupSpan group_span(const PrefixGroups& p, int i, in
     return good ? GroupSpan{a, e - a, n} : GroupSpan{0, 0, 0};
 }
 
-// Blocks that its group attends for row b of length L (T new tokens included): all that
-// the group shares where every query of the row sees them whole, else none, and the row
-// attends its context alone. g and member: its group and place in it. (All loads before
-// the first branch: two trips to memory.)
-__device__ __forceinline__ int shared_blocks(const PrefixGroups& p, int b, int L, int T, int max_blocks, int* g = nullptr,
-                                             int* member = nullptr) {
-    const int s = p.slot[b], i = p.group[b], n_groups = p.groups();
+// A row's part in a plan and its length, in two trips to memory: every load of a trip is
+// issued before the first branch.
+struct SharedRow {
+    int len, blocks, group, member;           // a length out of range: -1, blocks 0
+    GroupSpan span;
+};
+__device__ __forceinline__ SharedRow shared_row(const PrefixGroups& p, const int32_t* lens, int b, int T, int max_blocks) {
+    const int L = lens[b], s = p.slot[b], i = p.group[b], n_groups = p.groups();
     const int sc = min(max(s, 0), p.B - 1), ic = min(max(i, 0), p.B - 1);
     const int row = p.rows[sc];
-    const GroupSpan span = group_span(p, ic, max_blocks);
-    if (s != sc || i != ic || i >= n_groups || row != b || s < span.first || s >= span.first + span.rows) return 0;
-    if ((long long)span.blocks * kBlock + T - 1 > L) return 0;
-    if (g) *g = i;
-    if (member) *member = s - span.first;
-    return span.blocks;
+    SharedRow r{L, 0, ic, 0, group_span(p, ic, max_blocks)};
+    if (L < 0 || L > max_blocks * kBlock) {
+        r.len = -1;
+        return r;
+    }
+    // all the blocks that the group shares where every query of the row sees them whole,
+    // else none: the row then attends its context alone
+    if (s == sc && i == ic && i < n_groups && row == b && s >= r.span.first && s < r.span.first + r.span.rows &&
+        (long long)r.span.blocks * kBlock + T - 1 <= L) {
+        r.blocks = r.span.blocks;
+        r.member = s - r.span.first;
+    }
+    return r;
 }
 
 // ---- how the shared decode divides the GPU
@@ -63,7 +71,7 @@ __device__ __forceinline__ int shared_blocks(const PrefixGroups& p, int b, int L
 // be told from the plan and the lengths. Times are per SM.
 constexpr int kStepTokens = 64;                   // tokens of a step of the prefix kernel
 struct SplitModel {
-    int sms, ctas_per_sm, cta_rows;               // of the prefix kernel
+    int sms, ctas_per_sm, cta_rows, min_steps;    // of the prefix kernel; fewest steps of a CTA
     float step_us, prefix_us;                     // a step of an SM's CTAs, the kernel's start and end
     float unit_us, tail_us;                       // a (block, kv-head) of the tail, its start
 };
@@ -82,18 +90,20 @@ __device__ __forceinline__ Problem problem_of(const GroupSpan& s, int K, int GT,
 }
 
 // SMs for `steps` steps of the prefix beside `units` blocks of the tail: the fewest with
-// which the prefix ends no later than the tail on the others.
+// which the prefix ends no later than the tail on the others, but no more than its CTAs
+// have min_steps each for.
 __device__ __forceinline__ int prefix_sms(const SplitModel& m, int steps, int units) {
     if (steps == 0) return 0;
-    if (units == 0) return m.sms;
+    const int per_sm = m.min_steps * m.ctas_per_sm, most = min(m.sms, (steps + per_sm - 1) / per_sm);
+    if (units == 0) return most;
     const float wp = steps * m.step_us / m.ctas_per_sm, wt = units * m.unit_us;
-    int lo = 1, hi = m.sms - 1;                   // hi: the answer where nothing less does
+    int lo = 1, hi = max(1, min(most, m.sms - 1));   // hi: the answer where nothing less does
     while (lo < hi) {
         const int x = (lo + hi) >> 1;
-        if (m.prefix_us + wp / x <= m.tail_us + wt / (m.sms - x)) hi = x;
+        if (m.prefix_us + __fdividef(wp, (float)x) <= m.tail_us + __fdividef(wt, (float)(m.sms - x))) hi = x;
         else lo = x + 1;
     }
-    return max(lo, 1);
+    return lo;
 }
 
 }  // namespace gqa

@@ -78,7 +78,7 @@ struct SharedArgs {
     const int32_t* context_lens;
     int32_t* err;
     long long num_blocks;
-    int B, H, K, G, T, GT, max_blocks, min_units;
+    int B, H, K, G, T, GT, max_blocks;
     int map_perm[3], page_perm[2];
     float scale_log2;
     SplitModel split;
@@ -95,7 +95,7 @@ struct SharedCfg {
     static constexpr int kHalves = D / 64;               // 128-byte column halves of a row
     static constexpr int kCtaRows = kTiles * kRows;
     static constexpr int kSoftWarps = 8 * kTiles;        // four for each half of a step's tokens
-    static constexpr int kThreads = 32 * (kSoftWarps + kTiles + 2);   // + an MMA warp per tile, K and V copy warps
+    static constexpr int kThreads = 32 * (kSoftWarps + 2 * kTiles + 2);   // + S and P.V warps per tile, K and V copy warps
     static constexpr int kStages = kTiles == 2 || D == 64 ? 4 : 2;  // K and V stages
     static constexpr int kCtasPerSm = kTiles == 2 ? 1 : 2;
     static constexpr uint32_t kTmemCols = 256u * kTiles;
@@ -142,7 +142,7 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
 
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(kFull, tid >> 5, 0);               // uniform: addresses from it stay so
-    const bool softmax = warp < C::kSoftWarps, loader = warp >= C::kSoftWarps + kTiles;
+    const bool softmax = warp < C::kSoftWarps, loader = warp >= C::kSoftWarps + 2 * kTiles;
     const bool mma_warp = !softmax && !loader;
     const int tt = warp >> 3, hf = (warp >> 2) & 1;             // softmax warps: their tile and half
     if (tid == 0) {
@@ -173,20 +173,26 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
     // the first round's stay in registers.
     const PrefixGroups plan(a.groups, a.B);
     const int n_groups = plan.groups();
-    const int j = (int)blockIdx.x;
+    // CTAs are numbered SM by SM, as a grid of one wave is dealt out: those that take no
+    // part then leave whole SMs to the tail kernel
+    const int j = (int)blockIdx.x % a.split.sms * C::kCtasPerSm + (int)blockIdx.x / a.split.sms;
     constexpr int kWarps = C::kThreads / 32;
-    auto span_of = [&](int i) { return i < n_groups ? group_span(plan, i, a.max_blocks) : GroupSpan{0, 0, 0}; };
-    auto units_of = [&](const GroupSpan& x) { return problem_of(x, a.K, a.GT, C::kCtaRows).units; };
+    auto span_of = [&](int i) { return group_span(plan, min(i, a.B - 1), a.max_blocks); };
+    auto units_of = [&](const GroupSpan& x, int i) {
+        return i < n_groups ? problem_of(x, a.K, a.GT, C::kCtaRows).units : 0;
+    };
+    auto blocks_of = [&](int b) {
+        const SharedRow r = shared_row(plan, a.context_lens, min(b, a.B - 1), a.T, a.max_blocks);
+        return b < a.B && r.len > 0 ? (r.len + kBlock - 1) / kBlock - r.blocks : 0;
+    };
     GroupSpan mine = span_of(tid);
+    auto leader_of = [&](const GroupSpan& x) { return min(max(plan.rows[x.first], 0), a.B - 1); };
+    int lead = leader_of(mine);
     int U = 0, own = 0;
     {
-        int sum = units_of(mine), rows_own = 0;
-        for (int i = tid + C::kThreads; i < n_groups; i += C::kThreads) sum += units_of(span_of(i));
-        for (int b = tid; b < a.B; b += C::kThreads) {
-            const int L = a.context_lens[b];
-            if (L > 0 && L <= a.max_blocks * kBlock)
-                rows_own += (L + kBlock - 1) / kBlock - shared_blocks(plan, b, L, a.T, a.max_blocks);
-        }
+        int rows_own = blocks_of(tid), sum = units_of(mine, tid);
+        for (int i = tid + C::kThreads; i < n_groups; i += C::kThreads) sum += units_of(span_of(i), i);
+        for (int b = tid + C::kThreads; b < a.B; b += C::kThreads) rows_own += blocks_of(b);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
             sum += __shfl_xor_sync(kFull, sum, o);
@@ -204,7 +210,7 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
         }
     }
     const int P = max(1, prefix_sms(a.split, U, own * a.K) * C::kCtasPerSm);
-    const int R = max((U + P - 1) / P, a.min_units);
+    const int R = max((U + P - 1) / P, a.split.min_steps);
     const int u_lo = (int)min((long long)U, (long long)j * R), u_hi = (int)min((long long)U, (long long)(j + 1) * R);
     if (j == 0 && tid == 0) {
         a.hdr[0] = R;
@@ -213,8 +219,11 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
     }
     int carry = 0;
     for (int base = 0; base < n_groups; base += C::kThreads) {
-        if (base > 0) mine = span_of(base + tid);
-        const int x = units_of(mine);
+        if (base > 0) {
+            mine = span_of(base + tid);
+            lead = leader_of(mine);
+        }
+        const int x = units_of(mine, base + tid);
         int y = x;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -234,7 +243,10 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
         if (x > 0 && first <= u_lo && u_lo < first + x) {     // the group that the run begins in
             scan[128] = base + tid;
             scan[129] = first;
-            *reinterpret_cast<GroupSpan*>(scan + 130) = mine;
+            scan[130] = mine.first;
+            scan[131] = mine.rows;
+            scan[132] = mine.blocks;
+            scan[133] = lead;
         }
         if (j == 0 && base + tid < n_groups) a.first_unit[base + tid] = first;
     }
@@ -254,7 +266,7 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
         int g, rows, row0, c0, c1;
     };
     int w_group = scan[128], w_base = scan[129], w_u = u_lo;
-    GroupSpan w_span = *reinterpret_cast<const GroupSpan*>(scan + 130);
+    GroupSpan w_span{scan[130], scan[131], scan[132]};
     auto next_seg = [&](Seg& s) -> bool {
         if (w_u >= u_hi) return false;
         for (;;) {
@@ -283,12 +295,13 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
         // ================================================== copy warps: K, then V
         // A block that is missing (behind the prefix's last, or an entry that is no page) is
         // asked for at coordinate -1 and lands as zeros.
-        const bool k_warp = warp == C::kSoftWarps + kTiles;
+        const bool k_warp = warp == C::kSoftWarps + 2 * kTiles;
         const uint64_t once = l2_policy_evict_first(), again = l2_policy_evict_last();
         int issued = 0, G = 0;
         while (have && ok) {
             const uint64_t pol = it.rows > C::kCtaRows ? again : once;   // other tiles read the same pages
-            const int leader = min(max(plan.rows[it.span.first], 0), a.B - 1);
+            // the first segment's leader came with the scan
+            const int leader = G == 0 ? scan[133] : leader_of(it.span);
             const int32_t* table = a.block_tables + (long long)leader * a.max_blocks;
             int win_base = -(1 << 30), win_phys = -1;
             for (int c = it.c0; c < it.c1 && ok; ++c, ++G) {
@@ -345,76 +358,63 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
                 mbar_wait(k_warp ? bar_k(c) : bar_v(c), par_st(c), kWaitLimitNs / 4);
         }
     } else if (mma_warp) {
-        // ================================================== MMA warps: one per tile
-        // The whole warp walks along and one elected lane issues: from a branch of one lane
-        // the operands go through vector registers, 144 cycles a P.V product for 38.
-        const int t = warp - C::kSoftWarps;
+        // ================================================== MMA warps: two per tile, one for S and
+        // one for P.V, so that neither waits in the other's place (one warp for both takes
+        // 1790 cycles a step, its own chain of waits). A whole warp walks along and one
+        // elected lane issues: from a branch of one lane the operands go through vector
+        // registers, 144 cycles a P.V product for 38.
+        const int t = (warp - C::kSoftWarps) >> 1;
+        const bool s_warp = ((warp - C::kSoftWarps) & 1) == 0;
         auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(kFull, mbar_wait(bar, parity)); };
-        auto issue_s = [&](int G) {                // S_t(G) = Q_t K(G)^T into buffer G & 1
-            const uint32_t kb = sK + stage(G) * C::kKc, qb = sQ + t * C::kQt;
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-                const uint64_t ad = smem_desc_sw128(qb + (ks >> 2) * (kRows * 128) + (ks & 3) * 32, 16, 1024);
-                const uint64_t bd = smem_desc_sw128(kb + (ks >> 2) * (kChunk * 128) + (ks & 3) * 32, 16, 1024);
-                tc_mma_f16_elect(tmem + kColTile * t + kChunk * (G & 1), ad, bd, kIdescS, ks > 0);
-            }
-        };
-        auto issue_pv = [&](int G, bool first) {   // O_t (+)= P_t(G) V(G), high part then low part per block
-            const uint32_t vb = sV + stage(G) * C::kVc, pb = tmem + kColTile * t + kChunk * (G & 1);
-#pragma unroll
-            for (int jl = 0; jl < kChunkBlocks; ++jl)
-#pragma unroll
-                for (int part = 0; part < 2; ++part)
-                    tc_mma_f16_ta_elect(tmem + kColTile * t + kColO, pb + 16 * jl + 8 * part,
-                                        smem_desc_sw128(vb + jl * C::kVb, kBlock * 128, 1024), kIdescO,
-                                        !(first && jl == 0 && part == 0));
-        };
-        int s_done = 0, o_done = 0, gc = 0, qi = 0;   // commits issued (failure path), steps, segments
+        int G = 0, qi = 0;                         // commits issued, segments
         while (have && ok) {
             // a tile past the group's rows takes part in the barriers alone
             const bool live = it.row0 + kRows * t < it.rows;
             const int n = it.c1 - it.c0;
-            // Q_t of this segment stored; the last one's P.V done, so both S buffers
-            // are free (its commit covers every earlier product)
-            ok = wait(bar_q(t), (uint32_t)qi & 1u);
-            ++qi;
-            if (ok && gc > 0) ok = wait(bar_o(t, gc - 1), par4(gc - 1));
-            for (int c = 0; c < min(n, 2) && ok; ++c) {
-                ok = wait(bar_k(gc + c), par_st(gc + c));
-                tc_fence_after();
-                if (!ok) break;
-                if (live) issue_s(gc + c);
-                tc_commit_elect(bar_s(t, gc + c));
-                ++s_done;
-            }
-            for (int c = 0; c < n && ok; ++c) {
-                const int G = gc + c;
-                // V(G) landed, P_t(G) written over S_t(G)
-                ok = wait(bar_v(G), par_st(G)) && wait(bar_p(t, G), par4(G));
-                tc_fence_after();
-                if (!ok) break;
-                if (live) issue_pv(G, c == 0);
-                tc_commit_elect(bar_o(t, G));
-                ++o_done;
-                if (c + 2 < n) {
-                    // S_t(G+2) overwrites P_t(G): wait until PV_t(G) has read it
-                    ok = wait(bar_k(G + 2), par_st(G + 2)) && wait(bar_o(t, G), par4(G));
+            if (s_warp) {
+                ok = wait(bar_q(t), (uint32_t)qi & 1u);           // Q_t of this segment stored
+                ++qi;
+                for (int c = 0; c < n && ok; ++c, ++G) {
+                    // K(G) landed; P_t(G-2), which S_t(G) overwrites, read by its product
+                    ok = wait(bar_k(G), par_st(G)) && (G < 2 || wait(bar_o(t, G - 2), par4(G - 2)));
                     tc_fence_after();
                     if (!ok) break;
-                    if (live) issue_s(G + 2);
-                    tc_commit_elect(bar_s(t, G + 2));
-                    ++s_done;
+                    if (live) {                    // S_t(G) = Q_t K(G)^T into buffer G & 1
+                        const uint32_t kb = sK + stage(G) * C::kKc, qb = sQ + t * C::kQt;
+#pragma unroll
+                        for (int ks = 0; ks < D / 16; ++ks) {
+                            const uint64_t ad = smem_desc_sw128(qb + (ks >> 2) * (kRows * 128) + (ks & 3) * 32, 16, 1024);
+                            const uint64_t bd = smem_desc_sw128(kb + (ks >> 2) * (kChunk * 128) + (ks & 3) * 32, 16, 1024);
+                            tc_mma_f16_elect(tmem + kColTile * t + kChunk * (G & 1), ad, bd, kIdescS, ks > 0);
+                        }
+                    }
+                    tc_commit_elect(bar_s(t, G));
+                }
+            } else {
+                for (int c = 0; c < n && ok; ++c, ++G) {
+                    ok = wait(bar_v(G), par_st(G)) && wait(bar_p(t, G), par4(G));   // V(G) landed, P_t(G) over S_t(G)
+                    tc_fence_after();
+                    if (!ok) break;
+                    if (live) {                    // O_t (+)= P_t(G) V(G), high part then low part per block
+                        const uint32_t vb = sV + stage(G) * C::kVc, pb = tmem + kColTile * t + kChunk * (G & 1);
+#pragma unroll
+                        for (int jl = 0; jl < kChunkBlocks; ++jl)
+#pragma unroll
+                            for (int part = 0; part < 2; ++part)
+                                tc_mma_f16_ta_elect(tmem + kColTile * t + kColO, pb + 16 * jl + 8 * part,
+                                                    smem_desc_sw128(vb + jl * C::kVb, kBlock * 128, 1024), kIdescO,
+                                                    !(c == 0 && jl == 0 && part == 0));
+                    }
+                    tc_commit_elect(bar_o(t, G));
                 }
             }
-            gc += n;
             if (ok) have = next_seg(it);
         }
         if (!ok) {
-            // let this tile's MMAs land before the tensor memory goes, each
-            // barrier's events in order
+            // let this warp's MMAs land before the tensor memory goes, each barrier's events
+            // in order
             if (lane == 0) flag_error(a.err, GQA_DEVERR_TIMEOUT);
-            for (int k = max(0, s_done - kBufs); k < s_done; ++k) mbar_wait(bar_s(t, k), par4(k), kWaitLimitNs / 4);
-            for (int k = max(0, o_done - kBufs); k < o_done; ++k) mbar_wait(bar_o(t, k), par4(k), kWaitLimitNs / 4);
+            for (int k = max(0, G - kBufs); k < G; ++k) mbar_wait(s_warp ? bar_s(t, k) : bar_o(t, k), par4(k), kWaitLimitNs / 4);
         }
         __syncwarp();
     } else {
@@ -583,28 +583,38 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
                 const long long base = first ? (long long)it.span.first * a.GT * a.K + (long long)it.g * it.rows
                                              : (long long)j * C::kCtaRows - it.row0;
                 ex[hf * kRows + row_t] = l;
-                // Lanes 2i and 2i + 1 swap quarters of their rows, so that together they
-                // write whole 32-byte pieces, of the even lane's row and then of the odd's.
-                const int odd = lane & 1, row_e = row - odd;
-                float* dst = (first ? a.o_a : a.o_b) + (base + row_e) * D + hf * (D / 2) + 4 * odd;
+                // Four neighbouring lanes turn the 16 columns of their four rows around, so that
+                // they write 64 bytes of one row after the other.
+                const int l4 = lane & 3, row_4 = row - l4;
+                float* dst = (first ? a.o_a : a.o_b) + (base + row_4) * D + hf * (D / 2) + 4 * l4;
 #pragma unroll
                 for (int q = 0; q < D / 32; ++q) {
-                    uint32_t r16[16];
-                    tmem_ld16(t_o + 16 * q, r16);
+                    uint32_t x[16];                // quarter k of this lane's row: x[4k ..]
+                    tmem_ld16(t_o + 16 * q, x);
                     tmem_wait_ld();
+                    // quarter k of lane i goes to lane k as its piece i: exchange by bits
 #pragma unroll
-                    for (int k = 0; k < 16; k += 8) {
-                        float x[4], y[4];
+                    for (int s = 1; s < 4; s <<= 1) {
+                        const bool up = l4 & s;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t got = __shfl_xor_sync(kFull, odd ? r16[k + i] : r16[k + 4 + i], 1);
-                            x[i] = __uint_as_float(odd ? got : r16[k + i]);         // of the even row
-                            y[i] = __uint_as_float(odd ? r16[k + 4 + i] : got);     // of the odd row
+                        for (int k = 0; k < 4; ++k) {
+                            if (k & s) continue;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                uint32_t& lo = x[4 * k + i];
+                                uint32_t& hi = x[4 * (k + s) + i];
+                                const uint32_t got = __shfl_xor_sync(kFull, up ? lo : hi, s);
+                                if (up) lo = got;
+                                else hi = got;
+                            }
                         }
-                        float* to = dst + 16 * q + k;
-                        if (row_e < it.rows) *reinterpret_cast<float4*>(to) = make_float4(x[0], x[1], x[2], x[3]);
-                        if (row_e + 1 < it.rows) *reinterpret_cast<float4*>(to + D) = make_float4(y[0], y[1], y[2], y[3]);
                     }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (row_4 + k < it.rows)
+                            *reinterpret_cast<float4*>(dst + k * D + 16 * q) =
+                                make_float4(__uint_as_float(x[4 * k]), __uint_as_float(x[4 * k + 1]),
+                                            __uint_as_float(x[4 * k + 2]), __uint_as_float(x[4 * k + 3]));
                 }
                 pair_sync(pair_bar);
                 if (hf == 0 && row < it.rows)
@@ -645,16 +655,12 @@ __global__ void __launch_bounds__(kRowWarps * kCtaRows * 32) shared_merge_kernel
     const int gv = g * a.NRG + rg, hh = rr - rg * dec::kHeadsPerWarp;
     const long long orow = (long long)bh * D;
     // what the earlier kernels read too needs no wait (this one starts once they have begun)
-    const PrefixGroups plan(p.groups, a.B);
-    const int len = a.context_lens[b];
-    int grp = 0, member = 0;
-    const int shared = len < 0 || len > a.max_blocks * kBlock ? 0 : shared_blocks(plan, b, len, a.T, a.max_blocks, &grp, &member);
-    const GroupSpan span = group_span(plan, grp, a.max_blocks);
+    const SharedRow sr = shared_row(PrefixGroups(p.groups, a.B), a.context_lens, b, a.T, a.max_blocks);
     grid_dependency_wait();                    // the tail kernel, which ends after the prefix kernel
     if (blockIdx.x == 0 && tid == 0) *a.ws_ctr = 0ull;
     if (bh >= a.B * TH) return;                // uniform per warp, and per CTA where warps share a row
     const int p0 = a.ws_pref[b], nb = a.ws_pref[b + 1] - p0;
-    const int R = p.hdr[0], cta_rows = p.hdr[2], unit0 = p.first_unit[grp];
+    const int R = p.hdr[0], cta_rows = p.hdr[2], unit0 = p.first_unit[sr.group];
     Partition pt;
     pt.R = a.ws_hdr[0];
     pt.U = a.ws_hdr[1];
@@ -673,11 +679,11 @@ __global__ void __launch_bounds__(kRowWarps * kCtaRows * 32) shared_merge_kernel
     }
     int n2 = 0, j0 = 0, in_tile = 0;
     long long row_a = 0;
-    if (shared > 0) {
-        const Problem pr = problem_of(span, a.K, a.GT, cta_rows);
-        const int row = member * a.GT + rr, tile = row / cta_rows;
+    if (sr.blocks > 0) {
+        const Problem pr = problem_of(sr.span, a.K, a.GT, cta_rows);
+        const int row = sr.member * a.GT + rr, tile = row / cta_rows;
         in_tile = row - tile * cta_rows;
-        row_a = (long long)span.first * a.GT * a.K + (long long)g * pr.rows + row;
+        row_a = (long long)sr.span.first * a.GT * a.K + (long long)g * pr.rows + row;
         const int u0 = unit0 + (g * pr.tiles + tile) * pr.chunks;
         j0 = u0 / R;
         n2 = (u0 + pr.chunks - 1) / R - j0 + 1;
@@ -691,18 +697,25 @@ __global__ void __launch_bounds__(kRowWarps * kCtaRows * 32) shared_merge_kernel
         if (x < n1) return a.ws_o + ((first + x) * a.RS + hh) * D;
         return x == n1 ? p.o_a + row_a * D : p.o_b + ((long long)(j0 + x - n1) * cta_rows + in_tile) * D;
     };
+    // Each warp an even share, four pieces at a time: their outputs and, lane x, piece x's
+    // (m, l), all on the way before the first is used.
     const int per = (n + kRowWarps - 1) / kRowWarps;
     const int lo = min(n, sub * per), hi = min(n, lo + per);
     const bool has_dims = 4 * lane < D;
     float Mw = -INFINITY, L = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int base = lo; base < hi; base += 32) {
+    for (int base = lo; base < hi; base += 4) {
+        const int cnt = min(4, hi - base);
         float2 ml = make_float2(-INFINITY, 0.f);
-        if (base + lane < hi) ml = __ldcg(piece_ml(base + lane));
+        if (lane < cnt) ml = __ldcg(piece_ml(base + lane));
+        float4 o[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            if (x < cnt && has_dims) o[x] = __ldcg(reinterpret_cast<const float4*>(piece_o(base + x) + 4 * lane));
         float mc = ml.x;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mc = fmaxf(mc, __shfl_xor_sync(kFull, mc, o));
-        const float Mn = fmaxf(Mw, mc);
+        for (int s = 2; s > 0; s >>= 1) mc = fmaxf(mc, __shfl_xor_sync(kFull, mc, s));
+        const float Mn = fmaxf(Mw, __shfl_sync(kFull, mc, 0));
         if (Mn == -INFINITY) continue;         // warp-uniform: nothing seen yet
         const float sc = fast_exp2(Mw - Mn);   // 0 while Mw = -inf, 1 if unchanged
         acc.x *= sc; acc.y *= sc; acc.z *= sc; acc.w *= sc;
@@ -710,16 +723,11 @@ __global__ void __launch_bounds__(kRowWarps * kCtaRows * 32) shared_merge_kernel
         Mw = Mn;
         const float e = fast_exp2(ml.x - Mw);
         L += ml.y * e;
-        const int cnt = min(32, hi - base);
-        for (int q0 = 0; q0 < cnt; q0 += 8) {
 #pragma unroll
-            for (int qq = 0; qq < 8; ++qq) {
-                const int x = q0 + qq;
-                const float ex = __shfl_sync(kFull, e, x & 31);
-                if (x < cnt && has_dims) {
-                    const float4 o = __ldcg(reinterpret_cast<const float4*>(piece_o(base + x) + 4 * lane));
-                    acc.x += o.x * ex; acc.y += o.y * ex; acc.z += o.z * ex; acc.w += o.w * ex;
-                }
+        for (int x = 0; x < 4; ++x) {
+            const float ex = __shfl_sync(kFull, e, x);
+            if (x < cnt && has_dims) {
+                acc.x += o[x].x * ex; acc.y += o[x].y * ex; acc.z += o[x].z * ex; acc.w += o[x].w * ex;
             }
         }
     }
@@ -789,6 +797,18 @@ bool pick_form(const DecodeLaunch& L, Form& f) {
     }
 }
 
+template <int D>
+const void* pick_merge(int warps) {
+    switch (warps) {
+        case 1: return reinterpret_cast<const void*>(&shared_merge_kernel<D, 1, 8>);
+        case 2: return reinterpret_cast<const void*>(&shared_merge_kernel<D, 2, 4>);
+        case 4: return reinterpret_cast<const void*>(&shared_merge_kernel<D, 4, 2>);
+        case 8: return reinterpret_cast<const void*>(&shared_merge_kernel<D, 8, 1>);
+        case 16: return reinterpret_cast<const void*>(&shared_merge_kernel<D, 16, 1>);
+        default: return reinterpret_cast<const void*>(&shared_merge_kernel<D, 32, 1>);
+    }
+}
+
 constexpr int kMaxCtaRows = 2 * kRows;               // rows a CTA holds times its CTAs per SM, in every form
 
 struct PrefixWs {
@@ -809,16 +829,18 @@ PrefixWs prefix_ws(long long batch, long long rows, int d, int sms) {
 
 // The times behind the GPU's division, measured in the middle of long prefixes and tails of
 // 16-bit caches: a step of 256 rows takes an SM 1.05 us (of 128 rows in two CTAs 0.6), a
-// (block, kv-head) of the rows' own 32 bytes a nanosecond.
+// (block, kv-head) of the rows' own 40 bytes a nanosecond, with more than 8 query rows 25.
 SplitModel split_of(const DecodeLaunch& L, const Form& f, int sms) {
     const gqa_kv_cache_t& c = *L.cache;
     SplitModel m;
     m.sms = sms;
     m.ctas_per_sm = f.ctas_per_sm;
     m.cta_rows = f.rows;
+    m.min_steps = 2;
     m.step_us = (f.rows > kRows ? 1.05f : 1.2f) * (c.head_dim == 128 ? 1.f : 0.7f);
     m.prefix_us = 9.f;
-    m.unit_us = 2.f * kBlock * dtype_bytes(c.dtype, c.head_dim) / 40000.f;
+    const int GT = L.num_heads / c.num_kv_heads * L.tokens_per_seq;
+    m.unit_us = 2.f * kBlock * dtype_bytes(c.dtype, c.head_dim) / 40000.f * (GT > 8 ? 1.6f : 1.f);
     m.tail_us = 4.f;
     return m;
 }
@@ -840,7 +862,6 @@ SharedArgs make_args(const DecodeLaunch& L, const Form& f, uint8_t* ws, int sms)
     a.T = L.tokens_per_seq;
     a.GT = a.G * a.T;
     a.max_blocks = L.max_blocks;
-    a.min_units = 2;
     a.scale_log2 = L.scale * dec::kLog2e;
     a.split = split_of(L, f, sms);
     a.hdr = reinterpret_cast<int32_t*>(ws);
@@ -901,28 +922,21 @@ int dec::launch_shared_merge(const DecodeArgs& tail, const DecodeLaunch& L, uint
     SharedArgs p = make_args(L, f, ws, num_sms);
     DecodeArgs a = tail;
     // Warps per row from the expected pieces: about 1.5 workers' worth of the tail's
-    // segments per pair, and the prefix kernel's CTAs over one group's problems.
-    const long long rows = (long long)L.batch * a.GT, problems = (rows + f.rows - 1) / f.rows * a.K;
+    // segments per pair, and the prefix kernel's CTAs over the groups' problems.
+    const long long group = std::min(L.shared->max_group > 0 ? L.shared->max_group : L.batch, L.batch);
+    const long long problems = (group * a.GT + f.rows - 1) / f.rows * a.K * (L.batch / group);
     const long long est = (3LL * a.P) / (2LL * a.B * a.Kv) + 1 + num_sms * f.ctas_per_sm / problems + 1;
-    const bool d64 = L.cache->head_dim == 64;
-    const void* fn;
-    int per_cta = 1, threads = 256;
-    if (est <= 8) {
-        fn = d64 ? reinterpret_cast<const void*>(&shared_merge_kernel<64, 1, 8>)
-                 : reinterpret_cast<const void*>(&shared_merge_kernel<128, 1, 8>);
-        per_cta = 8;
-    } else if (est <= 64) {
-        fn = d64 ? reinterpret_cast<const void*>(&shared_merge_kernel<64, 4, 2>)
-                 : reinterpret_cast<const void*>(&shared_merge_kernel<128, 4, 2>);
-        per_cta = 2;
-    } else {
-        fn = d64 ? reinterpret_cast<const void*>(&shared_merge_kernel<64, 32, 1>)
-                 : reinterpret_cast<const void*>(&shared_merge_kernel<128, 32, 1>);
-        threads = 1024;
-    }
+    // As many warps per row as all rows together have room for at once (64 registers a
+    // thread: 32 warps an SM) and as there are pieces: a second wave costs what the first
+    // does, 4 us.
     const long long all = (long long)L.batch * a.T * a.H;
+    int warps = 32;
+    while (warps > 1 && (warps > est || all * warps > 32LL * num_sms)) warps >>= 1;
+    const bool d64 = L.cache->head_dim == 64;
+    const void* fn = d64 ? pick_merge<64>(warps) : pick_merge<128>(warps);
+    const int per_cta = std::max(1, 8 / warps);
     void* args[] = {&a, &p};
-    return launch_pdl(fn, (unsigned)((all + per_cta - 1) / per_cta), threads, 0, L.stream, args);
+    return launch_pdl(fn, (unsigned)((all + per_cta - 1) / per_cta), per_cta * warps * 32, 0, L.stream, args);
 }
 
 }  // namespace gqa
