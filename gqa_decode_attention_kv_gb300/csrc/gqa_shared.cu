@@ -16,6 +16,9 @@
 //                            as a high and a low 16-bit part over S (a 16-bit weight alone
 //                            would round it to the cache's type)
 //   O[128 x d]  += P V       P from tensor memory, V from shared memory
+// Coded caches (int8, e4m3, int4) take the same products in fp16: their copy warps widen
+// the codes of a step on the way (exact), K's scales go into the scores and V's into the
+// weights, which a power of two keeps where fp16 has its bits.
 // The (group, kv-head, tile) problems are laid out one behind the other in steps and cut
 // into equal runs, one per CTA of a single resident wave, so a long prefix is split over
 // the whole GPU however few rows share it, and the pieces are joined by the merge.
@@ -73,6 +76,8 @@ __device__ __forceinline__ void split2(float x, float y, uint64_t xy, uint32_t& 
 
 struct SharedArgs {
     const void* q;
+    const __half *k_scale, *v_scale;
+    int q_dtype;
     const int32_t* groups;
     const int32_t* block_tables;
     const int32_t* context_lens;
@@ -90,31 +95,74 @@ struct SharedArgs {
 
 // kTiles query tiles per CTA: two (one CTA per SM, all 512 tensor-memory columns, K/V read
 // once for 256 rows) or one (two CTAs per SM).
-template <int kTiles, int D>
+template <typename T, int kTiles, int D>
 struct SharedCfg {
+    static constexpr bool kI8 = std::is_same<T, int8_t>::value;
+    static constexpr bool kFp8 = std::is_same<T, __nv_fp8_e4m3>::value;
+    static constexpr bool kI4 = std::is_same<T, int4x2>::value;
+    static constexpr bool kCoded = kI8 || kFp8 || kI4;
+    static_assert(!kCoded || kTiles == 2, "coded caches have the two-tile form alone");
     static constexpr int kHalves = D / 64;               // 128-byte column halves of a row
     static constexpr int kCtaRows = kTiles * kRows;
     static constexpr int kSoftWarps = 8 * kTiles;        // four for each half of a step's tokens
-    static constexpr int kThreads = 32 * (kSoftWarps + 2 * kTiles + 2);   // + S and P.V warps per tile, K and V copy warps
-    static constexpr int kStages = kTiles == 2 || D == 64 ? 4 : 2;  // K and V stages
+    static constexpr int kCopyWarps = kCoded ? 4 : 2;    // K, V: one each, or two that also widen
+    static constexpr int kThreads = 32 * (kSoftWarps + 2 * kTiles + kCopyWarps);   // + S and P.V warps per tile
+    static constexpr int kStages = kCoded ? 2 : kTiles == 2 || D == 64 ? 4 : 2;    // K and V stages
+    static constexpr int kRaw = kCoded ? 4 : 0;          // stages of codes
     static constexpr int kCtasPerSm = kTiles == 2 ? 1 : 2;
     static constexpr uint32_t kTmemCols = 256u * kTiles;
     static constexpr int kQt = kRows * D * 2;            // one Q tile: halves x 128 rows x 128 B
     static constexpr int kKc = kChunk * D * 2;           // K chunk: halves x 64 rows x 128 B
     static constexpr int kVb = kBlock * D * 2;           // one V page
     static constexpr int kVc = kChunkBlocks * kVb;
-    static constexpr int kOffK = kTiles * kQt, kOffV = kOffK + kStages * kKc, kOffBar = kOffV + kStages * kVc;
+    static constexpr int kCodeRow = kI4 ? D / 2 : D;     // bytes of a row of codes
+    static constexpr int kCodes = kChunk * kCodeRow;     // a step's codes of K or V, then their scales
+    static constexpr int kRawStage = kCodes + 2 * 128;   // and which of the step's blocks there are
+    static constexpr int kOffK = kTiles * kQt, kOffV = kOffK + kStages * kKc, kOffRaw = kOffV + kStages * kVc,
+                         kOffBar = (kOffRaw + 2 * kRaw * kRawStage + 127) / 128 * 128;
     static constexpr int kOffEx = kOffBar + 1024;        // [tile][half][row]: maxima, then sums
-    static constexpr int kSmem = 1024 + kOffEx + kCtaRows * 8;
+    static constexpr int kOffSc = kOffEx + kCtaRows * 8; // coded: kSlots x (scales of K, of V, {factor, unlift})
+    static constexpr int kSlots = 4, kSlotF = 2 * kChunk + 4;
+    static constexpr int kSmem = 1024 + kOffSc + (kCoded ? kSlots * kSlotF * 4 : 0);
     static_assert((kSmem + 1024) * kCtasPerSm <= 228 * 1024, "CTAs per SM fit the shared memory");
 };
 
+// 16 codes of a row -> 8 words of two fp16 values each, exactly. w: 4 words of 8-bit
+// codes, 2 of 4-bit ones.
+template <class C>
+__device__ __forceinline__ void widen16(const uint32_t* w, uint32_t (&o)[8]) {
+    if constexpr (C::kI8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) i8x4_to_f16x4(w[i], o[2 * i], o[2 * i + 1]);
+    } else if constexpr (C::kFp8) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = e4m3x2_to_f16x2(w[i / 2] >> (16 * (i & 1)));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {          // bytes 0 and 2, then 1 and 3
+                const uint32_t lo = i4_lo_pair(w[i] >> (8 * e)), hi = i4_hi_pair(w[i] >> (8 * e));
+                o[4 * i + e] = __byte_perm(lo, hi, 0x5410);
+                o[4 * i + 2 + e] = __byte_perm(lo, hi, 0x7632);
+            }
+        }
+    }
+}
+
+// V's scales in the weights: w = p vs 2^lift, with the lift that puts the largest scale so
+// far into [2^3, 2^4), kept until a scale passes 2^7: p is at most 2^8, so that w stays
+// within fp16's range, and the low part's step is 2^-28 of that scale.
+__device__ __forceinline__ float power2(int e) { return __uint_as_float((uint32_t)(min(max(e, -126), 127) + 127) << 23); }
+constexpr int kLiftNone = 27;                     // before any scale: the least fp16 one is 2^-24
+
 template <typename T, int kTiles, int D>
-__global__ void __launch_bounds__(SharedCfg<kTiles, D>::kThreads, SharedCfg<kTiles, D>::kCtasPerSm)
+__global__ void __launch_bounds__(SharedCfg<T, kTiles, D>::kThreads, SharedCfg<T, kTiles, D>::kCtasPerSm)
 shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                      const SharedArgs a) {
-    using C = SharedCfg<kTiles, D>;
+    using C = SharedCfg<T, kTiles, D>;
     constexpr int kS = C::kStages;
+    constexpr bool kCoded = C::kCoded;
     constexpr bool kB = std::is_same<T, __nv_bfloat16>::value;
     constexpr uint32_t kIdescS = mma_idesc_f16(kRows, kChunk, kB, false, false);
     constexpr uint32_t kIdescO = mma_idesc_f16(kRows, D, kB, false, true);
@@ -138,6 +186,10 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
     auto bar_q = [&](int t) { return bar0 + 256 + 8 * t; };
     const uint32_t tslot = bar0 + 272;
     int* scan = reinterpret_cast<int*>(gb + C::kOffBar + 288);      // [128] sums, then the run's group and where it begins
+    // coded: "codes of K or V landed", "widened" (stage G % kRaw)
+    auto bar_full = [&](int v, int c) { return bar0 + 832 + 32 * v + 8 * (c & 3); };
+    auto bar_free = [&](int v, int c) { return bar0 + 896 + 32 * v + 8 * (c & 3); };
+    float* scales = reinterpret_cast<float*>(gb + C::kOffSc);
     auto par4 = [](int c) { return (uint32_t)(c >> 2) & 1u; };
 
     const int tid = threadIdx.x, lane = tid & 31;
@@ -149,8 +201,12 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
         prefetch_tensormap(&kmap);
         prefetch_tensormap(&vmap);
         for (int i = 0; i < kS; ++i) {
-            mbar_init(bar_k(i), 1);            // K, V stages
-            mbar_init(bar_v(i), 1);
+            mbar_init(bar_k(i), kCoded ? 2 : 1);   // K, V stages: the copy, or two warps that widen
+            mbar_init(bar_v(i), kCoded ? 2 : 1);
+        }
+        for (int i = 0; i < 2 * C::kRaw; ++i) {
+            mbar_init(bar_full(i >> 2, i), 1);
+            mbar_init(bar_free(i >> 2, i), 2);
         }
         for (int t = 0; t < kTiles; ++t) {
             for (int i = 0; i < kBufs; ++i) {
@@ -265,33 +321,169 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
         GroupSpan span;
         int g, rows, row0, c0, c1;
     };
-    int w_group = scan[128], w_base = scan[129], w_u = u_lo;
-    GroupSpan w_span{scan[130], scan[131], scan[132]};
-    auto next_seg = [&](Seg& s) -> bool {
-        if (w_u >= u_hi) return false;
+    struct Walk {
+        int group, base, u;
+        GroupSpan span;
+    };
+    Walk walk{scan[128], scan[129], u_lo, GroupSpan{scan[130], scan[131], scan[132]}};
+    auto step_seg = [&](Walk& w, Seg& s) -> bool {
+        if (w.u >= u_hi) return false;
         for (;;) {
-            const Problem p = problem_of(w_span, a.K, a.GT, C::kCtaRows);
-            const int rel = w_u - w_base;
+            const Problem p = problem_of(w.span, a.K, a.GT, C::kCtaRows);
+            const int rel = w.u - w.base;
             if (rel >= p.units) {              // steps are left, so a group is
-                w_base += p.units;
-                w_span = group_span(plan, ++w_group, a.max_blocks);
+                w.base += p.units;
+                w.span = group_span(plan, ++w.group, a.max_blocks);
                 continue;
             }
-            s.span = w_span;
             const int pair = rel / p.chunks;
+            s.span = w.span;
             s.c0 = rel - pair * p.chunks;
             s.g = pair / p.tiles;
             s.row0 = (pair - s.g * p.tiles) * C::kCtaRows;
             s.rows = p.rows;
-            s.c1 = min(p.chunks, s.c0 + (u_hi - w_u));
-            w_u += s.c1 - s.c0;
+            s.c1 = min(p.chunks, s.c0 + (u_hi - w.u));
+            w.u += s.c1 - s.c0;
             return true;
         }
     };
+    auto next_seg = [&](Seg& s) { return step_seg(walk, s); };
     Seg it;
     bool have = next_seg(it);
 
-    if (loader) {
+    if (kCoded && loader) {
+        // ================================================== copy warps of a coded cache: two for K,
+        // two for V. The first of each also asks for the codes, kRaw steps ahead; both wait
+        // for them, widen 32 of a step's tokens each into the stage that the tensor cores
+        // read, and put their scales where the softmax warps find them. A missing block
+        // lands as zero codes and gets zero scales.
+        constexpr int kRaw = C::kRaw > 0 ? C::kRaw : 1;
+        const int cw = warp - (C::kSoftWarps + 2 * kTiles), v = cw >> 1, part = cw & 1;
+        const uint32_t raw0 = sb + C::kOffRaw + v * kRaw * C::kRawStage;
+        const __half* gscale = v ? a.v_scale : a.k_scale;
+        const uint64_t once = l2_policy_evict_first(), again = l2_policy_evict_last();
+        auto par_raw = [](int c) { return (uint32_t)(c / kRaw) & 1u; };
+        Walk iw = walk;                            // the segment being asked for, and its next step
+        Seg is = it;
+        bool iss_have = have;
+        int iss_c = is.c0, issued = 0;
+        const int32_t* table = a.block_tables + (long long)scan[133] * a.max_blocks;
+        auto issue = [&]() -> bool {               // codes of step `issued`; false: a wait ran out
+            if (issued >= kRaw && !__all_sync(kFull, mbar_wait(bar_free(v, issued - kRaw), par_raw(issued - kRaw)))) return false;
+            const uint64_t pol = is.rows > C::kCtaRows ? again : once;
+            const uint32_t dst = raw0 + (issued % kRaw) * C::kRawStage, bar = bar_full(v, issued);
+            const int blk = kChunkBlocks * iss_c + lane;
+            int ph = -1;
+            if (lane < kChunkBlocks && blk < is.span.blocks) {
+                ph = table[blk];
+                if (ph < 0 || ph >= a.num_blocks) {
+                    flag_error(a.err, GQA_DEVERR_BLOCK_INDEX);
+                    ph = -1;
+                }
+            }
+            const uint32_t there = __ballot_sync(kFull, ph >= 0);
+            if (lane == 0) {
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + C::kCodes + 128), "r"(there) : "memory");
+                mbar_arrive_expect_tx(bar, C::kCodes + 32 * __popc(there));
+            }
+            __syncwarp();
+            if (lane < kChunkBlocks) {
+                auto coord = [&](int which) { return which == 0 ? 0 : (which == 1 ? is.g : ph); };
+                const uint32_t to = dst + C::kCodes + 32 * lane;
+                tma_load_4d(dst + lane * kBlock * C::kCodeRow, v ? &vmap : &kmap, 0, coord(a.map_perm[0]),
+                            coord(a.map_perm[1]), coord(a.map_perm[2]), bar, pol);
+                // a scale row shares L2 lines with the other heads'
+                if (ph >= 0) bulk_load(to, gscale + ((long long)ph * a.K + is.g) * kBlock, 32, bar, again);
+            }
+            ++issued;
+            if (++iss_c == is.c1 && (iss_have = step_seg(iw, is))) {
+                iss_c = is.c0;
+                table = a.block_tables + (long long)leader_of(is.span) * a.max_blocks;
+            }
+            return true;
+        };
+        int G = 0;
+        while (have && ok) {
+            int lift = kLiftNone;
+            for (int c = it.c0; c < it.c1 && ok; ++c, ++G) {
+                while (part == 0 && iss_have && issued < G + kRaw && ok) ok = issue();
+                // the codes are here; the stage's last step has been read by both tiles
+                bool w = ok && mbar_wait(bar_full(v, G), par_raw(G));
+                if (G >= kS)
+#pragma unroll
+                    for (int t = 0; t < kTiles; ++t)
+                        w = w && mbar_wait(v ? bar_o(t, G - kS) : bar_s(t, G - kS), par4(G - kS));
+                ok = __all_sync(kFull, w);
+                if (!ok) break;
+                const uint32_t src = raw0 + (G % kRaw) * C::kRawStage;
+                const uint32_t to = (v ? sV : sK) + stage(G) * C::kKc;
+                constexpr int kLanes = D / 16;         // lanes of a row, 16 codes each
+#pragma unroll 4
+                for (int i = lane; i < 32 * kLanes; i += 32) {
+                    const int tok = 32 * part + i / kLanes, x = i % kLanes;
+                    uint32_t codes[4], o[8];
+                    if constexpr (C::kI4) {
+                        const uint2 r = lds64(src + tok * C::kCodeRow + 8 * x);
+                        codes[0] = r.x;
+                        codes[1] = r.y;
+                    } else {
+                        const uint4 r = lds128(src + tok * C::kCodeRow + 16 * x);
+                        codes[0] = r.x; codes[1] = r.y; codes[2] = r.z; codes[3] = r.w;
+                    }
+                    widen16<C>(codes, o);
+                    // 16-byte chunks 2x, 2x + 1 of the row, swizzled; the lanes of the second
+                    // half begin with the other one, so that both halves' banks differ
+                    const int h = x >> 2, ck = 2 * (x & 3);
+                    const uint32_t row = v ? to + (tok / kBlock) * C::kVb + h * (kBlock * 128) + (tok % kBlock) * 128
+                                           : to + h * (kChunk * 128) + tok * 128;
+                    const uint4 c0 = make_uint4(o[0], o[1], o[2], o[3]), c1 = make_uint4(o[4], o[5], o[6], o[7]);
+                    const int s7 = tok & 7;
+                    sts128(row + (((ck + h) ^ s7) << 4), h ? c1 : c0);
+                    sts128(row + (((ck + 1 - h) ^ s7) << 4), h ? c0 : c1);
+                }
+                // scales: lane l those of tokens 2l and 2l + 1, zero where a block is missing
+                // (its codes are zeros, its scales are what the stage held)
+                float2 sc = unpack2<false>(lds32(src + C::kCodes + 4 * lane));
+                if (!((lds32(src + C::kCodes + 128) >> (lane / 8)) & 1u)) sc = make_float2(0.f, 0.f);
+                float* slot = scales + (G & 3) * C::kSlotF + v * kChunk;
+                if (v) {
+                    float most = fmaxf(sc.x, sc.y);
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(kFull, most, o));
+                    float factor = 1.f;
+                    if (most > power2(7 - lift)) {
+                        const int now = 3 - ((int)(__float_as_uint(most) >> 23) - 127);
+                        factor = power2(now - lift);
+                        lift = now;
+                    }
+                    const float up = power2(lift);
+                    sc.x *= up;
+                    sc.y *= up;
+                    if (part == 0 && lane == 0) {
+                        scales[(G & 3) * C::kSlotF + 2 * kChunk] = factor;
+                        scales[(G & 3) * C::kSlotF + 2 * kChunk + 1] = power2(-lift);
+                    }
+                } else {
+                    sc.x *= a.scale_log2;
+                    sc.y *= a.scale_log2;
+                }
+                if (lane / 16 == part) *reinterpret_cast<float2*>(slot + 2 * lane) = sc;
+                fence_proxy_async_smem();          // the widened rows visible to the tensor core
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(v ? bar_v(G) : bar_k(G));
+                    mbar_arrive(bar_free(v, G));
+                }
+            }
+            if (ok) have = next_seg(it);
+        }
+        if (!ok && lane == 0) {
+            // let this warp's copies land before the shared memory goes
+            flag_error(a.err, GQA_DEVERR_TIMEOUT);
+            for (int c = max(0, issued - kRaw); c < issued; ++c) mbar_wait(bar_full(v, c), par_raw(c), kWaitLimitNs / 4);
+        }
+        __syncwarp();
+    } else if (loader) {
         // ================================================== copy warps: K, then V
         // A block that is missing (behind the prefix's last, or an entry that is no page) is
         // asked for at coordinate -1 and lands as zeros.
@@ -442,6 +634,24 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
                 const int b = rq < x.rows ? plan.rows[x.span.first + member] : -1;
                 src[i] = b >= 0 && b < a.B ? (b * a.T + tok) * a.H + x.g * a.G + (w - tok * a.G) : -1;
             }
+            if constexpr (kCoded) {                // q as fp16
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i) {
+                    const int rl = rl0 + i * kRowsPerStep;
+                    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                    if (src[i] >= 0) {
+                        x = dec::ldg128(static_cast<const uint16_t*>(a.q) + (long long)src[i] * D + 8 * c16);
+                        if (a.q_dtype == GQA_DTYPE_BF16) {
+                            x.x = dec::bf16x2_to_f16x2(x.x);
+                            x.y = dec::bf16x2_to_f16x2(x.y);
+                            x.z = dec::bf16x2_to_f16x2(x.z);
+                            x.w = dec::bf16x2_to_f16x2(x.w);
+                        }
+                    }
+                    sts128(qt + (c16 >> 3) * (kRows * 128) + rl * 128 + (((c16 & 7) ^ (rl & 7)) << 4), x);
+                }
+                return;
+            }
 #pragma unroll
             for (int i = 0; i < kSteps; ++i) {
                 const int rl = rl0 + i * kRowsPerStep;
@@ -464,6 +674,7 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
             const int n = it.c1 - it.c0;
             const bool tile_live = it.row0 + kRows * tt < it.rows;
             float m = -INFINITY, l = 0.f;      // the row's maximum, this half's sum
+            float unlift = 1.f;                // coded: what takes the lift out of O
             for (int c = 0; c < n; ++c) {
                 const int G = gc + c;
                 ok = __all_sync(kFull, mbar_wait(bar_s(tt, G), par4(G)));   // S_t(G) done
@@ -480,6 +691,25 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
                 for (int u = 0; u < kHalf / 16; ++u) tmem_ld16(t_buf + 16 * u, r[u]);
                 tmem_wait_ld();
                 float scl = a.scale_log2;
+                float factor = 1.f;                // coded: of O, where V's lift changes
+                const float* slot = scales + (G & 3) * C::kSlotF + kHalf * hf;
+                if constexpr (kCoded) {            // scores by K's scales (the softmax scale is in them)
+#pragma unroll
+                    for (int u = 0; u < kHalf / 16; ++u)
+#pragma unroll
+                        for (int q = 0; q < 16; q += 4) {
+                            const float4 ks = *reinterpret_cast<const float4*>(slot + 16 * u + q);
+                            r[u][q] = __float_as_uint(__uint_as_float(r[u][q]) * ks.x);
+                            r[u][q + 1] = __float_as_uint(__uint_as_float(r[u][q + 1]) * ks.y);
+                            r[u][q + 2] = __float_as_uint(__uint_as_float(r[u][q + 2]) * ks.z);
+                            r[u][q + 3] = __float_as_uint(__uint_as_float(r[u][q + 3]) * ks.w);
+                        }
+                    scl = 1.f;
+                    ok = __all_sync(kFull, mbar_wait(bar_v(G), par_st(G)));      // V's are there as well
+                    if (!ok) break;
+                    factor = slot[2 * kChunk - kHalf * hf];
+                    unlift = slot[2 * kChunk + 1 - kHalf * hf];
+                }
                 const int blocks = it.span.blocks - kChunkBlocks * (it.c0 + c);   // of this step and after
                 if (blocks < kChunkBlocks || !(scl > 0.f)) {      // the prefix's last step; or no positive scale
 #pragma unroll
@@ -509,7 +739,7 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
                 }
                 // lazy rescale: keep the stale maximum while the new one stays within 2^slack
                 // of it for all rows of the two warps
-                if (pair_any(pair_bar, mx > m + kSlackLog2)) {
+                if (pair_any(pair_bar, mx > m + kSlackLog2 || factor != 1.f)) {
                     ex[hf * kRows + row_t] = mx;
                     pair_sync(pair_bar);
                     mx = fmaxf(mx, ex[(hf ^ 1) * kRows + row_t]);
@@ -518,11 +748,11 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
                     const float alpha = !resc ? 1.f : old_live ? fast_exp2(m - mx) : 0.f;
                     if (resc) m = mx;
                     l *= alpha;
-                    if (c > 0 && __any_sync(kFull, resc && old_live)) {       // O holds earlier steps: scale it
+                    if (c > 0 && __any_sync(kFull, (resc && old_live) || factor != 1.f)) {   // O holds earlier steps: scale it
                         // once P_t(G-1).V(G-1) has landed in it, this half its columns
                         ok = __all_sync(kFull, mbar_wait(bar_o(tt, G - 1), par4(G - 1)));
                         tc_fence_after();
-                        const float f = resc && old_live ? alpha : 1.f;
+                        const float f = (resc && old_live ? alpha : 1.f) * factor;
 #pragma unroll 1
                         for (int q = 0; q < D / 32; ++q) {
                             uint32_t r16[16];
@@ -548,7 +778,14 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
                         const float x = fast_exp2(d.x), y = fast_exp2(d.y);
                         const uint64_t xy = f2_make(x, y);
                         ps2[e & 1] = f2_add(ps2[e & 1], xy);
-                        split2<kB>(x, y, xy, w16[e], w16[8 + e]);
+                        if constexpr (kCoded) {
+                            const float2 vs = *reinterpret_cast<const float2*>(slot + kChunk + 16 * u + 2 * e);
+                            const uint64_t w2 = f2_mul(xy, f2_make(vs.x, vs.y));
+                            const float2 w = f2_split(w2);
+                            split2<false>(w.x, w.y, w2, w16[e], w16[8 + e]);
+                        } else {
+                            split2<kB>(x, y, xy, w16[e], w16[8 + e]);
+                        }
                     }
                     tmem_st16(t_buf + 16 * u, w16);
                 }
@@ -592,6 +829,9 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
                     uint32_t x[16];                // quarter k of this lane's row: x[4k ..]
                     tmem_ld16(t_o + 16 * q, x);
                     tmem_wait_ld();
+                    if constexpr (kCoded)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * unlift);
                     // quarter k of lane i goes to lane k as its piece i: exchange by bits
 #pragma unroll
                     for (int s = 1; s < 4; s <<= 1) {
@@ -771,13 +1011,14 @@ __global__ void __launch_bounds__(kRowWarps * kCtaRows * 32) shared_merge_kernel
 struct Form {
     const void* fn;
     int threads, smem, ctas_per_sm, rows;
+    int code_row;                                    // bytes of a row of codes
 };
 
 template <typename T, int kTiles, int D>
 Form form() {
-    using C = SharedCfg<kTiles, D>;
+    using C = SharedCfg<T, kTiles, D>;
     return Form{reinterpret_cast<const void*>(&shared_prefix_kernel<T, kTiles, D>), C::kThreads, C::kSmem, C::kCtasPerSm,
-                C::kCtaRows};
+                C::kCtaRows, C::kCodeRow};
 }
 
 template <typename T>
@@ -785,14 +1026,21 @@ Form pick_tiles(int d, bool two) {
     if (d == 64) return two ? form<T, 2, 64>() : form<T, 1, 64>();
     return two ? form<T, 2, 128>() : form<T, 1, 128>();
 }
+template <typename T>
+Form pick_coded(int d) {
+    return d == 64 ? form<T, 2, 64>() : form<T, 2, 128>();
+}
 
 bool pick_form(const DecodeLaunch& L, Form& f) {
-    const int GT = L.num_heads / L.cache->num_kv_heads * L.tokens_per_seq;
+    const int GT = L.num_heads / L.cache->num_kv_heads * L.tokens_per_seq, d = L.cache->head_dim;
     const long long rows = (long long)std::min(L.shared->max_group > 0 ? L.shared->max_group : L.batch, L.batch) * GT;
     const bool two = rows > kRows;
     switch (L.cache->dtype) {
-        case GQA_DTYPE_F16: f = pick_tiles<__half>(L.cache->head_dim, two); return true;
-        case GQA_DTYPE_BF16: f = pick_tiles<__nv_bfloat16>(L.cache->head_dim, two); return true;
+        case GQA_DTYPE_F16: f = pick_tiles<__half>(d, two); return true;
+        case GQA_DTYPE_BF16: f = pick_tiles<__nv_bfloat16>(d, two); return true;
+        case GQA_DTYPE_I8: f = pick_coded<int8_t>(d); return true;
+        case GQA_DTYPE_FP8_E4M3: f = pick_coded<__nv_fp8_e4m3>(d); return true;
+        case GQA_DTYPE_I4: f = pick_coded<int4x2>(d); return true;
         default: return false;
     }
 }
@@ -850,6 +1098,9 @@ SharedArgs make_args(const DecodeLaunch& L, const Form& f, uint8_t* ws, int sms)
     const PrefixWs w = prefix_ws(L.batch, (long long)L.batch * L.tokens_per_seq * L.num_heads, c.head_dim, sms);
     SharedArgs a = {};
     a.q = L.q;
+    a.q_dtype = L.q_dtype;
+    a.k_scale = static_cast<const __half*>(c.k_scale);
+    a.v_scale = static_cast<const __half*>(c.v_scale);
     a.groups = L.shared->groups;
     a.block_tables = L.block_tables;
     a.context_lens = L.context_lens;
@@ -896,7 +1147,7 @@ bool dec::split_model(const DecodeLaunch& L, int num_sms, SplitModel& m) {
     return true;
 }
 
-bool shared_prefix_supported(int dtype) { return dtype == GQA_DTYPE_F16 || dtype == GQA_DTYPE_BF16; }
+bool shared_prefix_supported(int dtype) { return dtype != GQA_DTYPE_F32 && dtype != GQA_DTYPE_I4_KC; }
 
 size_t shared_prefix_bytes(int batch, int num_heads, int head_dim, int tokens_per_seq, int num_sms) {
     return prefix_ws(batch, (long long)batch * std::max(1, tokens_per_seq) * num_heads, head_dim, num_sms).total;
@@ -908,9 +1159,12 @@ int launch_shared_prefix(const DecodeLaunch& L, uint8_t* ws, int num_sms) {
     if (!pick_form(L, f)) return GQA_ERR_UNSUPPORTED;
     SharedArgs a = make_args(L, f, ws, num_sms);
     CUtensorMap kmap, vmap;
-    if (!encode_cache_map(&kmap, c, c.k, 64, 128, a.map_perm) || !encode_cache_map(&vmap, c, c.v, 64, 128, a.map_perm))
+    const bool coded = dtype_coded(c.dtype);          // whole rows of codes, as they lie
+    const int inner = coded ? f.code_row : 64, swizzle = coded ? 0 : 128;
+    if (!encode_cache_map(&kmap, c, c.k, inner, swizzle, a.map_perm) ||
+        !encode_cache_map(&vmap, c, c.v, inner, swizzle, a.map_perm))
         return GQA_ERR_UNSUPPORTED;
-    if (c.head_dim == 128 && !encode_page_map(&vmap, c, c.v, a.page_perm)) return GQA_ERR_UNSUPPORTED;   // V a page per box
+    if (!coded && c.head_dim == 128 && !encode_page_map(&vmap, c, c.v, a.page_perm)) return GQA_ERR_UNSUPPORTED;   // V a page per box
     if (ctas_per_sm(f.fn, f.threads, f.smem) < 1) return GQA_ERR_CUDA;
     void* args[] = {&kmap, &vmap, &a};
     return launch_pdl(f.fn, (unsigned)(num_sms * f.ctas_per_sm), f.threads, f.smem, L.stream, args);

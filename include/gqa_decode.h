@@ -601,8 +601,9 @@ GQA_API int gqa_decode_sinks(const gqa_kv_cache_t *cache, const void *q, int32_t
  *                  it picks the kernel's form and changes no result.
  *  workspace       device, >= gqa_decode_shared_workspace_size(...) bytes, otherwise as
  *                  gqa_decode's (which it may be shared with).
- *  Cache dtypes: F16, BF16; others are GQA_ERR_UNSUPPORTED. Other arguments and limits as
- *  gqa_decode; batch <= 8191.
+ *  Cache dtypes: F16, BF16, I8, FP8_E4M3, I4; F32 and I4_KC are GQA_ERR_UNSUPPORTED. q of a
+ *  coded cache is taken as fp16 (exact from BF16 where 2^-17 <= |q| <= 65504). Other
+ *  arguments and limits as gqa_decode.
  */
 GQA_API size_t gqa_decode_shared_workspace_size(int32_t batch, int32_t num_heads, int32_t num_kv_heads,
                                  int32_t head_dim, int32_t tokens_per_seq, int32_t device);

@@ -75,6 +75,88 @@ def test_against_fp64(gq, kind, K, G, d, T, groups, alone):
     check(got, want, values)
 
 
+@pytest.mark.parametrize("kind,q_dtype", [("int8", torch.bfloat16), ("int8", torch.float16), ("fp8", torch.bfloat16),
+                                          ("fp8", torch.float16), ("int4", torch.bfloat16)])
+@pytest.mark.parametrize("K,G,d,T,groups,alone", SHAPES)
+def test_coded_against_fp64(gq, kind, q_dtype, K, G, d, T, groups, alone):
+    """The values are code * scale exactly, and so are the products in fp16."""
+    got, want, err, values, plan = run(gq, kind, K, G, d, T, groups, alone, q_dtype=q_dtype)
+    assert err == 0
+    assert plan.count.tolist()[0] == len(groups)
+    check(got, want, values)
+
+
+@pytest.mark.parametrize("kind", ["int8", "fp8", "int4"])
+@pytest.mark.parametrize("order", ["rising", "falling", "mixed"])
+def test_sizes_of_v_in_coded_caches(gq, kind, order):
+    """V's scales from 2^-22 to 2^4, rising, falling and mixed along the prefix: the error goes by the
+    largest |v| that a row sees, and rows of tiny V keep their bits."""
+    n = 60
+    size = {"rising": np.linspace(-20, 4, n), "falling": np.linspace(4, -20, n),
+            "mixed": np.random.default_rng(1).uniform(-20, 4, n)}[order]
+    for top in (4.0, -14.0):
+        amp = 2.0 ** (size - 4 + top)
+
+        def tweak(bt, cache, values):
+            lead = max(range(len(bt.lens)), key=lambda b: bt.lens[b])
+            scale = cache.v_scale.clone()
+            for j in range(n):
+                p = int(bt.table[lead, j])
+                old = scale[p].clone()
+                scale[p] = (old.float() * float(amp[j])).half()
+                f = scale[p].double().cpu().numpy() / old.double().cpu().numpy()      # [K, 16]
+                values[1][p] *= f.T[:, :, None]
+            scale_small = [int(x) for b in range(len(bt.lens)) for x in bt.table[b, n:] if x >= 0]
+            for p in scale_small:
+                old = scale[p].clone()
+                scale[p] = (old.float() * 2.0 ** (top - 8)).half()
+                f = scale[p].double().cpu().numpy() / old.double().cpu().numpy()
+                values[1][p] *= f.T[:, :, None]
+            cache.v_scale.copy_(scale)
+
+        got, want, err, values, _ = run(gq, kind, 2, 8, 128, 1, [(n, [16 * n + 5, 16 * n + 30, 16 * n + 1] * 3)], [],
+                                        tweak=tweak)
+        assert err == 0
+        seen = 2.0 ** top * 4.5
+        assert (np.abs(got - want) <= seen * 2.0 ** -11).all(), float(np.abs(got - want).max() / seen)
+
+
+@pytest.mark.parametrize("kind", ["int8", "int4"])
+def test_poisoned_scales_behind_the_rows(gq, kind):
+    """Scales of slots that no row owns are NaN."""
+    def tweak(bt, cache, values):
+        owned = np.zeros((bt.pages, 16), dtype=bool)
+        for b, L in enumerate(bt.lens):
+            for t in range(L):
+                owned[bt.table[b, t // 16], t % 16] = True
+        at = torch.from_numpy(~owned)
+        for t in (cache.k_scale, cache.v_scale):
+            x = t.cpu()                                             # [pages, K, 16]
+            x[at[:, None, :].expand(-1, x.shape[1], -1)] = float("nan")
+            t.copy_(x)
+
+    got, want, err, values, _ = run(gq, kind, 2, 4, 128, 1, [(5, [81, 95, 90]), (6, [97, 98])], [3, 0, 18], tweak=tweak)
+    assert err == 0
+    check(got, want, values)
+
+
+@pytest.mark.parametrize("kind", ["int8", "fp8", "int4"])
+def test_bad_pages_of_coded_caches_are_flagged(gq, kind):
+    bt = shared.batch([(9, [150, 160])], [40], 14)
+    cache, values = shared.pool(kind, bt.pages, 2, 128, 15, gq)
+    q = torch.randn(3, 1, 8, 128, generator=torch.Generator().manual_seed(16)).bfloat16()
+    table, lens = torch.from_numpy(bt.table).cuda(), torch.from_numpy(bt.lens).cuda()
+    plan = gq.kv_pages_groups(table, lens)
+    lead = plan.rows.tolist()[0]
+    for bad in (-1, bt.pages, 2 ** 31 - 1):
+        broken = table.clone()
+        broken[lead, 4] = bad
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        got = gq.gqa_decode_shared(cache, q[:, 0].contiguous().cuda(), broken, lens, 0.1, plan, err=err)
+        assert int(err) == gq.GQA_DEVERR_BLOCK_INDEX
+        assert torch.isfinite(got).all()
+
+
 @pytest.mark.parametrize("max_group", [1, 4, 500])
 @pytest.mark.parametrize("out", [torch.float16, torch.bfloat16, torch.float32])
 def test_forms_and_outputs(gq, max_group, out):
