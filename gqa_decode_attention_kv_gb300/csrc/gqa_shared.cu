@@ -116,10 +116,10 @@ struct SharedCfg {
     static constexpr int kVb = kBlock * D * 2;           // one V page
     static constexpr int kVc = kChunkBlocks * kVb;
     static constexpr int kCodeRow = kI4 ? D / 2 : D;     // bytes of a row of codes
-    static constexpr int kCodes = kChunk * kCodeRow;     // a step's codes of K or V, then their scales
-    static constexpr int kRawStage = kCodes + 2 * 128;   // and which of the step's blocks there are
+    static constexpr int kCodes = kHalf * kCodeRow;      // a copy warp's codes of a step, then the step's scales
+    static constexpr int kRawStage = kCodes + kChunk * 2;
     static constexpr int kOffK = kTiles * kQt, kOffV = kOffK + kStages * kKc, kOffRaw = kOffV + kStages * kVc,
-                         kOffBar = (kOffRaw + 2 * kRaw * kRawStage + 127) / 128 * 128;
+                         kOffBar = kOffRaw + 4 * kRaw * kRawStage;
     static constexpr int kOffEx = kOffBar + 1024;        // [tile][half][row]: maxima, then sums
     static constexpr int kOffSc = kOffEx + kCtaRows * 8; // coded: kSlots x (scales of K, of V, {factor, unlift})
     static constexpr int kSlots = 4, kSlotF = 2 * kChunk + 4;
@@ -186,9 +186,7 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
     auto bar_q = [&](int t) { return bar0 + 256 + 8 * t; };
     const uint32_t tslot = bar0 + 272;
     int* scan = reinterpret_cast<int*>(gb + C::kOffBar + 288);      // [128] sums, then the run's group and where it begins
-    // coded: "codes of K or V landed", "widened" (stage G % kRaw)
-    auto bar_full = [&](int v, int c) { return bar0 + 832 + 32 * v + 8 * (c & 3); };
-    auto bar_free = [&](int v, int c) { return bar0 + 896 + 32 * v + 8 * (c & 3); };
+    auto bar_full = [&](int cw, int c) { return bar0 + 832 + 32 * cw + 8 * (c & 3); };   // coded: copy warp cw's codes landed
     float* scales = reinterpret_cast<float*>(gb + C::kOffSc);
     auto par4 = [](int c) { return (uint32_t)(c >> 2) & 1u; };
 
@@ -204,10 +202,7 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
             mbar_init(bar_k(i), kCoded ? 2 : 1);   // K, V stages: the copy, or two warps that widen
             mbar_init(bar_v(i), kCoded ? 2 : 1);
         }
-        for (int i = 0; i < 2 * C::kRaw; ++i) {
-            mbar_init(bar_full(i >> 2, i), 1);
-            mbar_init(bar_free(i >> 2, i), 2);
-        }
+        for (int i = 0; i < 4 * C::kRaw; ++i) mbar_init(bar_full(i >> 2, i), 33);   // the copies, and each lane's scales
         for (int t = 0; t < kTiles; ++t) {
             for (int i = 0; i < kBufs; ++i) {
                 mbar_init(bar_s(t, i), 1);
@@ -353,13 +348,12 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
 
     if (kCoded && loader) {
         // ================================================== copy warps of a coded cache: two for K,
-        // two for V. The first of each also asks for the codes, kRaw steps ahead; both wait
-        // for them, widen 32 of a step's tokens each into the stage that the tensor cores
-        // read, and put their scales where the softmax warps find them. A missing block
-        // lands as zero codes and gets zero scales.
+        // two for V. Each asks for the codes of two of a step's pages, kRaw steps ahead,
+        // widens them into the stage that the tensor cores read, and puts the scales where the
+        // softmax warps find them. A missing block lands as zero codes with zero scales.
         constexpr int kRaw = C::kRaw > 0 ? C::kRaw : 1;
         const int cw = warp - (C::kSoftWarps + 2 * kTiles), v = cw >> 1, part = cw & 1;
-        const uint32_t raw0 = sb + C::kOffRaw + v * kRaw * C::kRawStage;
+        const uint32_t raw0 = sb + C::kOffRaw + cw * kRaw * C::kRawStage;
         const __half* gscale = v ? a.v_scale : a.k_scale;
         const uint64_t once = l2_policy_evict_first(), again = l2_policy_evict_last();
         auto par_raw = [](int c) { return (uint32_t)(c / kRaw) & 1u; };
@@ -368,47 +362,52 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
         bool iss_have = have;
         int iss_c = is.c0, issued = 0;
         const int32_t* table = a.block_tables + (long long)scan[133] * a.max_blocks;
-        auto issue = [&]() -> bool {               // codes of step `issued`; false: a wait ran out
-            if (issued >= kRaw && !__all_sync(kFull, mbar_wait(bar_free(v, issued - kRaw), par_raw(issued - kRaw)))) return false;
+        int win = -(1 << 30), entries = -1;        // lane l: entry win + l of the table
+        auto issue = [&]() {                       // codes and scales of step `issued`
             const uint64_t pol = is.rows > C::kCtaRows ? again : once;
-            const uint32_t dst = raw0 + (issued % kRaw) * C::kRawStage, bar = bar_full(v, issued);
-            const int blk = kChunkBlocks * iss_c + lane;
-            int ph = -1;
-            if (lane < kChunkBlocks && blk < is.span.blocks) {
-                ph = table[blk];
+            const uint32_t dst = raw0 + (issued % kRaw) * C::kRawStage, bar = bar_full(cw, issued);
+            const int blk = kChunkBlocks * iss_c;
+            if (blk - win >= 32 || blk < win) {
+                win = blk;
+                entries = blk + lane < is.span.blocks ? table[blk + lane] : -1;
+            }
+            auto page = [&](int i) {               // i-th page of the step, -1: none
+                int ph = __shfl_sync(kFull, entries, (blk - win + i) & 31);
+                if (blk + i >= is.span.blocks) return -1;
                 if (ph < 0 || ph >= a.num_blocks) {
                     flag_error(a.err, GQA_DEVERR_BLOCK_INDEX);
                     ph = -1;
                 }
-            }
-            const uint32_t there = __ballot_sync(kFull, ph >= 0);
-            if (lane == 0) {
-                asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + C::kCodes + 128), "r"(there) : "memory");
-                mbar_arrive_expect_tx(bar, C::kCodes + 32 * __popc(there));
-            }
+                return ph;
+            };
+            fence_proxy_async_smem();              // the stage's codes have been read
             __syncwarp();
-            if (lane < kChunkBlocks) {
+            if (lane == 0) mbar_arrive_expect_tx(bar, C::kCodes);
+            __syncwarp();
+            const int ph = page(2 * part + (lane & 1)), sp = page(lane / 8);
+            if (lane < 2) {
                 auto coord = [&](int which) { return which == 0 ? 0 : (which == 1 ? is.g : ph); };
-                const uint32_t to = dst + C::kCodes + 32 * lane;
                 tma_load_4d(dst + lane * kBlock * C::kCodeRow, v ? &vmap : &kmap, 0, coord(a.map_perm[0]),
                             coord(a.map_perm[1]), coord(a.map_perm[2]), bar, pol);
-                // a scale row shares L2 lines with the other heads'
-                if (ph >= 0) bulk_load(to, gscale + ((long long)ph * a.K + is.g) * kBlock, 32, bar, again);
             }
+            // lane l: the scales of tokens 2l and 2l + 1 of the step
+            cp_async4(dst + C::kCodes + 4 * lane, gscale + ((long long)max(sp, 0) * a.K + is.g) * kBlock + 2 * (lane & 7),
+                      sp >= 0 ? 4u : 0u);
+            cp_async_arrive(bar);
             ++issued;
             if (++iss_c == is.c1 && (iss_have = step_seg(iw, is))) {
                 iss_c = is.c0;
                 table = a.block_tables + (long long)leader_of(is.span) * a.max_blocks;
+                win = -(1 << 30);
             }
-            return true;
         };
+        while (iss_have && issued < kRaw) issue();
         int G = 0;
         while (have && ok) {
             int lift = kLiftNone;
             for (int c = it.c0; c < it.c1 && ok; ++c, ++G) {
-                while (part == 0 && iss_have && issued < G + kRaw && ok) ok = issue();
                 // the codes are here; the stage's last step has been read by both tiles
-                bool w = ok && mbar_wait(bar_full(v, G), par_raw(G));
+                bool w = mbar_wait(bar_full(cw, G), par_raw(G));
                 if (G >= kS)
 #pragma unroll
                     for (int t = 0; t < kTiles; ++t)
@@ -418,33 +417,38 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
                 const uint32_t src = raw0 + (G % kRaw) * C::kRawStage;
                 const uint32_t to = (v ? sV : sK) + stage(G) * C::kKc;
                 constexpr int kLanes = D / 16;         // lanes of a row, 16 codes each
-#pragma unroll 4
-                for (int i = lane; i < 32 * kLanes; i += 32) {
-                    const int tok = 32 * part + i / kLanes, x = i % kLanes;
-                    uint32_t codes[4], o[8];
-                    if constexpr (C::kI4) {
-                        const uint2 r = lds64(src + tok * C::kCodeRow + 8 * x);
-                        codes[0] = r.x;
-                        codes[1] = r.y;
-                    } else {
-                        const uint4 r = lds128(src + tok * C::kCodeRow + 16 * x);
-                        codes[0] = r.x; codes[1] = r.y; codes[2] = r.z; codes[3] = r.w;
+                constexpr int kBatch = 4;              // loads of codes on their way together
+#pragma unroll
+                for (int i0 = 0; i0 < 32 * kLanes; i0 += 32 * kBatch) {
+                    uint32_t codes[kBatch][4];
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k) {
+                        const int i = i0 + 32 * k + lane, tok = i / kLanes, x = i % kLanes;
+                        if constexpr (C::kI4) {
+                            const uint2 r = lds64(src + tok * C::kCodeRow + 8 * x);
+                            codes[k][0] = r.x; codes[k][1] = r.y;
+                        } else {
+                            const uint4 r = lds128(src + tok * C::kCodeRow + 16 * x);
+                            codes[k][0] = r.x; codes[k][1] = r.y; codes[k][2] = r.z; codes[k][3] = r.w;
+                        }
                     }
-                    widen16<C>(codes, o);
-                    // 16-byte chunks 2x, 2x + 1 of the row, swizzled; the lanes of the second
-                    // half begin with the other one, so that both halves' banks differ
-                    const int h = x >> 2, ck = 2 * (x & 3);
-                    const uint32_t row = v ? to + (tok / kBlock) * C::kVb + h * (kBlock * 128) + (tok % kBlock) * 128
-                                           : to + h * (kChunk * 128) + tok * 128;
-                    const uint4 c0 = make_uint4(o[0], o[1], o[2], o[3]), c1 = make_uint4(o[4], o[5], o[6], o[7]);
-                    const int s7 = tok & 7;
-                    sts128(row + (((ck + h) ^ s7) << 4), h ? c1 : c0);
-                    sts128(row + (((ck + 1 - h) ^ s7) << 4), h ? c0 : c1);
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k) {
+                        const int i = i0 + 32 * k + lane, tok = 32 * part + i / kLanes, x = i % kLanes;
+                        uint32_t o[8];
+                        widen16<C>(codes[k], o);
+                        // 16-byte chunks 2x, 2x + 1 of the row, swizzled; the lanes of the second
+                        // half begin with the other one, so that both halves' banks differ
+                        const int h = x >> 2, ck = 2 * (x & 3);
+                        const uint32_t row = v ? to + (tok / kBlock) * C::kVb + h * (kBlock * 128) + (tok % kBlock) * 128
+                                               : to + h * (kChunk * 128) + tok * 128;
+                        const uint4 c0 = make_uint4(o[0], o[1], o[2], o[3]), c1 = make_uint4(o[4], o[5], o[6], o[7]);
+                        const int s7 = tok & 7;
+                        sts128(row + (((ck + h) ^ s7) << 4), h ? c1 : c0);
+                        sts128(row + (((ck + 1 - h) ^ s7) << 4), h ? c0 : c1);
+                    }
                 }
-                // scales: lane l those of tokens 2l and 2l + 1, zero where a block is missing
-                // (its codes are zeros, its scales are what the stage held)
-                float2 sc = unpack2<false>(lds32(src + C::kCodes + 4 * lane));
-                if (!((lds32(src + C::kCodes + 128) >> (lane / 8)) & 1u)) sc = make_float2(0.f, 0.f);
+                float2 sc = unpack2<false>(lds32(src + C::kCodes + 4 * lane));   // of tokens 2l and 2l + 1
                 float* slot = scales + (G & 3) * C::kSlotF + v * kChunk;
                 if (v) {
                     float most = fmaxf(sc.x, sc.y);
@@ -472,16 +476,17 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(v ? bar_v(G) : bar_k(G));
-                    mbar_arrive(bar_free(v, G));
                 }
+                if (iss_have) issue();             // into the stage just read
             }
             if (ok) have = next_seg(it);
         }
         if (!ok && lane == 0) {
             // let this warp's copies land before the shared memory goes
             flag_error(a.err, GQA_DEVERR_TIMEOUT);
-            for (int c = max(0, issued - kRaw); c < issued; ++c) mbar_wait(bar_full(v, c), par_raw(c), kWaitLimitNs / 4);
+            for (int c = max(0, issued - kRaw); c < issued; ++c) mbar_wait(bar_full(cw, c), par_raw(c), kWaitLimitNs / 4);
         }
+        cp_async_wait_all();
         __syncwarp();
     } else if (loader) {
         // ================================================== copy warps: K, then V
@@ -650,13 +655,14 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
                     }
                     sts128(qt + (c16 >> 3) * (kRows * 128) + rl * 128 + (((c16 & 7) ^ (rl & 7)) << 4), x);
                 }
-                return;
-            }
+            } else {
 #pragma unroll
-            for (int i = 0; i < kSteps; ++i) {
-                const int rl = rl0 + i * kRowsPerStep;
-                cp_async16(qt + (c16 >> 3) * (kRows * 128) + rl * 128 + (((c16 & 7) ^ (rl & 7)) << 4),
-                           static_cast<const uint16_t*>(a.q) + (long long)max(src[i], 0) * D + 8 * c16, src[i] >= 0 ? 16u : 0u);
+                for (int i = 0; i < kSteps; ++i) {
+                    const int rl = rl0 + i * kRowsPerStep;
+                    cp_async16(qt + (c16 >> 3) * (kRows * 128) + rl * 128 + (((c16 & 7) ^ (rl & 7)) << 4),
+                               static_cast<const uint16_t*>(a.q) + (long long)max(src[i], 0) * D + 8 * c16,
+                               src[i] >= 0 ? 16u : 0u);
+                }
             }
         };
         auto q_stored = [&]() {
