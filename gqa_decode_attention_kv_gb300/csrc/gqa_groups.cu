@@ -47,43 +47,87 @@ __device__ __forceinline__ int pages_of(unsigned long long best) {
     return (int)((best >> kRankBits) / (kRankMask - (unsigned)(best & kRankMask) - 1u));
 }
 
-// Row b of B, by one warp: lead[r] is the leader of row r where it is a member of that
-// leader's group, else -1; shared: pages of b's own group.
-__device__ __forceinline__ void place_row(int32_t* plan, int B, const int* lead, int b, int shared, int lane) {
-    const int mine = lead[b];
-    int groups = 0, total = 0, before_groups = 0, before = 0;
-#pragma unroll 4
-    for (int r = lane; r < B; r += 32) {
-        const int w = lead[r];
-        total += w >= 0;
-        groups += w == r;
-        before_groups += w == r && r < mine;
-        before += w >= 0 && (w < mine || (w == mine && r < b));
+// Shared memory of the last step: for every row the leader whose group it is in (-1: none),
+// and for every leader its group's pages, then rows, then where they start, and its number.
+struct Places {
+    int *lead, *pages, *start, *number;
+    __device__ __forceinline__ Places(int* p, int B) : lead(p), pages(p + B), start(p + 2 * B), number(p + 3 * B) {}
+};
+
+// Rows first_row + warp of the plan, from lead and pages (all of the block's threads).
+__device__ __forceinline__ void place_rows(int32_t* plan, int B, const Places& s, int first_row, int2* s_sum) {
+    constexpr int kWarps = kPairThreads / 32;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int r = tid; r < B; r += kPairThreads) s.start[r] = 0;
+    __syncthreads();
+    for (int r = tid; r < B; r += kPairThreads)
+        if (s.lead[r] >= 0) atomicAdd(s.start + s.lead[r], 1);
+    __syncthreads();
+    // exclusive sums over the leaders: each thread some neighbours
+    const int per = (B + kPairThreads - 1) / kPairThreads, lo = min(B, tid * per), hi = min(B, lo + per);
+    int2 mine = make_int2(0, 0);               // rows, groups
+    for (int r = lo; r < hi; ++r) {
+        mine.x += s.start[r];
+        mine.y += s.start[r] > 0;
     }
+    int2 run = mine;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        groups += __shfl_xor_sync(kFull, groups, o);
-        total += __shfl_xor_sync(kFull, total, o);
-        before_groups += __shfl_xor_sync(kFull, before_groups, o);
-        before += __shfl_xor_sync(kFull, before, o);
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(kFull, run.x, o), y = __shfl_up_sync(kFull, run.y, o);
+        if (lane >= o) {
+            run.x += x;
+            run.y += y;
+        }
+    }
+    if (lane == 31) s_sum[warp] = run;
+    __syncthreads();
+    int2 at = make_int2(run.x - mine.x, run.y - mine.y), all = make_int2(0, 0);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        const int2 x = s_sum[w];
+        if (w < warp) {
+            at.x += x.x;
+            at.y += x.y;
+        }
+        all.x += x.x;
+        all.y += x.y;
+    }
+    for (int r = lo; r < hi; ++r) {
+        const int c = s.start[r];
+        s.start[r] = at.x;
+        s.number[r] = at.y;
+        at.x += c;
+        at.y += c > 0;
+    }
+    __syncthreads();
+    const int b = first_row + warp;
+    if (b >= B) return;
+    const int lead = s.lead[b];
+    int rank = 0;                              // members of the group before the row
+    if (lead >= 0) {
+#pragma unroll 4
+        for (int r = lead + lane; r < b; r += 32) rank += s.lead[r] == lead;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) rank += __shfl_xor_sync(kFull, rank, o);
     }
     if (lane != 0) return;
     const GroupsLayout l(B);
+    const int slot = lead >= 0 ? s.start[lead] + rank : -1, number = lead >= 0 ? s.number[lead] : -1;
     if (b == 0) {
-        plan[0] = groups;
-        plan[1] = total;
-        plan[l.start + B] = total;
+        plan[0] = all.y;
+        plan[1] = all.x;
+        plan[l.start + B] = all.x;
     }
-    plan[l.slot + b] = mine >= 0 ? before : -1;
-    plan[l.group + b] = mine >= 0 ? before_groups : -1;
-    if (mine >= 0) plan[l.rows + before] = b;
-    if (mine == b) {
-        plan[l.start + before_groups] = before;
-        plan[l.blocks + before_groups] = shared;
+    plan[l.slot + b] = slot;
+    plan[l.group + b] = number;
+    if (lead >= 0) plan[l.rows + slot] = b;
+    if (lead == b) {
+        plan[l.start + number] = slot;
+        plan[l.blocks + number] = s.pages[b];
     }
-    if (b >= total) plan[l.rows + b] = -1;
-    if (b >= groups) {
-        plan[l.start + b] = total;
+    if (b >= all.x) plan[l.rows + b] = -1;
+    if (b >= all.y) {
+        plan[l.start + b] = all.x;
         plan[l.blocks + b] = 0;
     }
 }
@@ -131,19 +175,19 @@ __global__ void __launch_bounds__(kRunThreads) runs_kernel(const GroupsArgs a) {
     const int32_t* lead = a.block_tables + (long long)leader * a.max_blocks;
     const int most = min(n, full_pages(a, leader));
     int run = most;
-    for (int base = 0; base < most; base += kRunThreads * kRunUnroll) {
+    for (int base = 0; base < most; base += kRunThreads * kRunUnroll * 2) {
         if (tid == 0) s_min = most;
         __syncthreads();
-        int x[kRunUnroll], y[kRunUnroll];
+        int x[2 * kRunUnroll], y[2 * kRunUnroll];
 #pragma unroll
-        for (int i = 0; i < kRunUnroll; ++i) {
+        for (int i = 0; i < 2 * kRunUnroll; ++i) {
             const int j = base + i * kRunThreads + tid;
             x[i] = j < most ? mine[j] : 0;
             y[i] = j < most ? lead[j] : 0;
         }
         int at = most;
 #pragma unroll
-        for (int i = kRunUnroll - 1; i >= 0; --i)
+        for (int i = 2 * kRunUnroll - 1; i >= 0; --i)
             if (x[i] != y[i] || x[i] < 0) at = base + i * kRunThreads + tid;
         if (at < most) atomicMin(&s_min, at);
         __syncthreads();
@@ -176,26 +220,28 @@ __global__ void __launch_bounds__(kPairThreads) counts_kernel(const GroupsArgs a
 }
 
 __global__ void __launch_bounds__(kPairThreads) places_kernel(const GroupsArgs a) {
-    extern __shared__ int s_lead[];            // [B], then the leaders' pages [B]
-    int* s_pages = s_lead + a.B;
-    const int b = blockIdx.x * kPairRows + (threadIdx.x >> 5);
+    extern __shared__ int s_places[];          // [4][B]
+    __shared__ int2 s_sum[kPairThreads / 32];
+    const Places s(s_places, a.B);
     launch_dependents();
     grid_dependency_wait();
-    for (int r = threadIdx.x; r < a.B; r += kPairThreads) s_pages[r] = pages_of(a.best[r]);
+    for (int r = threadIdx.x; r < a.B; r += kPairThreads) s.pages[r] = pages_of(a.best[r]);
     __syncthreads();
     for (int r = threadIdx.x; r < a.B; r += kPairThreads) {
         const int2 o = a.run[r];
-        s_lead[r] = s_pages[o.x] > 0 && o.y >= s_pages[o.x] ? o.x : -1;
+        s.lead[r] = s.pages[o.x] > 0 && o.y >= s.pages[o.x] ? o.x : -1;
     }
     __syncthreads();
-    if (b < a.B) place_row(a.plan, a.B, s_lead, b, s_pages[b], threadIdx.x & 31);
+    place_rows(a.plan, a.B, s, blockIdx.x * kPairRows, s_sum);
 }
 
 // All three steps for up to kSmallRows rows.
 __global__ void __cluster_dims__(kSmallCtas) __launch_bounds__(kPairThreads) small_kernel(const GroupsArgs a) {
     __shared__ int2 s_run[kSmallRows];
     __shared__ unsigned long long s_best[kSmallRows];
-    __shared__ int s_lead[kSmallRows];
+    __shared__ int s_places[4 * kSmallRows];
+    __shared__ int2 s_sum[kPairThreads / 32];
+    const Places s(s_places, a.B);
     const int tid = threadIdx.x, lane = tid & 31, b = blockIdx.x * kPairRows + (tid >> 5);
     launch_dependents();
     grid_dependency_wait();
@@ -261,10 +307,11 @@ __global__ void __cluster_dims__(kSmallCtas) __launch_bounds__(kPairThreads) sma
     for (int r = tid; r < a.B; r += kPairThreads) {
         const int2 o = s_run[r];
         const int pages = pages_of(s_best[o.x]);
-        s_lead[r] = pages > 0 && o.y >= pages ? o.x : -1;
+        s.pages[r] = pages_of(s_best[r]);
+        s.lead[r] = pages > 0 && o.y >= pages ? o.x : -1;
     }
     __syncthreads();
-    if (b < a.B) place_row(a.plan, a.B, s_lead, b, pages_of(s_best[b]), lane);
+    place_rows(a.plan, a.B, s, blockIdx.x * kPairRows, s_sum);
 }
 
 }  // namespace
@@ -305,11 +352,13 @@ cudaError_t launch_pages_groups(const int32_t* block_tables, int max_blocks, con
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3((batch + kPairRows - 1) / kPairRows);
     cfg.blockDim = dim3(kPairThreads);
-    cfg.dynamicSmemBytes = batch * sizeof(int2);               // both kernels: 8 bytes a row, 64 KB at most
-    if (ctas_per_sm(reinterpret_cast<const void*>(&counts_kernel), kPairThreads, cfg.dynamicSmemBytes) < 1 ||
-        ctas_per_sm(reinterpret_cast<const void*>(&places_kernel), kPairThreads, cfg.dynamicSmemBytes) < 1)
+    const int run_bytes = batch * (int)sizeof(int2), places_bytes = 4 * batch * (int)sizeof(int);   // 64 and 128 KB at most
+    if (ctas_per_sm(reinterpret_cast<const void*>(&counts_kernel), kPairThreads, run_bytes) < 1 ||
+        ctas_per_sm(reinterpret_cast<const void*>(&places_kernel), kPairThreads, places_bytes) < 1)
         return cudaErrorInvalidConfiguration;
+    cfg.dynamicSmemBytes = run_bytes;
     if ((e = cudaLaunchKernelEx(&cfg, counts_kernel, a)) != cudaSuccess) return e;
+    cfg.dynamicSmemBytes = places_bytes;
     return cudaLaunchKernelEx(&cfg, places_kernel, a);
 }
 

@@ -137,62 +137,74 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const ReadArgs a) {
     const int tiles = pages * 2 * a.K;         // (page, K or V, kv-head), kv-heads adjacent
     const int lane = threadIdx.x & 31;
     const int e = lane % kLanes * kElems, slot0 = lane / kLanes;
-    for (int tile = threadIdx.x >> 5; tile < tiles; tile += kReadThreads / 32) {
+    constexpr int kWarps = kReadThreads / 32;
+    // tiles of a warp whose loads are on their way together: codes are few bytes a row
+    constexpr int kTogether = kBits <= 8 ? 2 : 1;
+    struct Tile {
+        Raw<kKind> raw[kSteps];
+        uint4 kc;                              // channel scales of this lane's elements
+        float scale;                           // lane t: token t's
+        int lo, hi;                            // slots [lo, hi) are asked for
+        bool is_v;
+        long long out0;                        // element of slot slot0's row
+    };
+    auto fetch = [&](int tile, Tile& x) {
+        x.lo = x.hi = 0;
+        if (tile >= tiles) return;
         const int side = tile / a.K, g = tile - side * a.K;
-        const bool is_v = side & 1;
+        x.is_v = side & 1;
         const long long page = page0 + (side >> 1);
-        // slots [lo, hi) of the page are asked for
-        const int lo = (int)max(0ll, pos0 - page * kBlock), hi = (int)min((long long)kBlock, end - page * kBlock);
         if (page < 0 || page >= a.max_blocks) {
             if (g == 0 && lane == 0) flag_error(a.err, GQA_DEVERR_POSITION);
-            continue;
+            return;
         }
         const int ph = a.block_tables[(long long)b * a.max_blocks + page];
         if (ph < 0 || ph >= a.num_blocks) {
             if (g == 0 && lane == 0) flag_error(a.err, GQA_DEVERR_BLOCK_INDEX);
-            continue;
+            return;
         }
+        x.lo = (int)max(0ll, pos0 - page * kBlock);
+        x.hi = (int)min((long long)kBlock, end - page * kBlock);
         const long long at = ph * a.sb + g * a.sh + slot0 * a.st + e;
-        const uint8_t* src = static_cast<const uint8_t*>(is_v ? a.v : a.k) + at * kBits / 8;
+        const uint8_t* src = static_cast<const uint8_t*>(x.is_v ? a.v : a.k) + at * kBits / 8;
         const long long step = kRowsPerStep * a.st * kBits / 8;
-        Raw<kKind> raw[kSteps];
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
             const int slot = slot0 + i * kRowsPerStep;
-            if (slot >= lo && slot < hi) raw[i].load(src + i * step);
+            if (slot >= x.lo && slot < x.hi) x.raw[i].load(src + i * step);
         }
-        const bool channels = kKind == kReadI4Kc && !is_v;            // scales by channel, else by token
-        uint4 kc = make_uint4(0u, 0u, 0u, 0u);
-        float scale = 0.f;                     // lane t: token t's
         if constexpr (kCoded) {
             const long long head = (long long)ph * a.K + g;
-            if (channels) kc = *reinterpret_cast<const uint4*>(a.k_scale + head * D + e);
-            else if (lane < kBlock) scale = __half2float((is_v ? a.v_scale : a.k_scale)[head * kBlock + lane]);
+            if (kKind == kReadI4Kc && !x.is_v) x.kc = *reinterpret_cast<const uint4*>(a.k_scale + head * D + e);
+            else if (lane < kBlock) x.scale = __half2float((x.is_v ? a.v_scale : a.k_scale)[head * kBlock + lane]);
         }
         // the row of slot s is row0 + 16 page + s - pos0
-        const long long out0 = ((row0 + page * kBlock - pos0 + slot0) * a.K + g) * D + e;
-        void* out = is_v ? a.v_out : a.k_out;
+        x.out0 = ((row0 + page * kBlock - pos0 + slot0) * a.K + g) * D + e;
+    };
+    auto write = [&](const Tile& x) {
+        if (x.hi <= x.lo) return;              // uniform
+        void* out = x.is_v ? a.v_out : a.k_out;
         auto rows = [&](auto&& scaled) {
 #pragma unroll
             for (int i = 0; i < kSteps; ++i) {
                 const int slot = slot0 + i * kRowsPerStep;
                 float f[kElems];
-                raw[i].values(f);
+                x.raw[i].values(f);
                 scaled(f, i);
-                const Out<kKind, kOut> o(raw[i], f);
-                if (slot >= lo && slot < hi) o.store(out, out0 + (long long)i * kRowsPerStep * a.K * D);
+                const Out<kKind, kOut> o(x.raw[i], f);
+                if (slot >= x.lo && slot < x.hi) o.store(out, x.out0 + (long long)i * kRowsPerStep * a.K * D);
             }
         };
         if constexpr (!kCoded) {
             rows([](float (&)[kElems], int) {});
-        } else if (channels) {
+        } else if (kKind == kReadI4Kc && !x.is_v) {
             float c[kElems];
-            const uint32_t w[4] = {kc.x, kc.y, kc.z, kc.w};
+            const uint32_t w[4] = {x.kc.x, x.kc.y, x.kc.z, x.kc.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float2 x = unpack2<false>(w[j]);
-                c[2 * j] = x.x;
-                c[2 * j + 1] = x.y;
+                const float2 y = unpack2<false>(w[j]);
+                c[2 * j] = y.x;
+                c[2 * j + 1] = y.y;
             }
             rows([&](float (&f)[kElems], int) {
 #pragma unroll
@@ -200,11 +212,18 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const ReadArgs a) {
             });
         } else {
             rows([&](float (&f)[kElems], int i) {
-                const float x = __shfl_sync(kFull, scale, slot0 + i * kRowsPerStep);
+                const float y = __shfl_sync(kFull, x.scale, slot0 + i * kRowsPerStep);
 #pragma unroll
-                for (int j = 0; j < kElems; ++j) f[j] *= x;
+                for (int j = 0; j < kElems; ++j) f[j] *= y;
             });
         }
+    };
+    for (int tile = threadIdx.x >> 5; tile < tiles; tile += kWarps * kTogether) {
+        Tile x[kTogether];
+#pragma unroll
+        for (int i = 0; i < kTogether; ++i) fetch(tile + i * kWarps, x[i]);
+#pragma unroll
+        for (int i = 0; i < kTogether; ++i) write(x[i]);
     }
 }
 
