@@ -479,12 +479,18 @@ class PrefixGroups:
     int32 arrays, views of ``plan``. Group i holds ``rows[start[i]:start[i+1]]`` and shares
     ``blocks[i]`` pages; ``slot`` and ``group`` of a row are -1 where it shares nothing;
     ``count`` holds the groups and the rows in groups."""
-    __slots__ = ("plan", "batch", "count", "start", "blocks", "rows", "slot", "group")
+    _PARTS = ("count", "start", "blocks", "rows", "slot", "group")
 
     def __init__(self, plan: torch.Tensor, batch: int):
         self.plan, self.batch = plan, batch
-        self.count, self.start, self.blocks, self.rows, self.slot, self.group = plan.split_with_sizes(
-            (2, batch + 1, batch, batch, batch, batch, plan.shape[0] - 3 - 5 * batch))[:6]
+
+    def __getattr__(self, name):               # the views, made when one is first asked for (10 us)
+        if name not in self._PARTS:
+            raise AttributeError(name)
+        B = self.batch
+        parts = self.plan.split_with_sizes((2, B + 1, B, B, B, B, self.plan.shape[0] - 3 - 5 * B))
+        self.__dict__.update(zip(self._PARTS, parts))
+        return self.__dict__[name]
 
 
 @functools.lru_cache(maxsize=256)
