@@ -362,29 +362,26 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
         bool iss_have = have;
         int iss_c = is.c0, issued = 0;
         const int32_t* table = a.block_tables + (long long)scan[133] * a.max_blocks;
-        int win = -(1 << 30), entries = -1;        // lane l: entry win + l of the table
+        int win = -(1 << 30), entries = -1;        // lane l: the page of entry win + l, -1: none
         auto issue = [&]() {                       // codes and scales of step `issued`
             const uint64_t pol = is.rows > C::kCtaRows ? again : once;
             const uint32_t dst = raw0 + (issued % kRaw) * C::kRawStage, bar = bar_full(cw, issued);
             const int blk = kChunkBlocks * iss_c;
             if (blk - win >= 32 || blk < win) {
                 win = blk;
-                entries = blk + lane < is.span.blocks ? table[blk + lane] : -1;
-            }
-            auto page = [&](int i) {               // i-th page of the step, -1: none
-                int ph = __shfl_sync(kFull, entries, (blk - win + i) & 31);
-                if (blk + i >= is.span.blocks) return -1;
-                if (ph < 0 || ph >= a.num_blocks) {
-                    flag_error(a.err, GQA_DEVERR_BLOCK_INDEX);
-                    ph = -1;
+                entries = -1;
+                if (blk + lane < is.span.blocks) {
+                    const int p = table[blk + lane];
+                    if (p < 0 || p >= a.num_blocks) flag_error(a.err, GQA_DEVERR_BLOCK_INDEX);
+                    else entries = p;
                 }
-                return ph;
-            };
+            }
+            const int ph = __shfl_sync(kFull, entries, (blk - win + 2 * part + (lane & 1)) & 31);
+            const int sp = __shfl_sync(kFull, entries, (blk - win + lane / 8) & 31);
             fence_proxy_async_smem();              // the stage's codes have been read
             __syncwarp();
             if (lane == 0) mbar_arrive_expect_tx(bar, C::kCodes);
             __syncwarp();
-            const int ph = page(2 * part + (lane & 1)), sp = page(lane / 8);
             if (lane < 2) {
                 auto coord = [&](int which) { return which == 0 ? 0 : (which == 1 ? is.g : ph); };
                 tma_load_4d(dst + lane * kBlock * C::kCodeRow, v ? &vmap : &kmap, 0, coord(a.map_perm[0]),
@@ -705,10 +702,14 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
 #pragma unroll
                         for (int q = 0; q < 16; q += 4) {
                             const float4 ks = *reinterpret_cast<const float4*>(slot + 16 * u + q);
-                            r[u][q] = __float_as_uint(__uint_as_float(r[u][q]) * ks.x);
-                            r[u][q + 1] = __float_as_uint(__uint_as_float(r[u][q + 1]) * ks.y);
-                            r[u][q + 2] = __float_as_uint(__uint_as_float(r[u][q + 2]) * ks.z);
-                            r[u][q + 3] = __float_as_uint(__uint_as_float(r[u][q + 3]) * ks.w);
+                            const float2 x = f2_split(f2_mul(
+                                f2_make(__uint_as_float(r[u][q]), __uint_as_float(r[u][q + 1])), f2_make(ks.x, ks.y)));
+                            const float2 y = f2_split(f2_mul(
+                                f2_make(__uint_as_float(r[u][q + 2]), __uint_as_float(r[u][q + 3])), f2_make(ks.z, ks.w)));
+                            r[u][q] = __float_as_uint(x.x);
+                            r[u][q + 1] = __float_as_uint(x.y);
+                            r[u][q + 2] = __float_as_uint(y.x);
+                            r[u][q + 3] = __float_as_uint(y.y);
                         }
                     scl = 1.f;
                     ok = __all_sync(kFull, mbar_wait(bar_v(G), par_st(G)));      // V's are there as well
@@ -777,6 +778,7 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
 #pragma unroll
                 for (int u = 0; u < kHalf / 16; ++u) {
                     uint32_t w16[16];
+                    float4 vs = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const float2 d = f2_split(
@@ -785,8 +787,8 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
                         const uint64_t xy = f2_make(x, y);
                         ps2[e & 1] = f2_add(ps2[e & 1], xy);
                         if constexpr (kCoded) {
-                            const float2 vs = *reinterpret_cast<const float2*>(slot + kChunk + 16 * u + 2 * e);
-                            const uint64_t w2 = f2_mul(xy, f2_make(vs.x, vs.y));
+                            if (e % 2 == 0) vs = *reinterpret_cast<const float4*>(slot + kChunk + 16 * u + 2 * e);
+                            const uint64_t w2 = f2_mul(xy, e % 2 ? f2_make(vs.z, vs.w) : f2_make(vs.x, vs.y));
                             const float2 w = f2_split(w2);
                             split2<false>(w.x, w.y, w2, w16[e], w16[8 + e]);
                         } else {
