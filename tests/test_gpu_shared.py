@@ -63,6 +63,10 @@ SHAPES = [
     (1, 16, 64, 1, [(9, [150] * 9)], [3]),                       # 144 rows
     (2, 2, 128, 16, [(6, [112, 130])], [40]),
     (3, 5, 128, 1, [(7, [113, 120]), (7, [115, 200, 131])], []),
+    (1, 64, 128, 1, [(11, [177, 190, 201])], [20]),              # 64 query rows a kv-head
+    (1, 12, 64, 5, [(70, [1130, 1125, 1200, 1140])], []),        # 60, over two tiles of rows
+    (8, 1, 128, 1, [(1, [17] * 30)], [1] * 3),                   # no groups of heads
+    (2, 2, 64, 1, [(2, [33, 34])] * 20, [9]),                    # many small groups
 ]
 
 
@@ -172,6 +176,51 @@ def test_axis_orders(gq, order):
     got, want, err, values, _ = run(gq, "f16", 4, 2, 128, 1, [(10, [161, 170, 200])], [30], order=order)
     assert err == 0
     check(got, want, values)
+
+
+@pytest.mark.parametrize("kind", ["int8", "int4"])
+def test_axis_orders_of_coded_caches(gq, kind):
+    """Codes as [page][slot][head][row]: the scales stay [page][head][slot]."""
+    bt = shared.batch([(10, [161, 170, 200])], [30], 3)
+    cache, values = shared.pool(kind, bt.pages, 4, 128, 4, gq)
+    wide = 64 if kind == "int4" else 128
+    turned = [t.permute(0, 2, 1, 3).contiguous() for t in (cache.k, cache.v)]
+    other = gq.PagedKVCache(*turned, bt.pages, 4, 128, 4 * 16 * 128, 128, 4 * 128, cache.k_scale, cache.v_scale,
+                            cache.dtype_code)
+    assert turned[0].shape[-1] == wide
+    q = torch.randn(4, 1, 8, 128, generator=torch.Generator().manual_seed(5)).bfloat16()
+    table, lens = torch.from_numpy(bt.table).cuda(), torch.from_numpy(bt.lens).cuda()
+    got = gq.gqa_decode_shared(other, q[:, 0].contiguous().cuda(), table, lens, 0.09, gq.kv_pages_groups(table, lens))
+    want = shared.attend(q.double().numpy(), values, bt.table, bt.lens, 0.09)
+    check(got.view(q.shape).double().cpu().numpy(), want, values)
+
+
+def test_more_groups_than_threads(gq):
+    """A plan of 900 groups: the kernels scan it in rounds."""
+    groups = [(1 + i % 3, [16 * (1 + i % 3) + 1 + i % 5, 16 * (1 + i % 3) + 2]) for i in range(900)]
+    got, want, err, values, plan = run(gq, "bf16", 1, 2, 64, 1, groups, [3] * 7, max_group=2)
+    assert err == 0 and plan.count.tolist() == [900, 1800]
+    check(got, want, values)
+
+
+def test_replays_of_a_growing_batch(gq):
+    """One captured call serves later lengths: the division of the work is the device's."""
+    K, G, d, B = 2, 4, 128, 5
+    bt = shared.batch([(20, [321 + 40] * B)], [], 29)
+    cache, values = shared.pool("f16", bt.pages, K, d, 30, gq)
+    q = torch.randn(B, 1, K * G, d, generator=torch.Generator().manual_seed(31)).half()
+    table, lens = torch.from_numpy(bt.table).cuda(), torch.from_numpy(bt.lens).cuda()
+    plan, dq = gq.kv_pages_groups(table, lens), q[:, 0].contiguous().cuda()
+    gq.gqa_decode_shared(cache, dq, table, lens, 0.1, plan)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = gq.gqa_decode_shared(cache, dq, table, lens, 0.1, plan)
+    for now in ([321] * B, [361, 0, 17, 320, 340], [0] * B, [361] * B):
+        lens.copy_(torch.tensor(now, dtype=torch.int32))
+        g.replay()
+        want = shared.attend(q.double().numpy(), values, bt.table, np.array(now), 0.1)
+        check(out.view(q.shape).double().cpu().numpy(), want, values)
 
 
 def test_short_and_empty_rows_of_a_group(gq):
@@ -289,7 +338,7 @@ def test_streams_and_graphs(gq):
 
 
 def test_bad_pages_are_flagged(gq):
-    """A shared entry that is no page: flagged, its tokens are not seen, nothing else changes."""
+    """A shared entry that is no page: flagged; rows outside the group are as they were."""
     bt = shared.batch([(9, [150, 160])], [40], 14)
     cache, values = shared.pool("bf16", bt.pages, 2, 128, 15, gq)
     q = torch.randn(3, 1, 8, 128, generator=torch.Generator().manual_seed(16)).bfloat16()
