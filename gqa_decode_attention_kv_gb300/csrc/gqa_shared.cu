@@ -376,16 +376,17 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
                     else entries = p;
                 }
             }
-            const int ph = __shfl_sync(kFull, entries, (blk - win + 2 * part + (lane & 1)) & 31);
             const int sp = __shfl_sync(kFull, entries, (blk - win + lane / 8) & 31);
             fence_proxy_async_smem();              // the stage's codes have been read
             __syncwarp();
             if (lane == 0) mbar_arrive_expect_tx(bar, C::kCodes);
             __syncwarp();
-            if (lane < 2) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int ph = __shfl_sync(kFull, entries, blk - win + 2 * part + i);
                 auto coord = [&](int which) { return which == 0 ? 0 : (which == 1 ? is.g : ph); };
-                tma_load_4d(dst + lane * kBlock * C::kCodeRow, v ? &vmap : &kmap, 0, coord(a.map_perm[0]),
-                            coord(a.map_perm[1]), coord(a.map_perm[2]), bar, pol);
+                tma_load_4d_elect(dst + i * kBlock * C::kCodeRow, v ? &vmap : &kmap, 0, coord(a.map_perm[0]),
+                                  coord(a.map_perm[1]), coord(a.map_perm[2]), bar, pol);
             }
             // lane l: the scales of tokens 2l and 2l + 1 of the step
             cp_async4(dst + C::kCodes + 4 * lane, gscale + ((long long)max(sp, 0) * a.K + is.g) * kBlock + 2 * (lane & 7),
@@ -404,11 +405,11 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
             int lift = kLiftNone;
             for (int c = it.c0; c < it.c1 && ok; ++c, ++G) {
                 // the codes are here; the stage's last step has been read by both tiles
-                bool w = mbar_wait(bar_full(cw, G), par_raw(G));
+                bool w = mbar_wait_tries(bar_full(cw, G), par_raw(G));
                 if (G >= kS)
 #pragma unroll
                     for (int t = 0; t < kTiles; ++t)
-                        w = w && mbar_wait(v ? bar_o(t, G - kS) : bar_s(t, G - kS), par4(G - kS));
+                        w = w && mbar_wait_tries(v ? bar_o(t, G - kS) : bar_s(t, G - kS), par4(G - kS));
                 ok = __all_sync(kFull, w);
                 if (!ok) break;
                 const uint32_t src = raw0 + (G % kRaw) * C::kRawStage;
@@ -481,7 +482,7 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
         if (!ok && lane == 0) {
             // let this warp's copies land before the shared memory goes
             flag_error(a.err, GQA_DEVERR_TIMEOUT);
-            for (int c = max(0, issued - kRaw); c < issued; ++c) mbar_wait(bar_full(cw, c), par_raw(c), kWaitLimitNs / 4);
+            for (int c = max(0, issued - kRaw); c < issued; ++c) mbar_wait_tries(bar_full(cw, c), par_raw(c), kWaitTries / 4);
         }
         cp_async_wait_all();
         __syncwarp();
@@ -515,30 +516,33 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
                     bool w = true;
 #pragma unroll
                     for (int t = 0; t < kTiles; ++t)
-                        w = w && mbar_wait(k_warp ? bar_s(t, G - kS) : bar_o(t, G - kS), par4(G - kS));
+                        w = w && mbar_wait_tries(k_warp ? bar_s(t, G - kS) : bar_o(t, G - kS), par4(G - kS));
                     ok = __all_sync(kFull, w);
                     if (!ok) break;
                 }
                 const uint32_t bar = k_warp ? bar_k(G) : bar_v(G);
                 if (lane == 0) mbar_arrive_expect_tx(bar, C::kVc);
                 __syncwarp();
-                // K: one lane per (block, 64-element half) box; V: one box per page
-                // (head_dim 128: the page map lands it as [half][slot][128 B])
-                const int boxes = k_warp ? C::kHalves : 1;
-                const int q = lane / boxes, h = lane - q * boxes;
-                const int pq = __shfl_sync(kFull, win_phys, (v0 - win_base + q) & 31);
-                auto coord = [&](int which) { return which == 0 ? 0 : (which == 1 ? it.g : pq); };
-                const int y = coord(a.map_perm[0]), z = coord(a.map_perm[1]), w = coord(a.map_perm[2]);
-                if (q < kChunkBlocks) {
+                // K: a box per (block, 64-element half); V: one per page (head_dim 128: the page
+                // map lands it as [half][slot][128 B]). One lane issues them with operands that
+                // are the warp's: a lane per box takes 180 cycles each, and the 8 of K then
+                // are what a step waits for.
+#pragma unroll
+                for (int q = 0; q < kChunkBlocks; ++q) {
+                    const int pq = __shfl_sync(kFull, win_phys, v0 - win_base + q);
+                    auto coord = [&](int which) { return which == 0 ? 0 : (which == 1 ? it.g : pq); };
+                    const int y = coord(a.map_perm[0]), z = coord(a.map_perm[1]), w = coord(a.map_perm[2]);
                     if (k_warp) {
-                        tma_load_4d(sK + stage(G) * C::kKc + h * (kChunk * 128) + q * (kBlock * 128), &kmap, h * 64, y, z,
-                                    w, bar, pol);
+#pragma unroll
+                        for (int h = 0; h < C::kHalves; ++h)
+                            tma_load_4d_elect(sK + stage(G) * C::kKc + h * (kChunk * 128) + q * (kBlock * 128), &kmap, h * 64,
+                                              y, z, w, bar, pol);
                     } else {
                         const uint32_t dst = sV + stage(G) * C::kVc + q * C::kVb;
                         if constexpr (C::kHalves == 2)
-                            tma_load_5d(dst, &vmap, 0, 0, 0, coord(a.page_perm[0]), coord(a.page_perm[1]), bar, pol);
+                            tma_load_5d_elect(dst, &vmap, 0, 0, 0, coord(a.page_perm[0]), coord(a.page_perm[1]), bar, pol);
                         else
-                            tma_load_4d(dst, &vmap, 0, y, z, w, bar, pol);
+                            tma_load_4d_elect(dst, &vmap, 0, y, z, w, bar, pol);
                     }
                 }
                 ++issued;
@@ -549,7 +553,7 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
             // let this CTA's copies land before the shared memory goes
             flag_error(a.err, GQA_DEVERR_TIMEOUT);
             for (int c = max(0, issued - kS); c < issued; ++c)
-                mbar_wait(k_warp ? bar_k(c) : bar_v(c), par_st(c), kWaitLimitNs / 4);
+                mbar_wait_tries(k_warp ? bar_k(c) : bar_v(c), par_st(c), kWaitTries / 4);
         }
     } else if (mma_warp) {
         // ================================================== MMA warps: two per tile, one for S and
@@ -559,7 +563,7 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
         // registers, 144 cycles a P.V product for 38.
         const int t = (warp - C::kSoftWarps) >> 1;
         const bool s_warp = ((warp - C::kSoftWarps) & 1) == 0;
-        auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(kFull, mbar_wait(bar, parity)); };
+        auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(kFull, mbar_wait_tries(bar, parity)); };
         int G = 0, qi = 0;                         // commits issued, segments
         while (have && ok) {
             // a tile past the group's rows takes part in the barriers alone
@@ -608,7 +612,7 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
             // let this warp's MMAs land before the tensor memory goes, each barrier's events
             // in order
             if (lane == 0) flag_error(a.err, GQA_DEVERR_TIMEOUT);
-            for (int k = max(0, G - kBufs); k < G; ++k) mbar_wait(s_warp ? bar_s(t, k) : bar_o(t, k), par4(k), kWaitLimitNs / 4);
+            for (int k = max(0, G - kBufs); k < G; ++k) mbar_wait_tries(s_warp ? bar_s(t, k) : bar_o(t, k), par4(k), kWaitTries / 4);
         }
         __syncwarp();
     } else {
@@ -680,7 +684,7 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
             float unlift = 1.f;                // coded: what takes the lift out of O
             for (int c = 0; c < n; ++c) {
                 const int G = gc + c;
-                ok = __all_sync(kFull, mbar_wait(bar_s(tt, G), par4(G)));   // S_t(G) done
+                ok = __all_sync(kFull, mbar_wait_tries(bar_s(tt, G), par4(G)));   // S_t(G) done
                 if (!ok) break;
                 tc_fence_after();
                 if (!tile_live) {
@@ -712,7 +716,7 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
                             r[u][q + 3] = __float_as_uint(y.y);
                         }
                     scl = 1.f;
-                    ok = __all_sync(kFull, mbar_wait(bar_v(G), par_st(G)));      // V's are there as well
+                    ok = __all_sync(kFull, mbar_wait_tries(bar_v(G), par_st(G)));      // V's are there as well
                     if (!ok) break;
                     factor = slot[2 * kChunk - kHalf * hf];
                     unlift = slot[2 * kChunk + 1 - kHalf * hf];
@@ -757,7 +761,7 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
                     l *= alpha;
                     if (c > 0 && __any_sync(kFull, (resc && old_live) || factor != 1.f)) {   // O holds earlier steps: scale it
                         // once P_t(G-1).V(G-1) has landed in it, this half its columns
-                        ok = __all_sync(kFull, mbar_wait(bar_o(tt, G - 1), par4(G - 1)));
+                        ok = __all_sync(kFull, mbar_wait_tries(bar_o(tt, G - 1), par4(G - 1)));
                         tc_fence_after();
                         const float f = (resc && old_live ? alpha : 1.f) * factor;
 #pragma unroll 1
@@ -819,7 +823,7 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
             // ---- wait for this tile's last P.V, then leave the row's state: a problem's
             // first piece by its row, a continued one (only a CTA's first can be) by CTA
             const int G_last = gc + n - 1;
-            ok = __all_sync(kFull, mbar_wait(bar_o(tt, G_last), par4(G_last)));
+            ok = __all_sync(kFull, mbar_wait_tries(bar_o(tt, G_last), par4(G_last)));
             if (!ok) break;
             tc_fence_after();
             if (tile_live) {
