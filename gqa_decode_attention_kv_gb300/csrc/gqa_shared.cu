@@ -1087,20 +1087,24 @@ PrefixWs prefix_ws(long long batch, long long rows, int d, int sms) {
     return w;
 }
 
-// The times behind the GPU's division, measured in the middle of long prefixes and tails of
-// 16-bit caches: a step of 256 rows takes an SM 1.05 us (of 128 rows in two CTAs 0.6), a
-// (block, kv-head) of the rows' own 40 bytes a nanosecond, with more than 8 query rows 25.
+// The times behind the GPU's division, measured in the middle of long prefixes and tails: a
+// step of 256 rows takes an SM 0.95 us (coded 1.5; 128 rows in two CTAs 0.6), a (block,
+// kv-head) of the rows' own 0.19 us for a 16-bit cache of 128 dims, 0.16 with 8-bit codes,
+// 0.15 with 4-bit ones, 0.9 with codes on the CUDA cores (head_dim 64); more with more than 8
+// query rows. They pick how the SMs are dealt out and change no result.
 SplitModel split_of(const DecodeLaunch& L, const Form& f, int sms) {
     const gqa_kv_cache_t& c = *L.cache;
+    const int GT = L.num_heads / c.num_kv_heads * L.tokens_per_seq;
+    const bool coded = dtype_coded(c.dtype), wide = c.head_dim == 128;
     SplitModel m;
     m.sms = sms;
     m.ctas_per_sm = f.ctas_per_sm;
     m.cta_rows = f.rows;
     m.min_steps = 2;
-    m.step_us = (f.rows > kRows ? 1.05f : 1.2f) * (c.head_dim == 128 ? 1.f : 0.7f);
+    m.step_us = (coded ? 1.5f : f.rows > kRows ? 0.95f : 1.2f) * (wide ? 1.f : 0.7f);
     m.prefix_us = 9.f;
-    const int GT = L.num_heads / c.num_kv_heads * L.tokens_per_seq;
-    m.unit_us = 2.f * kBlock * dtype_bytes(c.dtype, c.head_dim) / 40000.f * (GT > 8 ? 1.6f : 1.f);
+    m.unit_us = coded ? (!wide ? 0.9f : dtype_bits(c.dtype) == 8 ? 0.16f : 0.15f) : wide ? 0.19f : 0.1f;
+    if (GT > 8) m.unit_us *= coded ? 2.f : 1.6f;
     m.tail_us = 4.f;
     return m;
 }
