@@ -106,7 +106,7 @@ __device__ __forceinline__ int prefix_sms(const SplitModel& m, int steps, int un
     for (int step = (cap + 31) / 32;; step = (step + 31) / 32) {
         const int x = min(lo + (lane + 1) * step, cap);
         const int first = __ffs(__ballot_sync(kFull, ends_first(x))) - 1;    // some lane's x is the cap, or past the answer
-        if (step == 1) return min(lo + first + 1, cap);
+        if (step == 1) return min((lo + first + 2) & ~1, cap);               // pairs of SMs: see the launch
         lo += first * step;
     }
 }
