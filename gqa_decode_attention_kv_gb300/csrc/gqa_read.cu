@@ -130,6 +130,7 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const ReadArgs a) {
         if (part == 0 && threadIdx.x == 0) flag_error(a.err, GQA_DEVERR_POSITION);
         return;
     }
+    if (n == 0) return;                        // wherever it stands
     const long long pos0 = a.positions[b], end = pos0 + n;
     // pages (pos0 >> 4) .. (end - 1) >> 4 hold the rows; this CTA's are page0 ..
     const long long page0 = (pos0 >> 4) + (long long)part * a.pages_per_cta;

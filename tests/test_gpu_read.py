@@ -123,6 +123,19 @@ def test_out_of_range(gq):
     assert err == gq.GQA_DEVERR_POSITION and (got == 7).all()
 
 
+def test_sequences_of_no_rows_stand_anywhere(gq):
+    """No row is asked for, so neither a position nor a table entry of theirs is at fault."""
+    cache, values = shared.pool("bf16", 4, 2, 64, 3, gq)
+    table = torch.tensor([[-1, -1], [2, 1], [9, 9], [0, -1]], dtype=torch.int32, device="cuda")
+    pos = torch.tensor([-3, 5, 7, 50], dtype=torch.int32, device="cuda")
+    start = torch.tensor([0, 0, 20, 20, 20], dtype=torch.int32, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    k, v = gq.kv_read(cache, table, pos, start, max_tokens=24, total_tokens=20, err=err)
+    assert int(err) == 0
+    assert (k.double().cpu().numpy() == np.concatenate([values[0][2], values[0][1]])[5:25]).all()
+    assert (v.double().cpu().numpy() == np.concatenate([values[1][2], values[1][1]])[5:25]).all()
+
+
 def test_prefill_over_a_coded_cache(gq):
     """A coded context read back as an un-paged 16-bit cache, then prefilled over."""
     import math
