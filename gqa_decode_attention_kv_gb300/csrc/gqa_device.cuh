@@ -98,9 +98,9 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity,
     }
 }
 
-// The same with a limit on the tries instead of a clock, whose reading a wait of a few
-// hundred cycles would feel.
-constexpr uint32_t kWaitTries = 1u << 23;
+// The same with a limit on the tries instead of a clock: less code in kernels of many
+// waits. A try that fails takes 4 us here, so this is a second as well.
+constexpr uint32_t kWaitTries = 1u << 18;
 __device__ __forceinline__ bool mbar_wait_tries(uint32_t bar, uint32_t parity, uint32_t tries = kWaitTries) {
     for (uint32_t i = 0; i < tries; ++i)
         if (mbar_try_wait(bar, parity)) return true;

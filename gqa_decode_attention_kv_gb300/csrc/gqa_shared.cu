@@ -58,7 +58,10 @@ __device__ __forceinline__ bool pair_any(int id, bool mine) {
 }
 
 // Two weights as a high and a low 16-bit part each. bf16's high part is the value cut
-// off, which takes no conversion (together 2^-16 of the weight; rounded 2^-17).
+// off, which takes no conversion (together 2^-16 of the weight; rounded 2^-17). fp16's
+// parts are exact to half its smallest step, 2^-25, so its weights come kUpF16 powers of
+// two up (at most 2^15 with the slack): what is lost is 2^-32 of a row's largest weight.
+constexpr float kUpF16 = 7.f;
 template <bool kBf16>
 __device__ __forceinline__ void split2(float x, float y, uint64_t xy, uint32_t& hi, uint32_t& lo) {
     float2 h;
@@ -151,10 +154,10 @@ __device__ __forceinline__ void widen16(const uint32_t* w, uint32_t (&o)[8]) {
 }
 
 // V's scales in the weights: w = p vs 2^lift, with the lift that puts the largest scale so
-// far into [2^3, 2^4), kept until a scale passes 2^7: p is at most 2^8, so that w stays
-// within fp16's range, and the low part's step is 2^-28 of that scale.
+// far into [2^5, 2^6), kept until a scale passes 2^7: p is at most 2^8, so that w stays
+// within fp16's range, and what its parts lose is 2^-30 of that scale and p's largest.
 __device__ __forceinline__ float power2(int e) { return __uint_as_float((uint32_t)(min(max(e, -126), 127) + 127) << 23); }
-constexpr int kLiftNone = 27;                     // before any scale: the least fp16 one is 2^-24
+constexpr int kLiftNone = 29;                     // before any scale: the least fp16 one is 2^-24
 
 template <typename T, int kTiles, int D>
 __global__ void __launch_bounds__(SharedCfg<T, kTiles, D>::kThreads, SharedCfg<T, kTiles, D>::kCtasPerSm)
@@ -164,6 +167,7 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
     constexpr int kS = C::kStages;
     constexpr bool kCoded = C::kCoded;
     constexpr bool kB = std::is_same<T, __nv_bfloat16>::value;
+    constexpr float kUp = std::is_same<T, __half>::value ? kUpF16 : 0.f;   // log2 of the weights' scaling
     constexpr uint32_t kIdescS = mma_idesc_f16(kRows, kChunk, kB, false, false);
     constexpr uint32_t kIdescO = mma_idesc_f16(kRows, D, kB, false, true);
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -172,9 +176,10 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
     uint8_t* gb = smem_raw + (sb - raw);
     const uint32_t sQ = sb, sK = sb + C::kOffK, sV = sb + C::kOffV;
     // Barriers, 8 B each: K stages, V stages (stage G % kS), then per tile t "S_t(G)
-    // done", "P_t(G).V(G) done", "P_t(G) ready" (copy G & 3), "Q_t stored"; then the TMEM
-    // address and the scan's scratch. G counts the CTA's steps across its segments. Per-step
-    // barriers come in four copies, so that no parity wait can fall two phases behind.
+    // done", "P_t(G).V(G) done", "P_t(G) ready" (copy G & 3), "Q_t stored"; the TMEM
+    // address; the scan's scratch; a coded cache's copies; warps that gave up. G counts the
+    // CTA's steps across its segments. Per-step barriers come in four copies, so that no
+    // parity wait can fall two phases behind.
     const uint32_t bar0 = sb + C::kOffBar;
     auto stage = [](int c) { return c % kS; };
     auto par_st = [](int c) { return (uint32_t)(c / kS) & 1u; };
@@ -185,7 +190,8 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
     auto bar_p = [&](int t, int c) { return bar0 + 128 + 96 * t + 8 * (c & 3); };
     auto bar_q = [&](int t) { return bar0 + 256 + 8 * t; };
     const uint32_t tslot = bar0 + 272;
-    int* scan = reinterpret_cast<int*>(gb + C::kOffBar + 288);      // [128] sums, then the run's group and where it begins
+    // [128] sums, then where the run begins: group, its step, its span, its leader
+    int* scan = reinterpret_cast<int*>(gb + C::kOffBar + 288);
     auto bar_full = [&](int cw, int c) { return bar0 + 832 + 32 * cw + 8 * (c & 3); };   // coded: copy warp cw's codes landed
     float* scales = reinterpret_cast<float*>(gb + C::kOffSc);
     auto par4 = [](int c) { return (uint32_t)(c >> 2) & 1u; };
@@ -211,6 +217,7 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
             }
             mbar_init(bar_q(t), 8);
         }
+        for (int i = 0; i < 2 * 4 * kTiles; ++i) scan[168 + i] = 0;      // "this pair's warp gave up"
         fence_mbar_init();
     }
     if (warp == 0) tmem_alloc(tslot, C::kTmemCols);
@@ -416,7 +423,7 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
                 const uint32_t to = (v ? sV : sK) + stage(G) * C::kKc;
                 constexpr int kLanes = D / 16;         // lanes of a row, 16 codes each
                 constexpr int kBatch = 4;              // loads of codes on their way together
-#pragma unroll
+#pragma unroll 1
                 for (int i0 = 0; i0 < 32 * kLanes; i0 += 32 * kBatch) {
                     uint32_t codes[kBatch][4];
 #pragma unroll
@@ -454,7 +461,7 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
                     for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(kFull, most, o));
                     float factor = 1.f;
                     if (most > power2(7 - lift)) {
-                        const int now = 3 - ((int)(__float_as_uint(most) >> 23) - 127);
+                        const int now = 5 - ((int)(__float_as_uint(most) >> 23) - 127);
                         factor = power2(now - lift);
                         lift = now;
                     }
@@ -472,9 +479,7 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
                 if (lane / 16 == part) *reinterpret_cast<float2*>(slot + 2 * lane) = sc;
                 fence_proxy_async_smem();          // the widened rows visible to the tensor core
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(v ? bar_v(G) : bar_k(G));
-                }
+                if (lane == 0) mbar_arrive(v ? bar_v(G) : bar_k(G));
                 if (iss_have) issue();             // into the stage just read
             }
             if (ok) have = next_seg(it);
@@ -524,9 +529,8 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
                 if (lane == 0) mbar_arrive_expect_tx(bar, C::kVc);
                 __syncwarp();
                 // K: a box per (block, 64-element half); V: one per page (head_dim 128: the page
-                // map lands it as [half][slot][128 B]). One lane issues them with operands that
-                // are the warp's: a lane per box takes 180 cycles each, and the 8 of K then
-                // are what a step waits for.
+                // map lands it as [half][slot][128 B]). One elected lane issues them with operands
+                // that are the warp's: from a lane's own registers a box takes 180 cycles.
 #pragma unroll
                 for (int q = 0; q < kChunkBlocks; ++q) {
                     const int pq = __shfl_sync(kFull, win_phys, v0 - win_base + q);
@@ -557,10 +561,10 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
         }
     } else if (mma_warp) {
         // ================================================== MMA warps: two per tile, one for S and
-        // one for P.V, so that neither waits in the other's place (one warp for both takes
-        // 1790 cycles a step, its own chain of waits). A whole warp walks along and one
-        // elected lane issues: from a branch of one lane the operands go through vector
-        // registers, 144 cycles a P.V product for 38.
+        // one for P.V, so that neither waits in the other's place (a step of 1790 cycles; of
+        // 1817 with one warp for both). A whole warp walks along and one elected lane issues:
+        // from a branch of one lane the operands go through vector registers, 144 cycles a
+        // P.V product for 38.
         const int t = (warp - C::kSoftWarps) >> 1;
         const bool s_warp = ((warp - C::kSoftWarps) & 1) == 0;
         auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(kFull, mbar_wait_tries(bar, parity)); };
@@ -624,6 +628,17 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
         const uint32_t qt = sQ + tt * C::kQt;
         float* ex = reinterpret_cast<float*>(gb + C::kOffEx) + tt * 2 * kRows;
         const int pair_bar = 1 + 4 * tt + quad;    // the two warps that hold the same rows
+        // A warp whose wait ran out says so at the pair's next vote (of step c, or behind the
+        // last one), so that its partner leaves with it: a word for odd and one for even steps,
+        // as the other may still read the last.
+        auto gone = [&](int c) -> volatile int& { return scan[168 + 2 * (4 * tt + quad) + (c & 1)]; };
+        auto give_up = [&](int c) {
+            if (lane == 0) gone(c) = 1;
+            __syncwarp();
+            pair_any(pair_bar, true);
+            pair_sync(pair_bar);
+        };
+        auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(kFull, mbar_wait_tries(bar, parity)); };
         // This warp's 16 Q rows of segment x into its tile's swizzled K-major layout by
         // cp.async (16 bytes a lane; rows past the group's are zero-filled), then "Q_t
         // stored" once they have landed. All of their places are looked up first.
@@ -677,15 +692,17 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
             q_stored();
         }
         int gc = 0;
-        while (have && ok) {
+        while (have) {
             const int n = it.c1 - it.c0;
             const bool tile_live = it.row0 + kRows * tt < it.rows;
             float m = -INFINITY, l = 0.f;      // the row's maximum, this half's sum
             float unlift = 1.f;                // coded: what takes the lift out of O
             for (int c = 0; c < n; ++c) {
                 const int G = gc + c;
-                ok = __all_sync(kFull, mbar_wait_tries(bar_s(tt, G), par4(G)));   // S_t(G) done
-                if (!ok) break;
+                if (!wait(bar_s(tt, G), par4(G))) {        // S_t(G) done
+                    if (tile_live) give_up(c);
+                    goto gave_up;
+                }
                 tc_fence_after();
                 if (!tile_live) {
                     __syncwarp();
@@ -716,8 +733,10 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
                             r[u][q + 3] = __float_as_uint(y.y);
                         }
                     scl = 1.f;
-                    ok = __all_sync(kFull, mbar_wait_tries(bar_v(G), par_st(G)));      // V's are there as well
-                    if (!ok) break;
+                    if (!wait(bar_v(G), par_st(G))) {      // V's are there as well
+                        give_up(c);
+                        goto gave_up;
+                    }
                     factor = slot[2 * kChunk - kHalf * hf];
                     unlift = slot[2 * kChunk + 1 - kHalf * hf];
                 }
@@ -753,6 +772,7 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
                 if (pair_any(pair_bar, mx > m + kSlackLog2 || factor != 1.f)) {
                     ex[hf * kRows + row_t] = mx;
                     pair_sync(pair_bar);
+                    if (gone(c)) goto gave_up;
                     mx = fmaxf(mx, ex[(hf ^ 1) * kRows + row_t]);
                     const bool old_live = m != -INFINITY;
                     const bool resc = mx > m + kSlackLog2;
@@ -761,7 +781,10 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
                     l *= alpha;
                     if (c > 0 && __any_sync(kFull, (resc && old_live) || factor != 1.f)) {   // O holds earlier steps: scale it
                         // once P_t(G-1).V(G-1) has landed in it, this half its columns
-                        ok = __all_sync(kFull, mbar_wait_tries(bar_o(tt, G - 1), par4(G - 1)));
+                        if (!wait(bar_o(tt, G - 1), par4(G - 1))) {
+                            give_up(c + 1);
+                            goto gave_up;
+                        }
                         tc_fence_after();
                         const float f = (resc && old_live ? alpha : 1.f) * factor;
 #pragma unroll 1
@@ -775,7 +798,7 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
                         }
                     }
                 }
-                const float mu = m == -INFINITY ? 0.f : -m;   // a row with nothing attended yet: p = 0
+                const float mu = m == -INFINITY ? 0.f : kUp - m;   // a row with nothing attended yet: p = 0
                 const uint64_t mu2 = f2_make(mu, mu), sc2 = f2_make(scl, scl);
                 uint64_t ps2[2] = {f2_make(0.f, 0.f), f2_make(0.f, 0.f)};
                 // P over S: a block's 16 tokens to its own columns, 8 high then 8 low ones
@@ -809,9 +832,7 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar_p(tt, G));
-                if (!ok) break;
             }
-            if (!ok) break;
             // every S_t of the segment is done, so Q_t's buffer is free: with the next one's
             // rows in it, its MMA warp may start on it
             Seg nx;
@@ -823,8 +844,10 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
             // ---- wait for this tile's last P.V, then leave the row's state: a problem's
             // first piece by its row, a continued one (only a CTA's first can be) by CTA
             const int G_last = gc + n - 1;
-            ok = __all_sync(kFull, mbar_wait_tries(bar_o(tt, G_last), par4(G_last)));
-            if (!ok) break;
+            if (!wait(bar_o(tt, G_last), par4(G_last))) {
+                if (tile_live) give_up(n);
+                goto gave_up;
+            }
             tc_fence_after();
             if (tile_live) {
                 const int row = it.row0 + kRows * tt + row_t;
@@ -868,16 +891,22 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
                                 make_float4(__uint_as_float(x[4 * k]), __uint_as_float(x[4 * k + 1]),
                                             __uint_as_float(x[4 * k + 2]), __uint_as_float(x[4 * k + 3]));
                 }
-                pair_sync(pair_bar);
+                if (pair_any(pair_bar, false)) {   // the other half's sums are there; or its warp gave up
+                    pair_sync(pair_bar);
+                    goto gave_up;
+                }
                 if (hf == 0 && row < it.rows)
-                    (first ? a.ml_a : a.ml_b)[base + row] = make_float2(m, l + ex[kRows + row_t]);
+                    (first ? a.ml_a : a.ml_b)[base + row] = make_float2(m - kUp, l + ex[kRows + row_t]);
                 pair_sync(pair_bar);               // ex has been read
             }
             gc += n;
             it = nx;
             have = have_nx;
         }
-        if (!ok && lane == 0) flag_error(a.err, GQA_DEVERR_TIMEOUT);
+        if (false) {
+        gave_up:
+            if (lane == 0) flag_error(a.err, GQA_DEVERR_TIMEOUT);
+        }
         cp_async_wait_all();                   // nothing of this warp's still lands in shared memory
     }
     tc_fence_before();
@@ -912,7 +941,7 @@ __global__ void __launch_bounds__(kRowWarps * kCtaRows * 32) shared_merge_kernel
     if (blockIdx.x == 0 && tid == 0) *a.ws_ctr = 0ull;
     if (bh >= a.B * TH) return;                // uniform per warp, and per CTA where warps share a row
     const int p0 = a.ws_pref[b], nb = a.ws_pref[b + 1] - p0;
-    const int R = p.hdr[0], cta_rows = p.hdr[2], unit0 = p.first_unit[sr.group];
+    const int R = p.hdr[0], U = p.hdr[1], cta_rows = p.hdr[2], unit0 = p.first_unit[sr.group];
     Partition pt;
     pt.R = a.ws_hdr[0];
     pt.U = a.ws_hdr[1];
@@ -939,6 +968,7 @@ __global__ void __launch_bounds__(kRowWarps * kCtaRows * 32) shared_merge_kernel
         const int u0 = unit0 + (g * pr.tiles + tile) * pr.chunks;
         j0 = u0 / R;
         n2 = (u0 + pr.chunks - 1) / R - j0 + 1;
+        if (u0 < 0 || pr.chunks > U - u0) n2 = 0;  // (a plan of overlapping groups: past 32 bits)
     }
     const int n = n1 + n2;
     auto piece_ml = [&](int x) -> const float2* {
@@ -968,7 +998,10 @@ __global__ void __launch_bounds__(kRowWarps * kCtaRows * 32) shared_merge_kernel
 #pragma unroll
         for (int s = 2; s > 0; s >>= 1) mc = fmaxf(mc, __shfl_xor_sync(kFull, mc, s));
         const float Mn = fmaxf(Mw, __shfl_sync(kFull, mc, 0));
-        if (Mn == -INFINITY) continue;         // warp-uniform: nothing seen yet
+        if (Mn == -INFINITY) {                 // warp-uniform: nothing seen yet, or NaN alone
+            L += ml.y;
+            continue;
+        }
         const float sc = fast_exp2(Mw - Mn);   // 0 while Mw = -inf, 1 if unchanged
         acc.x *= sc; acc.y *= sc; acc.z *= sc; acc.w *= sc;
         L *= sc;
@@ -997,11 +1030,11 @@ __global__ void __launch_bounds__(kRowWarps * kCtaRows * 32) shared_merge_kernel
         float M = s_m[rw][0];
 #pragma unroll
         for (int w = 1; w < kRowWarps; ++w) M = fmaxf(M, s_m[rw][w]);
-        auto share = [&](int w) { return s_m[rw][w] == -INFINITY ? 0.f : fast_exp2(s_m[rw][w] - M); };
+        auto share = [&](int w) { return s_m[rw][w] == -INFINITY ? 0.f : fast_exp2(s_m[rw][w] - M); };   // (0 NaN is NaN)
         float Lt = 0.f;
 #pragma unroll
         for (int w = 0; w < kRowWarps; ++w) Lt += s_l[rw][w] * share(w);
-        const float inv = Lt > 0.f ? 1.f / Lt : 0.f;
+        const float inv = Lt == 0.f ? 0.f : 1.f / Lt;
         for (int x = tid % (32 * kRowWarps); x < D; x += 32 * kRowWarps) {
             float v = 0.f;
 #pragma unroll
@@ -1009,7 +1042,7 @@ __global__ void __launch_bounds__(kRowWarps * kCtaRows * 32) shared_merge_kernel
             dec::store1(a.out, a.out_dtype, orow + x, v * inv);
         }
     } else if (has_dims) {
-        const float inv = L > 0.f ? 1.f / L : 0.f;
+        const float inv = L == 0.f ? 0.f : 1.f / L;
         dec::store1(a.out, a.out_dtype, orow + 4 * lane + 0, acc.x * inv);
         dec::store1(a.out, a.out_dtype, orow + 4 * lane + 1, acc.y * inv);
         dec::store1(a.out, a.out_dtype, orow + 4 * lane + 2, acc.z * inv);

@@ -588,8 +588,10 @@ GQA_API int gqa_decode_sinks(const gqa_kv_cache_t *cache, const void *q, int32_t
 /*
  * gqa_decode for a batch whose rows share long prefixes: the pages that a group of rows
  * has in common are read once and attended for all of its queries, every row's others on
- * their own, and the two joined by their log-sum-exp weights. The result is gqa_decode's,
- * to fp32 rounding (full attention; no window).
+ * their own, and the two joined by their log-sum-exp weights. The result is gqa_decode's
+ * (full attention; no window), to fp32 rounding and that of the shared tokens' weights: to
+ * 2^-16 of each for a BF16 cache, 2^-32 of a query's largest for F16, 2^-30 of the largest
+ * times the largest scale of V for a coded one.
  *  tokens_per_seq  T, as in gqa_decode_opts_t (0 meaning 1).
  *  groups          device, a plan of this batch as gqa_kv_pages_groups lays it out. The
  *                  shared pages are read through the table row of a group's first row. A
@@ -601,9 +603,9 @@ GQA_API int gqa_decode_sinks(const gqa_kv_cache_t *cache, const void *q, int32_t
  *                  it picks the kernel's form and changes no result.
  *  workspace       device, >= gqa_decode_shared_workspace_size(...) bytes, otherwise as
  *                  gqa_decode's (which it may be shared with).
- *  Cache dtypes: F16, BF16, I8, FP8_E4M3, I4; F32 and I4_KC are GQA_ERR_UNSUPPORTED. q of a
- *  coded cache is taken as fp16 (exact from BF16 where 2^-17 <= |q| <= 65504). Other
- *  arguments and limits as gqa_decode.
+ *  Cache dtypes: F16, BF16, I8, FP8_E4M3, I4; F32 and I4_KC are GQA_ERR_UNSUPPORTED. Scales
+ *  are not negative, as the appends write them. q of a coded cache is taken as fp16 (exact
+ *  from BF16 where 2^-17 <= |q| <= 65504). Other arguments and limits as gqa_decode.
  */
 GQA_API size_t gqa_decode_shared_workspace_size(int32_t batch, int32_t num_heads, int32_t num_kv_heads,
                                  int32_t head_dim, int32_t tokens_per_seq, int32_t device);

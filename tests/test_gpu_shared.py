@@ -246,6 +246,16 @@ def test_no_groups_and_one_row(gq):
     check(got, want, values)
 
 
+def test_no_rows(gq):
+    cache, _ = shared.pool("bf16", 3, 2, 64, 0, gq)
+    table = torch.full((0, 4), -1, dtype=torch.int32, device="cuda")
+    lens = torch.zeros(0, dtype=torch.int32, device="cuda")
+    plan = gq.kv_pages_groups(table, lens)
+    assert plan.count.tolist() == [0, 0]
+    q = torch.zeros(0, 4, 64, dtype=torch.bfloat16, device="cuda")
+    assert gq.gqa_decode_shared(cache, q, table, lens, 0.1, plan).shape == q.shape
+
+
 def test_poison_behind_the_rows(gq):
     """Slots behind a row's end and pages of no row hold NaN; nothing of them is seen."""
     def tweak(bt, cache, values):
@@ -287,6 +297,109 @@ def test_large_and_small_scores(gq):
         # scores up to amp * scale * sqrt(d) times larger than the bound above allows for
         bound = np.abs(values[1]).max() * 2.0 ** -11 * max(1.0, amp * abs(scale) * math.sqrt(128))
         assert (np.abs(got.view(q.shape).double().cpu().numpy() - want) <= bound).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "int8"])
+def test_many_small_weights_beside_a_large_one(gq, kind):
+    """One token whose score is 18 above all others': a weight of e^-18 each, whose sum over
+    the prefix is all that the output holds. Two 16-bit parts lose 2^-16 of a bf16 weight, at
+    most 2^-32 of the largest from an fp16 one (2^-6 of e^-18), 2^-30 with int8 codes (2^-4)."""
+    bt = shared.batch([(256, [4100, 4097])], [], 40)
+    cache, values = shared.pool(kind, bt.pages, 1, 64, 41, gq)
+    first = int(bt.table[0, 0])
+    if kind == "int8":
+        cache.k.zero_()
+        cache.k[first, 0, 0] = 1
+        cache.k_scale.fill_(2.25)
+        cache.v.fill_(1)
+        cache.v_scale.fill_(1)
+        cache.v[first, 0, 0] = 0
+    else:
+        cache.k.zero_()
+        cache.k[first, 0, 0] = 2.25                             # page, kv-head, token
+        cache.v.fill_(1)
+        cache.v[first, 0, 0] = 0
+    q = torch.ones(2, 2, 64, dtype=shared.DTYPES.get(kind, torch.bfloat16), device="cuda")
+    table, lens = torch.from_numpy(bt.table).cuda(), torch.from_numpy(bt.lens).cuda()
+    plan = gq.kv_pages_groups(table, lens)
+    assert plan.blocks.tolist()[0] == 256
+    got = gq.gqa_decode_shared(cache, q, table, lens, 0.125, plan).double().cpu().numpy()
+    x = (bt.lens.astype(np.float64) - 1) * math.exp(-18.0)
+    want = (x / (1 + x))[:, None, None]
+    # 18 = 64 products of 2.25 / 8, exact; exp2 of 18 log2(e) rounded: 2^-24 * 26 * ln 2
+    bound = {"bf16": 2.0 ** -16, "f16": 2.0 ** -6, "int8": 2.0 ** -4}[kind] + 2.0 ** -18
+    assert (np.abs(got - want) <= bound * want).all(), float(np.abs(got / want - 1).max())
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "int8"])
+def test_nan_and_infinite_inputs(gq, kind):
+    """A NaN query head gives NaN there and nowhere else; a V of infinity that is attended
+    leaves its column alone not finite (NaN where a weight's low part is zero or negative), and
+    a score of -inf takes its token out."""
+    bt = shared.batch([(20, [330, 340, 350])], [30], 60)
+    cache, values = shared.pool(kind, bt.pages, 2, 64, 61, gq)
+    table, lens = torch.from_numpy(bt.table).cuda(), torch.from_numpy(bt.lens).cuda()
+    plan = gq.kv_pages_groups(table, lens)
+    q = torch.randn(4, 1, 8, 64, generator=torch.Generator().manual_seed(62)).to(shared.DTYPES.get(kind, torch.bfloat16))
+    row = plan.rows.tolist()[1]
+    bad = q.clone()
+    bad[row, 0, 3] = float("nan")
+    got = gq.gqa_decode_shared(cache, bad[:, 0].contiguous().cuda(), table, lens, 0.125, plan)
+    got = got.view(q.shape).double().cpu().numpy()
+    want = shared.attend(q.double().numpy(), values, bt.table, bt.lens, 0.125)
+    assert np.isnan(got[row, 0, 3]).all()
+    got[row, 0, 3] = want[row, 0, 3]
+    check(got, want, values)
+    if kind == "int8":
+        return
+    page = int(bt.table[row, 5])                                 # in all three rows
+    cache.v[page, 1, 4, 7] = float("inf")
+    got = gq.gqa_decode_shared(cache, q[:, 0].contiguous().cuda(), table, lens, 0.125, plan)
+    got = got.view(q.shape).double().cpu().numpy()
+    for r in plan.rows.tolist()[:3]:
+        assert not np.isfinite(got[r, 0, 4:, 7]).any()
+        got[r, 0, 4:, 7] = want[r, 0, 4:, 7]
+    check(got, want, values)
+    # a key of -inf where the queries are positive
+    cache.v[page, 1, 4, 7] = 0
+    cache.k[page, 1, 4, 0] = -float("inf")
+    pos = q.abs()
+    held = values[0].copy()
+    held[page, 4, 1, 0] = -1e6
+    kept = values[1].copy()
+    kept[page, 4, 1, 7] = 0
+    want = shared.attend(pos.double().numpy(), [held, kept], bt.table, bt.lens, 0.125)
+    got = gq.gqa_decode_shared(cache, pos[:, 0].contiguous().cuda(), table, lens, 0.125, plan)
+    check(got.view(q.shape).double().cpu().numpy(), want, values)
+
+
+def test_two_threads_on_two_streams(gq):
+    """Calls of two host threads at once, each on its own stream with the workspace kept for it."""
+    import threading
+    bt = shared.batch([(60, [1000 + i for i in range(9)])], [70], 70)
+    cache, values = shared.pool("bf16", bt.pages, 2, 128, 71, gq)
+    table, lens = torch.from_numpy(bt.table).cuda(), torch.from_numpy(bt.lens).cuda()
+    plan = gq.kv_pages_groups(table, lens)
+    qs = [torch.randn(10, 16, 128, generator=torch.Generator().manual_seed(72 + i)).bfloat16().cuda() for i in range(2)]
+    want = [gq.gqa_decode_shared(cache, q, table, lens, 0.1, plan) for q in qs]
+    torch.cuda.synchronize()
+    got, streams = [[], []], [torch.cuda.Stream() for _ in qs]
+
+    def work(i):
+        with torch.cuda.stream(streams[i]):
+            for _ in range(30):
+                got[i].append(gq.gqa_decode_shared(cache, qs[i], table, lens, 0.1, plan))
+        streams[i].synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for i in range(2):
+        assert len(got[i]) == 30
+        for x in got[i]:
+            assert float((x - want[i]).abs().max()) <= 2 * np.abs(values[1]).max() * 2.0 ** -11
 
 
 def test_equals_decode_and_shares_its_workspace(gq):
@@ -388,6 +501,25 @@ def test_plans_that_point_astray_share_nothing(gq):
         getattr(plan, part).fill_(value)
         got = gq.gqa_decode_shared(cache, q[:, 0].contiguous().cuda(), table, lens, 0.1, plan)
         check(got.view(q.shape).double().cpu().numpy(), want, values)
+
+
+def test_plan_of_overlapping_groups(gq):
+    """Every group over all rows: what comes out is not defined, that nothing is read astray is."""
+    B, blocks = 64, 40
+    bt = shared.batch([(blocks, [16 * blocks + 1 + i for i in range(B)])], [], 26)
+    cache, values = shared.pool("bf16", bt.pages, 2, 64, 27, gq)
+    q = torch.randn(B, 8, 64, generator=torch.Generator().manual_seed(28)).bfloat16().cuda()
+    table, lens = torch.from_numpy(bt.table).cuda(), torch.from_numpy(bt.lens).cuda()
+    plan = gq.kv_pages_groups(table, lens)
+    good = gq.gqa_decode_shared(cache, q, table, lens, 0.1, plan)
+    plan.count.fill_(B)
+    plan.start.copy_(torch.tensor([0, B] * (B // 2) + [0]))
+    plan.blocks.fill_(blocks)
+    plan.group.copy_(2 * (torch.arange(B) // 2))
+    bad = gq.gqa_decode_shared(cache, q, table, lens, 0.1, plan)
+    torch.cuda.synchronize()
+    assert bad.shape == good.shape
+    assert torch.equal(gq.gqa_decode_shared(cache, q, table, lens, 0.1, gq.kv_pages_groups(table, lens)), good)
 
 
 def test_plan_written_by_the_caller(gq):
