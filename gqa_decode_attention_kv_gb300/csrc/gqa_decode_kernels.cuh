@@ -1346,23 +1346,33 @@ __device__ __forceinline__ Partition make_partition(const DecodeArgs& a, int U, 
 }
 
 // Workers of the tail flavour: those of the SMs that the prefix kernel leaves (the CTAs
-// after them find no room before it ends, and then nothing to do). units: blocks of the
-// rows' own times kv-heads; tmp: 32 ints of shared memory.
+// after them find no room before it ends, and then nothing to do). pref: the rows' own blocks
+// summed up; tmp: 32 ints of shared memory.
 template <class C>
-__device__ int tail_workers(const DecodeArgs& a, int units, int* tmp) {
+__device__ int tail_workers(const DecodeArgs& a, const int* pref, int* tmp) {
     const PrefixGroups plan(a.groups, a.B);
     const int n = plan.groups(), lane = threadIdx.x & 31;
-    int steps = 0;
+    int steps = 0, rows = 0;
     for (int i = threadIdx.x; i < n; i += blockDim.x)
         steps += problem_of(group_span(plan, i, a.max_blocks), a.K, a.GT, a.split.cta_rows).units;
+    for (int b = threadIdx.x; b < a.B; b += blockDim.x) rows += pref[b + 1] > pref[b];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) steps += __shfl_xor_sync(kFull, steps, o);
-    if (lane == 0) tmp[threadIdx.x >> 5] = steps;
+    for (int o = 16; o > 0; o >>= 1) {
+        steps += __shfl_xor_sync(kFull, steps, o);
+        rows += __shfl_xor_sync(kFull, rows, o);
+    }
+    if (lane == 0) {
+        tmp[threadIdx.x >> 5] = steps;
+        tmp[16 + (threadIdx.x >> 5)] = rows;
+    }
     __syncthreads();
-    steps = 0;
-    for (int i = 0; i < (int)blockDim.x / 32; ++i) steps += tmp[i];
+    steps = rows = 0;
+    for (int i = 0; i < (int)blockDim.x / 32; ++i) {
+        steps += tmp[i];
+        rows += tmp[16 + i];
+    }
     const int per_cta = C::kNw == 1 ? C::kWarps : 1;
-    const int ctas = a.P / per_cta, left = a.split.sms - prefix_sms(a.split, steps, units);
+    const int ctas = a.P / per_cta, left = a.split.sms - prefix_sms(a.split, steps, pref[a.B] * a.K, rows * a.K);
     return max(1, (int)((long long)ctas * left / a.split.sms)) * per_cta;
 }
 
@@ -1398,7 +1408,7 @@ split_kv_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
         return;
     }
     block_prefix<kGen, kSinks, kTail>(a, lens_s, pref, tmp, pref + a.B + 1);
-    const Partition pt = make_partition(a, a.Kv * pref[a.B], kTail ? tail_workers<C>(a, pref[a.B] * a.K, tmp) : a.P);
+    const Partition pt = make_partition(a, a.Kv * pref[a.B], kTail ? tail_workers<C>(a, pref, tmp) : a.P);
     if (blockIdx.x == 0) {
         for (int i = threadIdx.x; i <= a.B; i += blockDim.x) a.ws_pref[i] = pref[i];
         if (threadIdx.x == 0) {

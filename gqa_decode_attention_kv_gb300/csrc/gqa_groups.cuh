@@ -73,7 +73,7 @@ constexpr int kStepTokens = 64;                   // tokens of a step of the pre
 struct SplitModel {
     int sms, ctas_per_sm, cta_rows, min_steps;    // of the prefix kernel; fewest steps of a CTA
     float step_us, prefix_us;                     // a step of an SM's CTAs, the kernel's start and end
-    float unit_us, tail_us;                       // a (block, kv-head) of the tail, its start
+    float unit_us, pair_us, tail_us;              // a (block, kv-head) of the tail, a (row, kv-head), its start
 };
 
 // One group's rows for one kv-head, and how its steps lie.
@@ -89,25 +89,29 @@ __device__ __forceinline__ Problem problem_of(const GroupSpan& s, int K, int GT,
     return p;
 }
 
-// SMs for `steps` steps of the prefix beside `units` blocks of the tail: the fewest with
-// which the prefix ends no later than the tail on the others, but no more than its CTAs
-// have min_steps each for. Called by whole warps: the lanes try 32 numbers at a time (one
-// after the other, by halving, takes 1.1 us before the first copy).
-__device__ __forceinline__ int prefix_sms(const SplitModel& m, int steps, int units) {
+// SMs for `steps` steps of the prefix beside `units` blocks of `pairs` rows' own: those with
+// which the later of the two ends first, in whole pairs of SMs (see the launch) and no more
+// than its CTAs have min_steps each for. Called by whole warps: the lanes try 32 numbers at a
+// time (one after the other, by halving, takes 1.1 us before the first copy).
+__device__ __forceinline__ int prefix_sms(const SplitModel& m, int steps, int units, int pairs) {
     if (steps == 0) return 0;
     const int per_sm = m.min_steps * m.ctas_per_sm, most = min(m.sms, (steps + per_sm - 1) / per_sm);
     if (units == 0) return most;
-    const int lane = threadIdx.x & 31, cap = max(1, min(most, m.sms - 1));   // the answer where nothing less does
-    const float wp = steps * m.step_us / m.ctas_per_sm, wt = units * m.unit_us;
-    auto ends_first = [&](int x) {
-        return x >= cap || m.prefix_us + __fdividef(wp, (float)x) <= m.tail_us + __fdividef(wt, (float)(m.sms - x));
-    };
-    int lo = 0;                                   // too few
+    const int lane = threadIdx.x & 31, cap = max(1, min(most, m.sms - 2));
+    const float wp = steps * m.step_us / m.ctas_per_sm, wt = units * m.unit_us + pairs * m.pair_us;
+    auto prefix_end = [&](int x) { return m.prefix_us + __fdividef(wp, (float)x); };
+    auto tail_end = [&](int x) { return m.tail_us + __fdividef(wt, (float)(m.sms - x)); };
+    int lo = 0;                                   // there the prefix ends last
     for (int step = (cap + 31) / 32;; step = (step + 31) / 32) {
         const int x = min(lo + (lane + 1) * step, cap);
-        const int first = __ffs(__ballot_sync(kFull, ends_first(x))) - 1;    // some lane's x is the cap, or past the answer
-        if (step == 1) return min((lo + first + 2) & ~1, cap);               // pairs of SMs: see the launch
-        lo += first * step;
+        const bool first = x >= cap || prefix_end(x) <= tail_end(x);
+        const int n = __ffs(__ballot_sync(kFull, first)) - 1;                // some lane's x is the cap, or past the answer
+        if (step > 1) {
+            lo += n * step;
+            continue;
+        }
+        const int hi = min((lo + n + 2) & ~1, cap), less = (hi - 1) & ~1;    // the tail ends last; the prefix
+        return less > 0 && prefix_end(less) < fmaxf(prefix_end(hi), tail_end(hi)) ? less : hi;
     }
 }
 

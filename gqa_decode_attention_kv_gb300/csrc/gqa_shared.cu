@@ -246,28 +246,36 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
     GroupSpan mine = span_of(tid);
     auto leader_of = [&](const GroupSpan& x) { return min(max(plan.rows[x.first], 0), a.B - 1); };
     int lead = leader_of(mine);
-    int U = 0, own = 0;
+    int U = 0, own = 0, own_rows = 0;
     {
-        int rows_own = blocks_of(tid), sum = units_of(mine, tid);
+        const int x0 = blocks_of(tid);
+        int blocks = x0, rows = x0 > 0, sum = units_of(mine, tid);
         for (int i = tid + C::kThreads; i < n_groups; i += C::kThreads) sum += units_of(span_of(i), i);
-        for (int b = tid + C::kThreads; b < a.B; b += C::kThreads) rows_own += blocks_of(b);
+        for (int b = tid + C::kThreads; b < a.B; b += C::kThreads) {
+            const int x = blocks_of(b);
+            blocks += x;
+            rows += x > 0;
+        }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
             sum += __shfl_xor_sync(kFull, sum, o);
-            rows_own += __shfl_xor_sync(kFull, rows_own, o);
+            blocks += __shfl_xor_sync(kFull, blocks, o);
+            rows += __shfl_xor_sync(kFull, rows, o);
         }
         if (lane == 0) {
             scan[warp] = sum;
-            scan[32 + warp] = rows_own;
+            scan[32 + warp] = blocks;
+            scan[96 + warp] = rows;
         }
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kWarps; ++i) {
             U += scan[i];
             own += scan[32 + i];
+            own_rows += scan[96 + i];
         }
     }
-    const int P = max(1, prefix_sms(a.split, U, own * a.K) * C::kCtasPerSm);
+    const int P = max(1, prefix_sms(a.split, U, own * a.K, own_rows * a.K) * C::kCtasPerSm);
     const int R = max((U + P - 1) / P, a.split.min_steps);
     const int u_lo = (int)min((long long)U, (long long)j * R), u_hi = (int)min((long long)U, (long long)(j + 1) * R);
     if (j == 0 && tid == 0) {
@@ -1120,11 +1128,15 @@ PrefixWs prefix_ws(long long batch, long long rows, int d, int sms) {
     return w;
 }
 
-// The times behind the GPU's division, measured in the middle of long prefixes and tails: a
-// step of 256 rows takes an SM 0.95 us (coded 1.5; 128 rows in two CTAs 0.6), a (block,
-// kv-head) of the rows' own 0.19 us for a 16-bit cache of 128 dims, 0.16 with 8-bit codes,
-// 0.15 with 4-bit ones, 0.9 with codes on the CUDA cores (head_dim 64); more with more than 8
-// query rows. They pick how the SMs are dealt out and change no result.
+// The times behind the GPU's division, measured over prefixes of up to 32768 tokens and tails
+// of 1 to 60 blocks. A step of 256 rows takes an SM 0.95 us (coded 1.5; 128 rows in two CTAs
+// 0.6). Of the rows' own a (block, kv-head) takes 0.19 us in a 16-bit cache of 128 dims, 0.15
+// with 8-bit codes, 0.14 with 4-bit ones (0.135, 0.1 and 0.085 on a few SMs, where HBM keeps
+// up), 1.6 with codes on the CUDA cores (head_dim 64); a (row, kv-head) 0.13, coded 0.5, which
+// is most of it for rows that have just begun: 17 rows of up to 2 blocks behind 32768 tokens
+// take 53 us where they count as blocks alone 82. All at 8 query rows; 32 take about 3 times
+// as long for a block and 5 for a row. They pick how the SMs are dealt out and change no
+// result.
 SplitModel split_of(const DecodeLaunch& L, const Form& f, int sms) {
     const gqa_kv_cache_t& c = *L.cache;
     const int GT = L.num_heads / c.num_kv_heads * L.tokens_per_seq;
@@ -1136,8 +1148,12 @@ SplitModel split_of(const DecodeLaunch& L, const Form& f, int sms) {
     m.min_steps = 2;
     m.step_us = (coded ? 1.5f : f.rows > kRows ? 0.95f : 1.2f) * (wide ? 1.f : 0.7f);
     m.prefix_us = 9.f;
-    m.unit_us = coded ? (!wide ? 0.9f : dtype_bits(c.dtype) == 8 ? 0.16f : 0.15f) : wide ? 0.19f : 0.1f;
-    if (GT > 8) m.unit_us *= coded ? 2.f : 1.6f;
+    m.unit_us = coded ? (!wide ? 1.6f : dtype_bits(c.dtype) == 8 ? 0.15f : 0.14f) : wide ? 0.19f : 0.1f;
+    m.pair_us = coded ? 0.5f : wide ? 0.13f : 0.08f;
+    if (GT > 8) {
+        m.unit_us *= coded ? GT / 8.f : std::max(1.6f, GT / 13.f);
+        m.pair_us *= GT / 8.f;
+    }
     m.tail_us = 4.f;
     return m;
 }
