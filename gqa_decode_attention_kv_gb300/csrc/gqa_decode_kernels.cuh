@@ -1974,6 +1974,8 @@ bool pick_kind(int kind, int nw, Variant& v) {
     if constexpr (std::is_same<T, float>::value) {
         v = pick_width<kKernelFma, T, D, kGen, kSinks, kTail>(nw);
         return true;
+    } else if constexpr (kTail && (D == 128 || std::is_same<T, __half>::value || std::is_same<T, __nv_bfloat16>::value)) {
+        return false;                          // (AUTO picks the kind there)
     } else {
         // the CUDA-core kernel serves fp32 caches, and <= 8-head groups of the others
         if (nw > 1) return false;
@@ -1984,9 +1986,10 @@ bool pick_kind(int kind, int nw, Variant& v) {
 
 template <typename T, bool kGen, bool kSinks, bool kTail>
 bool pick_dim(int kind, int d, int nw, Variant& v) {
-    if (d == 64) return pick_kind<T, 64, kGen, kSinks, kTail>(kind, nw, v);
-    if (d == 128) return pick_kind<T, 128, kGen, kSinks, kTail>(kind, nw, v);
-    return false;
+    if constexpr (kTail && (std::is_same<T, float>::value || std::is_same<T, int4kc>::value)) return false;
+    else return d == 64    ? pick_kind<T, 64, kGen, kSinks, kTail>(kind, nw, v)
+                : d == 128 ? pick_kind<T, 128, kGen, kSinks, kTail>(kind, nw, v)
+                           : false;
 }
 
 // The split-KV kernel for a cache dtype, kernel kind, head_dim and warps per

@@ -1,7 +1,7 @@
-// gqa_device.cuh -- device helpers shared by the decode and append kernels:
-// inline PTX for mbarriers, TMA (cp.async.bulk.tensor / cp.async.bulk),
-// warp-level bf16/f16 tensor-core MMA, exp2 and small packing routines.
-// sm_103a only.
+// gqa_device.cuh -- device helpers shared by the kernels: inline PTX for
+// mbarriers, TMA (cp.async.bulk.tensor / cp.async.bulk), cp.async, warp-level
+// and 5th-generation (tcgen05) tensor-core MMA, packed fp32 pairs, exp2 and
+// small packing routines. sm_103a only.
 #pragma once
 
 #include <cuda.h>
@@ -99,7 +99,7 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity,
 }
 
 // The same with a limit on the tries instead of a clock: less code in kernels of many
-// waits. A try that fails takes 4 us here, so this is a second as well.
+// waits. A try that fails takes 4 us on a GB300, so this is a second as well.
 constexpr uint32_t kWaitTries = 1u << 18;
 __device__ __forceinline__ bool mbar_wait_tries(uint32_t bar, uint32_t parity, uint32_t tries = kWaitTries) {
     for (uint32_t i = 0; i < tries; ++i)
