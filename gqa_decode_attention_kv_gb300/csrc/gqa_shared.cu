@@ -22,6 +22,15 @@
 // The (group, kv-head, tile) problems are laid out one behind the other in steps and cut
 // into equal runs, one per CTA of a single resident wave, so a long prefix is split over
 // the whole GPU however few rows share it, and the pieces are joined by the merge.
+//
+// What bounds it: with 256 rows a step's products (S, and P V for both parts of P) are 1880
+// cycles at the rate of a library's bf16 product, and a step takes 1790, in which the softmax
+// issues as much; dropping the exponentials, one part of P or S alone changes that by less
+// than 5%. Coded steps take 2900 cycles, bound by the instructions that widen and scale. Few
+// rows leave K and V to wait for. Around the steps: 8 to 10 us until the first (launch, sums
+// of the plan, table, K), 4 for the last step's output, 4 to 6 for the merge. 32 rows of H=64,
+// K=8, d=128 behind 32768 tokens take 57 us (plain decode 465), 64 rows of H=32 behind 4096
+// and 100 to 700 of their own 37, 128 rows of H=64 in four groups over int8 103.
 #include <algorithm>
 
 #include "gqa_decode_kernels.cuh"
@@ -1084,6 +1093,11 @@ Form pick_coded(int d) {
     return d == 64 ? form<T, 2, 64>() : form<T, 2, 128>();
 }
 
+// The form: two tiles a CTA where a group has more than 128 query rows, else one, twice an SM.
+// d=128, K=8, behind 32768 tokens, one tile | two: 32 rows 37 | 43 us, 128 rows 43 | 78 (a
+// second tile that is empty), 136 rows 59 | 53, 256 rows 97 | 57; d=64: 37 | 39 with 128 rows,
+// 74 | 63 with 256. Behind 2048 tokens they differ by 2 us at most. Coded caches have two tiles
+// alone: their copy warps are half of what a second CTA would add.
 bool pick_form(const DecodeLaunch& L, Form& f) {
     const int GT = L.num_heads / L.cache->num_kv_heads * L.tokens_per_seq, d = L.cache->head_dim;
     const long long rows = (long long)std::min(L.shared->max_group > 0 ? L.shared->max_group : L.batch, L.batch) * GT;
@@ -1128,33 +1142,45 @@ PrefixWs prefix_ws(long long batch, long long rows, int d, int sms) {
     return w;
 }
 
-// The times behind the GPU's division, measured over prefixes of up to 32768 tokens and tails
-// of 1 to 60 blocks. A step of 256 rows takes an SM 0.95 us (coded 1.5; 128 rows in two CTAs
-// 0.6). Of the rows' own a (block, kv-head) takes 0.19 us in a 16-bit cache of 128 dims, 0.15
-// with 8-bit codes, 0.14 with 4-bit ones (0.135, 0.1 and 0.085 on a few SMs, where HBM keeps
-// up), 1.6 with codes on the CUDA cores (head_dim 64); a (row, kv-head) 0.13, coded 0.5, which
-// is most of it for rows that have just begun: 17 rows of up to 2 blocks behind 32768 tokens
-// take 53 us where they count as blocks alone 82. All at 8 query rows; 32 take about 3 times
-// as long for a block and 5 for a row. They pick how the SMs are dealt out and change no
-// result.
+// The times behind the GPU's division, in us of an SM, each from the difference of two lengths:
+// a step of the prefix kernel; a (block, kv-head) and a (row, kv-head) of the rows' own, the
+// latter most of it for rows that have just begun (17 rows of up to 2 blocks behind 32768
+// tokens take 53 us where they count as blocks alone 82). By the split-KV kernel's warps per
+// pair, 1 for up to 8 query rows; on the CUDA cores (codes at head_dim 64) by its rows. Rows
+// take half as long again beside the prefix kernel. Over 28 batches of every type, division by
+// these takes 2% less time than with the steps or the blocks 10% dearer, and 125 rows of 50
+// blocks of int4 codes, d=64, 110 us where a block counts 1.6 whatever the rows (296). They
+// pick how the SMs are dealt out and change no result.
 SplitModel split_of(const DecodeLaunch& L, const Form& f, int sms) {
     const gqa_kv_cache_t& c = *L.cache;
     const int GT = L.num_heads / c.num_kv_heads * L.tokens_per_seq;
     const bool coded = dtype_coded(c.dtype), wide = c.head_dim == 128;
+    const int w = GT <= 8 ? 0 : GT <= 16 ? 1 : GT <= 32 ? 2 : 3;
+    static const float kUnit[4][4] = {{0.178f, 0.178f, 0.42f, 0.82f},      // 16-bit, d = 128
+                                      {0.095f, 0.126f, 0.31f, 0.59f},      // d = 64
+                                      {0.133f, 0.218f, 0.465f, 0.98f},     // 8-bit codes
+                                      {0.122f, 0.206f, 0.425f, 0.9f}};     // 4-bit
+    static const float kPair[3][4] = {{0.2f, 0.47f, 1.1f, 2.25f}, {0.12f, 0.28f, 0.68f, 1.35f}, {0.75f, 1.35f, 2.7f, 5.4f}};
     SplitModel m;
     m.sms = sms;
     m.ctas_per_sm = f.ctas_per_sm;
     m.cta_rows = f.rows;
     m.min_steps = 2;
-    m.step_us = (coded ? 1.5f : f.rows > kRows ? 0.95f : 1.2f) * (wide ? 1.f : 0.7f);
     m.prefix_us = 9.f;
-    m.unit_us = coded ? (!wide ? 1.6f : dtype_bits(c.dtype) == 8 ? 0.15f : 0.14f) : wide ? 0.19f : 0.1f;
-    m.pair_us = coded ? 0.5f : wide ? 0.13f : 0.08f;
-    if (GT > 8) {
-        m.unit_us *= coded ? GT / 8.f : std::max(1.6f, GT / 13.f);
-        m.pair_us *= GT / 8.f;
-    }
     m.tail_us = 4.f;
+    if (coded) {
+        m.step_us = wide ? 1.5f : 1.3f;
+        m.unit_us = kUnit[dtype_bits(c.dtype) == 8 ? 2 : 3][w];
+        m.pair_us = kPair[2][w];
+        if (!wide) {
+            m.unit_us = (GT + 7) / 8 * (0.16f + 0.177f * std::min(GT, 8));
+            m.pair_us = (GT + 7) / 8 * 0.5f;
+        }
+    } else {
+        m.step_us = f.rows > kRows ? (wide ? 1.f : 0.8f) : (wide ? 1.4f : 1.f);
+        m.unit_us = kUnit[wide ? 0 : 1][w];
+        m.pair_us = kPair[wide ? 0 : 1][w];
+    }
     return m;
 }
 
