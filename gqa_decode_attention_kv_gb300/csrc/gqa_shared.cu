@@ -23,14 +23,15 @@
 // into equal runs, one per CTA of a single resident wave, so a long prefix is split over
 // the whole GPU however few rows share it, and the pieces are joined by the merge.
 //
-// What bounds it: with 256 rows a step's products (S, and P V for both parts of P) are 1880
-// cycles at the rate of a library's bf16 product, and a step takes 1790, in which the softmax
-// issues as much; dropping the exponentials, one part of P or S alone changes that by less
-// than 5%. Coded steps take 2900 cycles, bound by the instructions that widen and scale. Few
-// rows leave K and V to wait for. Around the steps: 8 to 10 us until the first (launch, sums
-// of the plan, table, K), 4 for the last step's output, 4 to 6 for the merge. 32 rows of H=64,
-// K=8, d=128 behind 32768 tokens take 57 us (plain decode 465), 64 rows of H=32 behind 4096
-// and 100 to 700 of their own 37, 128 rows of H=64 in four groups over int8 103.
+// What bounds it: with 256 rows a step's products (S, and P V for both parts of P) are 1536
+// cycles at the 8192 flop a cycle of an SM's tensor cores, and a step takes 1790, in which the
+// softmax issues about as long: dropping the exponentials, one part of P or S alone changes
+// that by less than 5%. Coded steps take 2900 cycles, bound by the instructions that widen and
+// scale. With few rows K and V arrive at the copy rate (two CTAs of 128 rows: 64 KB in 1.4 us
+// an SM, 6.9 TB/s). Around the steps: 8 to 10 us until the first (launch, sums of the plan,
+// table, K), 4 for the last step's output, 4 to 6 for the merge. 32 rows of H=64, K=8, d=128
+// behind 32768 tokens take 57 us (gqa_decode 464), 64 rows of H=32 behind 4096 and 100 to 700
+// of their own 37, 128 rows of H=64 in four groups over int8 103.
 #include <algorithm>
 
 #include "gqa_decode_kernels.cuh"
@@ -1094,10 +1095,11 @@ Form pick_coded(int d) {
 }
 
 // The form: two tiles a CTA where a group has more than 128 query rows, else one, twice an SM.
-// d=128, K=8, behind 32768 tokens, one tile | two: 32 rows 37 | 43 us, 128 rows 43 | 78 (a
-// second tile that is empty), 136 rows 59 | 53, 256 rows 97 | 57; d=64: 37 | 39 with 128 rows,
-// 74 | 63 with 256. Behind 2048 tokens they differ by 2 us at most. Coded caches have two tiles
-// alone: their copy warps are half of what a second CTA would add.
+// K=8, behind 32768 tokens, one tile | two: d=128 with 32 rows 37 | 43 us, 128 rows 43 | 47 (a
+// second tile that is empty), 136 rows 61 | 52, 256 rows 69 | 57; d=64 with 32 rows 31 | 37, 128
+// rows 38 | 39, 136 rows 48 | 45, 256 rows 62 | 47. Behind 2048 tokens they differ by 2 us
+// (d=64, 256 rows: 29 | 25). Coded caches have two tiles alone: their copy warps need the SM's
+// issue slots that a second CTA would take.
 bool pick_form(const DecodeLaunch& L, Form& f) {
     const int GT = L.num_heads / L.cache->num_kv_heads * L.tokens_per_seq, d = L.cache->head_dim;
     const long long rows = (long long)std::min(L.shared->max_group > 0 ? L.shared->max_group : L.batch, L.batch) * GT;
@@ -1147,17 +1149,19 @@ PrefixWs prefix_ws(long long batch, long long rows, int d, int sms) {
 // latter most of it for rows that have just begun (17 rows of up to 2 blocks behind 32768
 // tokens take 53 us where they count as blocks alone 82). By the split-KV kernel's warps per
 // pair, 1 for up to 8 query rows; on the CUDA cores (codes at head_dim 64) by its rows. Rows
-// take half as long again beside the prefix kernel. Over 28 batches of every type, division by
-// these takes 2% less time than with the steps or the blocks 10% dearer, and 125 rows of 50
-// blocks of int4 codes, d=64, 110 us where a block counts 1.6 whatever the rows (296). They
-// pick how the SMs are dealt out and change no result.
+// take half as long again beside the prefix kernel, and so does a block of 9 to 16 rows at
+// head_dim 64 by a quarter. 125 rows of 50 blocks of int4 codes, d=64: 110 us, where a block
+// counts 1.6 whatever the rows 296; over 28 batches of every type, steps or blocks that count a
+// tenth more cost up to 2%. Rounding the prefix's time to whole steps of a CTA costs its two
+// divisions, 1 us, and no batch gained that. The times pick how the SMs are dealt out and
+// change no result.
 SplitModel split_of(const DecodeLaunch& L, const Form& f, int sms) {
     const gqa_kv_cache_t& c = *L.cache;
     const int GT = L.num_heads / c.num_kv_heads * L.tokens_per_seq;
     const bool coded = dtype_coded(c.dtype), wide = c.head_dim == 128;
     const int w = GT <= 8 ? 0 : GT <= 16 ? 1 : GT <= 32 ? 2 : 3;
     static const float kUnit[4][4] = {{0.178f, 0.178f, 0.42f, 0.82f},      // 16-bit, d = 128
-                                      {0.095f, 0.126f, 0.31f, 0.59f},      // d = 64
+                                      {0.1f, 0.16f, 0.31f, 0.59f},      // d = 64
                                       {0.133f, 0.218f, 0.465f, 0.98f},     // 8-bit codes
                                       {0.122f, 0.206f, 0.425f, 0.9f}};     // 4-bit
     static const float kPair[3][4] = {{0.2f, 0.47f, 1.1f, 2.25f}, {0.12f, 0.28f, 0.68f, 1.35f}, {0.75f, 1.35f, 2.7f, 5.4f}};
@@ -1174,7 +1178,7 @@ SplitModel split_of(const DecodeLaunch& L, const Form& f, int sms) {
         m.pair_us = kPair[2][w];
         if (!wide) {
             m.unit_us = (GT + 7) / 8 * (0.16f + 0.177f * std::min(GT, 8));
-            m.pair_us = (GT + 7) / 8 * 0.5f;
+            m.pair_us = (GT + 7) / 8 * 0.5f + m.unit_us;
         }
     } else {
         m.step_us = f.rows > kRows ? (wide ? 1.f : 0.8f) : (wide ? 1.4f : 1.f);
