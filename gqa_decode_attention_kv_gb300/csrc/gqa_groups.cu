@@ -10,11 +10,13 @@
 //           saving, then fewer rows, so the larger P at equal saving)
 //   places  groups in the order of their leaders, members by row
 // The tables are read once as far as rows agree (the leaders' rows come from L2), which is
-// a few microseconds at most: the steps' latencies bound this. Up to 128 rows one cluster
-// of eight CTAs does all three, a warp per row, with one cluster barrier; more rows take a
-// launch per step over the whole GPU, where the two passes over all pairs of rows run from
-// shared memory. Replayed from a graph: 16 rows 6.3 us (8.2 in three launches), 256 rows 10.3,
-// 2048 rows of up to 1700 shared pages 23.2 (50 with the passes over pairs from L2).
+// a few microseconds at most: the steps' latencies bound this. Up to 256 rows one cluster
+// of eight CTAs does all three, a warp for one or two rows, with one cluster barrier; more rows
+// take a launch per step over the whole GPU, where the two passes over all pairs of rows run
+// from shared memory. Cluster | launches: in a graph 16 rows 8 us, 129 rows 10.3 | 10.3, 256
+// rows 14.4 | 10.3, 512 rows 26.6 | 12.4; a call from Python with its views 24.5 | 31 at any of
+// these, which is what a plan that is made once for many steps costs. 2048 rows of up to 1700
+// shared pages take 23 (50 with the passes over pairs from L2).
 #include "gqa_groups.cuh"
 #include "gqa_internal.h"
 
@@ -34,7 +36,7 @@ struct GroupsArgs {
 
 constexpr int kRunThreads = 128, kRunUnroll = 4;
 constexpr int kPairThreads = 512, kPairRows = kPairThreads / 32;   // a warp per row
-constexpr int kSmallCtas = 8, kSmallRows = kSmallCtas * kPairRows;
+constexpr int kSmallCtas = 8, kSmallWarps = kSmallCtas * kPairRows, kSmallRows = 256;
 constexpr int kRankBits = 14;
 constexpr unsigned kRankMask = (1u << kRankBits) - 1;
 
@@ -55,8 +57,9 @@ struct Places {
     __device__ __forceinline__ Places(int* p, int B) : lead(p), pages(p + B), start(p + 2 * B), number(p + 3 * B) {}
 };
 
-// Rows first_row + warp of the plan, from lead and pages (all of the block's threads).
-__device__ __forceinline__ void place_rows(int32_t* plan, int B, const Places& s, int first_row, int2* s_sum) {
+// Rows first_row + warp of the plan, and every `stride` after, from lead and pages (all of the
+// block's threads).
+__device__ __forceinline__ void place_rows(int32_t* plan, int B, const Places& s, int first_row, int stride, int2* s_sum) {
     constexpr int kWarps = kPairThreads / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     for (int r = tid; r < B; r += kPairThreads) s.start[r] = 0;
@@ -101,35 +104,35 @@ __device__ __forceinline__ void place_rows(int32_t* plan, int B, const Places& s
         at.y += c > 0;
     }
     __syncthreads();
-    const int b = first_row + warp;
-    if (b >= B) return;
-    const int lead = s.lead[b];
-    int rank = 0;                              // members of the group before the row
-    if (lead >= 0) {
-#pragma unroll 4
-        for (int r = lead + lane; r < b; r += 32) rank += s.lead[r] == lead;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) rank += __shfl_xor_sync(kFull, rank, o);
-    }
-    if (lane != 0) return;
     const GroupsLayout l(B);
-    const int slot = lead >= 0 ? s.start[lead] + rank : -1, number = lead >= 0 ? s.number[lead] : -1;
-    if (b == 0) {
-        plan[0] = all.y;
-        plan[1] = all.x;
-        plan[l.start + B] = all.x;
-    }
-    plan[l.slot + b] = slot;
-    plan[l.group + b] = number;
-    if (lead >= 0) plan[l.rows + slot] = b;
-    if (lead == b) {
-        plan[l.start + number] = slot;
-        plan[l.blocks + number] = s.pages[b];
-    }
-    if (b >= all.x) plan[l.rows + b] = -1;
-    if (b >= all.y) {
-        plan[l.start + b] = all.x;
-        plan[l.blocks + b] = 0;
+    for (int b = first_row + warp; b < B; b += stride) {
+        const int lead = s.lead[b];
+        int rank = 0;                          // members of the group before the row
+        if (lead >= 0) {
+#pragma unroll 4
+            for (int r = lead + lane; r < b; r += 32) rank += s.lead[r] == lead;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) rank += __shfl_xor_sync(kFull, rank, o);
+        }
+        if (lane != 0) continue;
+        const int slot = lead >= 0 ? s.start[lead] + rank : -1, number = lead >= 0 ? s.number[lead] : -1;
+        if (b == 0) {
+            plan[0] = all.y;
+            plan[1] = all.x;
+            plan[l.start + B] = all.x;
+        }
+        plan[l.slot + b] = slot;
+        plan[l.group + b] = number;
+        if (lead >= 0) plan[l.rows + slot] = b;
+        if (lead == b) {
+            plan[l.start + number] = slot;
+            plan[l.blocks + number] = s.pages[b];
+        }
+        if (b >= all.x) plan[l.rows + b] = -1;
+        if (b >= all.y) {
+            plan[l.start + b] = all.x;
+            plan[l.blocks + b] = 0;
+        }
     }
 }
 
@@ -233,7 +236,7 @@ __global__ void __launch_bounds__(kPairThreads) places_kernel(const GroupsArgs a
         s.lead[r] = s.pages[o.x] > 0 && o.y >= s.pages[o.x] ? o.x : -1;
     }
     __syncthreads();
-    place_rows(a.plan, a.B, s, blockIdx.x * kPairRows, s_sum);
+    place_rows(a.plan, a.B, s, blockIdx.x * kPairRows, kMaxGroupRows, s_sum);
 }
 
 // All three steps for up to kSmallRows rows.
@@ -243,23 +246,25 @@ __global__ void __cluster_dims__(kSmallCtas) __launch_bounds__(kPairThreads) sma
     __shared__ int s_places[4 * kSmallRows];
     __shared__ int2 s_sum[kPairThreads / 32];
     const Places s(s_places, a.B);
-    const int tid = threadIdx.x, lane = tid & 31, b = blockIdx.x * kPairRows + (tid >> 5);
+    const int tid = threadIdx.x, lane = tid & 31, row0 = blockIdx.x * kPairRows;
     launch_dependents();
     grid_dependency_wait();
-    if (b < a.B) {
+    for (int b = row0 + (tid >> 5); b < a.B; b += kSmallWarps) {
         const int32_t* mine = a.block_tables + (long long)b * a.max_blocks;
         const int n = full_pages(a, b);
         if (lane == 0 && n < 0) flag_error(a.err, GQA_DEVERR_CONTEXT_LEN);
         const int key = n > 0 ? mine[0] : -1;
         int leader = b, run = 0;
         if (key >= 0) {                        // uniform per warp
-            int first = b;
+            for (int base = 0; base < b && leader == b; base += 32 * kRunUnroll) {
+                int first = b;
 #pragma unroll
-            for (int i = kSmallRows / 32 - 1; i >= 0; --i) {
-                const int r = 32 * i + lane;
-                if (r < b && a.block_tables[(long long)r * a.max_blocks] == key && full_pages(a, r) > 0) first = r;
+                for (int i = kRunUnroll - 1; i >= 0; --i) {
+                    const int r = base + 32 * i + lane;
+                    if (r < b && a.block_tables[(long long)r * a.max_blocks] == key && full_pages(a, r) > 0) first = r;
+                }
+                leader = __reduce_min_sync(kFull, first);
             }
-            leader = __reduce_min_sync(kFull, first);
             const int32_t* lead = a.block_tables + (long long)leader * a.max_blocks;
             const int most = min(n, full_pages(a, leader));
             run = most;
@@ -287,10 +292,9 @@ __global__ void __cluster_dims__(kSmallCtas) __launch_bounds__(kPairThreads) sma
         s_best[r] = 0ull;
     }
     __syncthreads();
-    constexpr int kParts = kPairThreads / kSmallRows;          // threads of a row
-    static_assert(kParts == 4, "four neighbouring threads count for a row");
-    {
-        const int r = tid / kParts;
+    constexpr int kParts = 4;                  // neighbouring threads that count for a row
+    for (int r0 = 0; r0 < a.B; r0 += kPairThreads / kParts) {
+        const int r = r0 + tid / kParts;
         int c = 0;
         int2 me = make_int2(0, 0);
         if (r < a.B) {
@@ -312,7 +316,7 @@ __global__ void __cluster_dims__(kSmallCtas) __launch_bounds__(kPairThreads) sma
         s.lead[r] = pages > 0 && o.y >= pages ? o.x : -1;
     }
     __syncthreads();
-    place_rows(a.plan, a.B, s, blockIdx.x * kPairRows, s_sum);
+    place_rows(a.plan, a.B, s, row0, kSmallWarps, s_sum);
 }
 
 }  // namespace

@@ -55,6 +55,16 @@ def test_forests(gq, B, wide, roots, min_blocks):
     same(gq, *forest(rng, B, wide, roots), min_blocks)
 
 
+@pytest.mark.parametrize("B", [16, 127, 128, 129, 255, 256, 257, 511, 513])
+def test_one_launch_and_several(gq, B):
+    """Around the sizes where a warp takes another row and where a launch per step begins."""
+    rng = np.random.default_rng(B)
+    same(gq, *forest(rng, B, 150, max(1, B // 17)))
+    table, lens = forest(rng, B, 3, B)                       # hardly anything shared
+    lens[::5] = 16 * 3 + 1                                   # past the table
+    same(gq, table, lens, flag=gq.GQA_DEVERR_CONTEXT_LEN)
+
+
 def test_nothing_shared(gq):
     table = np.arange(50 * 7, dtype=np.int32).reshape(50, 7)
     got = same(gq, table, np.full(50, 100, dtype=np.int32))
