@@ -419,6 +419,49 @@ def test_equals_decode_and_shares_its_workspace(gq):
     assert float((outs[0] - outs[1]).abs().max()) <= 2 * np.abs(values[1]).max() * 2.0 ** -11
 
 
+@pytest.mark.parametrize("kind,d,G,T", [("bf16", 128, 8, 1), ("f16", 64, 4, 3), ("int8", 64, 16, 1)])
+def test_most_rows(gq, kind, d, G, T):
+    """8191 rows in three groups, against plain decode."""
+    B, K = 8191, 2
+    cache, values = shared.pool(kind, 64, K, d, 80, gq)
+    gen = torch.Generator().manual_seed(81)
+    table = torch.randint(0, 64, (B, 4), generator=gen, dtype=torch.int32)
+    table[:, 0] = torch.arange(B) % 3
+    table[:, 1] = 3 + torch.arange(B) % 3
+    lens = torch.randint(32 + T, 65, (B,), generator=gen, dtype=torch.int32).cuda()
+    table = table.cuda()
+    q = torch.randn(B, T, K * G, d, generator=gen).to(shared.DTYPES.get(kind, torch.bfloat16)).cuda()
+    q = q if T > 1 else q[:, 0].contiguous()
+    plan = gq.kv_pages_groups(table, lens)
+    assert plan.count.tolist() == [3, B]
+    got = gq.gqa_decode_shared(cache, q, table, lens, 0.1, plan)
+    assert float((got - gq.gqa_decode(cache, q, table, lens, 0.1)).abs().max()) <= 2 * np.abs(values[1]).max() * 2.0 ** -11
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int8"])
+def test_pages_past_32_bits(gq, kind):
+    """Pages whose elements lie past 2^31, shared and own, in a pool of 140000."""
+    K, d, pages = 8, 128, 140000
+    bt = shared.batch([(20, [330, 350, 321])], [40], 82)
+    small, values = shared.pool(kind, bt.pages, K, d, 83, gq)
+    cache = gq.PagedKVCache.allocate(pages, K, d, small.k.dtype)
+    at = pages - bt.pages                                        # the last pages of the pool
+    for name in ("k", "v", "k_scale", "v_scale"):
+        if getattr(small, name) is not None:
+            getattr(cache, name)[at:] = getattr(small, name)
+    table = torch.from_numpy(np.where(bt.table >= 0, bt.table + at, -1).astype(np.int32)).cuda()
+    lens = torch.from_numpy(bt.lens).cuda()
+    q = torch.randn(4, 1, 4 * K, d, generator=torch.Generator().manual_seed(84)).bfloat16()
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = gq.gqa_decode_shared(cache, q[:, 0].contiguous().cuda(), table, lens, 0.1, gq.kv_pages_groups(table, lens), err=err)
+    assert int(err) == 0
+    want = shared.attend(q.double().numpy(), values, bt.table, bt.lens, 0.1)
+    check(got.view(q.shape).double().cpu().numpy(), want, values)
+    k, v = gq.kv_read(cache, table, torch.zeros(4, dtype=torch.int32, device="cuda"), max_tokens=1, dtype=torch.float32)
+    for b in range(4):
+        assert (k[b, 0].double().cpu().numpy() == shared.rows_of(values[0], bt.table, b, 1)[0]).all()
+
+
 def test_streams_and_graphs(gq):
     """Captured calls of one stream replayed on two, interleaved with eager ones."""
     bt = shared.batch([(30, [500 + i for i in range(7)])], [40], 11)
