@@ -94,7 +94,7 @@ __device__ __forceinline__ Problem problem_of(const GroupSpan& s, int K, int GT,
 // than its CTAs have min_steps each for. Called by whole warps: the lanes try 32 numbers at a
 // time (one after the other, by halving, takes 1.1 us before the first copy).
 __device__ __forceinline__ int prefix_sms(const SplitModel& m, int steps, int units, int pairs) {
-    if (steps == 0) return 0;
+    if (steps <= 0) return 0;                     // (below 0: the sum of a plan of overlapping groups)
     const int per_sm = m.min_steps * m.ctas_per_sm, most = min(m.sms, (steps + per_sm - 1) / per_sm);
     if (units == 0) return most;
     const int lane = threadIdx.x & 31, cap = max(1, min(most, m.sms - 2));

@@ -200,7 +200,7 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
     auto bar_p = [&](int t, int c) { return bar0 + 128 + 96 * t + 8 * (c & 3); };
     auto bar_q = [&](int t) { return bar0 + 256 + 8 * t; };
     const uint32_t tslot = bar0 + 272;
-    // [128] sums, then where the run begins: group, its step, its span, its leader
+    // [128] sums by warp (word 24: groups overlap), then where the run begins: group, its step, its span, its leader
     int* scan = reinterpret_cast<int*>(gb + C::kOffBar + 288);
     auto bar_full = [&](int cw, int c) { return bar0 + 832 + 32 * cw + 8 * (c & 3); };   // coded: copy warp cw's codes landed
     float* scales = reinterpret_cast<float*>(gb + C::kOffSc);
@@ -259,8 +259,12 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
     int U = 0, own = 0, own_rows = 0;
     {
         const int x0 = blocks_of(tid);
-        int blocks = x0, rows = x0 > 0, sum = units_of(mine, tid);
-        for (int i = tid + C::kThreads; i < n_groups; i += C::kThreads) sum += units_of(span_of(i), i);
+        int blocks = x0, rows = x0 > 0, sum = units_of(mine, tid), grouped = tid < n_groups ? mine.rows : 0;
+        for (int i = tid + C::kThreads; i < n_groups; i += C::kThreads) {
+            const GroupSpan x = span_of(i);
+            sum += units_of(x, i);
+            grouped += x.rows;                 // at most B * B < 2^26 in all
+        }
         for (int b = tid + C::kThreads; b < a.B; b += C::kThreads) {
             const int x = blocks_of(b);
             blocks += x;
@@ -272,10 +276,11 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
             blocks += __shfl_xor_sync(kFull, blocks, o);
             rows += __shfl_xor_sync(kFull, rows, o);
         }
+        grouped = __reduce_add_sync(kFull, grouped);
         if (lane == 0) {
             scan[warp] = sum;
             scan[32 + warp] = blocks;
-            scan[96 + warp] = rows;
+            scan[96 + warp] = rows | min(grouped, kMaxBatch + 1) << 13;      // kWarps of them stay below 2^31
         }
         __syncthreads();
 #pragma unroll
@@ -285,12 +290,17 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
             own_rows += scan[96 + i];
         }
     }
+    // Groups of more rows than there are overlap. Their steps could pass 32 bits, and the walk
+    // below the plan's end: nothing is shared then, and the merge flags it. (By way of shared
+    // memory: held in a register it costs the coded kernels spills.)
+    if (tid == 0) scan[24] = own_rows >> 13 > a.B;
+    own_rows &= kMaxBatch;
     const int P = max(1, prefix_sms(a.split, U, own * a.K, own_rows * a.K) * C::kCtasPerSm);
     const int R = max((U + P - 1) / P, a.split.min_steps);
     const int u_lo = (int)min((long long)U, (long long)j * R), u_hi = (int)min((long long)U, (long long)(j + 1) * R);
     if (j == 0 && tid == 0) {
         a.hdr[0] = R;
-        a.hdr[1] = U;
+        a.hdr[1] = scan[24] ? 0 : U;
         a.hdr[2] = C::kCtaRows;
     }
     int carry = 0;
@@ -330,7 +340,7 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(kFull, *reinterpret_cast<volatile uint32_t*>(gb + (tslot - sb)), 0);
-    if (u_lo >= u_hi) {                        // uniform per CTA
+    if (u_lo >= u_hi || scan[24]) {            // uniform per CTA
         if (warp == 0) tmem_dealloc(tmem, C::kTmemCols);
         return;
     }
@@ -986,7 +996,10 @@ __global__ void __launch_bounds__(kRowWarps * kCtaRows * 32) shared_merge_kernel
         const int u0 = unit0 + (g * pr.tiles + tile) * pr.chunks;
         j0 = u0 / R;
         n2 = (u0 + pr.chunks - 1) / R - j0 + 1;
-        if (u0 < 0 || pr.chunks > U - u0) n2 = 0;  // (a plan of overlapping groups: past 32 bits)
+        if (u0 < 0 || pr.chunks > U - u0) {    // a plan of overlapping groups: no steps
+            n2 = 0;
+            if (lane == 0) flag_error(a.err, GQA_DEVERR_ROW);
+        }
     }
     const int n = n1 + n2;
     auto piece_ml = [&](int x) -> const float2* {

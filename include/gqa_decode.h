@@ -69,7 +69,8 @@ typedef enum {
 #define GQA_DEVERR_CONTEXT_LEN 2   /* context length < 0 or > max_blocks_per_seq * 16 */
 #define GQA_DEVERR_POSITION    4   /* append position < 0 or >= max_blocks_per_seq * 16 */
 #define GQA_DEVERR_TIMEOUT     8   /* a bounded wait for an asynchronous copy expired */
-#define GQA_DEVERR_ROW        16   /* a row index outside the table, or a fork that may not be (see gqa_kv_pages_fork) */
+#define GQA_DEVERR_ROW        16   /* a row index outside the table, a fork that may not be (see gqa_kv_pages_fork),
+                                      or a plan of groups that overlap (see gqa_decode_shared) */
 #define GQA_DEVERR_NO_PAGES   32   /* not enough free pages for a row */
 #define GQA_DEVERR_REF_COUNT  64   /* a released page that no entry held */
 
@@ -598,7 +599,9 @@ GQA_API int gqa_decode_sinks(const gqa_kv_cache_t *cache, const void *q, int32_t
  *                  row of a group that is shorter than the shared pages and its T - 1
  *                  first new tokens (an empty one, say) attends alone. Entries of a plan
  *                  that point outside it or the tables share nothing; a plan that names
- *                  pages rows do not share gives those rows another row's prefix.
+ *                  pages rows do not share gives those rows another row's prefix. Groups do
+ *                  not overlap: a plan of groups that hold more rows than there are is flagged
+ *                  (GQA_DEVERR_ROW).
  *  max_group       rows of the largest group as the host knows them, 0 where it does not:
  *                  it picks the kernel's form and changes no result.
  *  workspace       device, >= gqa_decode_shared_workspace_size(...) bytes, otherwise as
