@@ -254,7 +254,11 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
         return b < a.B && r.len > 0 ? (r.len + kBlock - 1) / kBlock - r.blocks : 0;
     };
     GroupSpan mine = span_of(tid);
-    auto leader_of = [&](const GroupSpan& x) { return min(max(plan.rows[x.first], 0), a.B - 1); };
+    // a group's first row, -1: outside the batch, and its pages then count as missing (the merge flags it)
+    auto leader_of = [&](const GroupSpan& x) {
+        const int r = plan.rows[x.first];
+        return r < a.B ? max(r, -1) : -1;
+    };
     int lead = leader_of(mine);
     int U = 0, own = 0, own_rows = 0;
     {
@@ -397,6 +401,7 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
         bool iss_have = have;
         int iss_c = is.c0, issued = 0;
         const int32_t* table = a.block_tables + (long long)scan[133] * a.max_blocks;
+        if (scan[133] < 0) is.span.blocks = 0;
         int win = -(1 << 30), entries = -1;        // lane l: the page of entry win + l, -1: none
         auto issue = [&]() {                       // codes and scales of step `issued`
             const uint64_t pol = is.rows > C::kCtaRows ? again : once;
@@ -430,7 +435,9 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
             ++issued;
             if (++iss_c == is.c1 && (iss_have = step_seg(iw, is))) {
                 iss_c = is.c0;
-                table = a.block_tables + (long long)leader_of(is.span) * a.max_blocks;
+                const int leader = leader_of(is.span);
+                table = a.block_tables + (long long)leader * a.max_blocks;
+                if (leader < 0) is.span.blocks = 0;
                 win = -(1 << 30);
             }
         };
@@ -531,6 +538,7 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
             // the first segment's leader came with the scan
             const int leader = G == 0 ? scan[133] : leader_of(it.span);
             const int32_t* table = a.block_tables + (long long)leader * a.max_blocks;
+            if (leader < 0) it.span.blocks = 0;
             int win_base = -(1 << 30), win_phys = -1;
             for (int c = it.c0; c < it.c1 && ok; ++c, ++G) {
                 const int v0 = kChunkBlocks * c;
@@ -964,12 +972,14 @@ __global__ void __launch_bounds__(kRowWarps * kCtaRows * 32) shared_merge_kernel
     const int gv = g * a.NRG + rg, hh = rr - rg * dec::kHeadsPerWarp;
     const long long orow = (long long)bh * D;
     // what the earlier kernels read too needs no wait (this one starts once they have begun)
-    const SharedRow sr = shared_row(PrefixGroups(p.groups, a.B), a.context_lens, b, a.T, a.max_blocks);
+    const PrefixGroups plan(p.groups, a.B);
+    const SharedRow sr = shared_row(plan, a.context_lens, b, a.T, a.max_blocks);
     grid_dependency_wait();                    // the tail kernel, which ends after the prefix kernel
     if (blockIdx.x == 0 && tid == 0) *a.ws_ctr = 0ull;
     if (bh >= a.B * TH) return;                // uniform per warp, and per CTA where warps share a row
     const int p0 = a.ws_pref[b], nb = a.ws_pref[b + 1] - p0;
     const int R = p.hdr[0], U = p.hdr[1], cta_rows = p.hdr[2], unit0 = p.first_unit[sr.group];
+    const int leader = plan.rows[sr.span.first];
     Partition pt;
     pt.R = a.ws_hdr[0];
     pt.U = a.ws_hdr[1];
@@ -996,7 +1006,8 @@ __global__ void __launch_bounds__(kRowWarps * kCtaRows * 32) shared_merge_kernel
         const int u0 = unit0 + (g * pr.tiles + tile) * pr.chunks;
         j0 = u0 / R;
         n2 = (u0 + pr.chunks - 1) / R - j0 + 1;
-        if (u0 < 0 || pr.chunks > U - u0) {    // a plan of overlapping groups: no steps
+        // a plan of overlapping groups (no steps), or of a first row outside the batch (another's table)
+        if (u0 < 0 || pr.chunks > U - u0 || leader < 0 || leader >= a.B) {
             n2 = 0;
             if (lane == 0) flag_error(a.err, GQA_DEVERR_ROW);
         }

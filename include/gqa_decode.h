@@ -70,7 +70,7 @@ typedef enum {
 #define GQA_DEVERR_POSITION    4   /* append position < 0 or >= max_blocks_per_seq * 16 */
 #define GQA_DEVERR_TIMEOUT     8   /* a bounded wait for an asynchronous copy expired */
 #define GQA_DEVERR_ROW        16   /* a row index outside the table, a fork that may not be (see gqa_kv_pages_fork),
-                                      or a plan of groups that overlap (see gqa_decode_shared) */
+                                      or a plan that may not be (see gqa_decode_shared) */
 #define GQA_DEVERR_NO_PAGES   32   /* not enough free pages for a row */
 #define GQA_DEVERR_REF_COUNT  64   /* a released page that no entry held */
 
@@ -601,7 +601,7 @@ GQA_API int gqa_decode_sinks(const gqa_kv_cache_t *cache, const void *q, int32_t
  *                  that point outside it or the tables share nothing; a plan that names
  *                  pages rows do not share gives those rows another row's prefix. Groups do
  *                  not overlap: a plan of groups that hold more rows than there are is flagged
- *                  (GQA_DEVERR_ROW).
+ *                  (GQA_DEVERR_ROW), and so is a group whose first row is outside the batch.
  *  max_group       rows of the largest group as the host knows them, 0 where it does not:
  *                  it picks the kernel's form and changes no result.
  *  workspace       device, >= gqa_decode_shared_workspace_size(...) bytes, otherwise as

@@ -65,3 +65,29 @@ def test_overlapping_groups_whose_steps_pass_32_bits(gq):
     got = gq.gqa_decode_shared(cache, q, table, lens, 0.1, plan, err=err)
     assert int(err) == gq.GQA_DEVERR_ROW
     assert torch.isfinite(got).all()
+
+
+@pytest.mark.parametrize("kind", ["f16", "int4"])
+@pytest.mark.parametrize("bad", [-9, 7, 2 ** 31 - 1])
+def test_a_first_row_outside_the_batch_is_flagged(gq, kind, bad):
+    """The shared pages are read through it: the group's other rows do not get another row's. Rows
+    of the other group and alone, and the first row itself (in no slot now), are as they were."""
+    bt = shared.batch([(9, [150, 160, 170]), (12, [200, 210, 220])], [60], 40)
+    cache, values = shared.pool(kind, bt.pages, 2, 128, 41, gq)
+    B = len(bt.lens)
+    assert B == 7
+    q = torch.randn(B, 1, 8, 128, generator=torch.Generator().manual_seed(42)).to(shared.DTYPES.get(kind, torch.bfloat16))
+    table, lens = torch.from_numpy(bt.table).cuda(), torch.from_numpy(bt.lens).cuda()
+    plan = gq.kv_pages_groups(table, lens)
+    for slot in (0, 3):                                          # the first rows of both groups
+        fresh = gq.kv_pages_groups(table, lens)
+        rows = fresh.rows.tolist()
+        fresh.rows[slot] = bad
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        got = gq.gqa_decode_shared(cache, q[:, 0].contiguous().cuda(), table, lens, 0.1, fresh, err=err)
+        assert int(err) == gq.GQA_DEVERR_ROW
+        assert torch.isfinite(got).all()
+        want = shared.attend(q.double().numpy(), values, bt.table, bt.lens, 0.1)
+        rest = [b for b in range(B) if b not in rows[slot + 1:slot + 3]]
+        assert np.abs((got.view(q.shape).double().cpu().numpy() - want)[rest]).max() <= np.abs(values[1]).max() * 2.0 ** -11
+    assert plan.count.tolist() == [2, 6]
