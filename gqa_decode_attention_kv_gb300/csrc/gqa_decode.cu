@@ -272,16 +272,16 @@ int launch_decode(const DecodeLaunch& L, int num_sms) {
         if (st != GQA_OK) return st;
     }
     void* args[] = {&kmap, &vmap, &a};
-    e = cudaLaunchKernelExC(&cfg, v.fn, args);
-    if (e != cudaSuccess) return GQA_ERR_CUDA;
-    // From here the split-KV kernel has advanced the pool's ticket counter,
-    // which only the combine rewinds: a failure before the combine is queued
-    // rewinds it on the stream instead, so the next call on this workspace
-    // starts from zero.
+    // The split-KV kernel advances the pool's ticket counter, which only the
+    // combine rewinds (and the prefix kernel sets a word that the merge clears):
+    // a failure before the combine is queued clears the header on the stream
+    // instead, so the next call on this workspace starts from zero.
     auto fail_after_split = [&]() {
-        cudaMemsetAsync(a.ws_ctr, 0, sizeof(unsigned long long), L.stream);
+        cudaMemsetAsync(a.ws_hdr, 0, kWsHeaderInts * sizeof(int32_t), L.stream);
         return GQA_ERR_CUDA;
     };
+    e = cudaLaunchKernelExC(&cfg, v.fn, args);
+    if (e != cudaSuccess) return tail ? fail_after_split() : GQA_ERR_CUDA;
     if (L.ev_end && cudaEventRecord(L.ev_end, L.stream) != cudaSuccess) return fail_after_split();
     if (tail) return launch_shared_merge(a, L, ws + wl.total, num_sms) == GQA_OK ? GQA_OK : fail_after_split();
 

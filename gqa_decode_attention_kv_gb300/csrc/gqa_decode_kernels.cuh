@@ -1378,8 +1378,12 @@ __device__ int tail_workers(const DecodeArgs& a, const int* pref, int* tmp) {
 
 // The tail flavour runs beside the kernel before it, which attends the shared blocks and
 // lets this one start only after its own wait for earlier work: nothing that the workers
-// read is still being written. Its one CTA past the workers ends after that kernel, so that
-// the merge behind has both.
+// read is still being written. That what was written is also seen here, griddepcontrol
+// promises to a grid that waits alone; the workers take it from a word that the kernel before
+// stores behind its wait (with release) and they read first (with acquire; a trip to L2, which
+// costs a decode whose tail ends last 1 us: 128 rows over int8 104 to 106). That a read of the
+// word finds the last call's, which the merge has cleared, is left to the order of one address
+// in L2. The one CTA past the workers ends after that kernel, so that the merge behind has both.
 template <int kKind, typename T, int D, int kHeadWarps, bool kGen, bool kSinks, bool kTail>
 __global__ void __launch_bounds__(Cfg<kKind, T, D, kHeadWarps, kGen, kSinks, kTail>::kWarps * 32,
                                   Cfg<kKind, T, D, kHeadWarps, kGen, kSinks, kTail>::kMinCtas)
@@ -1406,6 +1410,8 @@ split_kv_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
     } else if (blockIdx.x == gridDim.x - 1) {
         grid_dependency_wait();
         return;
+    } else if (!acquire_nonzero(a.ws_hdr + kWsBegun)) {
+        if (threadIdx.x == 0) flag_error(a.err, GQA_DEVERR_TIMEOUT);
     }
     block_prefix<kGen, kSinks, kTail>(a, lens_s, pref, tmp, pref + a.B + 1);
     const Partition pt = make_partition(a, a.Kv * pref[a.B], kTail ? tail_workers<C>(a, pref, tmp) : a.P);

@@ -50,6 +50,27 @@ __device__ __forceinline__ void launch_dependents() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// A word that one kernel sets and another, which may run beside it, waits for: what the
+// first could see when it stored the word is then seen by the second too (release and
+// acquire over the GPU), by its TMA copies as well. Limited to half a second of reads from L2.
+__device__ __forceinline__ void store_release(int32_t* p, int v) {
+    asm volatile("st.release.gpu.global.b32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+__device__ __forceinline__ int load_acquire(const int32_t* p) {
+    int v;
+    asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ bool acquire_nonzero(const int32_t* p) {
+    for (int i = 0; i < 1 << 20; ++i) {
+        if (load_acquire(p) != 0) {
+            asm volatile("fence.proxy.async.global;" ::: "memory");
+            return true;
+        }
+    }
+    return false;
+}
+
 // ---------------------------------------------------------------- mbarrier
 
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {

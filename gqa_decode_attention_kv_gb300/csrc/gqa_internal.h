@@ -35,6 +35,8 @@ enum KernelKind { kKernelMma = 1, kKernelFma = 2 };
 
 // Fixed part of the decode workspace (header ints) before the block prefix.
 constexpr int kWsHeaderInts = 64;
+// Header int that says, in a shared decode, that everything before it has ended (0 between calls).
+constexpr int kWsBegun = 40;
 // Upper bound on decode warps per SM used for sizing the workspace.
 constexpr int kMaxWarpsPerSm = 64;
 constexpr int kMaxBatch = 8191;

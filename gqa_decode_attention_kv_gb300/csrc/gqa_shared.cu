@@ -33,6 +33,7 @@
 // behind 32768 tokens take 57 us (gqa_decode 464), 64 rows of H=32 behind 4096 and 100 to 700
 // of their own 37, 128 rows of H=64 in four groups over int8 103.
 #include <algorithm>
+#include <climits>
 
 #include "gqa_decode_kernels.cuh"
 #include "gqa_groups.cuh"
@@ -100,8 +101,9 @@ struct SharedArgs {
     int map_perm[3], page_perm[2];
     float scale_log2;
     SplitModel split;
+    int32_t* begun;      // for the tail kernel: everything before this one has ended
     int32_t* hdr;        // [0] steps per CTA, [1] all steps, [2] rows of a CTA
-    int32_t* first_unit; // [groups] first step of each group
+    int32_t* first_unit; // [groups] first step of each group, INT_MIN where its first row is outside the batch
     float2 *ml_a, *ml_b; // (m, l) of a problem's first piece by row, and of CTA j's continued one
     float *o_a, *o_b;    // their un-normalised outputs
 };
@@ -234,6 +236,7 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
     // The tail kernel behind this one does not wait for it: it may start only once
     // everything before this kernel has ended, which this wait makes sure of.
     grid_dependency_wait();
+    if (blockIdx.x == 0 && tid == 0) store_release(a.begun, 1);
     launch_dependents();
 
     // ---- the steps of all problems and the rows' own blocks, from them the CTAs that take
@@ -287,12 +290,9 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
             scan[96 + warp] = rows | min(grouped, kMaxBatch + 1) << 13;      // kWarps of them stay below 2^31
         }
         __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kWarps; ++i) {
-            U += scan[i];
-            own += scan[32 + i];
-            own_rows += scan[96 + i];
-        }
+        U = __reduce_add_sync(kFull, lane < kWarps ? scan[lane] : 0);
+        own = __reduce_add_sync(kFull, lane < kWarps ? scan[32 + lane] : 0);
+        own_rows = __reduce_add_sync(kFull, lane < kWarps ? scan[96 + lane] : 0);
     }
     // Groups of more rows than there are overlap. Their steps could pass 32 bits, and the walk
     // below the plan's end: nothing is shared then, and the merge flags it. (By way of shared
@@ -338,7 +338,7 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
             scan[132] = mine.blocks;
             scan[133] = lead;
         }
-        if (j == 0 && base + tid < n_groups) a.first_unit[base + tid] = first;
+        if (j == 0 && base + tid < n_groups) a.first_unit[base + tid] = lead < 0 ? INT_MIN : first;
     }
     tc_fence_before();
     __syncthreads();
@@ -971,15 +971,19 @@ __global__ void __launch_bounds__(kRowWarps * kCtaRows * 32) shared_merge_kernel
     const int rg = a.NRG > 1 ? rr / dec::kHeadsPerWarp : 0;
     const int gv = g * a.NRG + rg, hh = rr - rg * dec::kHeadsPerWarp;
     const long long orow = (long long)bh * D;
-    // what the earlier kernels read too needs no wait (this one starts once they have begun)
-    const PrefixGroups plan(p.groups, a.B);
-    const SharedRow sr = shared_row(plan, a.context_lens, b, a.T, a.max_blocks);
-    grid_dependency_wait();                    // the tail kernel, which ends after the prefix kernel
-    if (blockIdx.x == 0 && tid == 0) *a.ws_ctr = 0ull;
+    // What the earlier kernels read too needs no wait for them where their word is seen; where
+    // it is not, CTA 0 has cleared it already and the wait is over at once.
+    const bool begun = load_acquire(a.ws_hdr + kWsBegun) != 0;
+    if (!begun) grid_dependency_wait();
+    const SharedRow sr = shared_row(PrefixGroups(p.groups, a.B), a.context_lens, b, a.T, a.max_blocks);
+    if (begun) grid_dependency_wait();         // the tail kernel, which ends after the prefix kernel
+    if (blockIdx.x == 0 && tid == 0) {
+        *a.ws_ctr = 0ull;
+        a.ws_hdr[kWsBegun] = 0;
+    }
     if (bh >= a.B * TH) return;                // uniform per warp, and per CTA where warps share a row
     const int p0 = a.ws_pref[b], nb = a.ws_pref[b + 1] - p0;
     const int R = p.hdr[0], U = p.hdr[1], cta_rows = p.hdr[2], unit0 = p.first_unit[sr.group];
-    const int leader = plan.rows[sr.span.first];
     Partition pt;
     pt.R = a.ws_hdr[0];
     pt.U = a.ws_hdr[1];
@@ -1006,8 +1010,7 @@ __global__ void __launch_bounds__(kRowWarps * kCtaRows * 32) shared_merge_kernel
         const int u0 = unit0 + (g * pr.tiles + tile) * pr.chunks;
         j0 = u0 / R;
         n2 = (u0 + pr.chunks - 1) / R - j0 + 1;
-        // a plan of overlapping groups (no steps), or of a first row outside the batch (another's table)
-        if (u0 < 0 || pr.chunks > U - u0 || leader < 0 || leader >= a.B) {
+        if (u0 < 0 || pr.chunks > U - u0) {    // a first row outside the batch; overlapping groups: no steps
             n2 = 0;
             if (lane == 0) flag_error(a.err, GQA_DEVERR_ROW);
         }
@@ -1234,6 +1237,7 @@ SharedArgs make_args(const DecodeLaunch& L, const Form& f, uint8_t* ws, int sms)
     a.max_blocks = L.max_blocks;
     a.scale_log2 = L.scale * dec::kLog2e;
     a.split = split_of(L, f, sms);
+    a.begun = static_cast<int32_t*>(L.workspace) + kWsBegun;
     a.hdr = reinterpret_cast<int32_t*>(ws);
     a.first_unit = reinterpret_cast<int32_t*>(ws + w.first_unit);
     a.ml_a = reinterpret_cast<float2*>(ws + w.ml_a);

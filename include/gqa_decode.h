@@ -552,11 +552,11 @@ GQA_API size_t gqa_decode_workspace_size(int32_t batch, int32_t num_heads, int32
  *  out            device [batch, T, num_heads, head_dim] of out_dtype (F32,
  *                 BF16 or F16); 16-byte aligned.
  *  workspace      device, >= gqa_decode_workspace_size(...) bytes, 256-byte
- *                 aligned, zero-filled before its first use (one word of it, the
- *                 run-time work counter, must start at zero; every call leaves it
- *                 at zero again, a call failing with GQA_ERR_CUDA after its first
- *                 kernel was queued by a reset queued on the stream). Otherwise
- *                 clobbered by each call. Calls that
+ *                 aligned, zero-filled before its first use (the run-time words of its
+ *                 first 256 bytes must start at zero; every call leaves them at zero
+ *                 again, a call failing with GQA_ERR_CUDA after its first kernel was
+ *                 queued by a reset queued on the stream). Otherwise clobbered by each
+ *                 call. Calls that
  *                 share a workspace must not overlap on the GPU.
  *  opts           NULL or options (gqa_decode_opts_t).
  *  Limits: num_heads % K == 0; T * num_heads / K <= 64 query rows per kv-head;
