@@ -525,8 +525,9 @@ def kv_pages_groups(block_tables: torch.Tensor, context_lens: torch.Tensor, min_
         _dev(groups.plan, "groups.plan", True)
         if groups.batch != B or groups.plan.dim() != 1 or groups.plan.numel() * 4 < need:
             raise ValueError(f"groups was made for {groups.batch} rows, not {B}")
-    if B == 0:
-        groups.plan.zero_()
+    if B == 0:                                 # nothing to launch: a plan of no groups
+        with torch.cuda.stream(stream):        # (None: the current one)
+            groups.plan.zero_()
         return groups
     st = load().gqa_kv_pages_groups(tp, int(block_tables.shape[1]), lp, B, int(min_blocks), groups.plan.data_ptr(),
                                     groups.plan.numel() * 4, ep, _stream_ptr(stream))

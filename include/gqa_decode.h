@@ -424,7 +424,8 @@ GQA_API int gqa_kv_pages_trim(int32_t *ref_counts, int64_t num_blocks, int32_t *
  *            group  [B]   its group, -1: in none
  *          one behind the other, then scratch. A caller who knows the groups may write
  *          the arrays.
- *  A row whose length is out of range shares nothing (GQA_DEVERR_CONTEXT_LEN). batch <= 8192.
+ *  A row whose length is out of range shares nothing (GQA_DEVERR_CONTEXT_LEN). batch <= 8192;
+ *  gqa_decode_shared, as gqa_decode, takes up to 8191 rows.
  *  A plan stays right while its rows only append; rows that are freed, forked into,
  *  trimmed or compacted need a new one.
  */

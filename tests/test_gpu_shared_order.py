@@ -87,3 +87,21 @@ def test_a_workspace_serves_both_decodes_in_turn(gq):
         assert torch.equal(a, first[0]) and torch.equal(b, first[1])
         assert int(ws[128:164].view(torch.int32)[0]) == 0 and int(ws[160:164].view(torch.int32)[0]) == 0
     assert int(err) == 0
+
+
+def test_a_plan_of_no_rows_is_cleared_on_the_calls_stream(gq):
+    table = torch.full((0, 4), -1, dtype=torch.int32, device="cuda")
+    lens = torch.zeros(0, dtype=torch.int32, device="cuda")
+    plan = gq.kv_pages_groups(table, lens)
+    assert plan.count.tolist() == [0, 0]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)          # 10 ms
+        plan.plan.fill_(7)
+    gq.kv_pages_groups(table, lens, groups=plan, stream=side)
+    torch.cuda.synchronize()
+    assert plan.count.tolist() == [0, 0]
+    made = gq.kv_pages_groups(table, lens, stream=side)
+    side.synchronize()
+    assert made.count.tolist() == [0, 0] and made.start.tolist() == [0]
