@@ -6,14 +6,18 @@
 // the 16 rows of one (page, K or V, kv-head) at a time, all of its loads in flight before
 // the first store; a lane holds 8 elements of every second or fourth row, so that a store
 // instruction writes whole 128- to 256-byte pieces of a token's row. Of the copy rate: 16
-// prompts of 8192 tokens from a KIVI-style INT4 cache to bf16 0.92 (110 us), 8 prompts of 3000
-// to 8192 tokens from bf16 to fp32 0.90 (90), 37 ragged ones of FP8, d=64, to fp16 0.67 (25).
+// prompts of 8192 tokens to bf16 from a KIVI-style INT4 cache 0.92 (110 us), from int8 0.95
+// (126), e4m3 0.94 (126), int4 0.92 (108), at d=64 to fp16 from int8 0.88 (68), e4m3 0.83 (72);
+// 8 prompts of 3000 to 8192 tokens from bf16 to fp32 0.90 (90), 37 ragged ones of FP8, d=64, to
+// fp16 0.67 (25).
 #include <algorithm>
 
 #include "gqa_device.cuh"
 #include "gqa_internal.h"
 
 namespace gqa {
+
+int device_sms(int device);   // gqa_capi.cu
 
 namespace {
 
@@ -277,11 +281,12 @@ cudaError_t launch_kv_read(const gqa_kv_cache_t& c, void* k_out, void* v_out, in
     a.K = c.num_kv_heads;
     a.max_tokens = max_tokens;
     a.max_blocks = max_blocks;
-    // Four tiles a warp where that still fills the GPU, else fewer: a CTA first walks
-    // positions, table entry and data, one behind the other.
+    // Four tiles a warp where that still gives every SM eight CTAs (two to three waves of them),
+    // else fewer: a CTA first walks positions, table entry and data, one behind the other.
+    const long long enough = 8LL * std::max(1, device_sms(-1));
     const long long pages = ((long long)max_tokens + 2 * kBlock - 2) / kBlock;   // an unaligned run touches one more
     a.pages_per_cta = std::max(1, 2 * kReadThreads / 32 / c.num_kv_heads);
-    while (a.pages_per_cta > 1 && pages * batch < 1216LL * a.pages_per_cta) a.pages_per_cta /= 2;
+    while (a.pages_per_cta > 1 && pages * batch < enough * a.pages_per_cta) a.pages_per_cta /= 2;
     a.ctas_per_seq = (int)((pages + a.pages_per_cta - 1) / a.pages_per_cta);
     const long long grid = (long long)a.ctas_per_seq * batch;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
