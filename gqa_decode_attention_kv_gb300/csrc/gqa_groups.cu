@@ -13,10 +13,13 @@
 // a few microseconds at most: the steps' latencies bound this. Up to 256 rows one cluster
 // of eight CTAs does all three, a warp for one or two rows, with one cluster barrier; more rows
 // take a launch per step over the whole GPU, where the two passes over all pairs of rows run
-// from shared memory. Cluster | launches: in a graph 16 rows 8 us, 129 rows 10.3 | 10.3, 256
-// rows 14.4 | 10.3, 512 rows 26.6 | 12.4; a call from Python with its views 24.5 | 31 at any of
-// these, which is what a plan that is made once for many steps costs. 2048 rows of up to 1700
-// shared pages take 23 (50 with the passes over pairs from L2).
+// from shared memory. One launch | three, both in turn: replayed in a graph up to 96 rows 8.2 |
+// 8.2 us, 128 and 129 10.3 | 8.2, 160 to 224 12.3 | 10.3, 256 12.6 | 10.2; a call from Python
+// with its views 25 | 32 at any of these, into a plan's old memory (back to back) 7.0 | 11.4 up
+// to 128, 8.5 | 11.5 at 129, 10.0 | 11.1 at 192, 11.4 | 11.3 at 256. A plan is made once for
+// many steps, so the call's cost on the host sets the limit; a captured one pays 2 us for it
+// from 128 rows on. 2048 rows of up to 1700 shared pages take 23 (50 with the passes over pairs
+// from L2).
 #include "gqa_groups.cuh"
 #include "gqa_internal.h"
 
