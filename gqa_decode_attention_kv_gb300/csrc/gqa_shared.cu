@@ -1001,6 +1001,7 @@ __global__ void __launch_bounds__(kRowWarps * kCtaRows * 32) shared_merge_kernel
         first = (long long)b * a.Kv + gv + s0;
     }
     int n2 = 0, j0 = 0, in_tile = 0;
+    bool astray = false;
     long long row_a = 0;
     if (sr.blocks > 0) {
         const Problem pr = problem_of(sr.span, a.K, a.GT, cta_rows);
@@ -1010,11 +1011,10 @@ __global__ void __launch_bounds__(kRowWarps * kCtaRows * 32) shared_merge_kernel
         const int u0 = unit0 + (g * pr.tiles + tile) * pr.chunks;
         j0 = u0 / R;
         n2 = (u0 + pr.chunks - 1) / R - j0 + 1;
-        if (u0 < 0 || pr.chunks > U - u0) {    // a first row outside the batch; overlapping groups: no steps
-            n2 = 0;
-            if (lane == 0) flag_error(a.err, GQA_DEVERR_ROW);
-        }
+        astray = u0 < 0 || pr.chunks > U - u0; // a first row outside the batch; overlapping groups: no steps
+        if (astray) n2 = 0;
     }
+    if (astray && lane == 0) flag_error(a.err, GQA_DEVERR_ROW);      // (in the branch it costs the merge 1 us)
     const int n = n1 + n2;
     auto piece_ml = [&](int x) -> const float2* {
         if (x < n1) return a.ws_ml + (first + x) * a.RS + hh;
