@@ -15,7 +15,7 @@ would repeat the module name):
                               sliding window)
 * ``kv_append_varlen``     -- the same for a different number of new tokens per sequence
 * ``kv_read``              -- cached rows back as dense K and V, from any cache type
-* ``gqa_decode_shared``    -- ``gqa_decode`` for rows that share long prefixes, each attended once
+* ``gqa_decode_shared``    -- ``gqa_decode`` for rows that share long prefixes, each attended for all at once
 * ``rope_table``           -- (cos, sin) of every position and pair, for the two calls below
 * ``qk_norm_rope``         -- per-head norm of queries and keys and their rotation, one pass
 * ``qk_norm_rope_append``  -- the same with K and V written into the paged cache
@@ -503,7 +503,8 @@ def kv_pages_groups(block_tables: torch.Tensor, context_lens: torch.Tensor, min_
                     stream=None) -> PrefixGroups:
     """The rows of ``block_tables`` that begin with the same pages, for
     ``gqa_decode_shared``: of the rows with one first page those that have at least P full
-    pages in common with the lowest of them, where P >= ``min_blocks`` saves most reads.
+    pages in common with the lowest of them, where P >= ``min_blocks`` saves most reads
+    (a lowest row that is short or parts early costs its group the pages behind).
     Made once, it serves every step while rows only append; rows freed, forked into,
     trimmed or compacted need a new one (``groups`` takes the memory of an old one)."""
     tp, lp = _dev(block_tables, "block_tables", True), _dev(context_lens, "context_lens", True)
@@ -548,9 +549,10 @@ def gqa_decode_shared(cache: PagedKVCache, q: torch.Tensor, block_tables: torch.
                       out_dtype: torch.dtype = torch.float32, workspace: Optional[torch.Tensor] = None,
                       max_group: int = 0, err: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """``gqa_decode`` (full attention; q [B, H, d] or [B, T, H, d]) for rows that share
-    long prefixes: the pages a group of ``groups`` shares are read once for all of its
-    rows. ``max_group``, the rows of the largest group where the host knows them, picks
-    the kernel's form and changes no result."""
+    long prefixes: the pages a group of ``groups`` shares are read for all of its rows
+    together, once for every 256 query rows (rows * T * H / K) that it has for a kv-head.
+    ``max_group``, the rows of the largest group where the host knows them, picks the
+    kernel's form and changes no result; one that is too small costs further passes."""
     T = 1 if q.dim() == 3 else int(q.shape[1])
     B, H, d = q.shape[0], q.shape[-2], q.shape[-1]
     qp, tp, lp = _dev(q, "q"), _dev(block_tables, "block_tables", True), _dev(context_lens, "context_lens", True)

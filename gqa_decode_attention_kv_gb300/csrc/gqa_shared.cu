@@ -1,7 +1,8 @@
 // gqa_shared.cu -- decode attention for a batch whose rows share long prefixes. A group
 // of rows holds the same pages at the front of their block tables; its K and V are read
-// once and multiplied with the queries of all of them, one (kv-head, group) being a
-// problem of rows * G * T query rows. Three kernels, one behind the other:
+// and multiplied with the queries of all of them, one (kv-head, group) being a problem of
+// rows * G * T query rows: once for every 256 of those (a CTA's two tiles), or every 128 in
+// the form for groups of no more. Three kernels, one behind the other:
 //   prefix   (here) the shared blocks, for all rows of a group at once
 //   tail     (gqa_decode_tail.cu) every row's own blocks; runs beside the prefix kernel
 //   merge    (here) a row's pieces of both, with their log-sum-exp weights
@@ -27,11 +28,14 @@
 // cycles at the 8192 flop a cycle of an SM's tensor cores, and a step takes 1790, in which the
 // softmax issues about as long: dropping the exponentials, one part of P or S alone changes
 // that by less than 5%. Coded steps take 2900 cycles, bound by the instructions that widen and
-// scale. With few rows K and V arrive at the copy rate (two CTAs of 128 rows: 64 KB in 1.4 us
-// an SM, 6.9 TB/s). Around the steps: 8 to 10 us until the first (launch, sums of the plan,
-// table, K), 4 for the last step's output, 4 to 6 for the merge. 32 rows of H=64, K=8, d=128
-// behind 32768 tokens take 57 us (gqa_decode 464), 64 rows of H=32 behind 4096 and 100 to 700
-// of their own 37, 128 rows of H=64 in four groups over int8 103.
+// scale: over 48 int8 steps a scheduler issues 2475 a step. From 32768 to 98304 shared tokens
+// a step adds 1.10 us (bf16, fp16), 1.43 (int8), 1.49 (int4), 1.51 (e4m3). With few rows K and
+// V arrive at the copy rate (two CTAs of 128 rows: 64 KB in 1.4 us an SM, 6.9 TB/s). Around the
+// steps: 8 to 10 us until the first (launch, sums of the plan, table, K), 4 for the last step's
+// output, 4 to 6 for the merge. 32 rows of H=64, K=8, d=128 behind 32768 tokens take 56 us
+// (gqa_decode 464), 64 rows of H=32 behind 4096 and 100 to 700 of their own 36, 128 rows of H=64
+// in four groups behind 8192 and 100 to 900 over int8 106, e4m3 108, int4 107 (gqa_decode 484,
+// 496, 418), bf16 95 (500).
 #include <algorithm>
 #include <climits>
 
@@ -1177,7 +1181,8 @@ PrefixWs prefix_ws(long long batch, long long rows, int d, int sms) {
 // tokens take 53 us where they count as blocks alone 82). By the split-KV kernel's warps per
 // pair, 1 for up to 8 query rows; on the CUDA cores (codes at head_dim 64) by its rows. Rows
 // take half as long again beside the prefix kernel, and so does a block of 9 to 16 rows at
-// head_dim 64 by a quarter. 125 rows of 50 blocks of int4 codes, d=64: 110 us, where a block
+// head_dim 64 by a quarter (12 query rows over bf16, d=64, 41 us, where it does not 44; 1 query
+// row over int8, d=64, whose rows count a block besides, 39, where they do not 45). 125 rows of 50 blocks of int4 codes, d=64: 110 us, where a block
 // counts 1.6 whatever the rows 296; over 28 batches of every type, steps or blocks that count a
 // tenth more cost up to 2%. Rounding the prefix's time to whole steps of a CTA costs its two
 // divisions, 1 us, and no batch gained that. The times pick how the SMs are dealt out and
