@@ -341,6 +341,12 @@ def _check_new_rows(cache: "PagedKVCache", k_new: torch.Tensor, v_new: torch.Ten
                          f"head_dim are {(cache.num_kv_heads, cache.head_dim)}")
 
 
+def _int32(n: int) -> int:
+    """A bound as the C ABI takes it (ctypes would cut it to its low half): no count passes 2^31 - 1,
+    and what is below 0 is refused there."""
+    return max(-1, min(int(n), 2 ** 31 - 1))
+
+
 def _check(status: int, where: str):
     if status != 0:
         raise GqaError(status, where)
@@ -530,7 +536,7 @@ def kv_pages_groups(block_tables: torch.Tensor, context_lens: torch.Tensor, min_
         with torch.cuda.stream(stream):        # (None: the current one)
             groups.plan.zero_()
         return groups
-    st = load().gqa_kv_pages_groups(tp, int(block_tables.shape[1]), lp, B, int(min_blocks), groups.plan.data_ptr(),
+    st = load().gqa_kv_pages_groups(tp, int(block_tables.shape[1]), lp, B, _int32(min_blocks), groups.plan.data_ptr(),
                                     groups.plan.numel() * 4, ep, _stream_ptr(stream))
     _check(st, "gqa_kv_pages_groups")
     return groups
@@ -575,7 +581,7 @@ def gqa_decode_shared(cache: PagedKVCache, q: torch.Tensor, block_tables: torch.
     op, wp = _dev(out, "out"), _dev(workspace, "workspace")
     desc = cache.desc()
     st = load().gqa_decode_shared(ctypes.byref(desc), qp, DTYPE_CODE[q.dtype], H, tp, int(block_tables.shape[1]), lp, B,
-                                  T, float(scale), gp, int(max_group), op, DTYPE_CODE[out.dtype], wp,
+                                  T, float(scale), gp, _int32(max_group), op, DTYPE_CODE[out.dtype], wp,
                                   workspace.numel() * workspace.element_size(), ep, _stream_ptr(stream))
     _check(st, "gqa_decode_shared")
     return out
@@ -673,7 +679,7 @@ def kv_read(cache: PagedKVCache, block_tables: torch.Tensor, positions: torch.Te
         if int(total_tokens) < 0:
             raise ValueError(f"total_tokens must not be negative: {total_tokens}")
         shape = (int(total_tokens), cache.num_kv_heads, cache.head_dim)
-        n = min(int(total_tokens) if max_tokens is None else n, 2 ** 31 - 1)   # the C ABI's int32; no row count passes it
+        n = _int32(total_tokens if max_tokens is None else n)
     if dtype is None:
         dtype = k_out.dtype if k_out is not None else cache.k.dtype if cache.k.dtype in _ROW_DTYPES else torch.float32
     if dtype not in _ROW_DTYPES:

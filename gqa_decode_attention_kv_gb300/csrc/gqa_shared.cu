@@ -267,6 +267,7 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
         return r < a.B ? max(r, -1) : -1;
     };
     int lead = leader_of(mine);
+    static_assert(kWarps <= 24, "the sums by warp leave word 24 of the scan");
     int U = 0, own = 0, own_rows = 0;
     {
         const int x0 = blocks_of(tid);

@@ -91,3 +91,29 @@ def test_a_first_row_outside_the_batch_is_flagged(gq, kind, bad):
         rest = [b for b in range(B) if b not in rows[slot + 1:slot + 3]]
         assert np.abs((got.view(q.shape).double().cpu().numpy() - want)[rest]).max() <= np.abs(values[1]).max() * 2.0 ** -11
     assert plan.count.tolist() == [2, 6]
+
+
+@pytest.mark.parametrize("bound", [2 ** 31 - 1, 2 ** 31, 2 ** 32, 2 ** 32 + 1])
+def test_bounds_past_32_bits(gq, bound):
+    """No row shares so many pages; so large a group is one of more than 128 query rows."""
+    bt = shared.batch([(9, [150, 160, 170])], [60], 60)
+    cache, values = shared.pool("bf16", bt.pages, 2, 64, 61, gq)
+    table, lens = torch.from_numpy(bt.table).cuda(), torch.from_numpy(bt.lens).cuda()
+    assert gq.kv_pages_groups(table, lens, bound).count.tolist() == [0, 0]
+    q = torch.randn(4, 1, 8, 64, generator=torch.Generator().manual_seed(62)).bfloat16()
+    got = gq.gqa_decode_shared(cache, q[:, 0].contiguous().cuda(), table, lens, 0.1, gq.kv_pages_groups(table, lens),
+                               max_group=bound)
+    want = shared.attend(q.double().numpy(), values, bt.table, bt.lens, 0.1)
+    assert np.abs(got.view(q.shape).double().cpu().numpy() - want).max() <= np.abs(values[1]).max() * 2.0 ** -11
+
+
+@pytest.mark.parametrize("bound", [-1, -2 ** 32, -2 ** 32 + 7])
+def test_bounds_below_zero_are_refused(gq, bound):
+    table = torch.zeros(2, 4, dtype=torch.int32, device="cuda")
+    lens = torch.full((2,), 40, dtype=torch.int32, device="cuda")
+    with pytest.raises(gq.GqaError):
+        gq.kv_pages_groups(table, lens, bound)
+    cache, _ = shared.pool("bf16", 2, 2, 64, 63, gq)
+    q = torch.zeros(2, 8, 64, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(gq.GqaError):
+        gq.gqa_decode_shared(cache, q, table, lens, 0.1, gq.kv_pages_groups(table, lens), max_group=bound)
