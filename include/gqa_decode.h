@@ -413,11 +413,10 @@ GQA_API int gqa_kv_pages_trim(int32_t *ref_counts, int64_t num_blocks, int32_t *
  * group that shares P pages, where P >= max(1, min_blocks) makes P * (rows - 1) largest
  * (the larger P where two are equal); without a second row there is none. Groups are in
  * the order of their leaders, rows of a group in ascending order, the leader first.
- * One group for a first page, measured against one row, is what a single pass finds: where
- * the lowest row is short or parts early, so does its group (20 tokens in row 0 in front of
- * 31 rows with 40 pages in common: 32 rows over one page), and prompts behind one header
- * page are one group over that page. A caller who knows better puts a long row of a family
- * first, or writes the plan.
+ * All runs are measured against that one row: where it is short or parts early, its group
+ * shares as little (row 0 of 20 tokens in front of 31 rows with 40 pages in common: 32 rows
+ * over one page), and prompts behind one header page are one group over that page. A caller
+ * who knows better puts a long row of a family first, or writes the plan.
  *  groups  device int32, 16-byte aligned, gqa_kv_pages_groups_size(batch) bytes, with
  *          B = batch:
  *            [0], [1]     groups, rows in groups
@@ -610,10 +609,10 @@ GQA_API int gqa_decode_sinks(const gqa_kv_cache_t *cache, const void *q, int32_t
  *                  not overlap: a plan of groups that hold more rows than there are is flagged
  *                  (GQA_DEVERR_ROW), and so is a group whose first row is outside the batch.
  *  max_group       rows of the largest group as the host knows them, 0 where it does not
- *                  (the batch): it picks the kernel's form and changes no result. At up to
- *                  128 query rows a F16 or BF16 cache is read once for every 128, which is
- *                  faster where no group has more; a max_group that is too small makes
- *                  passes of a larger group's pages.
+ *                  (the batch): it picks the kernel's form and changes no result but its
+ *                  rounding. At up to 128 query rows an F16 or BF16 cache is read once for
+ *                  every 128, which is faster where no group has more; a max_group that is
+ *                  too small costs a larger group further passes.
  *  workspace       device, >= gqa_decode_shared_workspace_size(...) bytes, otherwise as
  *                  gqa_decode's (which it may be shared with).
  *  Cache dtypes: F16, BF16, I8, FP8_E4M3, I4; F32 and I4_KC are GQA_ERR_UNSUPPORTED. Scales
